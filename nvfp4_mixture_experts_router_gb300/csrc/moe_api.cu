@@ -2,13 +2,11 @@
 // tensor-map encoding and the launch sequence of the layer forward.  No
 // host synchronization and no allocation on the forward path: the expert
 // counts never leave the device (the GEMM tile schedulers read them).
-#include <cudaTypedefs.h>
-
 #include <cstring>
-#include <mutex>
 
 #include "../../include/moe_nvfp4.h"
 #include "common.cuh"
+#include "host.h"
 #include "kernels.h"
 #include "w4a16_swap.h"
 #include "layout.h"
@@ -16,65 +14,6 @@
 using namespace moe;
 
 namespace {
-
-struct DeviceState {
-    bool ready = false;
-    moe_status status = MOE_ERR_UNSUPPORTED;
-    int sms = 0;
-};
-
-std::mutex g_mu;
-DeviceState g_dev[64];
-PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
-
-moe_status device_state(int* sms, int* device = nullptr) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
-    if (dev < 0 || dev >= 64) return MOE_ERR_UNSUPPORTED;
-    std::lock_guard<std::mutex> lock(g_mu);
-    DeviceState& d = g_dev[dev];
-    if (!d.ready) {
-        d.ready = true;
-        int major = 0, minor = 0;
-        if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-            d.status = MOE_ERR_CUDA;
-        } else if (major != 10 || minor != 3) {
-            d.status = MOE_ERR_UNSUPPORTED;  // the binary carries sm_103a code only
-        } else if (setup_routing_kernels() != cudaSuccess || setup_gemm_kernels() != cudaSuccess ||
-                   setup_gemm_w4a16_kernels() != cudaSuccess || setup_gemm_pair_kernels(dev, d.sms) != cudaSuccess ||
-                   setup_gemm_w4a16_pair_kernels(dev, d.sms) != cudaSuccess ||
-                   setup_fused_layer_kernel() != cudaSuccess || setup_gemm_swap_kernels() != cudaSuccess ||
-                   setup_gemm_w4a16_swap_kernels() != cudaSuccess ||
-                   setup_router_gemm_kernel() != cudaSuccess) {
-            d.status = MOE_ERR_CUDA;
-        } else {
-            d.status = MOE_OK;
-        }
-        if (d.status == MOE_OK && g_encode == nullptr) {
-            void* fn = nullptr;
-            cudaDriverEntryPointQueryResult q;
-            if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) !=
-                    cudaSuccess ||
-                q != cudaDriverEntryPointSuccess || fn == nullptr) {
-                d.status = MOE_ERR_CUDA;
-            } else {
-                g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-            }
-        }
-    }
-    *sms = d.sms;
-    if (device) *device = dev;
-    return d.status;
-}
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + nb && y < x + na;
-}
 
 moe_status validate_shape(moe_shape s, uint32_t flags) {
     if (flags & ~MOE_FLAGS_KNOWN) return MOE_ERR_INVALID_ARG;
@@ -120,7 +59,7 @@ bool encode_operand_map(CUtensorMap* map, const void* base, uint64_t rows, uint6
     const cuuint64_t strides[1] = {row_bytes};
     const cuuint32_t box[2] = {box_bytes, box_rows};
     const cuuint32_t estr[2] = {1, 1};
-    const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
+    const CUresult r = tensor_map_encoder()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
                                 estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                                 box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -137,7 +76,7 @@ bool encode_chunk_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_
     const cuuint64_t strides[2] = {row_bytes, 128};
     const cuuint32_t box[3] = {128, box_rows, 2};
     const cuuint32_t estr[3] = {1, 1, 1};
-    const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box,
+    const CUresult r = tensor_map_encoder()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box,
                                 estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
@@ -154,7 +93,7 @@ bool encode_swap_weight_map(CUtensorMap* map, const void* base, uint64_t rows, u
     const cuuint64_t strides[2] = {row_bytes, 128 * row_bytes};
     const cuuint32_t box[3] = {box_bytes, 64, 2};
     const cuuint32_t estr[3] = {1, 1, 1};
-    const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box,
+    const CUresult r = tensor_map_encoder()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box,
                                 estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                                 box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -181,8 +120,6 @@ bool use_swap_gemm(moe_shape s, uint32_t flags) {
     const int64_t busy = routes < s.E ? routes : s.E;
     return routes >= kSwapMinRoutes && routes <= kSwapMaxRoutesPerExpert * busy;
 }
-
-moe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
 // Run a W4A4 GEMM with `n` weight rows per expert on CTA pairs?  Pair tiles
 // cover 256 routes of one expert; by default they are used when the experts
