@@ -40,6 +40,8 @@ MOE_DEBUG_FC1_SKIP_STAGE = 1 << 13
 MOE_ROUTER_GEMM = 1 << 14
 MOE_W8A8_MXFP8 = 3 << 2
 
+MOE_DTYPE_BF16, MOE_DTYPE_F32 = 0, 1
+
 
 class MoEError(RuntimeError):
     def __init__(self, fn: str, code: int):
@@ -75,6 +77,7 @@ def lib():
         L = ctypes.CDLL(LIB_PATH)
         P, S = ctypes.c_void_p, moe_shape
         u32, i64, sz = ctypes.c_uint32, ctypes.c_int64, ctypes.c_size_t
+        c, f = ctypes.c_int, ctypes.c_float
         sig = {
             "moe_nvfp4_version": (ctypes.c_char_p, []),
             "moe_nvfp4_prepared_bytes": (sz, [S, u32]),
@@ -92,6 +95,22 @@ def lib():
                                                        P, P, P, P, P, P, P, P]),
             "moe_nvfp4_router_logits": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_int, P, P, P, P]),
             "moe_nvfp4_forward_gate": (ctypes.c_int, [S, u32, P, P, P, P, P, P, P, sz, P, P]),
+            # training operators (moe_nvfp4_train.h)
+            "moe_nvfp4_sort_workspace_bytes": (sz, [c, c, c]),
+            "moe_nvfp4_sort_routes": (c, [c, c, c, P, P, P, P, P, P, sz, P]),
+            "moe_nvfp4_dispatch": (c, [c, c, c, i64, c, P, i64, P, P, P, P]),
+            "moe_nvfp4_dispatch_backward": (c, [c, c, c, i64, c, P, P, P, i64, P]),
+            "moe_nvfp4_combine": (c, [c, c, c, i64, c, P, P, P, P, i64, P]),
+            "moe_nvfp4_combine_backward": (c, [c, c, c, i64, c, P, i64, P, P, P, P, P, P, P]),
+            "moe_nvfp4_expert_linear": (c, [i64, c, c, c, P, P, P, P, P, P, P]),
+            "moe_nvfp4_expert_linear_dgrad": (c, [i64, c, c, c, P, P, P, P, P, P, P]),
+            "moe_nvfp4_expert_linear_wgrad": (c, [i64, c, c, c, P, P, P, P, P, P, P]),
+            "moe_nvfp4_layer_norm": (c, [c, c, c, P, i64, P, P, f, P, i64, P, P, P]),
+            "moe_nvfp4_layer_norm_workspace_bytes": (sz, [c, c]),
+            "moe_nvfp4_layer_norm_backward": (c, [c, c, c, P, i64, P, i64, P, P, P, P, i64, P, P, P, sz, P]),
+            "moe_nvfp4_grad_norm_workspace_bytes": (sz, [c]),
+            "moe_nvfp4_grad_norm": (c, [c, P, P, P, P, P, sz, P]),
+            "moe_nvfp4_grad_clip": (c, [c, P, P, P, P, P, f, f, P]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -108,6 +127,12 @@ EXPORTED = ["moe_nvfp4_version", "moe_nvfp4_prepared_bytes", "moe_nvfp4_prepare_
             "moe_nvfp4_last_device_status", "moe_nvfp4_debug_convert", "moe_nvfp4_route_noalloc",
             "moe_nvfp4_router_logits", "moe_nvfp4_forward_gate"]
 EXPORTED.sort()
+EXPORTED_TRAIN = ["moe_nvfp4_sort_workspace_bytes", "moe_nvfp4_sort_routes", "moe_nvfp4_dispatch",
+                  "moe_nvfp4_dispatch_backward", "moe_nvfp4_combine", "moe_nvfp4_combine_backward",
+                  "moe_nvfp4_expert_linear", "moe_nvfp4_expert_linear_dgrad", "moe_nvfp4_expert_linear_wgrad",
+                  "moe_nvfp4_layer_norm", "moe_nvfp4_layer_norm_workspace_bytes", "moe_nvfp4_layer_norm_backward",
+                  "moe_nvfp4_grad_norm_workspace_bytes", "moe_nvfp4_grad_norm", "moe_nvfp4_grad_clip"]
+EXPORTED_TRAIN.sort()
 NUM_STAGE_EVENTS = 8
 STAGES = ["router", "permute", "quantize_x", "fc1", "quantize_h", "fc2", "finalize"]
 
@@ -261,6 +286,269 @@ def moe_nvfp4_route_noalloc(T: int, E: int, K: int, flags: int, router_logits: t
                                          _ptr(out["offsets"]), _ptr(out["padded_offsets"]),
                                          _ptr(out["row_of_route"]), _ptr(out["route_of_row"]), _stream(stream))
     _check("moe_nvfp4_route_noalloc", code)
+
+
+# ---- training operators (moe_nvfp4_train.h) --------------------------------------
+
+def _rows2d(name: str, t: torch.Tensor, dtype: Optional[torch.dtype] = None) -> tuple:
+    """(tensor, row stride in elements) of a [T, H] tensor with contiguous rows."""
+    if t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor [T, H]")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if t.dtype not in _DTYPES:
+        raise TypeError(f"{name} must be bfloat16 or float32")
+    T, H = t.shape
+    if H > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    # the stride of a single row, and of none, says nothing
+    return t, (t.stride(0) if T > 1 else H)
+
+
+def _flat(name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple) -> torch.Tensor:
+    if t.dtype != dtype or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor of {dtype}")
+    if tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {list(shape)}")
+    return t
+
+
+_DTYPES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_F32}
+
+
+def moe_nvfp4_sort_workspace_bytes(T: int, E: int, K: int) -> int:
+    return int(lib().moe_nvfp4_sort_workspace_bytes(T, E, K))
+
+
+def moe_nvfp4_sort_routes(E: int, topk_ids: torch.Tensor, count: torch.Tensor, offsets: torch.Tensor,
+                          row_of_route: torch.Tensor, route_of_row: torch.Tensor, workspace: torch.Tensor,
+                          stream=None) -> None:
+    """Routes of topk_ids [T, K] sorted by expert (stable; ids outside [0, E)
+    are dropped): count [E], offsets [E + 1], row_of_route [T, K] and
+    route_of_row [T * K], all int32."""
+    T, K = topk_ids.shape
+    i32 = torch.int32
+    _flat("topk_ids", topk_ids, i32, (T, K))
+    _flat("count", count, i32, (E,))
+    _flat("offsets", offsets, i32, (E + 1,))
+    _flat("row_of_route", row_of_route, i32, (T, K))
+    _flat("route_of_row", route_of_row, i32, (T * K,))
+    code = lib().moe_nvfp4_sort_routes(T, E, K, topk_ids.data_ptr(), count.data_ptr(), offsets.data_ptr(),
+                                       row_of_route.data_ptr(), route_of_row.data_ptr(), workspace.data_ptr(),
+                                       workspace.numel() * workspace.element_size(), _stream(stream))
+    _check("moe_nvfp4_sort_routes", code)
+
+
+def _row_args(tokens: torch.Tensor, rows: torch.Tensor, row_of_route: torch.Tensor, what: str) -> tuple:
+    """Checks token rows [T, H], expert-ordered rows [rows, H] of the same type
+    and row_of_route [T, K]; returns (T, H, K, rows, dtype, token stride)."""
+    tokens, stride = _rows2d(what, tokens)
+    T, H = tokens.shape
+    if rows.dim() != 2 or rows.dtype != tokens.dtype or not rows.is_cuda or rows.shape[1] != H \
+            or not rows.is_contiguous():
+        raise ValueError(f"the expert-ordered rows must be contiguous [rows, {H}] of {tokens.dtype}")
+    K = row_of_route.shape[-1]
+    _flat("row_of_route", row_of_route, torch.int32, (T, K))
+    return T, H, K, rows.shape[0], _DTYPES[tokens.dtype], stride
+
+
+def _scalar_i32(name: str, t: Optional[torch.Tensor]):
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or not t.is_cuda or t.numel() != 1:
+        raise ValueError(f"{name} must be one CUDA int32")
+    return t.data_ptr()
+
+
+def moe_nvfp4_dispatch(x: torch.Tensor, row_of_route: torch.Tensor, rows_used: Optional[torch.Tensor],
+                       x_rows: torch.Tensor, stream=None) -> None:
+    """x_rows[row_of_route[t, k]] = x[t]; rows from rows_used (one device int32,
+    None: none) on are set to zero."""
+    T, H, K, rows, dt, stride = _row_args(x, x_rows, row_of_route, "x")
+    code = lib().moe_nvfp4_dispatch(T, H, K, rows, dt, x.data_ptr(), stride, row_of_route.data_ptr(),
+                                    _scalar_i32("rows_used", rows_used), x_rows.data_ptr(), _stream(stream))
+    _check("moe_nvfp4_dispatch", code)
+
+
+def moe_nvfp4_dispatch_backward(dx_rows: torch.Tensor, row_of_route: torch.Tensor, dx: torch.Tensor,
+                                stream=None) -> None:
+    """dx[t] = sum_k dx_rows[row_of_route[t, k]]."""
+    T, H, K, rows, dt, stride = _row_args(dx, dx_rows, row_of_route, "dx")
+    code = lib().moe_nvfp4_dispatch_backward(T, H, K, rows, dt, dx_rows.data_ptr(), row_of_route.data_ptr(),
+                                             dx.data_ptr(), stride, _stream(stream))
+    _check("moe_nvfp4_dispatch_backward", code)
+
+
+def moe_nvfp4_combine(o_rows: torch.Tensor, row_of_route: torch.Tensor, topk_w: torch.Tensor, y: torch.Tensor,
+                      stream=None) -> None:
+    """y[t] = sum_k topk_w[t, k] * o_rows[row_of_route[t, k]]."""
+    T, H, K, rows, dt, stride = _row_args(y, o_rows, row_of_route, "y")
+    _flat("topk_w", topk_w, torch.float32, (T, K))
+    code = lib().moe_nvfp4_combine(T, H, K, rows, dt, o_rows.data_ptr(), row_of_route.data_ptr(), topk_w.data_ptr(),
+                                   y.data_ptr(), stride, _stream(stream))
+    _check("moe_nvfp4_combine", code)
+
+
+def moe_nvfp4_combine_backward(dy: torch.Tensor, o_rows: torch.Tensor, row_of_route: torch.Tensor,
+                               topk_w: torch.Tensor, rows_used: Optional[torch.Tensor], do_rows: torch.Tensor,
+                               dw: torch.Tensor, stream=None) -> None:
+    """do_rows[row_of_route[t, k]] = topk_w[t, k] * dy[t] (rows from rows_used on
+    set to zero) and dw[t, k] = <dy[t], o_rows[row_of_route[t, k]]>."""
+    T, H, K, rows, dt, stride = _row_args(dy, o_rows, row_of_route, "dy")
+    _flat("topk_w", topk_w, torch.float32, (T, K))
+    _flat("dw", dw, torch.float32, (T, K))
+    _flat("do_rows", do_rows, dy.dtype, (rows, H))
+    code = lib().moe_nvfp4_combine_backward(T, H, K, rows, dt, dy.data_ptr(), stride, o_rows.data_ptr(),
+                                            row_of_route.data_ptr(), topk_w.data_ptr(),
+                                            _scalar_i32("rows_used", rows_used), do_rows.data_ptr(), dw.data_ptr(),
+                                            _stream(stream))
+    _check("moe_nvfp4_combine_backward", code)
+
+
+def _segments(count: torch.Tensor, offsets: torch.Tensor, E: int) -> None:
+    if count.dtype != torch.int32 or offsets.dtype != torch.int32 or not (count.is_cuda and offsets.is_cuda):
+        raise TypeError("count and offsets must be CUDA int32")
+    if count.numel() != E or offsets.numel() < E or not (count.is_contiguous() and offsets.is_contiguous()):
+        raise ValueError(f"count must be [{E}] and offsets [{E}] or longer, contiguous")
+
+
+def _expert_product(fn: str, a: torch.Tensor, b: torch.Tensor, out: torch.Tensor, rows: int, N: int, K: int, E: int,
+                    shapes: tuple, count, offsets, status, stream) -> None:
+    for t, shape in zip((a, b, out), shapes):
+        _flat(fn + " operand", t, torch.bfloat16, shape)
+    _segments(count, offsets, E)
+    if status is not None and (status.element_size() != 4 or not status.is_cuda or status.numel() != 1):
+        raise ValueError("status must be one CUDA 32-bit integer")
+    code = getattr(lib(), fn)(rows, N, K, E, a.data_ptr(), b.data_ptr(), count.data_ptr(), offsets.data_ptr(),
+                              out.data_ptr(), None if status is None else status.data_ptr(), _stream(stream))
+    _check(fn, code)
+
+
+def moe_nvfp4_expert_linear(x_rows: torch.Tensor, w: torch.Tensor, count: torch.Tensor, offsets: torch.Tensor,
+                            y_rows: torch.Tensor, status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """y_rows[r] = x_rows[r] w[e]^T for the rows [offsets[e], offsets[e] + count[e])
+    of every expert e: x_rows [rows, K], w [E, N, K], y_rows [rows, N], BF16."""
+    E, N, K = w.shape
+    R = x_rows.shape[0]
+    _expert_product("moe_nvfp4_expert_linear", x_rows, w, y_rows, R, N, K, E, ((R, K), (E, N, K), (R, N)), count,
+                    offsets, status, stream)
+
+
+def moe_nvfp4_expert_linear_dgrad(dy_rows: torch.Tensor, w: torch.Tensor, count: torch.Tensor, offsets: torch.Tensor,
+                                  dx_rows: torch.Tensor, status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """dx_rows[r] = dy_rows[r] w[e]: dy_rows [rows, N], w [E, N, K], dx_rows [rows, K], BF16."""
+    E, N, K = w.shape
+    R = dy_rows.shape[0]
+    _expert_product("moe_nvfp4_expert_linear_dgrad", dy_rows, w, dx_rows, R, N, K, E, ((R, N), (E, N, K), (R, K)),
+                    count, offsets, status, stream)
+
+
+def moe_nvfp4_expert_linear_wgrad(dy_rows: torch.Tensor, x_rows: torch.Tensor, count: torch.Tensor,
+                                  offsets: torch.Tensor, dw: torch.Tensor, status: Optional[torch.Tensor] = None,
+                                  stream=None) -> None:
+    """dw[e] = sum over expert e's rows r of dy_rows[r]^T x_rows[r]: dw [E, N, K], BF16."""
+    E, N, K = dw.shape
+    R = dy_rows.shape[0]
+    _expert_product("moe_nvfp4_expert_linear_wgrad", dy_rows, x_rows, dw, R, N, K, E, ((R, N), (R, K), (E, N, K)),
+                    count, offsets, status, stream)
+
+
+def moe_nvfp4_layer_norm(x: torch.Tensor, gamma: torch.Tensor, beta: Optional[torch.Tensor], eps: float,
+                         y: torch.Tensor, mean: Optional[torch.Tensor] = None, rstd: Optional[torch.Tensor] = None,
+                         stream=None) -> None:
+    """y = (x - mean) * rstd * gamma + beta over the rows of x [T, H]; gamma, beta
+    [H], mean and rstd [T] float32 (mean and rstd may both be None)."""
+    x, xs = _rows2d("x", x)
+    y, ys = _rows2d("y", y, x.dtype)
+    T, H = x.shape
+    if y.shape != x.shape:
+        raise ValueError("y must have the shape of x")
+    f32 = torch.float32
+    _flat("gamma", gamma, f32, (H,))
+    if beta is not None:
+        _flat("beta", beta, f32, (H,))
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        if t is not None:
+            _flat(name, t, f32, (T,))
+    code = lib().moe_nvfp4_layer_norm(T, H, _DTYPES[x.dtype], x.data_ptr(), xs, gamma.data_ptr(),
+                                      None if beta is None else beta.data_ptr(), eps, y.data_ptr(), ys,
+                                      None if mean is None else mean.data_ptr(),
+                                      None if rstd is None else rstd.data_ptr(), _stream(stream))
+    _check("moe_nvfp4_layer_norm", code)
+
+
+def moe_nvfp4_layer_norm_workspace_bytes(T: int, H: int) -> int:
+    return int(lib().moe_nvfp4_layer_norm_workspace_bytes(T, H))
+
+
+def moe_nvfp4_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor, mean: torch.Tensor,
+                                  rstd: torch.Tensor, dx: torch.Tensor, dgamma: torch.Tensor,
+                                  dbeta: Optional[torch.Tensor], workspace: torch.Tensor, stream=None) -> None:
+    """dx [T, H], dgamma and dbeta [H] of the layer norm with the forward's mean and rstd [T]."""
+    x, xs = _rows2d("x", x)
+    dy, dys = _rows2d("dy", dy, x.dtype)
+    dx, dxs = _rows2d("dx", dx, x.dtype)
+    T, H = x.shape
+    if dy.shape != x.shape or dx.shape != x.shape:
+        raise ValueError("dy and dx must have the shape of x")
+    f32 = torch.float32
+    _flat("gamma", gamma, f32, (H,))
+    _flat("mean", mean, f32, (T,))
+    _flat("rstd", rstd, f32, (T,))
+    _flat("dgamma", dgamma, f32, (H,))
+    if dbeta is not None:
+        _flat("dbeta", dbeta, f32, (H,))
+    code = lib().moe_nvfp4_layer_norm_backward(T, H, _DTYPES[x.dtype], dy.data_ptr(), dys, x.data_ptr(), xs,
+                                               gamma.data_ptr(), mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(), dxs,
+                                               dgamma.data_ptr(), None if dbeta is None else dbeta.data_ptr(),
+                                               workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                               _stream(stream))
+    _check("moe_nvfp4_layer_norm_backward", code)
+
+
+class GradList:
+    """A list of gradients (contiguous CUDA tensors, bfloat16 or float32) and
+    where their clipped values go (``out``; the gradients themselves without
+    it).  Built once for buffers that stay where they are; it holds the tensors
+    and their addresses."""
+
+    def __init__(self, grads, out=None):
+        self.grads = list(grads)
+        self.out = self.grads if out is None else list(out)
+        if len(self.out) != len(self.grads):
+            raise ValueError("as many outputs as gradients")
+        for g, o in zip(self.grads, self.out):
+            if g.dtype not in _DTYPES or o.dtype != g.dtype or not (g.is_cuda and o.is_cuda):
+                raise TypeError("gradients must be bfloat16 or float32 CUDA tensors, each output of its gradient's type")
+            if o.numel() != g.numel() or not (g.is_contiguous() and o.is_contiguous()):
+                raise ValueError("gradients and outputs must be contiguous and of the same size")
+        n = self.n = len(self.grads)
+        self.c_grads = (ctypes.c_void_p * n)(*[g.data_ptr() for g in self.grads])
+        self.c_out = (ctypes.c_void_p * n)(*[o.data_ptr() for o in self.out])
+        self.c_numels = (ctypes.c_int64 * n)(*[g.numel() for g in self.grads])
+        self.c_dtypes = (ctypes.c_int32 * n)(*[_DTYPES[g.dtype] for g in self.grads])
+
+
+def moe_nvfp4_grad_norm_workspace_bytes(n: int) -> int:
+    return int(lib().moe_nvfp4_grad_norm_workspace_bytes(n))
+
+
+def moe_nvfp4_grad_norm(grads: GradList, norm: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
+    """norm[0] (float32) = sqrt of the sum of the squares of every gradient's elements."""
+    _flat("norm", norm, torch.float32, (1,))
+    code = lib().moe_nvfp4_grad_norm(grads.n, grads.c_grads, grads.c_numels, grads.c_dtypes, norm.data_ptr(),
+                                     workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                     _stream(stream))
+    _check("moe_nvfp4_grad_norm", code)
+
+
+def moe_nvfp4_grad_clip(grads: GradList, norm: torch.Tensor, max_norm: float, eps: float = 1e-6,
+                        stream=None) -> None:
+    """out = gradient * min(1, max_norm / (norm + eps)) for every gradient of the list."""
+    _flat("norm", norm, torch.float32, (1,))
+    code = lib().moe_nvfp4_grad_clip(grads.n, grads.c_grads, grads.c_out, grads.c_numels, grads.c_dtypes,
+                                     norm.data_ptr(), max_norm, eps, _stream(stream))
+    _check("moe_nvfp4_grad_clip", code)
 
 
 # ---- convenience ---------------------------------------------------------------

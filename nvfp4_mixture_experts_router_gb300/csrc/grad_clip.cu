@@ -1,0 +1,210 @@
+// Global norm of a list of gradients, and the list scaled down to a largest
+// norm.
+//
+//   norm = sqrt(sum_i sum_j g_ij^2)
+//   out_ij = g_ij s,  s = min(1, max_norm / (norm + eps)), NaN if it is one
+//
+// The list travels as a kernel argument (pointers, sizes, types), a launch per
+// kListMax tensors: nothing is copied to the device beforehand, and a captured
+// graph replays it.  Tensors are cut into chunks of kChunk elements that the
+// blocks take in turn.  HBM is the bound: one read for the norm, one read and
+// one write for the scaling.
+#include "row_vec.cuh"
+#include "train_kernels.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kClipThreads = 512;
+constexpr int kListMax = 96;
+constexpr int64_t kChunk = 16384;
+constexpr int kNormBlocks = 304;      // partial sums per launch
+
+struct GradEntry {
+    const void* in;
+    void* out;
+    int64_t numel;
+    int32_t last_chunk;   // one past this tensor's last chunk in the launch
+    int32_t elem;         // bytes of an element
+};
+struct GradTable {
+    int n;
+    int chunks;
+    GradEntry e[kListMax];
+};
+
+// Sum of squares of a chunk's part of this thread.
+template <typename T_, int VEC>
+__device__ __forceinline__ float square_part(const void* base, int64_t at, int64_t count) {
+    using RV = RowVec<T_, VEC>;
+    const typename RV::Raw* p = reinterpret_cast<const typename RV::Raw*>(static_cast<const T_*>(base) + at);
+    const int n = (int)(count / VEC);
+    float s = 0.0f;
+    for (int i = threadIdx.x; i < n; i += kClipThreads) {
+        float v[VEC];
+        RV::unpack(p[i], v);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) s = fmaf(v[j], v[j], s);
+    }
+    const int64_t i = (int64_t)n * VEC + threadIdx.x;
+    if (i < count) {
+        const float v = (float)static_cast<const T_*>(base)[at + i];
+        s = fmaf(v, v, s);
+    }
+    return s;
+}
+
+template <typename T_, int VEC>
+__device__ __forceinline__ void scale_part(const void* base, void* out, int64_t at, int64_t count, float scale) {
+    using RV = RowVec<T_, VEC>;
+    const typename RV::Raw* p = reinterpret_cast<const typename RV::Raw*>(static_cast<const T_*>(base) + at);
+    typename RV::Raw* q = reinterpret_cast<typename RV::Raw*>(static_cast<T_*>(out) + at);
+    const int n = (int)(count / VEC);
+    for (int i = threadIdx.x; i < n; i += kClipThreads) {
+        float v[VEC];
+        RV::unpack(p[i], v);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) v[j] *= scale;
+        q[i] = RV::pack(v);
+    }
+    const int64_t i = (int64_t)n * VEC + threadIdx.x;
+    if (i < count) static_cast<T_*>(out)[at + i] = (T_)((float)static_cast<const T_*>(base)[at + i] * scale);
+}
+
+// Entry that holds chunk c of the launch.
+__device__ __forceinline__ int entry_of(const GradTable& t, int c) {
+    int lo = 0, hi = t.n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (c < t.e[mid].last_chunk) hi = mid;
+        else lo = mid + 1;
+    }
+    return lo;
+}
+
+__global__ void __launch_bounds__(kClipThreads) grad_square_kernel(const __grid_constant__ GradTable t, float* part) {
+    __shared__ float s_part[kClipThreads / 32];
+    pdl_wait();
+    float sum = 0.0f;
+    for (int c = blockIdx.x; c < t.chunks; c += gridDim.x) {
+        const int i = entry_of(t, c);
+        const GradEntry& e = t.e[i];
+        const int64_t at = (int64_t)(c - (i ? t.e[i - 1].last_chunk : 0)) * kChunk;
+        const int64_t count = min(kChunk, e.numel - at);
+        const bool wide = reinterpret_cast<uintptr_t>(e.in) % 16 == 0;
+        if (e.elem == 2)
+            sum += wide ? square_part<__nv_bfloat16, 8>(e.in, at, count) : square_part<__nv_bfloat16, 1>(e.in, at, count);
+        else
+            sum += wide ? square_part<float, 4>(e.in, at, count) : square_part<float, 1>(e.in, at, count);
+    }
+    sum = warp_sum(sum);
+    if ((threadIdx.x & 31) == 0) s_part[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const float v = warp_sum(threadIdx.x < kClipThreads / 32 ? s_part[threadIdx.x] : 0.0f);
+        if (threadIdx.x == 0) part[blockIdx.x] = v;
+    }
+    pdl_launch_dependents();
+}
+
+__global__ void __launch_bounds__(1024) grad_norm_kernel(int n, const float* part, float* norm) {
+    __shared__ float s_part[32];
+    pdl_wait();
+    float s = 0.0f;
+    for (int i = threadIdx.x; i < n; i += 1024) s += part[i];
+    s = warp_sum(s);
+    if ((threadIdx.x & 31) == 0) s_part[threadIdx.x >> 5] = s;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        s = warp_sum(s_part[threadIdx.x]);
+        if (threadIdx.x == 0) norm[0] = sqrtf(s);
+    }
+    pdl_launch_dependents();
+}
+
+__global__ void __launch_bounds__(kClipThreads) grad_scale_kernel(const __grid_constant__ GradTable t,
+                                                                  const float* norm, float max_norm, float eps) {
+    pdl_wait();
+    const float q = max_norm / (norm[0] + eps);
+    const float scale = q > 1.0f ? 1.0f : q;      // NaN stays NaN
+    for (int c = blockIdx.x; c < t.chunks; c += gridDim.x) {
+        const int i = entry_of(t, c);
+        const GradEntry& e = t.e[i];
+        if (scale == 1.0f && e.in == e.out) continue;
+        const int64_t at = (int64_t)(c - (i ? t.e[i - 1].last_chunk : 0)) * kChunk;
+        const int64_t count = min(kChunk, e.numel - at);
+        const bool wide = (reinterpret_cast<uintptr_t>(e.in) | reinterpret_cast<uintptr_t>(e.out)) % 16 == 0;
+        if (e.elem == 2) {
+            if (wide) scale_part<__nv_bfloat16, 8>(e.in, e.out, at, count, scale);
+            else scale_part<__nv_bfloat16, 1>(e.in, e.out, at, count, scale);
+        } else {
+            if (wide) scale_part<float, 4>(e.in, e.out, at, count, scale);
+            else scale_part<float, 1>(e.in, e.out, at, count, scale);
+        }
+    }
+}
+
+// Calls f(table) for every launch's share of the list: at most kListMax
+// tensors and 2^30 chunks; tensors without elements are left out.
+template <typename F>
+cudaError_t for_tables(int n, const void* const* in, void* const* out, const int64_t* numels, const int32_t* dtypes,
+                       F f) {
+    GradTable t;
+    int64_t chunks = 0;
+    t.n = 0;
+    auto flush = [&]() {
+        if (t.n == 0) return cudaSuccess;
+        t.chunks = (int)chunks;
+        const cudaError_t e = f(t);
+        t.n = 0;
+        chunks = 0;
+        return e;
+    };
+    for (int i = 0; i < n; ++i) {
+        if (numels[i] == 0) continue;
+        const int64_t c = (numels[i] + kChunk - 1) / kChunk;
+        if (t.n == kListMax || chunks + c > (1 << 30)) {
+            const cudaError_t e = flush();
+            if (e != cudaSuccess) return e;
+        }
+        chunks += c;
+        t.e[t.n++] = GradEntry{in[i], out ? out[i] : nullptr, numels[i], (int32_t)chunks,
+                               dtypes[i] == MOE_DTYPE_F32 ? 4 : 2};
+    }
+    return flush();
+}
+
+}  // namespace
+
+// A launch holds kListMax tensors at least (or fewer, when 2^30 chunks are
+// full: one launch more for each 2^40 elements, so a launch per tensor and one
+// per kListMax bound their number).
+size_t grad_norm_workspace_bytes(int n) {
+    return align_up((uint64_t)(n < 1 ? 1 : n) * kNormBlocks * 4, 256);
+}
+
+cudaError_t launch_grad_norm(const LaunchCtx& c, int sms, int n, const void* const* grads, const int64_t* numels,
+                             const int32_t* dtypes, float* norm, float* workspace) {
+    (void)sms;
+    int used = 0;
+    cudaError_t e = for_tables(n, grads, nullptr, numels, dtypes, [&](const GradTable& t) {
+        const int blocks = t.chunks < kNormBlocks ? t.chunks : kNormBlocks;
+        float* part = workspace + used;
+        used += blocks;
+        return c.launch(grad_square_kernel, dim3(blocks), dim3(kClipThreads), 0, t, part);
+    });
+    if (e != cudaSuccess) return e;
+    return c.launch(grad_norm_kernel, dim3(1), dim3(1024), 0, used, (const float*)workspace, norm);
+}
+
+cudaError_t launch_grad_clip(const LaunchCtx& c, int sms, int n, const void* const* grads, void* const* out,
+                             const int64_t* numels, const int32_t* dtypes, const float* norm, float max_norm,
+                             float eps) {
+    return for_tables(n, grads, out, numels, dtypes, [&](const GradTable& t) {
+        const int blocks = t.chunks < 8 * sms ? t.chunks : 8 * sms;
+        return c.launch(grad_scale_kernel, dim3(blocks), dim3(kClipThreads), 0, t, norm, max_norm, eps);
+    });
+}
+
+}  // namespace moe
