@@ -1,100 +1,528 @@
 // The experts' BF16 matrix products over rows ordered by expert, with FP32
-// accumulation:
-//   forward  y[r]  = x[r] w[e]^T              (sum over K)
-//   dgrad    dx[r] = dy[r] w[e]               (sum over N)
-//   wgrad    dw[e] = sum over e's rows dy[r]^T x[r]
+// accumulation on the tensor cores:
+//   forward  y[r]  = x[r] w[e]^T                       (sum over K)
+//   dgrad    dx[r] = dy[r] w[e]                        (sum over N)
+//   wgrad    dw[e] = sum over e's rows dy[r]^T x[r]    (sum over the rows)
+//
+// All three are one kernel computing D[m][n] = sum_d A(m, d) B(n, d) in tiles
+// of 256 x TN per pair of SMs (tcgen05.mma.cta_group::2, kind::f16; each SM
+// holds 128 of the 256 rows of A and D and half of the TN rows of B):
+//   forward  m: output column, A = w[e] (d contiguous);  n: row, B = x
+//   dgrad    m: output column, A = w[e] (m contiguous);  n: row, B = dy
+//   wgrad    m: N, A = dy (m contiguous);  n: K, B = x (n contiguous);  d: row
+// The weights sit on the M side, so that the tile's row extent TN follows the
+// experts' segment lengths: an expert with one row streams its weights past a
+// 32-row tile.  An operand whose m or n is contiguous in memory is copied as
+// it lies (64 x 64 boxes, 128-byte swizzle) and read by the MMA as an MN-major
+// operand: no transposed copy of w, dy or x is ever made.
+//
+// Segments are ragged and unpadded.  forward / dgrad: rows of a tile past the
+// segment's end hold another expert's values (or the copy's zero fill), which
+// reach only their own columns of D and are not stored.  wgrad sums over the
+// rows, so there the last block of a segment is cut: the MMA issues only the
+// 16-row steps that hold rows, and the rows of the last step past the end are
+// overwritten with zeros in shared memory before the MMA reads them (a factor
+// of zero on one side alone would let a neighbour's NaN through).
+//
+// Roles per CTA: warp 0 producer of the copies, warp 1 tensor-memory
+// allocation and, in rank 0, the MMA issuer, warp 3 the cutter of ragged ends
+// (wgrad), the last four or eight warps the epilogue.  Two accumulators: the
+// epilogue of one tile overlaps the main loop of the next.  The grid is
+// persistent, one pair per two SMs; every CTA scans the experts' counts for
+// its tile list, so nothing runs ahead of the kernel and the counts never
+// leave the device.  Every wait is bounded (1 s); a timeout sets a status bit,
+// marks both CTAs aborted, and all roles drain to the final pair barrier.
+#include <cudaTypedefs.h>
+
 #include "common.cuh"
+#include "host.h"
 #include "train_kernels.h"
 
 namespace moe {
 
 namespace {
 
-constexpr int kTile = 64, kDepth = 16;
+constexpr int kDepth = 64;                     // reduction elements per stage
+constexpr int kHalfM = 128;                    // A rows per CTA
+constexpr int kTileA = kHalfM * kDepth * 2;    // bytes
+constexpr int kMGroup = 8;                     // m tiles walked together (L2 reuse)
+constexpr int kMaxExperts = 1024;
 
-// Rows of expert e; a segment outside [0, rows) is empty and raises a bit.
-__device__ __forceinline__ int2 segment(const ExpertArgs& a, int e) {
-    const int64_t first = a.offsets[e], n = a.count[e];
-    if (n < 0 || first < 0 || first + n > a.rows) {
-        if (a.status && threadIdx.x == 0) atomicOr(a.status, kStatusBadRow);
-        return make_int2(0, 0);
-    }
-    return make_int2((int)first, (int)n);
+struct ExpertParams {
+    int m_extent;          // D rows that exist: output columns (forward, dgrad) or N (wgrad)
+    int n_extent;          // wgrad: K
+    int depth;             // forward, dgrad: reduction length
+    int E;
+    int64_t rows;
+    const int* count;
+    const int* offsets;
+    __nv_bfloat16* out;
+    unsigned int* status;  // may be null
+};
+
+template <int TN>
+struct ExpertCfg {
+    static constexpr int kHalfN = TN / 2;                          // B rows per CTA
+    static constexpr int kTileB = kHalfN * kDepth * 2;
+    static constexpr int kStages = TN == 256 ? 6 : TN == 128 ? 8 : TN == 64 ? 10 : 11;
+    static constexpr int kEpiWarps = TN >= 64 ? 8 : 4;
+    static constexpr int kThreads = (4 + kEpiWarps) * 32;
+    static constexpr uint32_t kTmemCols = 2 * TN;
+    static constexpr int kBars = 3 * kStages + 5;
+    static constexpr int kSmemBytes =
+        1024 + kStages * (kTileA + kTileB) + 3 * kMaxExperts * 4 + kBars * 8 + 64;
+    static_assert(kSmemBytes <= 232448, "shared memory budget");
+};
+
+__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// MN-major operand tile: chunks of 64 m (or n) elements, each [64 d][128 B]
+// with the 128-byte swizzle; `chunk` = bytes from chunk to chunk (the leading
+// offset), 1024 bytes from one group of eight d to the next (the stride).
+__device__ __forceinline__ uint64_t sdesc_mnmajor_sw128(uint32_t saddr, uint32_t chunk) {
+    return sdesc(saddr, chunk, 1024, kSwizzle128B);
 }
 
-// A block per 64 x 64 tile of one expert's product C[m][n] = sum_k A(m,k) B(n,k).
-template <int PRODUCT>
-__global__ void __launch_bounds__(256) expert_tile_kernel(const ExpertArgs a) {
-    __shared__ float s_a[kDepth][kTile + 1], s_b[kDepth][kTile + 1];
-    pdl_wait();
-    const int e = blockIdx.z;
-    const int2 seg = segment(a, e);
-    const __nv_bfloat16* A = static_cast<const __nv_bfloat16*>(a.a);
-    const __nv_bfloat16* B = static_cast<const __nv_bfloat16*>(a.b);
-    __nv_bfloat16* C = static_cast<__nv_bfloat16*>(a.out);
-    const int M = PRODUCT == kExpertWgrad ? a.N : seg.y;
-    const int Nc = PRODUCT == kExpertForward ? a.N : a.K;
-    const int D = PRODUCT == kExpertForward ? a.K : PRODUCT == kExpertDgrad ? a.N : seg.y;
-    const size_t w0 = (size_t)e * a.N * a.K;
-    for (int m0 = blockIdx.y * kTile; m0 < M; m0 += gridDim.y * kTile) {
-        const int n0 = blockIdx.x * kTile;
-        float acc[4][4] = {};
-        const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-        for (int d0 = 0; d0 < D; d0 += kDepth) {
-            for (int i = threadIdx.x; i < kTile * kDepth; i += 256) {
-                const int r = i / kDepth, d = i % kDepth;
-                const int m = m0 + r, n = n0 + r, k = d0 + d;
-                float va = 0.0f, vb = 0.0f;
-                if (k < D) {
-                    if (m < M)
-                        va = PRODUCT == kExpertWgrad ? (float)A[(size_t)(seg.x + k) * a.N + m]
-                                                     : (float)A[(size_t)(seg.x + m) * D + k];
-                    if (n < Nc)
-                        vb = PRODUCT == kExpertForward ? (float)B[w0 + (size_t)n * a.K + k]
-                             : PRODUCT == kExpertDgrad ? (float)B[w0 + (size_t)k * a.K + n]
-                                                       : (float)B[(size_t)(seg.x + k) * a.K + n];
-                }
-                s_a[d][r] = va;
-                s_b[d][r] = vb;
-            }
-            __syncthreads();
-#pragma unroll
-            for (int d = 0; d < kDepth; ++d) {
-                float x[4], w[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    x[i] = s_a[d][ty * 4 + i];
-                    w[i] = s_b[d][tx * 4 + i];
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(x[i], w[j], acc[i][j]);
-            }
-            __syncthreads();
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
-                if (m >= M || n >= Nc) continue;
-                const size_t at = PRODUCT == kExpertWgrad ? w0 + (size_t)m * a.K + n : (size_t)(seg.x + m) * Nc + n;
-                C[at] = __float2bfloat16_rn(acc[i][j]);
-            }
+// Bits 15 / 16 of the instruction descriptor: A / B is MN-major.
+constexpr uint32_t kIdescAMn = 1u << 15, kIdescBMn = 1u << 16;
+
+struct ExpertTile {
+    int e, m0, n0;         // expert, first m of the pair's tile, first n
+    int first, count;      // the expert's segment
+};
+
+// The tile list: experts in order, an expert's tiles in groups of kMGroup m
+// tiles, n outer and m inner, so that the pairs running at a time share both
+// operands in L2.  s_end[e] = tiles of experts 0..e.
+template <int TN, bool WGRAD>
+__device__ __forceinline__ ExpertTile expert_tile(const ExpertParams& p, int tile, const int* s_end,
+                                                  const int* s_first, const int* s_count) {
+    int lo = 0, hi = p.E - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (tile < s_end[mid]) hi = mid;
+        else lo = mid + 1;
     }
+    ExpertTile t;
+    t.e = lo;
+    t.first = s_first[lo];
+    t.count = s_count[lo];
+    const int local = tile - (lo ? s_end[lo - 1] : 0);
+    const int mt = (p.m_extent + 255) / 256;
+    const int nt = ((WGRAD ? p.n_extent : t.count) + TN - 1) / TN;
+    const int g = local / (kMGroup * nt), in = local % (kMGroup * nt);
+    const int gm = min(kMGroup, mt - g * kMGroup);
+    t.n0 = in / gm * TN;
+    t.m0 = (g * kMGroup + in % gm) * 256;
+    return t;
+}
+
+template <int PRODUCT, int TN>
+__global__ void __launch_bounds__(ExpertCfg<TN>::kThreads, 1)
+    expert_linear_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                         const ExpertParams p) {
+    using C = ExpertCfg<TN>;
+    constexpr bool kWgrad = PRODUCT == kExpertWgrad;
+    constexpr bool kAMn = PRODUCT != kExpertForward;      // A's m contiguous
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* s_a = base;
+    uint8_t* s_b = s_a + C::kStages * kTileA;
+    uint64_t* full = reinterpret_cast<uint64_t*>(s_b + C::kStages * C::kTileB);   // rank 0: a stage of both CTAs
+    uint64_t* empty = full + C::kStages;                                          // both: the stage's MMAs are done
+    uint64_t* landed = empty + C::kStages;                                        // own copies of a stage to be cut
+    uint64_t* acc_full = landed + C::kStages;
+    uint64_t* acc_empty = acc_full + 2;                                           // rank 0
+    uint64_t* drain = acc_empty + 2;
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile int* abort = reinterpret_cast<volatile int*>(tmem_holder + 1);
+    int* s_end = reinterpret_cast<int*>(tmem_holder + 4);
+    int* s_first = s_end + kMaxExperts;
+    int* s_count = s_first + kMaxExperts;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_cta_rank();
+    const int slot = blockIdx.x >> 1, slots = gridDim.x >> 1;
+    volatile int no_abort = 0;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(&full[i], 2);        // one arrival per CTA
+            mbar_init(&empty[i], 1);
+            mbar_init(&landed[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_empty[i], 2 * C::kEpiWarps);
+        }
+        mbar_init(drain, 1);
+        *abort = 0;
+        fence_mbar_init();
+        prefetch_tensormap(&tmA);
+        prefetch_tensormap(&tmB);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_holder, C::kTmemCols);
+        tmem_relinquish_pair();
+    }
+    pdl_wait();
+    {
+        const int mt = (p.m_extent + 255) / 256;
+        for (int e = threadIdx.x; e < p.E; e += C::kThreads) {
+            int64_t first = p.offsets[e], n = p.count[e];
+            if (n < 0 || first < 0 || first + n > p.rows) {
+                if (p.status && blockIdx.x == 0) atomicOr(p.status, kStatusBadRow);
+                first = n = 0;
+            }
+            s_first[e] = (int)first;
+            s_count[e] = (int)n;
+            s_end[e] = mt * (int)(((kWgrad ? p.n_extent : n) + TN - 1) / TN);
+        }
+        __syncthreads();
+        if (warp == 0) {
+            const int per = (p.E + 31) / 32, e0 = min(p.E, lane * per), e1 = min(p.E, e0 + per);
+            int sum = 0;
+            for (int e = e0; e < e1; ++e) sum += s_end[e];
+            int incl = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int a = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += a;
+            }
+            int run = incl - sum;
+            for (int e = e0; e < e1; ++e) {
+                run += s_end[e];
+                s_end[e] = run;
+            }
+        }
+    }
+    // both CTAs' barriers initialized and tensor memory allocated before any
+    // cross-CTA copy, arrival or pair MMA
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_holder;
+    const int total = s_end[p.E - 1];
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const uint64_t pol = policy_evict_normal();
+            const uint32_t full0 = cluster_map(full, 0);
+            const uint32_t landed_own = cluster_map(landed, rank);
+            int stage = 0;
+            uint32_t phase = 0;
+            for (int tile = slot; tile < total; tile += slots) {
+                const ExpertTile t = expert_tile<TN, kWgrad>(p, tile, s_end, s_first, s_count);
+                const int depth = kWgrad ? t.count : p.depth;
+                const int m0 = t.m0 + (int)rank * kHalfM, n0 = t.n0 + (int)rank * C::kHalfN;
+                for (int d = 0; d < depth; d += kDepth) {
+                    // completed by rank 0's commit: acquire at cluster scope
+                    if (!mbar_wait<true>(&empty[stage], phase ^ 1u, abort, p.status, kStatusTimeoutProducer)) goto done;
+                    constexpr uint32_t kBytes = kTileA + C::kTileB;
+                    uint8_t* a_dst = s_a + stage * kTileA;
+                    uint8_t* b_dst = s_b + stage * C::kTileB;
+                    // a stage to be cut: counted on this CTA's own barrier,
+                    // and warp 3 announces it
+                    const bool cut = kWgrad && depth - d < kDepth && (depth & 15) != 0;
+                    const uint32_t bar = (cut ? landed_own : full0) + (uint32_t)stage * 8u;
+                    if (cut) mbar_arrive_expect_tx(&landed[stage], kBytes);
+                    else if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2u * kBytes);
+                    else mbar_arrive_cluster(full0 + (uint32_t)stage * 8u);
+                    if (kWgrad) {
+#pragma unroll
+                        for (int j = 0; j < kHalfM / 64; ++j)
+                            tma_load_2d_pair(a_dst + j * 8192, &tmA, bar, m0 + 64 * j, t.first + d, pol);
+#pragma unroll
+                        for (int j = 0; j < C::kHalfN / 64; ++j)
+                            tma_load_2d_pair(b_dst + j * 8192, &tmB, bar, n0 + 64 * j, t.first + d, pol);
+                    } else {
+                        if (kAMn) {
+#pragma unroll
+                            for (int j = 0; j < kHalfM / 64; ++j)
+                                tma_load_3d_pair(a_dst + j * 8192, &tmA, bar, m0 + 64 * j, d, t.e, pol);
+                        } else {
+                            tma_load_3d_pair(a_dst, &tmA, bar, d, m0, t.e, pol);
+                        }
+                        tma_load_2d_pair(b_dst, &tmB, bar, d, t.first + n0, pol);
+                    }
+                    if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            constexpr uint32_t idesc = idesc_bf16(256, TN) | (kAMn ? kIdescAMn : 0u) | (kWgrad ? kIdescBMn : 0u);
+            // 16 d further: 16 rows of 128 bytes (MN-major) or 32 bytes, in
+            // units of 16 bytes
+            constexpr uint64_t kStepA = kAMn ? 128 : 2, kStepB = kWgrad ? 128 : 2;
+            int stage = 0, acc = 0;
+            uint32_t phase = 0, acc_phase = 0;
+            for (int tile = slot; tile < total; tile += slots) {
+                const ExpertTile t = expert_tile<TN, kWgrad>(p, tile, s_end, s_first, s_count);
+                const int depth = kWgrad ? t.count : p.depth;
+                if (depth == 0) continue;
+                if (!mbar_wait<true>(&acc_empty[acc], acc_phase ^ 1u, abort, p.status, kStatusTimeoutMma)) goto done;
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + (uint32_t)acc * TN;
+                for (int d = 0; d < depth; d += kDepth) {
+                    if (!mbar_wait<true>(&full[stage], phase, abort, p.status, kStatusTimeoutMma)) goto done;
+                    tc_fence_after();
+                    const uint32_t a_s = smem_u32(s_a + stage * kTileA), b_s = smem_u32(s_b + stage * C::kTileB);
+                    const uint64_t adesc = kAMn ? sdesc_mnmajor_sw128(a_s, 8192) : sdesc_kmajor_sw128(a_s);
+                    const uint64_t bdesc = kWgrad ? sdesc_mnmajor_sw128(b_s, 8192) : sdesc_kmajor_sw128(b_s);
+                    if (depth - d >= kDepth) {
+#pragma unroll
+                        for (int j = 0; j < kDepth / 16; ++j)
+                            tc_mma_bf16_pair(d_tmem, adesc + kStepA * j, bdesc + kStepB * j, idesc, (d | j) != 0);
+                    } else {
+                        for (int j = 0; j < (depth - d + 15) / 16; ++j)
+                            tc_mma_bf16_pair(d_tmem, adesc + kStepA * j, bdesc + kStepB * j, idesc, (d | j) != 0);
+                    }
+                    tc_commit_pair_mc(&empty[stage], 0x3);
+                    if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
+                }
+                tc_commit_pair_mc(&acc_full[acc], 0x3);
+                acc ^= 1;
+                if (acc == 0) acc_phase ^= 1u;
+            }
+        }
+    } else if (warp == 3) {
+        if (kWgrad) {
+            // the ragged ends: zeros from the segment's end to the end of its
+            // last 16-row step, in this CTA's halves of both operands
+            const uint32_t full0 = cluster_map(full, 0);
+            int stage = 0;
+            uint32_t phases = 0;           // bit s: parity of landed[s]
+            for (int tile = slot; tile < total; tile += slots) {
+                const ExpertTile t = expert_tile<TN, kWgrad>(p, tile, s_end, s_first, s_count);
+                const int blocks = (t.count + kDepth - 1) / kDepth;
+                if ((t.count & 15) != 0) {
+                    const int s = (stage + blocks - 1) % C::kStages;
+                    if (!__all_sync(0xffffffffu, mbar_wait(&landed[s], (phases >> s) & 1u, abort, p.status,
+                                                           kStatusTimeoutProducer)))
+                        goto done;
+                    phases ^= 1u << s;
+                    const int r0 = t.count - (blocks - 1) * kDepth, r1 = (r0 + 15) / 16 * 16;
+                    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+                    // a row of a chunk is 128 bytes (the swizzle permutes within it)
+                    for (int r = r0 + (lane >> 3); r < r1; r += 4) {
+#pragma unroll
+                        for (int j = 0; j < kHalfM / 64; ++j)
+                            *reinterpret_cast<uint4*>(s_a + s * kTileA + j * 8192 + r * 128 + (lane & 7) * 16) = zero;
+#pragma unroll
+                        for (int j = 0; j < C::kHalfN / 64; ++j)
+                            *reinterpret_cast<uint4*>(s_b + s * C::kTileB + j * 8192 + r * 128 + (lane & 7) * 16) = zero;
+                    }
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (rank == 0) mbar_arrive(&full[s]);
+                        else mbar_arrive_remote_cta_release(full0 + (uint32_t)s * 8u);
+                    }
+                }
+                stage = (stage + blocks) % C::kStages;
+            }
+        }
+    } else if (warp >= 4) {
+        const int q = warp & 3;                            // tensor-memory lane quadrant
+        constexpr int kCols = TN / (C::kEpiWarps / 4);     // accumulator columns per warp
+        const int col0 = ((warp - 4) >> 2) * kCols;
+        const uint32_t release0 = cluster_map(acc_empty, 0);
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        for (int tile = slot; tile < total; tile += slots) {
+            const ExpertTile t = expert_tile<TN, kWgrad>(p, tile, s_end, s_first, s_count);
+            const int m = t.m0 + (int)rank * kHalfM + q * 32 + lane;
+            const bool nothing = kWgrad && t.count == 0;   // no rows: zeros, no accumulator
+            if (!nothing) {
+                // warp-uniform outcome: tcgen05.ld below is a warp-collective instruction
+                if (!__all_sync(0xffffffffu, mbar_wait<true>(&acc_full[acc], acc_phase, abort, p.status,
+                                                             kStatusTimeoutEpilogue)))
+                    break;
+                tc_fence_after();
+            }
+            const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)acc * TN + (uint32_t)col0;
+            const int limit = kWgrad ? p.n_extent - t.n0 : t.count - t.n0;   // columns that exist
+#pragma unroll 1
+            for (int c = 0; c < kCols; c += 32) {
+                if (col0 + c >= limit) break;              // warp-uniform
+                float v[32];
+                if (nothing) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+                } else {
+                    tmem_ld32(taddr + c, v);
+                    tmem_ld_wait();
+                }
+                if (m < p.m_extent) {
+                    if (kWgrad) {
+                        // lane = row of dw[e], columns contiguous
+                        __nv_bfloat16* o = p.out + ((size_t)t.e * p.m_extent + m) * p.n_extent + t.n0 + col0 + c;
+#pragma unroll
+                        for (int j = 0; j < 32; j += 8) {
+                            if (col0 + c + j < limit) {
+                                const float w[8] = {v[j], v[j + 1], v[j + 2], v[j + 3],
+                                                    v[j + 4], v[j + 5], v[j + 6], v[j + 7]};
+                                *reinterpret_cast<uint4*>(o + j) = pack_bf16x8(w);
+                            }
+                        }
+                    } else {
+                        // lane = output column, accumulator column = row of the segment
+                        __nv_bfloat16* o = p.out + (size_t)(t.first + t.n0 + col0 + c) * p.m_extent + m;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (col0 + c + j < limit) o[(size_t)j * p.m_extent] = __float2bfloat16_rn(v[j]);
+                    }
+                }
+                __syncwarp();
+            }
+            if (!nothing) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (rank == 0) mbar_arrive(&acc_empty[acc]);
+                    else mbar_arrive_cluster(release0 + (uint32_t)acc * 8u);
+                }
+                acc ^= 1;
+                if (acc == 0) acc_phase ^= 1u;
+            }
+        }
+    }
+done:
+    if (*abort) {
+        // tell the other CTA, let in-flight copies land and retire every
+        // issued MMA before the memories go away
+        st_cluster_u32(cluster_map((const void*)abort, rank ^ 1u), 1u);
+        if (warp == 1 && lane == 0 && rank == 0) {
+            tc_commit_pair(drain);
+            mbar_wait(drain, 0, &no_abort, p.status, kStatusTimeoutMma);
+        }
+        for (int i = 0; i < 100; ++i) __nanosleep(10000);
+    }
+    tc_fence_before();
+    __syncthreads();
+    // neither CTA frees tensor memory or leaves before both are done
+    cluster_sync_all();
+    pdl_launch_dependents();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, C::kTmemCols);
+    }
+}
+
+// Tensor map of a BF16 array: dims[0] contiguous, byte strides of the others,
+// 128-byte boxes with the 128-byte swizzle.
+bool encode_bf16_map(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                     const cuuint32_t* box) {
+    const cuuint32_t step[3] = {1, 1, 1};
+    return tensor_map_encoder()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box,
+                                step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int g_expert_grid[64] = {};
+
+template <int PRODUCT, int TN>
+cudaError_t launch_tiles(const LaunchCtx& c, int grid, const CUtensorMap& a, const CUtensorMap& b,
+                         const ExpertParams& p) {
+    return c.launch(expert_linear_kernel<PRODUCT, TN>, dim3((unsigned)grid), dim3(ExpertCfg<TN>::kThreads),
+                    (size_t)ExpertCfg<TN>::kSmemBytes, a, b, p);
+}
+
+template <int PRODUCT, int TN>
+cudaError_t set_tiles() {
+    return cudaFuncSetAttribute(expert_linear_kernel<PRODUCT, TN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                ExpertCfg<TN>::kSmemBytes);
+}
+
+template <int PRODUCT>
+cudaError_t launch_rows(const LaunchCtx& c, int tn, int grid, const CUtensorMap& a, const CUtensorMap& b,
+                        const ExpertParams& p) {
+    switch (tn) {
+        case 32: return launch_tiles<PRODUCT, 32>(c, grid, a, b, p);
+        case 64: return launch_tiles<PRODUCT, 64>(c, grid, a, b, p);
+        case 128: return launch_tiles<PRODUCT, 128>(c, grid, a, b, p);
+        default: return launch_tiles<PRODUCT, 256>(c, grid, a, b, p);
+    }
+}
+
+// Rows of a tile for segments of `rows` / (experts that can hold any) rows on
+// average: the narrowest that holds a segment of one and a third times the
+// mean, so that most experts' weights pass the tensor cores once.
+int tile_rows(int64_t rows, int E) {
+    const int64_t busy = rows < E ? rows : E;
+    if (3 * 32 * busy >= 4 * rows) return 32;
+    if (3 * 64 * busy >= 4 * rows) return 64;
+    if (3 * 128 * busy >= 4 * rows) return 128;
+    return 256;
 }
 
 }  // namespace
 
-cudaError_t launch_expert_linear(const LaunchCtx& c, int product, const ExpertArgs& a) {
-    const int cols = product == kExpertForward ? a.N : a.K;
-    const int64_t most = product == kExpertWgrad ? a.N : a.rows;
-    const int64_t mt = (most + kTile - 1) / kTile;
-    const dim3 grid((unsigned)((cols + kTile - 1) / kTile), (unsigned)(mt < 256 ? mt : 256), (unsigned)a.E);
-    if (product == kExpertForward) return c.launch(expert_tile_kernel<kExpertForward>, grid, dim3(256), 0, a);
-    if (product == kExpertDgrad) return c.launch(expert_tile_kernel<kExpertDgrad>, grid, dim3(256), 0, a);
-    return c.launch(expert_tile_kernel<kExpertWgrad>, grid, dim3(256), 0, a);
+cudaError_t setup_expert_linear_kernels(int device, int num_sms) {
+    cudaError_t e;
+    if ((e = set_tiles<kExpertForward, 32>()) || (e = set_tiles<kExpertForward, 64>()) ||
+        (e = set_tiles<kExpertForward, 128>()) || (e = set_tiles<kExpertForward, 256>()) ||
+        (e = set_tiles<kExpertDgrad, 32>()) || (e = set_tiles<kExpertDgrad, 64>()) ||
+        (e = set_tiles<kExpertDgrad, 128>()) || (e = set_tiles<kExpertDgrad, 256>()) ||
+        (e = set_tiles<kExpertWgrad, 256>()))
+        return e;
+    // persistent grid: as many CTA pairs as can be resident at once
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(num_sms / 2 * 2));
+    cfg.blockDim = dim3(ExpertCfg<256>::kThreads);
+    cfg.dynamicSmemBytes = ExpertCfg<64>::kSmemBytes;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    if ((e = cudaOccupancyMaxActiveClusters(&clusters, expert_linear_kernel<kExpertForward, 64>, &cfg))) return e;
+    if (clusters < 1) return cudaErrorInvalidConfiguration;
+    if (device >= 0 && device < 64) g_expert_grid[device] = 2 * (clusters < num_sms / 2 ? clusters : num_sms / 2);
+    return cudaSuccess;
+}
+
+cudaError_t launch_expert_linear(const LaunchCtx& c, int product, int device, const ExpertArgs& a) {
+    if (device < 0 || device >= 64 || g_expert_grid[device] < 2) return cudaErrorInvalidValue;
+    if (a.rows == 0)   // wgrad only: no rows, a gradient of zeros
+        return cudaMemsetAsync(a.out, 0, (size_t)a.E * a.N * a.K * 2, c.stream);
+    const cuuint64_t N = (cuuint64_t)a.N, K = (cuuint64_t)a.K, R = (cuuint64_t)a.rows;
+    const int tn = product == kExpertWgrad ? 256 : tile_rows(a.rows, a.E);
+    CUtensorMap ta, tb;
+    bool ok;
+    if (product == kExpertWgrad) {
+        const cuuint64_t da[2] = {N, R}, sa[1] = {N * 2}, db[2] = {K, R}, sb[1] = {K * 2};
+        const cuuint32_t box[2] = {64, 64};
+        ok = encode_bf16_map(&ta, a.a, 2, da, sa, box) && encode_bf16_map(&tb, a.b, 2, db, sb, box);
+    } else {
+        const bool fwd = product == kExpertForward;
+        const cuuint64_t dw[3] = {K, N, (cuuint64_t)a.E}, sw[2] = {K * 2, N * K * 2};
+        const cuuint32_t boxw[3] = {64, fwd ? 128u : 64u, 1};
+        const cuuint64_t dr[2] = {fwd ? K : N, R}, sr[1] = {(fwd ? K : N) * 2};
+        const cuuint32_t boxr[2] = {64, (cuuint32_t)(tn / 2)};
+        ok = encode_bf16_map(&ta, a.b, 3, dw, sw, boxw) && encode_bf16_map(&tb, a.a, 2, dr, sr, boxr);
+    }
+    if (!ok) return cudaErrorInvalidValue;
+    ExpertParams p{};
+    p.m_extent = product == kExpertDgrad ? a.K : a.N;
+    p.n_extent = a.K;
+    p.depth = product == kExpertDgrad ? a.N : a.K;
+    p.E = a.E;
+    p.rows = a.rows;
+    p.count = a.count;
+    p.offsets = a.offsets;
+    p.out = static_cast<__nv_bfloat16*>(a.out);
+    p.status = a.status;
+    LaunchCtx cc = c;
+    cc.cluster = 2;
+    const int grid = g_expert_grid[device];
+    if (product == kExpertForward) return launch_rows<kExpertForward>(cc, tn, grid, ta, tb, p);
+    if (product == kExpertDgrad) return launch_rows<kExpertDgrad>(cc, tn, grid, ta, tb, p);
+    return launch_tiles<kExpertWgrad, 256>(cc, grid, ta, tb, p);
 }
 
 }  // namespace moe

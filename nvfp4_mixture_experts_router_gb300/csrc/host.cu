@@ -6,6 +6,7 @@
 
 #include "host.h"
 #include "kernels.h"
+#include "train_kernels.h"
 #include "w4a16_swap.h"
 
 namespace moe {
@@ -44,7 +45,8 @@ moe_status device_state(int* sms, int* device) {
                    setup_gemm_w4a16_pair_kernels(dev, d.sms) != cudaSuccess ||
                    setup_fused_layer_kernel() != cudaSuccess || setup_gemm_swap_kernels() != cudaSuccess ||
                    setup_gemm_w4a16_swap_kernels() != cudaSuccess ||
-                   setup_router_gemm_kernel() != cudaSuccess) {
+                   setup_router_gemm_kernel() != cudaSuccess ||
+                   setup_expert_linear_kernels(dev, d.sms) != cudaSuccess) {
             d.status = MOE_ERR_CUDA;
         } else {
             d.status = MOE_OK;

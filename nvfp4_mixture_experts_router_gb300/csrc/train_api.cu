@@ -48,8 +48,8 @@ bool spans_ok(const Span* s, int n, const uintptr_t* align) {
 
 // The launch context of one call.  Every kernel waits for its predecessor
 // before it touches memory, so all may start early.
-moe_status begin(void* stream, LaunchCtx* c, int* sms) {
-    const moe_status st = device_state(sms);
+moe_status begin(void* stream, LaunchCtx* c, int* sms, int* device = nullptr) {
+    const moe_status st = device_state(sms, device);
     if (st != MOE_OK) return st;
     c->stream = static_cast<cudaStream_t>(stream);
     c->pdl = true;
@@ -178,11 +178,11 @@ static moe_status expert_product(int product, int64_t rows, int N, int K, int E,
     if (!spans_ok(s, 6, al)) return MOE_ERR_INVALID_ARG;
     if (rows == 0 && !wg) return MOE_OK;
     LaunchCtx c;
-    int sms = 0;
-    const moe_status st = begin(stream, &c, &sms);
+    int sms = 0, device = 0;
+    const moe_status st = begin(stream, &c, &sms, &device);
     if (st != MOE_OK) return st;
     const ExpertArgs args{rows, N, K, E, a, b, out, count, offsets, status};
-    return cuda_status(launch_expert_linear(c, product, args));
+    return cuda_status(launch_expert_linear(c, product, device, args));
 }
 
 moe_status moe_nvfp4_expert_linear(int64_t rows, int N, int K, int E, const void* x_rows, const void* w,

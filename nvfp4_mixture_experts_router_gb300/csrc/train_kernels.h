@@ -49,6 +49,7 @@ struct ExpertArgs {
     const int* offsets;    // [E]
     unsigned int* status;  // may be null
 };
-cudaError_t launch_expert_linear(const LaunchCtx& c, int product, const ExpertArgs& a);
+cudaError_t setup_expert_linear_kernels(int device, int num_sms);
+cudaError_t launch_expert_linear(const LaunchCtx& c, int product, int device, const ExpertArgs& a);
 
 }  // namespace moe
