@@ -9,6 +9,16 @@
 // The variance is the second pass's sum of squared differences, not
 // E[x^2] - mean^2: a row whose mean is far larger than its spread would lose
 // the difference of the two.  HBM is the bound: x and dy in, y or dx out.
+//
+// Up to 8192 columns (the row kernels): a row lies in the registers of
+// ceil(H / 256) warps, eight columns a thread, and is read once.  The backward
+// kernel is persistent: a block walks rows with the next two rows' loads in
+// flight, and each thread keeps the dgamma / dbeta sums of its eight columns
+// in registers until the end, so that dy and x are read once for both
+// gradients; the blocks' sums go through the workspace to a reduction in a
+// fixed order.  Longer rows are walked three times (forward) or twice (dx),
+// the re-reads served by the caches, and the column sums are a pass of their
+// own.
 #include "row_vec.cuh"
 #include "train_kernels.h"
 
@@ -17,7 +27,485 @@ namespace moe {
 namespace {
 
 constexpr int kNormThreads = 256;
-constexpr int kNormParts = 64;     // row groups of the dgamma / dbeta partial sums
+constexpr int kNormParts = 64;      // row groups of the column sums, long rows
+constexpr int kNormSms = 152;       // the persistent backward kernels' grids are multiples of this
+constexpr int kCols = 8;            // columns per thread of the row kernels
+constexpr int kRowColumns = 32 * 32 * kCols;
+constexpr int kRingCols = 16;       // columns per thread of the ring kernel
+constexpr int kRingMin = 1024;      // columns
+constexpr int kRingMax = 4;         // stages in flight in shared memory (at most)
+constexpr int kRingBytes = 200 * 1024;
+
+// The row kernels' shape: W warps a row, G rows a block (256 threads at least).
+struct NormShape {
+    int W, G;
+    int threads() const { return W * G * 32; }
+};
+NormShape norm_shape(int H, int cols = kCols) {
+    const int W = (H + 32 * cols - 1) / (32 * cols);
+    return NormShape{W, W >= 8 ? 1 : 8 / W};
+}
+
+// Sums of (a, b) over the W warps of a row; every thread gets them.  `turn`
+// alternates between calls: one barrier a call suffices.
+__device__ __forceinline__ float2 row_sum2(float a, float b, int W, int turn, float2 (*s)[32]) {
+    a = warp_sum(a);
+    b = warp_sum(b);
+    if (W > 1) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        if (lane == 0) s[turn][warp] = make_float2(a, b);
+        __syncthreads();
+        const float2 v = lane < W ? s[turn][warp / W * W + lane] : make_float2(0.0f, 0.0f);
+        a = warp_sum(v.x);
+        b = warp_sum(v.y);
+    }
+    return make_float2(a, b);
+}
+
+// Two FP32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<unsigned long long&>(d))
+        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+          "l"(reinterpret_cast<unsigned long long&>(c)));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<unsigned long long&>(d))
+        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<unsigned long long&>(d))
+        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+    return d;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+constexpr int kPairs = kCols / 2;     // of the row kernels
+
+// A thread's C columns: C / VEC vectors, `lanes` vectors apart.
+template <typename T_, int VEC, int C>
+__device__ __forceinline__ void unpack_cols(const typename RowVec<T_, VEC>::Raw (&r)[C / VEC], float2 (&v)[C / 2]) {
+    float f[C];
+#pragma unroll
+    for (int i = 0; i < C / VEC; ++i) {
+        float u[VEC];
+        RowVec<T_, VEC>::unpack(r[i], u);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) f[i * VEC + k] = u[k];
+    }
+#pragma unroll
+    for (int q = 0; q < C / 2; ++q) v[q] = make_float2(f[2 * q], f[2 * q + 1]);
+}
+template <typename T_, int VEC, int C>
+__device__ __forceinline__ typename RowVec<T_, VEC>::Raw pack_cols(const float2 (&v)[C / 2], int i) {
+    float u[VEC];
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) {
+        const int q = i * VEC + k;
+        u[k] = q & 1 ? v[q >> 1].y : v[q >> 1].x;
+    }
+    return RowVec<T_, VEC>::pack(u);
+}
+
+// VEC consecutive parameters, of vector c of the row.  `wide`: 16-byte loads
+// (an aligned array; vectors of four or eight).
+template <int VEC>
+__device__ __forceinline__ void load_vector(const float* p, int c, bool wide, float2 (&v)[(VEC + 1) / 2]) {
+    p += (size_t)c * VEC;
+    if constexpr (VEC % 4 == 0) {
+        if (wide) {
+#pragma unroll
+            for (int k = 0; k < VEC / 4; ++k) {
+                const float4 w = reinterpret_cast<const float4*>(p)[k];
+                v[2 * k] = make_float2(w.x, w.y);
+                v[2 * k + 1] = make_float2(w.z, w.w);
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) {
+        if (k & 1) v[k >> 1].y = p[k];
+        else v[k >> 1] = make_float2(p[k], 0.0f);
+    }
+}
+
+// The parameters of the thread's C columns (0 past the row's end).
+template <int VEC, int C>
+__device__ __forceinline__ void load_params(const float* p, int j, int lanes, int n, bool wide, float2 (&v)[C / 2]) {
+#pragma unroll
+    for (int i = 0; i < C / VEC; ++i) {
+        float2 u[(VEC + 1) / 2];
+#pragma unroll
+        for (int q = 0; q < (VEC + 1) / 2; ++q) u[q] = both(0.0f);
+        if (j + i * lanes < n) load_vector<VEC>(p, j + i * lanes, wide, u);
+        if constexpr (VEC == 1) {
+            if (i & 1) v[i >> 1].y = u[0].x;
+            else v[i >> 1].x = u[0].x;
+        } else {
+#pragma unroll
+            for (int q = 0; q < VEC / 2; ++q) v[i * (VEC / 2) + q] = u[q];
+        }
+    }
+}
+
+// C columns a thread.  The row stays packed in registers and is unpacked for
+// each of the three passes.
+template <typename T_, int VEC, int C, int MAXT>
+__global__ void __launch_bounds__(MAXT) norm_rows_kernel(int T, int H, int W, const typename RowVec<T_, VEC>::Raw* x,
+                                                         int64_t x_stride, const float* gamma, const float* beta,
+                                                         float eps, typename RowVec<T_, VEC>::Raw* y, int64_t y_stride,
+                                                         float* mean_out, float* rstd_out, bool wide_params) {
+    using Raw = typename RowVec<T_, VEC>::Raw;
+    constexpr int V = C / VEC;
+    __shared__ float2 s_red[2][32];
+    pdl_wait();
+    const int lanes = W * 32, j = threadIdx.x % lanes;
+    const int64_t t = (int64_t)blockIdx.x * (blockDim.x / lanes) + threadIdx.x / lanes;
+    const bool live = t < T;
+    const int n = H / VEC;
+    Raw r[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) r[i] = live && j + i * lanes < n ? x[t * x_stride + j + i * lanes] : Raw{};
+    float2 sum = both(0.0f), sq = both(0.0f);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        float u[VEC];
+        RowVec<T_, VEC>::unpack(r[i], u);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) (k & 1 ? sum.y : sum.x) += u[k];
+    }
+    const float mean = row_sum2(sum.x + sum.y, 0.0f, W, 0, s_red).x / (float)H;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        float u[VEC];
+        RowVec<T_, VEC>::unpack(r[i], u);
+        if (j + i * lanes < n)                    // columns past the row's end do not count
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) {
+                const float c = u[k] - mean;
+                float& s = k & 1 ? sq.y : sq.x;
+                s = fmaf(c, c, s);
+            }
+    }
+    const float rstd = 1.0f / sqrtf(row_sum2(sq.x + sq.y, 0.0f, W, 1, s_red).x / (float)H + eps);
+    if (live) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = j + i * lanes;
+            if (c >= n) continue;
+            float2 ga[(VEC + 1) / 2], be[(VEC + 1) / 2];
+            float u[VEC];
+            RowVec<T_, VEC>::unpack(r[i], u);
+            load_vector<VEC>(gamma, c, wide_params, ga);
+            if (beta) {
+                load_vector<VEC>(beta, c, wide_params, be);
+            } else {
+#pragma unroll
+                for (int q = 0; q < (VEC + 1) / 2; ++q) be[q] = both(0.0f);
+            }
+#pragma unroll
+            for (int k = 0; k < VEC; ++k)
+                u[k] = fmaf((u[k] - mean) * rstd, k & 1 ? ga[k >> 1].y : ga[k >> 1].x, k & 1 ? be[k >> 1].y : be[k >> 1].x);
+            y[t * y_stride + c] = RowVec<T_, VEC>::pack(u);
+        }
+        if (j == 0 && mean_out) {
+            mean_out[t] = mean;
+            rstd_out[t] = rstd;
+        }
+    }
+    pdl_launch_dependents();
+}
+
+// A row of dy and x in flight.
+template <typename Raw, int V>
+struct NormRow {
+    Raw dy[V], x[V];
+    float mean, rstd;
+};
+
+// D rows in flight beyond the current one.  Blocks of more than 256 threads
+// (64 registers a thread) keep gamma in shared memory.  FULL: the threads'
+// columns are the row's, no guards.  Columns past the row's end have dy = 0
+// and so add nothing to any sum.
+template <typename T_, int VEC, int MAXT, int D, bool FULL>
+__global__ void __launch_bounds__(MAXT)
+    norm_rows_backward_kernel(int T, int H, int W, const typename RowVec<T_, VEC>::Raw* dy, int64_t dy_stride,
+                              const typename RowVec<T_, VEC>::Raw* x, int64_t x_stride, const float* gamma,
+                              const float* mean, const float* rstd, typename RowVec<T_, VEC>::Raw* dx,
+                              int64_t dx_stride, float* part, bool wide_params) {
+    using Raw = typename RowVec<T_, VEC>::Raw;
+    constexpr int V = kCols / VEC;
+    constexpr bool kHeld = MAXT <= 256;
+    __shared__ float2 s_red[2][32];
+    extern __shared__ float2 s_dyn[];        // G > 1: [G][2][W * 128] sums; else gamma [4][MAXT]
+    pdl_wait();
+    const int lanes = W * 32, j = threadIdx.x % lanes, G = blockDim.x / lanes, g = threadIdx.x / lanes;
+    const int n = H / VEC;
+    const int64_t step = (int64_t)gridDim.x * G;
+    float2 ga[kPairs], dg[kPairs], db[kPairs];
+    load_params<VEC, kCols>(gamma, j, lanes, n, wide_params, ga);
+#pragma unroll
+    for (int q = 0; q < kPairs; ++q) {
+        dg[q] = db[q] = both(0.0f);
+        if (!kHeld) s_dyn[q * MAXT + threadIdx.x] = ga[q];           // read by this thread alone
+    }
+    const int64_t first = (int64_t)blockIdx.x * G + g;
+    dy += first * dy_stride + j;
+    x += first * x_stride + j;
+    dx += first * dx_stride + j;
+    const int64_t dy_step = step * dy_stride, x_step = step * x_stride, dx_step = step * dx_stride;
+    auto load = [&](int64_t t) {             // the next row in turn
+        NormRow<Raw, V> r;
+        const bool live = t < T;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const bool there = live && (FULL || j + i * lanes < n);
+            r.dy[i] = there ? dy[i * lanes] : Raw{};
+            r.x[i] = there ? x[i * lanes] : Raw{};
+        }
+        r.mean = live ? mean[t] : 0.0f;
+        r.rstd = live ? rstd[t] : 0.0f;
+        dy += dy_step;
+        x += x_step;
+        return r;
+    };
+    NormRow<Raw, V> ahead[D];
+#pragma unroll
+    for (int q = 0; q < D; ++q) ahead[q] = load(first + q * step);
+    const float inv = 1.0f / (float)H;
+    int turn = 0;
+    for (int64_t tb = first; tb - g < T; tb += D * step) {   // uniform over the block
+        // unrolled over the D buffers: a buffer moved to another register
+        // would wait for its load
+#pragma unroll
+        for (int u = 0; u < D; ++u) {
+            const int64_t t = tb + u * step;
+            if (D > 1 && t - g >= T) break;
+            const float2 m = both(-ahead[u].mean), r = both(ahead[u].rstd);
+            float2 d[kPairs], hat[kPairs];
+            unpack_cols<T_, VEC, kCols>(ahead[u].dy, d);
+            unpack_cols<T_, VEC, kCols>(ahead[u].x, hat);
+            ahead[u] = load(t + D * step);
+            float2 sg = both(0.0f), sgx = both(0.0f);
+#pragma unroll
+            for (int q = 0; q < kPairs; ++q) {
+                hat[q] = mul2(add2(hat[q], m), r);
+                dg[q] = fma2(d[q], hat[q], dg[q]);
+                db[q] = add2(db[q], d[q]);
+                d[q] = mul2(d[q], kHeld ? ga[q] : s_dyn[q * MAXT + threadIdx.x]);
+                sg = add2(sg, d[q]);
+                sgx = fma2(d[q], hat[q], sgx);
+            }
+            const float2 s = row_sum2(sg.x + sg.y, sgx.x + sgx.y, W, turn, s_red);
+            turn ^= 1;
+            if (t < T) {
+                const float2 a = both(-(s.x * inv)), b = both(-(s.y * inv));
+#pragma unroll
+                for (int q = 0; q < kPairs; ++q) d[q] = mul2(fma2(hat[q], b, add2(d[q], a)), r);
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (FULL || j + i * lanes < n) dx[i * lanes] = pack_cols<T_, VEC, kCols>(d, i);
+            }
+            dx += dx_step;
+        }
+    }
+    // this block's sums: its rows' groups in order.  Column of pair q's first
+    // element: eight columns in V vectors
+    float* out = part + (size_t)blockIdx.x * 2 * H;
+    if (G > 1) {
+        float* sums = reinterpret_cast<float*>(s_dyn);
+        const int cols = lanes * kCols;
+#pragma unroll
+        for (int q = 0; q < kCols; ++q) {
+            const int h = (j + q / VEC * lanes) * VEC + q % VEC;
+            sums[(g * 2) * cols + h] = q & 1 ? dg[q >> 1].y : dg[q >> 1].x;
+            sums[(g * 2 + 1) * cols + h] = q & 1 ? db[q >> 1].y : db[q >> 1].x;
+        }
+        __syncthreads();
+        for (int h = threadIdx.x; h < H; h += blockDim.x) {
+            float a = 0.0f, b = 0.0f;
+            for (int q = 0; q < G; ++q) {
+                a += sums[(q * 2) * cols + h];
+                b += sums[(q * 2 + 1) * cols + h];
+            }
+            out[h] = a;
+            out[H + h] = b;
+        }
+    } else if constexpr (VEC % 4 == 0) {
+        // 16-byte stores: H is a multiple of VEC, part 256-byte aligned
+#pragma unroll
+        for (int q = 0; q < kPairs; q += 2) {
+            const int h = (j + 2 * q / VEC * lanes) * VEC + 2 * q % VEC;
+            if (h < H) {
+                *reinterpret_cast<float4*>(out + h) = make_float4(dg[q].x, dg[q].y, dg[q + 1].x, dg[q + 1].y);
+                *reinterpret_cast<float4*>(out + H + h) = make_float4(db[q].x, db[q].y, db[q + 1].x, db[q + 1].y);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int q = 0; q < kCols; ++q) {
+            const int h = (j + q / VEC * lanes) * VEC + q % VEC;
+            if (h < H) {
+                out[h] = q & 1 ? dg[q >> 1].y : dg[q >> 1].x;
+                out[H + h] = q & 1 ? db[q >> 1].y : db[q >> 1].x;
+            }
+        }
+    }
+    pdl_launch_dependents();
+}
+
+// The same for rows of more than kRingMin columns in 16-byte vectors: sixteen
+// columns a thread, 512 threads an SM (one block of 512 or up to four of 128).  The rows ahead
+// wait in shared memory (the copy engine's bulk copies, a ring of S rows of dy
+// and x) instead of registers, which the column sums and the row at hand fill.
+// A stage is free once the row's reduction has passed its barrier: every
+// thread has read its columns by then.  The wait for a copy is bounded (1 s);
+// a block that gave up stops at the barrier, all its threads together.
+template <typename T_, int VEC>
+__global__ void __launch_bounds__(512, 1)
+    norm_ring_backward_kernel(int T, int H, int S, const typename RowVec<T_, VEC>::Raw* dy, int64_t dy_stride,
+                              const typename RowVec<T_, VEC>::Raw* x, int64_t x_stride, const float* gamma,
+                              const float* mean, const float* rstd, typename RowVec<T_, VEC>::Raw* dx,
+                              int64_t dx_stride, float* part, bool wide_params) {
+    using Raw = typename RowVec<T_, VEC>::Raw;
+    constexpr int C = kRingCols, V = C / VEC, P = C / 2;
+    __shared__ float2 s_red[2][16];
+    __shared__ uint64_t s_full[kRingMax];
+    extern __shared__ __align__(16) uint8_t s_ring[];      // gamma [P][threads] float2, then [S][dy, x][n] vectors
+    pdl_wait();
+    const int lanes = blockDim.x, j = threadIdx.x, lane = j & 31, warp = j >> 5, W = lanes >> 5;
+    const int n = H / VEC;
+    float2* s_gamma = reinterpret_cast<float2*>(s_ring);
+    Raw* s_rows = reinterpret_cast<Raw*>(s_ring + (size_t)lanes * C * 4);
+    const uint32_t row_bytes = (uint32_t)n * 16u;
+    const int64_t step = gridDim.x, first = blockIdx.x;
+    uint64_t policy = 0;
+    auto fetch = [&](int64_t t, int stage) {               // thread 0
+        Raw* to = s_rows + (size_t)stage * 2 * n;
+        mbar_arrive_expect_tx(&s_full[stage], 2u * row_bytes);
+        bulk_load(to, dy + t * dy_stride, row_bytes, &s_full[stage], policy);
+        bulk_load(to + n, x + t * x_stride, row_bytes, &s_full[stage], policy);
+    };
+    if (j == 0) {
+        policy = policy_evict_first();                     // dy and x are read once
+        for (int q = 0; q < S; ++q) mbar_init(&s_full[q], 1);
+        fence_mbar_init();
+        for (int q = 0; q < S; ++q)
+            if (first + q * step < T) fetch(first + q * step, q);
+    }
+    float2 dg[P], db[P];
+    {
+        float2 ga[P];
+        load_params<VEC, C>(gamma, j, lanes, n, wide_params, ga);
+#pragma unroll
+        for (int q = 0; q < P; ++q) {
+            s_gamma[q * lanes + j] = ga[q];                // read by this thread alone
+            dg[q] = db[q] = both(0.0f);
+        }
+    }
+    __syncthreads();
+    const float inv = 1.0f / (float)H;
+    int stage = 0, turn = 0;
+    uint32_t parity = 0;
+    float next_mean = first < T ? mean[first] : 0.0f, next_rstd = first < T ? rstd[first] : 0.0f;
+    dx += first * dx_stride + j;
+    const int64_t dx_step = step * dx_stride;
+    volatile int never = 0;
+    for (int64_t t = first; t < T; t += step) {
+        const float2 m = both(-next_mean), r = both(next_rstd);
+        if (t + step < T) {
+            next_mean = mean[t + step];
+            next_rstd = rstd[t + step];
+        }
+        const bool landed = mbar_wait(&s_full[stage], parity, &never, nullptr, 0);
+        float2 d[P], hat[P];
+        {
+            const Raw* at = s_rows + (size_t)stage * 2 * n + j;
+            Raw rd[V], rx[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const bool there = j + v * lanes < n;
+                rd[v] = there ? at[v * lanes] : Raw{};
+                rx[v] = there ? at[n + v * lanes] : Raw{};
+            }
+            unpack_cols<T_, VEC, C>(rd, d);
+            unpack_cols<T_, VEC, C>(rx, hat);
+        }
+        float2 sg = both(0.0f), sgx = both(0.0f);
+#pragma unroll
+        for (int q = 0; q < P; ++q) {
+            hat[q] = mul2(add2(hat[q], m), r);
+            dg[q] = fma2(d[q], hat[q], dg[q]);
+            db[q] = add2(db[q], d[q]);
+            d[q] = mul2(d[q], s_gamma[q * lanes + j]);
+            sg = add2(sg, d[q]);
+            sgx = fma2(d[q], hat[q], sgx);
+        }
+        const float wa = warp_sum(sg.x + sg.y), wb = warp_sum(sgx.x + sgx.y);
+        if (lane == 0) s_red[turn][warp] = make_float2(wa, wb);
+        if (__syncthreads_or(!landed)) {
+            for (int i = 0; i < 100; ++i) __nanosleep(10000);   // copies in flight land before the block leaves
+            break;
+        }
+        if (j == 0 && t + S * step < T) fetch(t + S * step, stage);
+        const float2 w = lane < W ? s_red[turn][lane & 15] : both(0.0f);
+        const float2 a = both(-(warp_sum(w.x) * inv)), b = both(-(warp_sum(w.y) * inv));
+#pragma unroll
+        for (int q = 0; q < P; ++q) d[q] = mul2(fma2(hat[q], b, add2(d[q], a)), r);
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (j + v * lanes < n) dx[v * lanes] = pack_cols<T_, VEC, C>(d, v);
+        turn ^= 1;
+        dx += dx_step;
+        if (++stage == S) { stage = 0; parity ^= 1u; }
+    }
+    // 16-byte stores: H is a multiple of VEC (4 or 8), part 256-byte aligned
+    float* out = part + (size_t)blockIdx.x * 2 * H;
+#pragma unroll
+    for (int q = 0; q < P; q += 2) {
+        const int v = j + 2 * q / VEC * lanes, h = v * VEC + 2 * q % VEC;
+        if (v < n) {
+            *reinterpret_cast<float4*>(out + h) = make_float4(dg[q].x, dg[q].y, dg[q + 1].x, dg[q + 1].y);
+            *reinterpret_cast<float4*>(out + H + h) = make_float4(db[q].x, db[q].y, db[q + 1].x, db[q + 1].y);
+        }
+    }
+    pdl_launch_dependents();
+}
+
+// dgamma and dbeta from `parts` partial sums [parts][2][H]: 32 columns a block,
+// a warp per 32nd of the parts.
+__global__ void __launch_bounds__(1024) norm_reduce_kernel(int H, int parts, const float* part, float* dgamma,
+                                                           float* dbeta) {
+    __shared__ float s[32][33];
+    pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int h = blockIdx.x * 32 + lane;
+    const size_t at = blockIdx.y ? H : 0;
+    float v = 0.0f;
+    if (h < H)
+#pragma unroll 4
+        for (int p = warp; p < parts; p += 32) v += part[(size_t)p * 2 * H + at + h];
+    s[warp][lane] = v;
+    __syncthreads();
+    // warp w sums column w's 32 partial sums
+    v = warp_sum(s[lane][warp]);
+    const int col = blockIdx.x * 32 + warp;
+    if (lane == 0 && col < H) {
+        if (blockIdx.y == 0) dgamma[col] = v;
+        else dbeta[col] = v;
+    }
+    pdl_launch_dependents();
+}
+
+// ---- rows of more than kRowColumns columns -------------------------------------
 
 // Sum over the block; every thread gets it.
 __device__ __forceinline__ float block_sum(float v, float* s) {
@@ -99,20 +587,6 @@ __global__ void __launch_bounds__(kNormThreads) layer_norm_partial_kernel(int T,
     part[(size_t)blockIdx.y * 2 * H + H + h] = db;
 }
 
-__global__ void __launch_bounds__(kNormThreads) layer_norm_reduce_kernel(int H, const float* part, float* dgamma,
-                                                                         float* dbeta) {
-    pdl_wait();
-    const int h = blockIdx.x * kNormThreads + threadIdx.x;
-    if (h >= H) return;
-    float dg = 0.0f, db = 0.0f;
-    for (int p = 0; p < kNormParts; ++p) {
-        dg += part[(size_t)p * 2 * H + h];
-        db += part[(size_t)p * 2 * H + H + h];
-    }
-    dgamma[h] = dg;
-    if (dbeta) dbeta[h] = db;
-}
-
 template <typename T_, int VEC>
 __global__ void __launch_bounds__(kNormThreads)
     layer_norm_dx_kernel(int H, const typename RowVec<T_, VEC>::Raw* dy, int64_t dy_stride,
@@ -150,16 +624,26 @@ __global__ void __launch_bounds__(kNormThreads)
     }
 }
 
-bool vec16(const void* p, int64_t stride, int elem) {
-    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride * elem % 16 == 0;
-}
-
 template <typename T_, int VEC>
 cudaError_t forward_any(const LaunchCtx& c, int T, int H, const void* x, int64_t x_stride, const float* gamma,
                         const float* beta, float eps, void* y, int64_t y_stride, float* mean, float* rstd) {
     using Raw = typename RowVec<T_, VEC>::Raw;
-    return c.launch(layer_norm_kernel<T_, VEC>, dim3(T), dim3(kNormThreads), 0, H, static_cast<const Raw*>(x),
-                    x_stride / VEC, gamma, beta, eps, static_cast<Raw*>(y), y_stride / VEC, mean, rstd);
+    const Raw* xv = static_cast<const Raw*>(x);
+    Raw* yv = static_cast<Raw*>(y);
+    if (H > kRowColumns)
+        return c.launch(layer_norm_kernel<T_, VEC>, dim3(T), dim3(kNormThreads), 0, H, xv, x_stride / VEC, gamma, beta,
+                        eps, yv, y_stride / VEC, mean, rstd);
+    const bool wide_params = (row_at(gamma) | row_at(beta)) % 16 == 0;
+    // long rows, enough of them to fill the SMs: 32 columns a thread, so that
+    // several rows share an SM and overlap their loads with their reductions
+    const bool many = H > 32 * 8 * kCols && T > 152;
+    const NormShape s = norm_shape(H, many ? 32 : kCols);
+    const dim3 grid((unsigned)((T + s.G - 1) / s.G)), block(s.threads());
+    auto kernel = many                 ? norm_rows_kernel<T_, VEC, 32, 256>
+                  : s.threads() <= 256 ? norm_rows_kernel<T_, VEC, kCols, 256>
+                                       : norm_rows_kernel<T_, VEC, kCols, 1024>;
+    return c.launch(kernel, grid, block, 0, T, H, s.W, xv, x_stride / VEC, gamma, beta, eps, yv, y_stride / VEC, mean,
+                    rstd, wide_params);
 }
 
 template <typename T_, int VEC>
@@ -172,32 +656,109 @@ cudaError_t dx_any(const LaunchCtx& c, int T, int H, const void* dy, int64_t dy_
                     static_cast<Raw*>(dx), dx_stride / VEC);
 }
 
+// Resident blocks of the ring kernel on an SM (its shared memory leaves two
+// stages to each: the longest FP32 rows of a share take 16 KB of gamma and 64
+// KB a stage, or a quarter of it).
+int ring_blocks(int H) {
+    const int share = (H + 32 * kRingCols - 1) / (32 * kRingCols);   // warps, of 16
+    return share <= 4 ? 4 : share <= 8 ? 2 : 1;
+}
+
+// Blocks of a persistent backward kernel with `rows` rows at a time: the
+// resident ones, or as many as there are rows for.
+int backward_blocks(int T, int rows, int resident) {
+    const int64_t most = ((int64_t)T + rows - 1) / rows;
+    return (int)(most < 1 ? 1 : most < resident ? most : resident);
+}
+
+template <typename T_, int VEC>
+cudaError_t backward_rows_any(const LaunchCtx& c, int T, int H, const void* dy, int64_t dy_stride, const void* x,
+                              int64_t x_stride, const float* gamma, const float* mean, const float* rstd, void* dx,
+                              int64_t dx_stride, float* part, int* blocks) {
+    using Raw = typename RowVec<T_, VEC>::Raw;
+    const bool wide_params = row_at(gamma) % 16 == 0;
+    const NormShape s = norm_shape(H);
+    if constexpr (sizeof(Raw) == 16) {
+        if (H > kRingMin) {
+            const int threads = (H + 32 * kRingCols - 1) / (32 * kRingCols) * 32;
+            const int per_sm = ring_blocks(H);
+            const int held = threads * kRingCols * 4, stage = 2 * H * (int)sizeof(T_);
+            const int fit = (kRingBytes / per_sm - held) / stage;
+            const int S = fit > kRingMax ? kRingMax : fit;
+            *blocks = backward_blocks(T, 1, per_sm * kNormSms);
+            return c.launch(norm_ring_backward_kernel<T_, VEC>, dim3(*blocks), dim3(threads),
+                            (size_t)held + (size_t)S * stage, T, H, S, static_cast<const Raw*>(dy), dy_stride / VEC,
+                            static_cast<const Raw*>(x), x_stride / VEC, gamma, mean, rstd, static_cast<Raw*>(dx),
+                            dx_stride / VEC, part, wide_params);
+        }
+    }
+    const bool full = s.W * 32 * kCols == H;
+    auto kernel = s.threads() <= 256 ? (full ? norm_rows_backward_kernel<T_, VEC, 256, 2, true>
+                                             : norm_rows_backward_kernel<T_, VEC, 256, 2, false>)
+                                     : norm_rows_backward_kernel<T_, VEC, 1024, 1, false>;
+    const size_t smem = s.threads() > 256 ? (size_t)kCols * 1024 * 4 : s.G > 1 ? (size_t)s.G * 2 * s.W * 32 * kCols * 4 : 0;
+    *blocks = backward_blocks(T, s.G, (s.threads() > 512 ? 1 : 2) * kNormSms);
+    return c.launch(kernel, dim3(*blocks), dim3(s.threads()), smem, T, H, s.W, static_cast<const Raw*>(dy),
+                    dy_stride / VEC, static_cast<const Raw*>(x), x_stride / VEC, gamma, mean, rstd,
+                    static_cast<Raw*>(dx), dx_stride / VEC, part, wide_params);
+}
+
 }  // namespace
 
 cudaError_t launch_layer_norm(const LaunchCtx& c, int T, int H, int elem, const void* x, int64_t x_stride,
                               const float* gamma, const float* beta, float eps, void* y, int64_t y_stride, float* mean,
                               float* rstd) {
-    const bool wide = (int64_t)H * elem % 16 == 0 && vec16(x, x_stride, elem) && vec16(y, y_stride, elem);
-    if (elem == 2)
-        return wide ? forward_any<__nv_bfloat16, 8>(c, T, H, x, x_stride, gamma, beta, eps, y, y_stride, mean, rstd)
-                    : forward_any<__nv_bfloat16, 1>(c, T, H, x, x_stride, gamma, beta, eps, y, y_stride, mean, rstd);
-    return wide ? forward_any<float, 4>(c, T, H, x, x_stride, gamma, beta, eps, y, y_stride, mean, rstd)
-                : forward_any<float, 1>(c, T, H, x, x_stride, gamma, beta, eps, y, y_stride, mean, rstd);
+    const int bytes = row_vec_bytes(H, elem, row_at(x, x_stride, elem) | row_at(y, y_stride, elem));
+    MOE_ROW_VEC(elem, bytes, forward_any, c, T, H, x, x_stride, gamma, beta, eps, y, y_stride, mean, rstd);
+}
+
+cudaError_t setup_layer_norm_kernels() {
+    static_assert(512 * kRingCols * 4 + 2 * 2 * kRowColumns * 4 <= kRingBytes, "two stages of the longest rows");
+    cudaError_t e;
+    if ((e = cudaFuncSetAttribute(norm_ring_backward_kernel<__nv_bfloat16, 8>,
+                                  cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes)))
+        return e;
+    return cudaFuncSetAttribute(norm_ring_backward_kernel<float, 4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                kRingBytes);
 }
 
 size_t layer_norm_workspace_bytes(int T, int H) {
-    (void)T;
-    return align_up((uint64_t)kNormParts * 2 * H * 4, 256);
+    // a block has a row at least
+    const int most = H > kRowColumns ? kNormParts : H > kRingMin && H <= 2048 ? 4 * kNormSms : 2 * kNormSms;
+    return align_up((uint64_t)(H > kRowColumns || T > most ? most : T < 1 ? 1 : T) * 2 * H * 4, 256);
+}
+
+static cudaError_t launch_dx(const LaunchCtx& c, int bytes, int T, int H, int elem, const void* dy, int64_t dy_stride,
+                             const void* x, int64_t x_stride, const float* gamma, const float* mean, const float* rstd,
+                             void* dx, int64_t dx_stride) {
+    MOE_ROW_VEC(elem, bytes, dx_any, c, T, H, dy, dy_stride, x, x_stride, gamma, mean, rstd, dx, dx_stride);
+}
+
+static cudaError_t launch_backward_rows(const LaunchCtx& c, int bytes, int T, int H, int elem, const void* dy,
+                                        int64_t dy_stride, const void* x, int64_t x_stride, const float* gamma,
+                                        const float* mean, const float* rstd, void* dx, int64_t dx_stride,
+                                        float* part, int* blocks) {
+    MOE_ROW_VEC(elem, bytes, backward_rows_any, c, T, H, dy, dy_stride, x, x_stride, gamma, mean, rstd, dx, dx_stride,
+                part, blocks);
 }
 
 cudaError_t launch_layer_norm_backward(const LaunchCtx& c, int T, int H, int elem, const void* dy, int64_t dy_stride,
                                        const void* x, int64_t x_stride, const float* gamma, const float* mean,
                                        const float* rstd, void* dx, int64_t dx_stride, float* dgamma, float* dbeta,
                                        float* workspace) {
-    // the column sums first: dx may overwrite dy or x
-    const dim3 cols((unsigned)((H + kNormThreads - 1) / kNormThreads));
-    const dim3 parts(cols.x, kNormParts);
+    const int bytes = row_vec_bytes(
+        H, elem, row_at(x, x_stride, elem) | row_at(dy, dy_stride, elem) | row_at(dx, dx_stride, elem));
+    const dim3 reduce((unsigned)((H + 31) / 32), dbeta ? 2 : 1);
     cudaError_t e;
+    if (H <= kRowColumns) {
+        int blocks = 0;
+        e = launch_backward_rows(c, bytes, T, H, elem, dy, dy_stride, x, x_stride, gamma, mean, rstd, dx, dx_stride,
+                                 workspace, &blocks);
+        if (e != cudaSuccess) return e;
+        return c.launch(norm_reduce_kernel, reduce, dim3(1024), 0, H, blocks, (const float*)workspace, dgamma, dbeta);
+    }
+    // the column sums first: dx may overwrite dy or x
+    const dim3 parts((unsigned)((H + kNormThreads - 1) / kNormThreads), kNormParts);
     if (elem == 2)
         e = c.launch(layer_norm_partial_kernel<__nv_bfloat16>, parts, dim3(kNormThreads), 0, T, H,
                      static_cast<const uint16_t*>(dy), dy_stride, static_cast<const uint16_t*>(x), x_stride, mean,
@@ -207,15 +768,9 @@ cudaError_t launch_layer_norm_backward(const LaunchCtx& c, int T, int H, int ele
                      static_cast<const uint32_t*>(dy), dy_stride, static_cast<const uint32_t*>(x), x_stride, mean,
                      rstd, workspace);
     if (e != cudaSuccess) return e;
-    e = c.launch(layer_norm_reduce_kernel, cols, dim3(kNormThreads), 0, H, (const float*)workspace, dgamma, dbeta);
+    e = c.launch(norm_reduce_kernel, reduce, dim3(1024), 0, H, kNormParts, (const float*)workspace, dgamma, dbeta);
     if (e != cudaSuccess || T == 0) return e;
-    const bool wide = (int64_t)H * elem % 16 == 0 && vec16(x, x_stride, elem) && vec16(dy, dy_stride, elem) &&
-                      vec16(dx, dx_stride, elem);
-    if (elem == 2)
-        return wide ? dx_any<__nv_bfloat16, 8>(c, T, H, dy, dy_stride, x, x_stride, gamma, mean, rstd, dx, dx_stride)
-                    : dx_any<__nv_bfloat16, 1>(c, T, H, dy, dy_stride, x, x_stride, gamma, mean, rstd, dx, dx_stride);
-    return wide ? dx_any<float, 4>(c, T, H, dy, dy_stride, x, x_stride, gamma, mean, rstd, dx, dx_stride)
-                : dx_any<float, 1>(c, T, H, dy, dy_stride, x, x_stride, gamma, mean, rstd, dx, dx_stride);
+    return launch_dx(c, bytes, T, H, elem, dy, dy_stride, x, x_stride, gamma, mean, rstd, dx, dx_stride);
 }
 
 }  // namespace moe

@@ -94,6 +94,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(int64_t routes
             if (blocks == 1) {
                 for (int w = 0; w < kSortWarps; ++w) total += s_warp[w * E + e];
             } else {
+#pragma unroll 16
                 for (int b = 0; b < blocks; ++b) {
                     const int c = block_count[(size_t)b * E + e];
                     before += b < (int)blockIdx.x ? c : 0;
@@ -162,12 +163,18 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(int64_t routes
 
 constexpr int kRowThreads = 256;
 
-// Threads per token: a power of two in 32..kRowThreads, about `per` vectors
-// each.
-inline int lanes_for(int vectors, int per) {
-    int lanes = 32;
-    while (lanes < kRowThreads && lanes * per < vectors) lanes *= 2;
-    return lanes;
+// A route's row, or -1: lane k of every warp of the token loads route k (at
+// most 32 a token) in one access, instead of one dependent load per route.
+__device__ __forceinline__ int token_route_row(const int* row_of_route, int t, int T, int K, int64_t rows) {
+    const int lane = threadIdx.x & 31;
+    const int row = t < T && lane < K ? row_of_route[(int64_t)t * K + lane] : -1;
+    return row < rows ? row : -1;
+}
+
+// Route k's weight in lane k (a dropped route's weight is never used).
+__device__ __forceinline__ float token_route_weight(const float* topk_w, int t, int T, int K) {
+    const int lane = threadIdx.x & 31;
+    return t < T && lane < K ? topk_w[(int64_t)t * K + lane] : 0.0f;
 }
 
 // V vectors of a token's row in registers, then a store per route.  The grid's
@@ -181,18 +188,19 @@ __global__ void __launch_bounds__(kRowThreads) dispatch_kernel(int T, int n, int
     pdl_wait();
     const int t = blockIdx.x * (kRowThreads / lanes) + threadIdx.x / lanes;
     const int c0 = blockIdx.y * lanes * V + threadIdx.x % lanes;
-    if (c0 >= n) return;
-    if (t < T) {
+    const int my_row = token_route_row(row_of_route, t, T, K, rows);
+    if (t < T) {                             // warp-uniform: a warp holds one token
         Raw v[V];
 #pragma unroll
         for (int i = 0; i < V; ++i)
             if (c0 + i * lanes < n) v[i] = x[(int64_t)t * x_stride + c0 + i * lanes];
+#pragma unroll 4
         for (int k = 0; k < K; ++k) {
-            const int64_t row = row_of_route[(int64_t)t * K + k];
-            if (row < 0 || row >= rows) continue;
+            const int row = __shfl_sync(0xffffffffu, my_row, k);
+            if (row < 0) continue;
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                if (c0 + i * lanes < n) x_rows[row * n + c0 + i * lanes] = v[i];
+                if (c0 + i * lanes < n) x_rows[(int64_t)row * n + c0 + i * lanes] = v[i];
         }
     }
     if (rows_used) {
@@ -203,11 +211,12 @@ __global__ void __launch_bounds__(kRowThreads) dispatch_kernel(int T, int n, int
             for (int i = 0; i < V; ++i)
                 if (c0 + i * lanes < n) x_rows[row * n + c0 + i * lanes] = zero;
     }
+    pdl_launch_dependents();
 }
 
-// One vector of a token's row per thread: the weighted sum over its routes,
-// k ascending, four rows in flight.
-template <typename T_, int VEC, bool WEIGHTED>
+// V vectors of a token's row per thread: the weighted sum over its routes, k
+// ascending, KB rows in flight.
+template <typename T_, int VEC, int V, int KB, bool WEIGHTED>
 __global__ void __launch_bounds__(kRowThreads) combine_kernel(int T, int n, int K, int64_t rows,
                                                               const typename RowVec<T_, VEC>::Raw* __restrict__ o,
                                                               const int* __restrict__ row_of_route,
@@ -217,39 +226,47 @@ __global__ void __launch_bounds__(kRowThreads) combine_kernel(int T, int n, int 
     using RV = RowVec<T_, VEC>;
     pdl_wait();
     const int t = blockIdx.x * (kRowThreads / lanes) + threadIdx.x / lanes;
+    const int c0 = blockIdx.y * lanes * V + threadIdx.x % lanes;
+    const int my_row = token_route_row(row_of_route, t, T, K, rows);
+    const float my_w = WEIGHTED ? token_route_weight(topk_w, t, T, K) : 1.0f;
     if (t >= T) return;
-    const int c = blockIdx.y * lanes + threadIdx.x % lanes;
-    if (c >= n) return;
-    float acc[VEC];
+    float acc[V][VEC];
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) acc[j] = 0.0f;
-    for (int k0 = 0; k0 < K; k0 += 4) {
-        typename RV::Raw v[4];
-        float w[4];
-        bool there[4];
+    for (int i = 0; i < V; ++i)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t row = k0 + i < K ? row_of_route[(int64_t)t * K + k0 + i] : -1;
-            there[i] = row >= 0 && row < rows;
-            if (there[i]) {
-                v[i] = o[row * n + c];
-                w[i] = WEIGHTED ? topk_w[(int64_t)t * K + k0 + i] : 1.0f;
+        for (int j = 0; j < VEC; ++j) acc[i][j] = 0.0f;
+    for (int k0 = 0; k0 < K; k0 += KB) {
+        typename RV::Raw v[KB][V];
+        int row[KB];
+#pragma unroll
+        for (int k = 0; k < KB; ++k) {
+            row[k] = __shfl_sync(0xffffffffu, my_row, k0 + k);
+            if (k0 + k >= K) row[k] = -1;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (row[k] >= 0 && c0 + i * lanes < n) v[k][i] = o[(int64_t)row[k] * n + c0 + i * lanes];
+        }
+#pragma unroll
+        for (int k = 0; k < KB; ++k) {
+            const float w = WEIGHTED ? __shfl_sync(0xffffffffu, my_w, k0 + k) : 1.0f;
+            if (row[k] < 0) continue;              // warp-uniform
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                float f[VEC];
+                RV::unpack(v[k][i], f);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) acc[i][j] = WEIGHTED ? fmaf(w, f[j], acc[i][j]) : acc[i][j] + f[j];
             }
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (!there[i]) continue;
-            float f[VEC];
-            RV::unpack(v[i], f);
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) acc[j] = WEIGHTED ? fmaf(w[i], f[j], acc[j]) : acc[j] + f[j];
-        }
     }
-    y[(int64_t)t * y_stride + c] = RV::pack(acc);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if (c0 + i * lanes < n) y[(int64_t)t * y_stride + c0 + i * lanes] = RV::pack(acc[i]);
+    pdl_launch_dependents();
 }
 
-// A token's row of dy against its routes' rows of o, eight routes at a time.
-template <typename T_, int VEC>
+// A token's row of dy against its routes' rows of o, kK routes at a time.
+template <typename T_, int VEC, int V, int kK>
 __global__ void __launch_bounds__(kRowThreads)
     combine_backward_kernel(int T, int n, int K, int64_t rows, const typename RowVec<T_, VEC>::Raw* __restrict__ dy,
                             int64_t dy_stride, const typename RowVec<T_, VEC>::Raw* __restrict__ o,
@@ -257,44 +274,58 @@ __global__ void __launch_bounds__(kRowThreads)
                             const int* __restrict__ rows_used, typename RowVec<T_, VEC>::Raw* __restrict__ d_o,
                             float* __restrict__ dw, int lanes) {
     using RV = RowVec<T_, VEC>;
-    constexpr int kK = 8;
     __shared__ float s_part[kRowThreads / 32][kK];
     pdl_wait();
     const int t = blockIdx.x * (kRowThreads / lanes) + threadIdx.x / lanes;
     const int tl = threadIdx.x % lanes, warp = threadIdx.x >> 5;
     const bool live = t < T;
+    const int my_row = token_route_row(row_of_route, t, T, K, rows);
+    const float my_w = token_route_weight(topk_w, t, T, K);
     for (int k0 = 0; k0 < K; k0 += kK) {
-        int64_t row[kK];
+        int row[kK];
         float w[kK], acc[kK];
 #pragma unroll
-        for (int i = 0; i < kK; ++i) {
-            row[i] = live && k0 + i < K ? row_of_route[(int64_t)t * K + k0 + i] : -1;
-            if (row[i] >= rows) row[i] = -1;
-            w[i] = row[i] >= 0 ? topk_w[(int64_t)t * K + k0 + i] : 0.0f;
-            acc[i] = 0.0f;
+        for (int k = 0; k < kK; ++k) {
+            row[k] = __shfl_sync(0xffffffffu, my_row, k0 + k);
+            w[k] = __shfl_sync(0xffffffffu, my_w, k0 + k);
+            if (k0 + k >= K) row[k] = -1;
+            acc[k] = 0.0f;
         }
         if (live) {
-            for (int c = tl; c < n; c += lanes) {
-                float g[VEC];
-                RV::unpack(dy[(int64_t)t * dy_stride + c], g);
+            for (int c = tl; c < n; c += lanes * V) {
+                typename RV::Raw gr[V], fr[kK][V];
 #pragma unroll
-                for (int i = 0; i < kK; ++i) {
-                    if (row[i] < 0) continue;
-                    float f[VEC], d[VEC];
-                    RV::unpack(o[row[i] * n + c], f);
+                for (int i = 0; i < V; ++i)
+                    if (c + i * lanes < n) gr[i] = dy[(int64_t)t * dy_stride + c + i * lanes];
 #pragma unroll
-                    for (int j = 0; j < VEC; ++j) {
-                        acc[i] = fmaf(g[j], f[j], acc[i]);
-                        d[j] = w[i] * g[j];
+                for (int k = 0; k < kK; ++k)
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+                        if (row[k] >= 0 && c + i * lanes < n) fr[k][i] = o[(int64_t)row[k] * n + c + i * lanes];
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    if (c + i * lanes >= n) continue;
+                    float g[VEC];
+                    RV::unpack(gr[i], g);
+#pragma unroll
+                    for (int k = 0; k < kK; ++k) {
+                        if (row[k] < 0) continue;
+                        float f[VEC], d[VEC];
+                        RV::unpack(fr[k][i], f);
+#pragma unroll
+                        for (int j = 0; j < VEC; ++j) {
+                            acc[k] = fmaf(g[j], f[j], acc[k]);
+                            d[j] = w[k] * g[j];
+                        }
+                        d_o[(int64_t)row[k] * n + c + i * lanes] = RV::pack(d);
                     }
-                    d_o[row[i] * n + c] = RV::pack(d);
                 }
             }
         }
 #pragma unroll
-        for (int i = 0; i < kK; ++i) {
-            const float s = warp_sum(acc[i]);
-            if ((threadIdx.x & 31) == 0) s_part[warp][i] = s;
+        for (int k = 0; k < kK; ++k) {
+            const float s = warp_sum(acc[k]);
+            if ((threadIdx.x & 31) == 0) s_part[warp][k] = s;
         }
         __syncthreads();
         if (live && tl < kK && k0 + tl < K) {
@@ -305,13 +336,13 @@ __global__ void __launch_bounds__(kRowThreads)
         __syncthreads();
     }
     if (rows_used) {
+        const typename RV::Raw zero = {};
         const int groups = gridDim.x * (kRowThreads / lanes);
         for (int64_t r = (int64_t)max(0, *rows_used) + t; r < rows; r += groups)
-            for (int c = tl; c < n; c += lanes) d_o[r * n + c] = RV::zero();
+            for (int c = tl; c < n; c += lanes) d_o[r * n + c] = zero;
     }
+    pdl_launch_dependents();
 }
-
-bool vec16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 // Blocks for T tokens, `lanes` threads each (one for none: rows to clear).
 unsigned token_blocks(int T, int lanes) {
@@ -319,8 +350,20 @@ unsigned token_blocks(int T, int lanes) {
     return (unsigned)(T < 1 ? 1 : (T + per - 1) / per);
 }
 
-// Rows of H elements, `stride` apart, that all start on 16-byte boundaries.
-bool vec16_rows(const void* p, int64_t stride, int elem) { return vec16(p) && stride * elem % 16 == 0; }
+// Threads per token (a power of two in 32..kRowThreads) for rows of n items,
+// an item a thread at a time: the most threads among the counts that leave
+// the fewest idle in the last step.
+int lanes_for(int n) {
+    int best = 32, best_cost = 1 << 30;
+    for (int lanes = 32; lanes <= kRowThreads; lanes *= 2) {
+        const int cost = (n + lanes - 1) / lanes * lanes;
+        if (cost <= best_cost) {
+            best = lanes;
+            best_cost = cost;
+        }
+    }
+    return best;
+}
 
 }  // namespace
 
@@ -346,19 +389,24 @@ cudaError_t launch_sort_routes(const LaunchCtx& c, int T, int E, int K, const in
 
 cudaError_t launch_dispatch(const LaunchCtx& c, int T, int H, int K, int64_t rows, int elem, const void* x,
                             int64_t x_stride, const int* row_of_route, const int* rows_used, void* x_rows) {
-    const bool wide = H * elem % 16 == 0 && vec16_rows(x, x_stride, elem) && vec16(x_rows);
-    const int per = wide ? 16 / elem : 1;
+    const int bytes = row_vec_bytes(H, elem, row_at(x, x_stride, elem) | row_at(x_rows));
+    const int per = bytes / elem;
     const int n = H / per;
-    constexpr int V = 4;
-    const int lanes = lanes_for(n, V);
-    const dim3 grid(token_blocks(T, lanes),
-                    (unsigned)((n + lanes * V - 1) / (lanes * V)));
-#define MOE_DISPATCH(RAW)                                                                                      \
+    // few tokens: a vector a thread over more blocks; else four, so that a
+    // thread has four loads in flight
+    const bool few = T < 64;
+    const int lanes = lanes_for(few ? n : (n + 3) / 4);
+    const int slice = lanes * (few ? 1 : 4);
+    const dim3 grid(token_blocks(T, lanes), (unsigned)((n + slice - 1) / slice));
+#define MOE_DISPATCH(RAW, V)                                                                                   \
     c.launch(dispatch_kernel<RAW, V>, grid, dim3(kRowThreads), 0, T, n, K, rows, static_cast<const RAW*>(x),    \
              x_stride / per, row_of_route, rows_used, static_cast<RAW*>(x_rows), lanes)
-    if (wide) return MOE_DISPATCH(uint4);
-    if (elem == 4) return MOE_DISPATCH(uint32_t);
-    return MOE_DISPATCH(uint16_t);
+    switch (bytes) {
+        case 16: return few ? MOE_DISPATCH(uint4, 1) : MOE_DISPATCH(uint4, 4);
+        case 8: return few ? MOE_DISPATCH(uint2, 1) : MOE_DISPATCH(uint2, 4);
+        case 4: return few ? MOE_DISPATCH(uint32_t, 1) : MOE_DISPATCH(uint32_t, 4);
+        default: return few ? MOE_DISPATCH(uint16_t, 1) : MOE_DISPATCH(uint16_t, 4);
+    }
 #undef MOE_DISPATCH
 }
 
@@ -366,25 +414,23 @@ template <typename T_, int VEC>
 static cudaError_t combine_any(const LaunchCtx& c, int T, int H, int K, int64_t rows, const void* o,
                                const int* row_of_route, const float* w, void* y, int64_t y_stride) {
     using Raw = typename RowVec<T_, VEC>::Raw;
+    // 16-byte vectors: one a thread, eight rows in flight; narrower ones: four
+    // a thread, four rows in flight
+    constexpr int V = sizeof(Raw) == 16 ? 1 : 4, KB = sizeof(Raw) == 16 ? 8 : 4;
     const int n = H / VEC;
-    const int lanes = lanes_for(n, 1);
-    const dim3 grid(token_blocks(T, lanes),
-                    (unsigned)((n + lanes - 1) / lanes));
+    const int lanes = lanes_for((n + V - 1) / V);
+    const dim3 grid(token_blocks(T, lanes), (unsigned)((n + lanes * V - 1) / (lanes * V)));
     if (w)
-        return c.launch(combine_kernel<T_, VEC, true>, grid, dim3(kRowThreads), 0, T, n, K, rows,
+        return c.launch(combine_kernel<T_, VEC, V, KB, true>, grid, dim3(kRowThreads), 0, T, n, K, rows,
                         static_cast<const Raw*>(o), row_of_route, w, static_cast<Raw*>(y), y_stride / VEC, lanes);
-    return c.launch(combine_kernel<T_, VEC, false>, grid, dim3(kRowThreads), 0, T, n, K, rows,
+    return c.launch(combine_kernel<T_, VEC, V, KB, false>, grid, dim3(kRowThreads), 0, T, n, K, rows,
                     static_cast<const Raw*>(o), row_of_route, w, static_cast<Raw*>(y), y_stride / VEC, lanes);
 }
 
 cudaError_t launch_combine(const LaunchCtx& c, int T, int H, int K, int64_t rows, int elem, const void* o,
                            const int* row_of_route, const float* w, void* y, int64_t y_stride) {
-    const bool wide = H * elem % 16 == 0 && vec16(o) && vec16_rows(y, y_stride, elem);
-    if (elem == 2)
-        return wide ? combine_any<__nv_bfloat16, 8>(c, T, H, K, rows, o, row_of_route, w, y, y_stride)
-                    : combine_any<__nv_bfloat16, 1>(c, T, H, K, rows, o, row_of_route, w, y, y_stride);
-    return wide ? combine_any<float, 4>(c, T, H, K, rows, o, row_of_route, w, y, y_stride)
-                : combine_any<float, 1>(c, T, H, K, rows, o, row_of_route, w, y, y_stride);
+    const int bytes = row_vec_bytes(H, elem, row_at(o) | row_at(y, y_stride, elem));
+    MOE_ROW_VEC(elem, bytes, combine_any, c, T, H, K, rows, o, row_of_route, w, y, y_stride);
 }
 
 template <typename T_, int VEC>
@@ -393,26 +439,25 @@ static cudaError_t combine_backward_any(const LaunchCtx& c, int T, int H, int K,
                                         const int* rows_used, void* d_o, float* dw) {
     using Raw = typename RowVec<T_, VEC>::Raw;
     const int n = H / VEC;
-    const int lanes = lanes_for(n, 2);
-    return c.launch(combine_backward_kernel<T_, VEC>,
-                    dim3(token_blocks(T, lanes)), dim3(kRowThreads), 0, T, n,
-                    K, rows, static_cast<const Raw*>(dy), dy_stride / VEC, static_cast<const Raw*>(o), row_of_route, w,
+    // eight loads of o in flight: a vector of eight routes, or two of four
+    if (K <= 4) {
+        const int lanes = lanes_for((n + 1) / 2);
+        return c.launch(combine_backward_kernel<T_, VEC, 2, 4>, dim3(token_blocks(T, lanes)), dim3(kRowThreads), 0, T, n,
+                        K, rows, static_cast<const Raw*>(dy), dy_stride / VEC, static_cast<const Raw*>(o), row_of_route,
+                        w, rows_used, static_cast<Raw*>(d_o), dw, lanes);
+    }
+    const int lanes = lanes_for(n);
+    return c.launch(combine_backward_kernel<T_, VEC, 1, 8>, dim3(token_blocks(T, lanes)), dim3(kRowThreads), 0, T, n, K,
+                    rows, static_cast<const Raw*>(dy), dy_stride / VEC, static_cast<const Raw*>(o), row_of_route, w,
                     rows_used, static_cast<Raw*>(d_o), dw, lanes);
 }
 
 cudaError_t launch_combine_backward(const LaunchCtx& c, int T, int H, int K, int64_t rows, int elem, const void* dy,
                                     int64_t dy_stride, const void* o, const int* row_of_route, const float* w,
                                     const int* rows_used, void* d_o, float* dw) {
-    const bool wide = H * elem % 16 == 0 && vec16(o) && vec16(d_o) && vec16_rows(dy, dy_stride, elem);
-    if (elem == 2)
-        return wide ? combine_backward_any<__nv_bfloat16, 8>(c, T, H, K, rows, dy, dy_stride, o, row_of_route, w,
-                                                             rows_used, d_o, dw)
-                    : combine_backward_any<__nv_bfloat16, 1>(c, T, H, K, rows, dy, dy_stride, o, row_of_route, w,
-                                                             rows_used, d_o, dw);
-    return wide ? combine_backward_any<float, 4>(c, T, H, K, rows, dy, dy_stride, o, row_of_route, w, rows_used, d_o,
-                                                 dw)
-                : combine_backward_any<float, 1>(c, T, H, K, rows, dy, dy_stride, o, row_of_route, w, rows_used, d_o,
-                                                 dw);
+    const int bytes = row_vec_bytes(H, elem, row_at(o) | row_at(d_o) | row_at(dy, dy_stride, elem));
+    MOE_ROW_VEC(elem, bytes, combine_backward_any, c, T, H, K, rows, dy, dy_stride, o, row_of_route, w, rows_used, d_o,
+                dw);
 }
 
 }  // namespace moe

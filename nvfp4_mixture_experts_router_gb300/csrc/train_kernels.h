@@ -23,6 +23,7 @@ cudaError_t launch_combine_backward(const LaunchCtx& c, int T, int H, int K, int
 cudaError_t launch_layer_norm(const LaunchCtx& c, int T, int H, int elem, const void* x, int64_t x_stride,
                               const float* gamma, const float* beta, float eps, void* y, int64_t y_stride, float* mean,
                               float* rstd);
+cudaError_t setup_layer_norm_kernels();
 size_t layer_norm_workspace_bytes(int T, int H);
 cudaError_t launch_layer_norm_backward(const LaunchCtx& c, int T, int H, int elem, const void* dy, int64_t dy_stride,
                                        const void* x, int64_t x_stride, const float* gamma, const float* mean,
