@@ -13,7 +13,7 @@
 // The weights sit on the M side, so that the tile's row extent TN follows the
 // experts' segment lengths: an expert with one row streams its weights past a
 // 32-row tile.  An operand whose m or n is contiguous in memory is copied as
-// it lies (64 x 64 boxes, 128-byte swizzle) and read by the MMA as an MN-major
+// it lies (64 x 128 boxes, 128-byte swizzle) and read by the MMA as an MN-major
 // operand: no transposed copy of w, dy or x is ever made.
 //
 // Segments are ragged and unpadded.  forward / dgrad: rows of a tile past the
@@ -42,9 +42,7 @@ namespace moe {
 
 namespace {
 
-constexpr int kDepth = 64;                     // reduction elements per stage
 constexpr int kHalfM = 128;                    // A rows per CTA
-constexpr int kTileA = kHalfM * kDepth * 2;    // bytes
 constexpr int kMGroup = 8;                     // m tiles walked together (L2 reuse)
 constexpr int kMaxExperts = 1024;
 
@@ -58,38 +56,88 @@ struct ExpertParams {
     const int* offsets;
     __nv_bfloat16* out;
     unsigned int* status;  // may be null
+    int half_m;            // D rows per CTA of a tile, up to kHalfM
+    int box_n;             // forward, dgrad: B rows per copy
 };
 
-template <int TN>
+// DEPTH: reduction elements per stage.  Deep stages (64 KB a CTA at TN = 256)
+// halve the barrier hand-offs per MMA; the shallow wgrad leaves room for wider
+// stores (see kWgradDeepRows).
+template <int PRODUCT, int TN, int DEPTH>
 struct ExpertCfg {
+    static constexpr bool kWgrad = PRODUCT == kExpertWgrad;
+    static_assert(DEPTH == 128 || (DEPTH == 64 && kWgrad), "K-major rows come in two chunks of 64");
     static constexpr int kHalfN = TN / 2;                          // B rows per CTA
-    static constexpr int kTileB = kHalfN * kDepth * 2;
-    static constexpr int kStages = TN == 256 ? 6 : TN == 128 ? 8 : TN == 64 ? 10 : 11;
+    static constexpr int kTileA = kHalfM * DEPTH * 2;              // bytes
+    static constexpr int kTileB = kHalfN * DEPTH * 2;
+    static constexpr int kChunkMn = DEPTH * 128;                   // bytes of an MN-major chunk
+    static constexpr int kStages = DEPTH == 64 ? 5 : TN == 256 ? 3 : TN == 128 ? 4 : 5;
+    static constexpr int kOutCols = DEPTH == 64 ? 64 : 32;         // wgrad: columns a warp stores at a time
+    static constexpr int kOutBytes = 32 * kOutCols * 2;
     static constexpr int kEpiWarps = TN >= 64 ? 8 : 4;
     static constexpr int kThreads = (4 + kEpiWarps) * 32;
     static constexpr uint32_t kTmemCols = 2 * TN;
     static constexpr int kBars = 3 * kStages + 5;
+    static constexpr int kOut = kWgrad ? kEpiWarps * kOutBytes : 0;
     static constexpr int kSmemBytes =
-        1024 + kStages * (kTileA + kTileB) + 3 * kMaxExperts * 4 + kBars * 8 + 64;
+        1024 + kStages * (kTileA + kTileB) + kOut + 3 * kMaxExperts * 4 + kBars * 8 + 64;
     static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
 
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// MN-major operand tile: chunks of 64 m (or n) elements, each [64 d][128 B]
+// MN-major operand tile: chunks of 64 m (or n) elements, each [depth][128 B]
 // with the 128-byte swizzle; `chunk` = bytes from chunk to chunk (the leading
 // offset), 1024 bytes from one group of eight d to the next (the stride).
 __device__ __forceinline__ uint64_t sdesc_mnmajor_sw128(uint32_t saddr, uint32_t chunk) {
     return sdesc(saddr, chunk, 1024, kSwizzle128B);
 }
 
+// Descriptor offset (16-byte units) of a stage's j-th 16 reduction elements:
+// 16 rows of 128 bytes further in every chunk (MN-major), or 32 bytes further
+// in the rows of the 64-element chunk j / 4 (K-major, TILE bytes in two chunks).
+template <bool MN, int TILE>
+__device__ __forceinline__ uint64_t operand_step(int j) {
+    return MN ? (uint64_t)j * 128 : (uint64_t)((j >> 2) * (TILE / 2 / 16) + (j & 3) * 2);
+}
+
+// Place of 16-byte chunk c of row r in a store buffer of COLS columns: the 128-
+// or 64-byte swizzle of its tensor map, which keeps the writes of a warp's 32
+// rows on different banks.
+template <int COLS>
+__device__ __forceinline__ int out_chunk(int r, int c) {
+    return COLS == 64 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
+
+// Store of a shared-memory box (the part inside the map's extents).
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* smem, int x, int y, int z) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(smem_u32(smem)), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void tma_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void tma_store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 // Bits 15 / 16 of the instruction descriptor: A / B is MN-major.
 constexpr uint32_t kIdescAMn = 1u << 15, kIdescBMn = 1u << 16;
 
 struct ExpertTile {
     int e, m0, n0;         // expert, first m of the pair's tile, first n
+    int n;                 // columns of D the MMAs compute, a multiple of 32 up to TN
     int first, count;      // the expert's segment
 };
+
+// Columns of an expert's tiles.  forward / dgrad: the segment in equal parts of
+// at most TN (the MMAs' time follows N, so 300 rows cost two tiles of 160, not
+// of 256).  wgrad: TN, whose stores leave in 64-column boxes.
+template <int TN, bool WGRAD>
+__device__ __forceinline__ int tile_columns(int extent) {
+    if (WGRAD) return TN;
+    const int parts = (extent + TN - 1) / TN;
+    return parts ? min(TN, ((extent + parts - 1) / parts + 31) / 32 * 32) : TN;
+}
 
 // The tile list: experts in order, an expert's tiles in groups of kMGroup m
 // tiles, n outer and m inner, so that the pairs running at a time share both
@@ -108,27 +156,31 @@ __device__ __forceinline__ ExpertTile expert_tile(const ExpertParams& p, int til
     t.first = s_first[lo];
     t.count = s_count[lo];
     const int local = tile - (lo ? s_end[lo - 1] : 0);
-    const int mt = (p.m_extent + 255) / 256;
-    const int nt = ((WGRAD ? p.n_extent : t.count) + TN - 1) / TN;
+    const int mt = (p.m_extent + 2 * p.half_m - 1) / (2 * p.half_m);
+    const int extent = WGRAD ? p.n_extent : t.count;
+    t.n = tile_columns<TN, WGRAD>(extent);
+    const int nt = (extent + t.n - 1) / t.n;
     const int g = local / (kMGroup * nt), in = local % (kMGroup * nt);
     const int gm = min(kMGroup, mt - g * kMGroup);
-    t.n0 = in / gm * TN;
-    t.m0 = (g * kMGroup + in % gm) * 256;
+    t.n0 = in / gm * t.n;
+    if (WGRAD) t.n = min(TN, (extent - t.n0 + 31) / 32 * 32);
+    t.m0 = (g * kMGroup + in % gm) * 2 * p.half_m;
     return t;
 }
 
-template <int PRODUCT, int TN>
-__global__ void __launch_bounds__(ExpertCfg<TN>::kThreads, 1)
+template <int PRODUCT, int TN, int DEPTH>
+__global__ void __launch_bounds__(ExpertCfg<PRODUCT, TN, DEPTH>::kThreads, 1)
     expert_linear_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                         const ExpertParams p) {
-    using C = ExpertCfg<TN>;
+                         const __grid_constant__ CUtensorMap tmC, const ExpertParams p) {
+    using C = ExpertCfg<PRODUCT, TN, DEPTH>;
     constexpr bool kWgrad = PRODUCT == kExpertWgrad;
     constexpr bool kAMn = PRODUCT != kExpertForward;      // A's m contiguous
     extern __shared__ uint8_t smem_raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* s_a = base;
-    uint8_t* s_b = s_a + C::kStages * kTileA;
-    uint64_t* full = reinterpret_cast<uint64_t*>(s_b + C::kStages * C::kTileB);   // rank 0: a stage of both CTAs
+    uint8_t* s_b = s_a + C::kStages * C::kTileA;
+    uint8_t* s_out = s_b + C::kStages * C::kTileB;
+    uint64_t* full = reinterpret_cast<uint64_t*>(s_out + C::kOut);                // rank 0: a stage of both CTAs
     uint64_t* empty = full + C::kStages;                                          // both: the stage's MMAs are done
     uint64_t* landed = empty + C::kStages;                                        // own copies of a stage to be cut
     uint64_t* acc_full = landed + C::kStages;
@@ -159,6 +211,7 @@ __global__ void __launch_bounds__(ExpertCfg<TN>::kThreads, 1)
         fence_mbar_init();
         prefetch_tensormap(&tmA);
         prefetch_tensormap(&tmB);
+        if (kWgrad) prefetch_tensormap(&tmC);
     }
     if (warp == 1) {
         tmem_alloc_pair(tmem_holder, C::kTmemCols);
@@ -166,7 +219,7 @@ __global__ void __launch_bounds__(ExpertCfg<TN>::kThreads, 1)
     }
     pdl_wait();
     {
-        const int mt = (p.m_extent + 255) / 256;
+        const int mt = (p.m_extent + 2 * p.half_m - 1) / (2 * p.half_m);
         for (int e = threadIdx.x; e < p.E; e += C::kThreads) {
             int64_t first = p.offsets[e], n = p.count[e];
             if (n < 0 || first < 0 || first + n > p.rows) {
@@ -175,7 +228,8 @@ __global__ void __launch_bounds__(ExpertCfg<TN>::kThreads, 1)
             }
             s_first[e] = (int)first;
             s_count[e] = (int)n;
-            s_end[e] = mt * (int)(((kWgrad ? p.n_extent : n) + TN - 1) / TN);
+            const int extent = kWgrad ? p.n_extent : (int)n, cols = tile_columns<TN, kWgrad>(extent);
+            s_end[e] = mt * ((extent + cols - 1) / cols);
         }
         __syncthreads();
         if (warp == 0) {
@@ -214,36 +268,43 @@ __global__ void __launch_bounds__(ExpertCfg<TN>::kThreads, 1)
             for (int tile = slot; tile < total; tile += slots) {
                 const ExpertTile t = expert_tile<TN, kWgrad>(p, tile, s_end, s_first, s_count);
                 const int depth = kWgrad ? t.count : p.depth;
-                const int m0 = t.m0 + (int)rank * kHalfM, n0 = t.n0 + (int)rank * C::kHalfN;
-                for (int d = 0; d < depth; d += kDepth) {
+                const int m0 = t.m0 + (int)rank * p.half_m, n0 = t.n0 + (int)rank * (t.n / 2);
+                // forward, dgrad: a half of B with no row of the segment is
+                // left as it is (its columns of D are not stored)
+                const bool b1 = kWgrad || t.n0 + t.n / 2 < t.count;
+                const bool b_mine = rank == 0 || b1;
+                for (int d = 0; d < depth; d += DEPTH) {
                     // completed by rank 0's commit: acquire at cluster scope
                     if (!mbar_wait<true>(&empty[stage], phase ^ 1u, abort, p.status, kStatusTimeoutProducer)) goto done;
-                    constexpr uint32_t kBytes = kTileA + C::kTileB;
-                    uint8_t* a_dst = s_a + stage * kTileA;
+                    uint8_t* a_dst = s_a + stage * C::kTileA;
                     uint8_t* b_dst = s_b + stage * C::kTileB;
                     // a stage to be cut: counted on this CTA's own barrier,
                     // and warp 3 announces it
-                    const bool cut = kWgrad && depth - d < kDepth && (depth & 15) != 0;
+                    const bool cut = kWgrad && depth - d < DEPTH && (depth & 15) != 0;
+                    const int chunks = depth - d > 64 ? 2 : 1;             // of K-major rows
+                    const uint32_t a_bytes = kAMn ? C::kTileA : (uint32_t)(chunks * p.half_m * 128);
+                    const uint32_t b_bytes = kWgrad ? C::kTileB : (uint32_t)(chunks * p.box_n * 128);
                     const uint32_t bar = (cut ? landed_own : full0) + (uint32_t)stage * 8u;
-                    if (cut) mbar_arrive_expect_tx(&landed[stage], kBytes);
-                    else if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2u * kBytes);
+                    if (cut) mbar_arrive_expect_tx(&landed[stage], a_bytes + b_bytes);
+                    else if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2u * a_bytes + (b1 ? 2u : 1u) * b_bytes);
                     else mbar_arrive_cluster(full0 + (uint32_t)stage * 8u);
+                    if (kAMn) {
+#pragma unroll
+                        for (int j = 0; j < kHalfM / 64; ++j) {
+                            if (kWgrad) tma_load_2d_pair(a_dst + j * C::kChunkMn, &tmA, bar, m0 + 64 * j, t.first + d, pol);
+                            else tma_load_3d_pair(a_dst + j * C::kChunkMn, &tmA, bar, m0 + 64 * j, d, t.e, pol);
+                        }
+                    } else {
+                        for (int c = 0; c < chunks; ++c)
+                            tma_load_3d_pair(a_dst + c * (C::kTileA / 2), &tmA, bar, d + 64 * c, m0, t.e, pol);
+                    }
                     if (kWgrad) {
 #pragma unroll
-                        for (int j = 0; j < kHalfM / 64; ++j)
-                            tma_load_2d_pair(a_dst + j * 8192, &tmA, bar, m0 + 64 * j, t.first + d, pol);
-#pragma unroll
                         for (int j = 0; j < C::kHalfN / 64; ++j)
-                            tma_load_2d_pair(b_dst + j * 8192, &tmB, bar, n0 + 64 * j, t.first + d, pol);
-                    } else {
-                        if (kAMn) {
-#pragma unroll
-                            for (int j = 0; j < kHalfM / 64; ++j)
-                                tma_load_3d_pair(a_dst + j * 8192, &tmA, bar, m0 + 64 * j, d, t.e, pol);
-                        } else {
-                            tma_load_3d_pair(a_dst, &tmA, bar, d, m0, t.e, pol);
-                        }
-                        tma_load_2d_pair(b_dst, &tmB, bar, d, t.first + n0, pol);
+                            tma_load_2d_pair(b_dst + j * C::kChunkMn, &tmB, bar, n0 + 64 * j, t.first + d, pol);
+                    } else if (b_mine) {
+                        for (int c = 0; c < chunks; ++c)
+                            tma_load_2d_pair(b_dst + c * (C::kTileB / 2), &tmB, bar, d + 64 * c, t.first + n0, pol);
                     }
                     if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
                 }
@@ -251,10 +312,7 @@ __global__ void __launch_bounds__(ExpertCfg<TN>::kThreads, 1)
         }
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {
-            constexpr uint32_t idesc = idesc_bf16(256, TN) | (kAMn ? kIdescAMn : 0u) | (kWgrad ? kIdescBMn : 0u);
-            // 16 d further: 16 rows of 128 bytes (MN-major) or 32 bytes, in
-            // units of 16 bytes
-            constexpr uint64_t kStepA = kAMn ? 128 : 2, kStepB = kWgrad ? 128 : 2;
+            constexpr uint32_t kMajor = (kAMn ? kIdescAMn : 0u) | (kWgrad ? kIdescBMn : 0u);
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
             for (int tile = slot; tile < total; tile += slots) {
@@ -263,20 +321,23 @@ __global__ void __launch_bounds__(ExpertCfg<TN>::kThreads, 1)
                 if (depth == 0) continue;
                 if (!mbar_wait<true>(&acc_empty[acc], acc_phase ^ 1u, abort, p.status, kStatusTimeoutMma)) goto done;
                 tc_fence_after();
+                const uint32_t idesc = idesc_bf16(256, t.n) | kMajor;
                 const uint32_t d_tmem = tmem_base + (uint32_t)acc * TN;
-                for (int d = 0; d < depth; d += kDepth) {
+                for (int d = 0; d < depth; d += DEPTH) {
                     if (!mbar_wait<true>(&full[stage], phase, abort, p.status, kStatusTimeoutMma)) goto done;
                     tc_fence_after();
-                    const uint32_t a_s = smem_u32(s_a + stage * kTileA), b_s = smem_u32(s_b + stage * C::kTileB);
-                    const uint64_t adesc = kAMn ? sdesc_mnmajor_sw128(a_s, 8192) : sdesc_kmajor_sw128(a_s);
-                    const uint64_t bdesc = kWgrad ? sdesc_mnmajor_sw128(b_s, 8192) : sdesc_kmajor_sw128(b_s);
-                    if (depth - d >= kDepth) {
+                    const uint32_t a_s = smem_u32(s_a + stage * C::kTileA), b_s = smem_u32(s_b + stage * C::kTileB);
+                    const uint64_t adesc = kAMn ? sdesc_mnmajor_sw128(a_s, C::kChunkMn) : sdesc_kmajor_sw128(a_s);
+                    const uint64_t bdesc = kWgrad ? sdesc_mnmajor_sw128(b_s, C::kChunkMn) : sdesc_kmajor_sw128(b_s);
+                    if (depth - d >= DEPTH) {
 #pragma unroll
-                        for (int j = 0; j < kDepth / 16; ++j)
-                            tc_mma_bf16_pair(d_tmem, adesc + kStepA * j, bdesc + kStepB * j, idesc, (d | j) != 0);
+                        for (int j = 0; j < DEPTH / 16; ++j)
+                            tc_mma_bf16_pair(d_tmem, adesc + operand_step<kAMn, C::kTileA>(j),
+                                             bdesc + operand_step<kWgrad, C::kTileB>(j), idesc, (d | j) != 0);
                     } else {
                         for (int j = 0; j < (depth - d + 15) / 16; ++j)
-                            tc_mma_bf16_pair(d_tmem, adesc + kStepA * j, bdesc + kStepB * j, idesc, (d | j) != 0);
+                            tc_mma_bf16_pair(d_tmem, adesc + operand_step<kAMn, C::kTileA>(j),
+                                             bdesc + operand_step<kWgrad, C::kTileB>(j), idesc, (d | j) != 0);
                     }
                     tc_commit_pair_mc(&empty[stage], 0x3);
                     if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
@@ -295,23 +356,23 @@ __global__ void __launch_bounds__(ExpertCfg<TN>::kThreads, 1)
             uint32_t phases = 0;           // bit s: parity of landed[s]
             for (int tile = slot; tile < total; tile += slots) {
                 const ExpertTile t = expert_tile<TN, kWgrad>(p, tile, s_end, s_first, s_count);
-                const int blocks = (t.count + kDepth - 1) / kDepth;
+                const int blocks = (t.count + DEPTH - 1) / DEPTH;
                 if ((t.count & 15) != 0) {
                     const int s = (stage + blocks - 1) % C::kStages;
                     if (!__all_sync(0xffffffffu, mbar_wait(&landed[s], (phases >> s) & 1u, abort, p.status,
                                                            kStatusTimeoutProducer)))
                         goto done;
                     phases ^= 1u << s;
-                    const int r0 = t.count - (blocks - 1) * kDepth, r1 = (r0 + 15) / 16 * 16;
+                    const int r0 = t.count - (blocks - 1) * DEPTH, r1 = (r0 + 15) / 16 * 16;
                     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
                     // a row of a chunk is 128 bytes (the swizzle permutes within it)
                     for (int r = r0 + (lane >> 3); r < r1; r += 4) {
 #pragma unroll
                         for (int j = 0; j < kHalfM / 64; ++j)
-                            *reinterpret_cast<uint4*>(s_a + s * kTileA + j * 8192 + r * 128 + (lane & 7) * 16) = zero;
+                            *reinterpret_cast<uint4*>(s_a + s * C::kTileA + j * C::kChunkMn + r * 128 + (lane & 7) * 16) = zero;
 #pragma unroll
                         for (int j = 0; j < C::kHalfN / 64; ++j)
-                            *reinterpret_cast<uint4*>(s_b + s * C::kTileB + j * 8192 + r * 128 + (lane & 7) * 16) = zero;
+                            *reinterpret_cast<uint4*>(s_b + s * C::kTileB + j * C::kChunkMn + r * 128 + (lane & 7) * 16) = zero;
                     }
                     fence_proxy_async();
                     __syncwarp();
@@ -332,7 +393,8 @@ __global__ void __launch_bounds__(ExpertCfg<TN>::kThreads, 1)
         uint32_t acc_phase = 0;
         for (int tile = slot; tile < total; tile += slots) {
             const ExpertTile t = expert_tile<TN, kWgrad>(p, tile, s_end, s_first, s_count);
-            const int m = t.m0 + (int)rank * kHalfM + q * 32 + lane;
+            const int mw = t.m0 + (int)rank * p.half_m + q * 32;     // the warp's first D row
+            const bool m_there = q * 32 + lane < p.half_m && mw + lane < p.m_extent;
             const bool nothing = kWgrad && t.count == 0;   // no rows: zeros, no accumulator
             if (!nothing) {
                 // warp-uniform outcome: tcgen05.ld below is a warp-collective instruction
@@ -342,39 +404,56 @@ __global__ void __launch_bounds__(ExpertCfg<TN>::kThreads, 1)
                 tc_fence_after();
             }
             const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)acc * TN + (uint32_t)col0;
-            const int limit = kWgrad ? p.n_extent - t.n0 : t.count - t.n0;   // columns that exist
+            const int limit = min(t.n, (kWgrad ? p.n_extent : t.count) - t.n0);   // columns that exist
+            if (kWgrad) {
+                // lane = row of dw[e], columns contiguous: kOutCols of them at a
+                // time through shared memory, so that whole sectors or lines
+                // leave; the map's extents cut what lies past N or K
+                uint8_t* out = s_out + (warp - 4) * C::kOutBytes;
 #pragma unroll 1
-            for (int c = 0; c < kCols; c += 32) {
-                if (col0 + c >= limit) break;              // warp-uniform
-                float v[32];
-                if (nothing) {
+                for (int c = 0; c < kCols; c += C::kOutCols) {
+                    if (col0 + c >= limit || mw >= p.m_extent) break;      // warp-uniform
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = 0.0f;
-                } else {
+                    for (int h = 0; h < C::kOutCols; h += 32) {
+                        float v[32];
+                        if (nothing) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+                        } else {
+                            tmem_ld32(taddr + c + h, v);
+                            tmem_ld_wait();
+                        }
+                        if (h == 0) {
+                            if (lane == 0) tma_store_wait_read();          // the buffer's last store has read it
+                            __syncwarp();
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float w[8] = {v[8 * j],     v[8 * j + 1], v[8 * j + 2], v[8 * j + 3],
+                                                v[8 * j + 4], v[8 * j + 5], v[8 * j + 6], v[8 * j + 7]};
+                            *reinterpret_cast<uint4*>(out + out_chunk<C::kOutCols>(lane, h / 8 + j)) = pack_bf16x8(w);
+                        }
+                    }
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) tma_store_3d(&tmC, out, t.n0 + col0 + c, mw, t.e);
+                }
+            } else {
+#pragma unroll 1
+                for (int c = 0; c < kCols; c += 32) {
+                    if (col0 + c >= limit) break;          // warp-uniform
+                    float v[32];
                     tmem_ld32(taddr + c, v);
                     tmem_ld_wait();
-                }
-                if (m < p.m_extent) {
-                    if (kWgrad) {
-                        // lane = row of dw[e], columns contiguous
-                        __nv_bfloat16* o = p.out + ((size_t)t.e * p.m_extent + m) * p.n_extent + t.n0 + col0 + c;
-#pragma unroll
-                        for (int j = 0; j < 32; j += 8) {
-                            if (col0 + c + j < limit) {
-                                const float w[8] = {v[j], v[j + 1], v[j + 2], v[j + 3],
-                                                    v[j + 4], v[j + 5], v[j + 6], v[j + 7]};
-                                *reinterpret_cast<uint4*>(o + j) = pack_bf16x8(w);
-                            }
-                        }
-                    } else {
-                        // lane = output column, accumulator column = row of the segment
-                        __nv_bfloat16* o = p.out + (size_t)(t.first + t.n0 + col0 + c) * p.m_extent + m;
+                    // lane = output column, accumulator column = row of the segment
+                    __nv_bfloat16* o = p.out + (size_t)(t.first + t.n0 + col0 + c) * p.m_extent + mw + lane;
+                    if (m_there) {
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
                             if (col0 + c + j < limit) o[(size_t)j * p.m_extent] = __float2bfloat16_rn(v[j]);
                     }
+                    __syncwarp();
                 }
-                __syncwarp();
             }
             if (!nothing) {
                 tc_fence_before();
@@ -387,6 +466,7 @@ __global__ void __launch_bounds__(ExpertCfg<TN>::kThreads, 1)
                 if (acc == 0) acc_phase ^= 1u;
             }
         }
+        if (kWgrad && lane == 0) tma_store_wait();
     }
 done:
     if (*abort) {
@@ -411,67 +491,87 @@ done:
 }
 
 // Tensor map of a BF16 array: dims[0] contiguous, byte strides of the others,
-// 128-byte boxes with the 128-byte swizzle.
+// boxes as wide as the swizzle.
 bool encode_bf16_map(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
-                     const cuuint32_t* box) {
+                     const cuuint32_t* box, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
     const cuuint32_t step[3] = {1, 1, 1};
     return tensor_map_encoder()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box,
-                                step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                step, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int g_expert_grid[64] = {};
 
-template <int PRODUCT, int TN>
+template <int PRODUCT, int TN, int DEPTH>
 cudaError_t launch_tiles(const LaunchCtx& c, int grid, const CUtensorMap& a, const CUtensorMap& b,
-                         const ExpertParams& p) {
-    return c.launch(expert_linear_kernel<PRODUCT, TN>, dim3((unsigned)grid), dim3(ExpertCfg<TN>::kThreads),
-                    (size_t)ExpertCfg<TN>::kSmemBytes, a, b, p);
+                         const CUtensorMap& d, const ExpertParams& p) {
+    return c.launch(expert_linear_kernel<PRODUCT, TN, DEPTH>, dim3((unsigned)grid), dim3(ExpertCfg<PRODUCT, TN, DEPTH>::kThreads),
+                    (size_t)ExpertCfg<PRODUCT, TN, DEPTH>::kSmemBytes, a, b, d, p);
 }
 
-template <int PRODUCT, int TN>
+template <int PRODUCT, int TN, int DEPTH>
 cudaError_t set_tiles() {
-    return cudaFuncSetAttribute(expert_linear_kernel<PRODUCT, TN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                ExpertCfg<TN>::kSmemBytes);
+    return cudaFuncSetAttribute(expert_linear_kernel<PRODUCT, TN, DEPTH>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                ExpertCfg<PRODUCT, TN, DEPTH>::kSmemBytes);
 }
 
 template <int PRODUCT>
 cudaError_t launch_rows(const LaunchCtx& c, int tn, int grid, const CUtensorMap& a, const CUtensorMap& b,
                         const ExpertParams& p) {
     switch (tn) {
-        case 32: return launch_tiles<PRODUCT, 32>(c, grid, a, b, p);
-        case 64: return launch_tiles<PRODUCT, 64>(c, grid, a, b, p);
-        case 128: return launch_tiles<PRODUCT, 128>(c, grid, a, b, p);
-        default: return launch_tiles<PRODUCT, 256>(c, grid, a, b, p);
+        case 32: return launch_tiles<PRODUCT, 32, 128>(c, grid, a, b, b, p);
+        case 64: return launch_tiles<PRODUCT, 64, 128>(c, grid, a, b, b, p);
+        case 128: return launch_tiles<PRODUCT, 128, 128>(c, grid, a, b, b, p);
+        default: return launch_tiles<PRODUCT, 256, 128>(c, grid, a, b, b, p);
     }
 }
 
-// Rows of a tile for segments of `rows` / (experts that can hold any) rows on
-// average: the narrowest that holds a segment of one and a third times the
-// mean, so that most experts' weights pass the tensor cores once.
-int tile_rows(int64_t rows, int E) {
-    const int64_t busy = rows < E ? rows : E;
-    if (3 * 32 * busy >= 4 * rows) return 32;
-    if (3 * 64 * busy >= 4 * rows) return 64;
-    if (3 * 128 * busy >= 4 * rows) return 128;
-    return 256;
+// Rows of a tile (its TN) for segments of `mean` rows on average.  Measured on
+// GB300 (dgrad, 16 experts of 4096 x 7168; us at TN = 32, 64, 128, 256):
+//   4 rows 138 138 139 186;  16 rows 147 140 141 152;  32 rows 186 147 143 149;
+//   64 rows 316 195 151 150;  128 rows 542 300 194 161.
+int tile_rows(double mean) { return mean <= 8 ? 32 : mean <= 20 ? 64 : mean <= 80 ? 128 : 256; }
+
+// Rows per busy expert from which wgrad takes the deep stages.  Measured on GB300
+// (16 experts of 4096 x 7168; us shallow, deep): 4 rows 143 181;  128 rows 171
+// 189;  256 rows 240 239;  384 rows 330 317;  1024 rows 665 652.
+constexpr int kWgradDeepRows = 300;
+
+// D rows per CTA (forward with narrow tiles, where the weights' bytes bound the
+// time and an MMA row without a weight costs nothing): the height, in steps of
+// eight rows, with the least work for the busiest pair if every busy expert
+// has one tile of rows.  8 experts of 4096 rows on 76 pairs: 16 tiles of 256
+// rows each are 128 tiles, two rounds of 128 rows per CTA; 19 tiles of 224
+// are 152, two rounds of 112.
+int tile_height(int m_extent, int64_t busy, int pairs) {
+    int best = kHalfM;
+    int64_t best_work = INT64_MAX;
+    for (int h = kHalfM; h >= 64; h -= 8) {
+        const int64_t tiles = busy * ((m_extent + 2 * h - 1) / (2 * h));
+        const int64_t work = (tiles + pairs - 1) / pairs * h;
+        if (work < best_work) {
+            best = h;
+            best_work = work;
+        }
+    }
+    return best;
 }
 
 }  // namespace
 
 cudaError_t setup_expert_linear_kernels(int device, int num_sms) {
     cudaError_t e;
-    if ((e = set_tiles<kExpertForward, 32>()) || (e = set_tiles<kExpertForward, 64>()) ||
-        (e = set_tiles<kExpertForward, 128>()) || (e = set_tiles<kExpertForward, 256>()) ||
-        (e = set_tiles<kExpertDgrad, 32>()) || (e = set_tiles<kExpertDgrad, 64>()) ||
-        (e = set_tiles<kExpertDgrad, 128>()) || (e = set_tiles<kExpertDgrad, 256>()) ||
-        (e = set_tiles<kExpertWgrad, 256>()))
+    if ((e = set_tiles<kExpertForward, 32, 128>()) || (e = set_tiles<kExpertForward, 64, 128>()) ||
+        (e = set_tiles<kExpertForward, 128, 128>()) || (e = set_tiles<kExpertForward, 256, 128>()) ||
+        (e = set_tiles<kExpertDgrad, 32, 128>()) || (e = set_tiles<kExpertDgrad, 64, 128>()) ||
+        (e = set_tiles<kExpertDgrad, 128, 128>()) || (e = set_tiles<kExpertDgrad, 256, 128>()) ||
+        (e = set_tiles<kExpertWgrad, 256, 128>()) || (e = set_tiles<kExpertWgrad, 256, 64>()))
         return e;
     // persistent grid: as many CTA pairs as can be resident at once
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(num_sms / 2 * 2));
-    cfg.blockDim = dim3(ExpertCfg<256>::kThreads);
-    cfg.dynamicSmemBytes = ExpertCfg<64>::kSmemBytes;
+    cfg.blockDim = dim3(ExpertCfg<kExpertForward, 64, 128>::kThreads);
+    cfg.dynamicSmemBytes = ExpertCfg<kExpertForward, 64, 128>::kSmemBytes;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
@@ -480,7 +580,7 @@ cudaError_t setup_expert_linear_kernels(int device, int num_sms) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int clusters = 0;
-    if ((e = cudaOccupancyMaxActiveClusters(&clusters, expert_linear_kernel<kExpertForward, 64>, &cfg))) return e;
+    if ((e = cudaOccupancyMaxActiveClusters(&clusters, expert_linear_kernel<kExpertForward, 64, 128>, &cfg))) return e;
     if (clusters < 1) return cudaErrorInvalidConfiguration;
     if (device >= 0 && device < 64) g_expert_grid[device] = 2 * (clusters < num_sms / 2 ? clusters : num_sms / 2);
     return cudaSuccess;
@@ -491,23 +591,34 @@ cudaError_t launch_expert_linear(const LaunchCtx& c, int product, int device, co
     if (a.rows == 0)   // wgrad only: no rows, a gradient of zeros
         return cudaMemsetAsync(a.out, 0, (size_t)a.E * a.N * a.K * 2, c.stream);
     const cuuint64_t N = (cuuint64_t)a.N, K = (cuuint64_t)a.K, R = (cuuint64_t)a.rows;
-    const int tn = product == kExpertWgrad ? 256 : tile_rows(a.rows, a.E);
-    CUtensorMap ta, tb;
+    const int64_t busy = a.rows < a.E ? a.rows : a.E;
+    const int tn = product == kExpertWgrad ? 256 : tile_rows((double)a.rows / (double)busy);
+    const bool wgrad_deep = a.rows >= kWgradDeepRows * busy;
+    const int grid = g_expert_grid[device];
+    ExpertParams p{};
+    p.half_m = kHalfM;
+    CUtensorMap ta, tb, td;
     bool ok;
     if (product == kExpertWgrad) {
         const cuuint64_t da[2] = {N, R}, sa[1] = {N * 2}, db[2] = {K, R}, sb[1] = {K * 2};
-        const cuuint32_t box[2] = {64, 64};
-        ok = encode_bf16_map(&ta, a.a, 2, da, sa, box) && encode_bf16_map(&tb, a.b, 2, db, sb, box);
+        const cuuint32_t box[2] = {64, wgrad_deep ? 128u : 64u};
+        const cuuint64_t dd[3] = {K, N, (cuuint64_t)a.E}, sd[2] = {K * 2, N * K * 2};
+        const cuuint32_t boxd[3] = {wgrad_deep ? 32u : 64u, 32, 1};
+        ok = encode_bf16_map(&ta, a.a, 2, da, sa, box) && encode_bf16_map(&tb, a.b, 2, db, sb, box) &&
+             encode_bf16_map(&td, a.out, 3, dd, sd, boxd,
+                             wgrad_deep ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
     } else {
         const bool fwd = product == kExpertForward;
         const cuuint64_t dw[3] = {K, N, (cuuint64_t)a.E}, sw[2] = {K * 2, N * K * 2};
-        const cuuint32_t boxw[3] = {64, fwd ? 128u : 64u, 1};
+        if (fwd && tn < 256) p.half_m = tile_height(a.N, busy, grid / 2);
+        // no more rows than there are: the copies of one token's rows are short
+        p.box_n = (int)(a.rows < tn / 2 ? (a.rows + 7) / 8 * 8 : tn / 2);
+        const cuuint32_t boxw[3] = {64, fwd ? (cuuint32_t)p.half_m : 128u, 1};
         const cuuint64_t dr[2] = {fwd ? K : N, R}, sr[1] = {(fwd ? K : N) * 2};
-        const cuuint32_t boxr[2] = {64, (cuuint32_t)(tn / 2)};
+        const cuuint32_t boxr[2] = {64, (cuuint32_t)p.box_n};
         ok = encode_bf16_map(&ta, a.b, 3, dw, sw, boxw) && encode_bf16_map(&tb, a.a, 2, dr, sr, boxr);
     }
     if (!ok) return cudaErrorInvalidValue;
-    ExpertParams p{};
     p.m_extent = product == kExpertDgrad ? a.K : a.N;
     p.n_extent = a.K;
     p.depth = product == kExpertDgrad ? a.N : a.K;
@@ -519,10 +630,10 @@ cudaError_t launch_expert_linear(const LaunchCtx& c, int product, int device, co
     p.status = a.status;
     LaunchCtx cc = c;
     cc.cluster = 2;
-    const int grid = g_expert_grid[device];
     if (product == kExpertForward) return launch_rows<kExpertForward>(cc, tn, grid, ta, tb, p);
     if (product == kExpertDgrad) return launch_rows<kExpertDgrad>(cc, tn, grid, ta, tb, p);
-    return launch_tiles<kExpertWgrad, 256>(cc, grid, ta, tb, p);
+    return wgrad_deep ? launch_tiles<kExpertWgrad, 256, 128>(cc, grid, ta, tb, td, p)
+                      : launch_tiles<kExpertWgrad, 256, 64>(cc, grid, ta, tb, td, p);
 }
 
 }  // namespace moe
