@@ -18,8 +18,9 @@ namespace {
 
 constexpr int kClipThreads = 512;
 constexpr int kListMax = 96;
-constexpr int64_t kChunk = 16384;
-constexpr int kNormBlocks = 304;      // partial sums per launch
+constexpr int kChunk = 16384;
+constexpr int kInFlight = 4;          // 16-byte loads of a thread: a chunk of BF16 at once
+constexpr int kNormBlocks = 608;      // partial sums per launch: four blocks an SM
 
 struct GradEntry {
     const void* in;
@@ -34,64 +35,77 @@ struct GradTable {
     GradEntry e[kListMax];
 };
 
-// Sum of squares of a chunk's part of this thread.
-template <typename T_, int VEC>
-__device__ __forceinline__ float square_part(const void* base, int64_t at, int64_t count) {
+// A chunk [at, at + count) of a tensor as vectors of VEC, kInFlight of them
+// loaded by a thread before the first is used; f(vector's values, its index),
+// then f1(element's index) for the elements past the last vector.
+template <typename T_, int VEC, typename F, typename F1>
+__device__ __forceinline__ void for_chunk(const void* base, int64_t at, int count, F f, F1 f1) {
     using RV = RowVec<T_, VEC>;
     const typename RV::Raw* p = reinterpret_cast<const typename RV::Raw*>(static_cast<const T_*>(base) + at);
-    const int n = (int)(count / VEC);
-    float s = 0.0f;
-    for (int i = threadIdx.x; i < n; i += kClipThreads) {
-        float v[VEC];
-        RV::unpack(p[i], v);
+    const int n = count / VEC;
+    for (int i0 = threadIdx.x; i0 < n; i0 += kClipThreads * kInFlight) {
+        typename RV::Raw r[kInFlight];
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) s = fmaf(v[j], v[j], s);
+        for (int u = 0; u < kInFlight; ++u)
+            if (i0 + u * kClipThreads < n) r[u] = p[i0 + u * kClipThreads];
+#pragma unroll
+        for (int u = 0; u < kInFlight; ++u)
+            if (i0 + u * kClipThreads < n) {
+                float v[VEC];
+                RV::unpack(r[u], v);
+                f(v, i0 + u * kClipThreads);
+            }
     }
-    const int64_t i = (int64_t)n * VEC + threadIdx.x;
-    if (i < count) {
-        const float v = (float)static_cast<const T_*>(base)[at + i];
-        s = fmaf(v, v, s);
-    }
+    if ((int)threadIdx.x < count - n * VEC) f1(n * VEC + (int)threadIdx.x);
+}
+
+// Sum of squares of a chunk's part of this thread.
+template <typename T_, int VEC>
+__device__ __forceinline__ float square_part(const void* base, int64_t at, int count) {
+    float s = 0.0f;
+    for_chunk<T_, VEC>(
+        base, at, count,
+        [&](const float (&v)[VEC], int) {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) s = fmaf(v[j], v[j], s);
+        },
+        [&](int i) {
+            const float v = (float)static_cast<const T_*>(base)[at + i];
+            s = fmaf(v, v, s);
+        });
     return s;
 }
 
+// `in` and `out` may be the same tensor: a thread writes what it has read.
 template <typename T_, int VEC>
-__device__ __forceinline__ void scale_part(const void* base, void* out, int64_t at, int64_t count, float scale) {
+__device__ __forceinline__ void scale_part(const void* in, void* out, int64_t at, int count, float scale) {
     using RV = RowVec<T_, VEC>;
-    const typename RV::Raw* p = reinterpret_cast<const typename RV::Raw*>(static_cast<const T_*>(base) + at);
     typename RV::Raw* q = reinterpret_cast<typename RV::Raw*>(static_cast<T_*>(out) + at);
-    const int n = (int)(count / VEC);
-    for (int i = threadIdx.x; i < n; i += kClipThreads) {
-        float v[VEC];
-        RV::unpack(p[i], v);
+    for_chunk<T_, VEC>(
+        in, at, count,
+        [&](const float (&v)[VEC], int i) {
+            float w[VEC];
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) v[j] *= scale;
-        q[i] = RV::pack(v);
-    }
-    const int64_t i = (int64_t)n * VEC + threadIdx.x;
-    if (i < count) static_cast<T_*>(out)[at + i] = (T_)((float)static_cast<const T_*>(base)[at + i] * scale);
+            for (int j = 0; j < VEC; ++j) w[j] = v[j] * scale;
+            // the result is not read again here: it leaves L2 first
+            __stcs(q + i, RV::pack(w));
+        },
+        [&](int i) { static_cast<T_*>(out)[at + i] = (T_)((float)static_cast<const T_*>(in)[at + i] * scale); });
 }
 
-// Entry that holds chunk c of the launch.
-__device__ __forceinline__ int entry_of(const GradTable& t, int c) {
-    int lo = 0, hi = t.n - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (c < t.e[mid].last_chunk) hi = mid;
-        else lo = mid + 1;
-    }
-    return lo;
-}
+// First chunk of entry i.
+__device__ __forceinline__ int first_chunk(const GradTable& t, int i) { return i ? t.e[i - 1].last_chunk : 0; }
 
 __global__ void __launch_bounds__(kClipThreads) grad_square_kernel(const __grid_constant__ GradTable t, float* part) {
     __shared__ float s_part[kClipThreads / 32];
     pdl_wait();
     float sum = 0.0f;
+    int i = 0;
     for (int c = blockIdx.x; c < t.chunks; c += gridDim.x) {
-        const int i = entry_of(t, c);
+        while (c >= t.e[i].last_chunk) ++i;
         const GradEntry& e = t.e[i];
-        const int64_t at = (int64_t)(c - (i ? t.e[i - 1].last_chunk : 0)) * kChunk;
-        const int64_t count = min(kChunk, e.numel - at);
+        const int64_t at = (int64_t)(c - first_chunk(t, i)) * kChunk;
+        const int count = (int)min((int64_t)kChunk, e.numel - at);
         const bool wide = reinterpret_cast<uintptr_t>(e.in) % 16 == 0;
         if (e.elem == 2)
             sum += wide ? square_part<__nv_bfloat16, 8>(e.in, at, count) : square_part<__nv_bfloat16, 1>(e.in, at, count);
@@ -128,12 +142,14 @@ __global__ void __launch_bounds__(kClipThreads) grad_scale_kernel(const __grid_c
     pdl_wait();
     const float q = max_norm / (norm[0] + eps);
     const float scale = q > 1.0f ? 1.0f : q;      // NaN stays NaN
-    for (int c = blockIdx.x; c < t.chunks; c += gridDim.x) {
-        const int i = entry_of(t, c);
+    // from the list's end: what the norm's pass has read last may still be in L2
+    int i = t.n - 1;
+    for (int c = t.chunks - 1 - (int)blockIdx.x; c >= 0; c -= gridDim.x) {
+        while (c < first_chunk(t, i)) --i;
         const GradEntry& e = t.e[i];
         if (scale == 1.0f && e.in == e.out) continue;
-        const int64_t at = (int64_t)(c - (i ? t.e[i - 1].last_chunk : 0)) * kChunk;
-        const int64_t count = min(kChunk, e.numel - at);
+        const int64_t at = (int64_t)(c - first_chunk(t, i)) * kChunk;
+        const int count = (int)min((int64_t)kChunk, e.numel - at);
         const bool wide = (reinterpret_cast<uintptr_t>(e.in) | reinterpret_cast<uintptr_t>(e.out)) % 16 == 0;
         if (e.elem == 2) {
             if (wide) scale_part<__nv_bfloat16, 8>(e.in, e.out, at, count, scale);
@@ -202,7 +218,7 @@ cudaError_t launch_grad_clip(const LaunchCtx& c, int sms, int n, const void* con
                              const int64_t* numels, const int32_t* dtypes, const float* norm, float max_norm,
                              float eps) {
     return for_tables(n, grads, out, numels, dtypes, [&](const GradTable& t) {
-        const int blocks = t.chunks < 8 * sms ? t.chunks : 8 * sms;
+        const int blocks = t.chunks < 4 * sms ? t.chunks : 4 * sms;
         return c.launch(grad_scale_kernel, dim3(blocks), dim3(kClipThreads), 0, t, norm, max_norm, eps);
     });
 }
