@@ -289,47 +289,24 @@ def moe_nvfp4_route_noalloc(T: int, E: int, K: int, flags: int, router_logits: t
 
 
 # ---- training operators (moe_nvfp4_train.h) --------------------------------------
+# Bound by _binding.so (csrc/binding.cpp), which checks the tensors: TypeError
+# for an element type or device, ValueError for a shape; MoEError for what the
+# C entry point refuses.
 
-def _handle(stream) -> int:
-    """The cudaStream_t of ``stream``, or of the current device's current stream
-    (read without building a torch.cuda.Stream: 0.1 us instead of 3)."""
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+_native = None
 
 
-def _rows2d(name: str, t: torch.Tensor, dtype: Optional[torch.dtype] = None) -> tuple:
-    """(T, H, row stride in elements) of a CUDA tensor [T, H] with contiguous rows."""
-    if t.dim() != 2 or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor [T, H]")
-    if (dtype is not None and t.dtype is not dtype) or t.dtype not in _DTYPES:
-        raise TypeError(f"{name} must be {dtype or 'bfloat16 or float32'}")
-    T, H = t.shape
-    if t.is_contiguous():
-        return T, H, H
-    if H > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name} must have contiguous rows")
-    # the stride of a single row, and of none, says nothing
-    return T, H, (t.stride(0) if T > 1 else H)
-
-
-def _space(workspace: torch.Tensor) -> tuple:
-    """Address and size of a workspace."""
-    if not workspace.is_cuda or not workspace.is_contiguous():
-        raise ValueError("the workspace must be a contiguous CUDA tensor")
-    return workspace.data_ptr(), workspace.nbytes
-
-
-def _flat(name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple) -> int:
-    """The address of a contiguous CUDA tensor of the given type and shape."""
-    if t.dtype is not dtype or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor of {dtype}")
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous {list(shape)}")
-    return t.data_ptr()
-
-
-_DTYPES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_F32}
+def native():
+    """Load _binding.so (raises if it has not been built for this torch)."""
+    global _native
+    if _native is None:
+        lib()
+        from . import _binding
+        if _binding.torch_version != torch.__version__.split("+")[0]:
+            raise RuntimeError(f"_binding.so was built for torch {_binding.torch_version}: rebuild it with "
+                               "`python -m nvfp4_mixture_experts_router_gb300.build --force`")
+        _native = _binding
+    return _native
 
 
 def moe_nvfp4_sort_workspace_bytes(T: int, E: int, K: int) -> int:
@@ -342,61 +319,27 @@ def moe_nvfp4_sort_routes(E: int, topk_ids: torch.Tensor, count: torch.Tensor, o
     """Routes of topk_ids [T, K] sorted by expert (stable; ids outside [0, E)
     are dropped): count [E], offsets [E + 1], row_of_route [T, K] and
     route_of_row [T * K], all int32."""
-    T, K = topk_ids.shape
-    i32 = torch.int32
-    code = lib().moe_nvfp4_sort_routes(
-        T, E, K, _flat("topk_ids", topk_ids, i32, (T, K)), _flat("count", count, i32, (E,)),
-        _flat("offsets", offsets, i32, (E + 1,)), _flat("row_of_route", row_of_route, i32, (T, K)),
-        _flat("route_of_row", route_of_row, i32, (T * K,)), *_space(workspace), _handle(stream))
-    _check("moe_nvfp4_sort_routes", code)
-
-
-def _row_args(what: str, tokens: torch.Tensor, rows: torch.Tensor, row_of_route: torch.Tensor) -> tuple:
-    """Checks token rows [T, H], expert-ordered rows [rows, H] of the same type
-    and row_of_route [T, K]; returns (T, H, K, rows, dtype), the tokens' row
-    stride and row_of_route's address."""
-    T, H, stride = _rows2d(what, tokens)
-    if rows.dim() != 2 or rows.dtype is not tokens.dtype or not rows.is_cuda or rows.shape[1] != H \
-            or not rows.is_contiguous():
-        raise ValueError(f"the expert-ordered rows must be contiguous [rows, {H}] of {tokens.dtype}")
-    K = row_of_route.shape[-1]
-    return (T, H, K, rows.shape[0], _DTYPES[tokens.dtype]), stride, \
-        _flat("row_of_route", row_of_route, torch.int32, (T, K))
-
-
-def _scalar_i32(name: str, t: Optional[torch.Tensor]):
-    if t is None:
-        return None
-    if t.dtype is not torch.int32 or not t.is_cuda or t.numel() != 1:
-        raise ValueError(f"{name} must be one CUDA int32")
-    return t.data_ptr()
+    _check("moe_nvfp4_sort_routes", (_native or native()).sort_routes(
+        E, topk_ids, count, offsets, row_of_route, route_of_row, workspace, stream))
 
 
 def moe_nvfp4_dispatch(x: torch.Tensor, row_of_route: torch.Tensor, rows_used: Optional[torch.Tensor],
                        x_rows: torch.Tensor, stream=None) -> None:
     """x_rows[row_of_route[t, k]] = x[t]; rows from rows_used (one device int32,
     None: none) on are set to zero."""
-    sizes, stride, ror = _row_args("x", x, x_rows, row_of_route)
-    code = lib().moe_nvfp4_dispatch(*sizes, x.data_ptr(), stride, ror, _scalar_i32("rows_used", rows_used),
-                                    x_rows.data_ptr(), _handle(stream))
-    _check("moe_nvfp4_dispatch", code)
+    _check("moe_nvfp4_dispatch", (_native or native()).dispatch(x, row_of_route, rows_used, x_rows, stream))
 
 
 def moe_nvfp4_dispatch_backward(dx_rows: torch.Tensor, row_of_route: torch.Tensor, dx: torch.Tensor,
                                 stream=None) -> None:
     """dx[t] = sum_k dx_rows[row_of_route[t, k]]."""
-    sizes, stride, ror = _row_args("dx", dx, dx_rows, row_of_route)
-    code = lib().moe_nvfp4_dispatch_backward(*sizes, dx_rows.data_ptr(), ror, dx.data_ptr(), stride, _handle(stream))
-    _check("moe_nvfp4_dispatch_backward", code)
+    _check("moe_nvfp4_dispatch_backward", (_native or native()).dispatch_backward(dx_rows, row_of_route, dx, stream))
 
 
 def moe_nvfp4_combine(o_rows: torch.Tensor, row_of_route: torch.Tensor, topk_w: torch.Tensor, y: torch.Tensor,
                       stream=None) -> None:
     """y[t] = sum_k topk_w[t, k] * o_rows[row_of_route[t, k]]."""
-    sizes, stride, ror = _row_args("y", y, o_rows, row_of_route)
-    w = _flat("topk_w", topk_w, torch.float32, (sizes[0], sizes[2]))
-    code = lib().moe_nvfp4_combine(*sizes, o_rows.data_ptr(), ror, w, y.data_ptr(), stride, _handle(stream))
-    _check("moe_nvfp4_combine", code)
+    _check("moe_nvfp4_combine", (_native or native()).combine(o_rows, row_of_route, topk_w, y, stream))
 
 
 def moe_nvfp4_combine_backward(dy: torch.Tensor, o_rows: torch.Tensor, row_of_route: torch.Tensor,
@@ -404,59 +347,31 @@ def moe_nvfp4_combine_backward(dy: torch.Tensor, o_rows: torch.Tensor, row_of_ro
                                dw: torch.Tensor, stream=None) -> None:
     """do_rows[row_of_route[t, k]] = topk_w[t, k] * dy[t] (rows from rows_used on
     set to zero) and dw[t, k] = <dy[t], o_rows[row_of_route[t, k]]>."""
-    sizes, stride, ror = _row_args("dy", dy, o_rows, row_of_route)
-    T, H, K, rows, _ = sizes
-    code = lib().moe_nvfp4_combine_backward(
-        *sizes, dy.data_ptr(), stride, o_rows.data_ptr(), ror, _flat("topk_w", topk_w, torch.float32, (T, K)),
-        _scalar_i32("rows_used", rows_used), _flat("do_rows", do_rows, dy.dtype, (rows, H)),
-        _flat("dw", dw, torch.float32, (T, K)), _handle(stream))
-    _check("moe_nvfp4_combine_backward", code)
-
-
-def _expert_product(fn: str, sizes: tuple, a: torch.Tensor, a_shape: tuple, b: torch.Tensor, b_shape: tuple,
-                    count: torch.Tensor, offsets: torch.Tensor, out: torch.Tensor, out_shape: tuple,
-                    status: Optional[torch.Tensor], stream) -> None:
-    bf16, E = torch.bfloat16, sizes[3]
-    if offsets.dtype is not torch.int32 or not offsets.is_cuda:
-        raise TypeError("offsets must be CUDA int32")
-    if offsets.dim() != 1 or offsets.shape[0] < E or not offsets.is_contiguous():
-        raise ValueError(f"offsets must be contiguous [{E}] or longer")
-    if status is not None and (status.element_size() != 4 or not status.is_cuda or status.numel() != 1):
-        raise ValueError("status must be one CUDA 32-bit integer")
-    code = getattr(lib(), fn)(*sizes, _flat("the first operand", a, bf16, a_shape),
-                              _flat("the second operand", b, bf16, b_shape), _flat("count", count, torch.int32, (E,)),
-                              offsets.data_ptr(), _flat("the output", out, bf16, out_shape),
-                              None if status is None else status.data_ptr(), _handle(stream))
-    _check(fn, code)
+    _check("moe_nvfp4_combine_backward", (_native or native()).combine_backward(
+        dy, o_rows, row_of_route, topk_w, rows_used, do_rows, dw, stream))
 
 
 def moe_nvfp4_expert_linear(x_rows: torch.Tensor, w: torch.Tensor, count: torch.Tensor, offsets: torch.Tensor,
                             y_rows: torch.Tensor, status: Optional[torch.Tensor] = None, stream=None) -> None:
     """y_rows[r] = x_rows[r] w[e]^T for the rows [offsets[e], offsets[e] + count[e])
     of every expert e: x_rows [rows, K], w [E, N, K], y_rows [rows, N], BF16."""
-    E, N, K = w.shape
-    R = x_rows.shape[0]
-    _expert_product("moe_nvfp4_expert_linear", (R, N, K, E), x_rows, (R, K), w, (E, N, K), count, offsets, y_rows,
-                    (R, N), status, stream)
+    _check("moe_nvfp4_expert_linear", (_native or native()).expert_linear(
+        x_rows, w, count, offsets, y_rows, status, stream))
 
 
 def moe_nvfp4_expert_linear_dgrad(dy_rows: torch.Tensor, w: torch.Tensor, count: torch.Tensor, offsets: torch.Tensor,
                                   dx_rows: torch.Tensor, status: Optional[torch.Tensor] = None, stream=None) -> None:
     """dx_rows[r] = dy_rows[r] w[e]: dy_rows [rows, N], w [E, N, K], dx_rows [rows, K], BF16."""
-    E, N, K = w.shape
-    R = dy_rows.shape[0]
-    _expert_product("moe_nvfp4_expert_linear_dgrad", (R, N, K, E), dy_rows, (R, N), w, (E, N, K), count, offsets,
-                    dx_rows, (R, K), status, stream)
+    _check("moe_nvfp4_expert_linear_dgrad", (_native or native()).expert_linear_dgrad(
+        dy_rows, w, count, offsets, dx_rows, status, stream))
 
 
 def moe_nvfp4_expert_linear_wgrad(dy_rows: torch.Tensor, x_rows: torch.Tensor, count: torch.Tensor,
                                   offsets: torch.Tensor, dw: torch.Tensor, status: Optional[torch.Tensor] = None,
                                   stream=None) -> None:
     """dw[e] = sum over expert e's rows r of dy_rows[r]^T x_rows[r]: dw [E, N, K], BF16."""
-    E, N, K = dw.shape
-    R = dy_rows.shape[0]
-    _expert_product("moe_nvfp4_expert_linear_wgrad", (R, N, K, E), dy_rows, (R, N), x_rows, (R, K), count, offsets, dw,
-                    (E, N, K), status, stream)
+    _check("moe_nvfp4_expert_linear_wgrad", (_native or native()).expert_linear_wgrad(
+        dy_rows, x_rows, count, offsets, dw, status, stream))
 
 
 def moe_nvfp4_layer_norm(x: torch.Tensor, gamma: torch.Tensor, beta: Optional[torch.Tensor], eps: float,
@@ -464,17 +379,7 @@ def moe_nvfp4_layer_norm(x: torch.Tensor, gamma: torch.Tensor, beta: Optional[to
                          stream=None) -> None:
     """y = (x - mean) * rstd * gamma + beta over the rows of x [T, H]; gamma, beta
     [H], mean and rstd [T] float32 (mean and rstd may both be None)."""
-    T, H, xs = _rows2d("x", x)
-    ys = _rows2d("y", y, x.dtype)[2]
-    if y.shape != x.shape:
-        raise ValueError("y must have the shape of x")
-    f32 = torch.float32
-    code = lib().moe_nvfp4_layer_norm(
-        T, H, _DTYPES[x.dtype], x.data_ptr(), xs, _flat("gamma", gamma, f32, (H,)),
-        None if beta is None else _flat("beta", beta, f32, (H,)), eps, y.data_ptr(), ys,
-        None if mean is None else _flat("mean", mean, f32, (T,)),
-        None if rstd is None else _flat("rstd", rstd, f32, (T,)), _handle(stream))
-    _check("moe_nvfp4_layer_norm", code)
+    _check("moe_nvfp4_layer_norm", (_native or native()).layer_norm(x, gamma, beta, eps, y, mean, rstd, stream))
 
 
 def moe_nvfp4_layer_norm_workspace_bytes(T: int, H: int) -> int:
@@ -485,17 +390,11 @@ def moe_nvfp4_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: torc
                                   rstd: torch.Tensor, dx: torch.Tensor, dgamma: torch.Tensor,
                                   dbeta: Optional[torch.Tensor], workspace: torch.Tensor, stream=None) -> None:
     """dx [T, H], dgamma and dbeta [H] of the layer norm with the forward's mean and rstd [T]."""
-    T, H, xs = _rows2d("x", x)
-    dys, dxs = _rows2d("dy", dy, x.dtype)[2], _rows2d("dx", dx, x.dtype)[2]
-    if dy.shape != x.shape or dx.shape != x.shape:
-        raise ValueError("dy and dx must have the shape of x")
-    f32 = torch.float32
-    code = lib().moe_nvfp4_layer_norm_backward(
-        T, H, _DTYPES[x.dtype], dy.data_ptr(), dys, x.data_ptr(), xs, _flat("gamma", gamma, f32, (H,)),
-        _flat("mean", mean, f32, (T,)), _flat("rstd", rstd, f32, (T,)), dx.data_ptr(), dxs,
-        _flat("dgamma", dgamma, f32, (H,)), None if dbeta is None else _flat("dbeta", dbeta, f32, (H,)),
-        *_space(workspace), _handle(stream))
-    _check("moe_nvfp4_layer_norm_backward", code)
+    _check("moe_nvfp4_layer_norm_backward", (_native or native()).layer_norm_backward(
+        dy, x, gamma, mean, rstd, dx, dgamma, dbeta, workspace, stream))
+
+
+_DTYPES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_F32}
 
 
 class GradList:
@@ -515,10 +414,12 @@ class GradList:
             if o.numel() != g.numel() or not (g.is_contiguous() and o.is_contiguous()):
                 raise ValueError("gradients and outputs must be contiguous and of the same size")
         n = self.n = len(self.grads)
-        self.c_grads = (ctypes.c_void_p * n)(*[g.data_ptr() for g in self.grads])
-        self.c_out = (ctypes.c_void_p * n)(*[o.data_ptr() for o in self.out])
-        self.c_numels = (ctypes.c_int64 * n)(*[g.numel() for g in self.grads])
-        self.c_dtypes = (ctypes.c_int32 * n)(*[_DTYPES[g.dtype] for g in self.grads])
+        # the host arrays of the C calls, and their addresses
+        self._arrays = ((ctypes.c_void_p * n)(*[g.data_ptr() for g in self.grads]),
+                        (ctypes.c_void_p * n)(*[o.data_ptr() for o in self.out]),
+                        (ctypes.c_int64 * n)(*[g.numel() for g in self.grads]),
+                        (ctypes.c_int32 * n)(*[_DTYPES[g.dtype] for g in self.grads]))
+        self._grads, self._out, self._numels, self._dtypes = map(ctypes.addressof, self._arrays)
 
 
 def moe_nvfp4_grad_norm_workspace_bytes(n: int) -> int:
@@ -527,18 +428,15 @@ def moe_nvfp4_grad_norm_workspace_bytes(n: int) -> int:
 
 def moe_nvfp4_grad_norm(grads: GradList, norm: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
     """norm[0] (float32) = sqrt of the sum of the squares of every gradient's elements."""
-    code = lib().moe_nvfp4_grad_norm(grads.n, grads.c_grads, grads.c_numels, grads.c_dtypes,
-                                     _flat("norm", norm, torch.float32, (1,)), *_space(workspace),
-                                     _handle(stream))
-    _check("moe_nvfp4_grad_norm", code)
+    _check("moe_nvfp4_grad_norm", (_native or native()).grad_norm(
+        grads.n, grads._grads, grads._numels, grads._dtypes, norm, workspace, stream))
 
 
 def moe_nvfp4_grad_clip(grads: GradList, norm: torch.Tensor, max_norm: float, eps: float = 1e-6,
                         stream=None) -> None:
     """out = gradient * min(1, max_norm / (norm + eps)) for every gradient of the list."""
-    code = lib().moe_nvfp4_grad_clip(grads.n, grads.c_grads, grads.c_out, grads.c_numels, grads.c_dtypes,
-                                     _flat("norm", norm, torch.float32, (1,)), max_norm, eps, _handle(stream))
-    _check("moe_nvfp4_grad_clip", code)
+    _check("moe_nvfp4_grad_clip", (_native or native()).grad_clip(
+        grads.n, grads._grads, grads._out, grads._numels, grads._dtypes, norm, max_norm, eps, stream))
 
 
 # ---- convenience ---------------------------------------------------------------

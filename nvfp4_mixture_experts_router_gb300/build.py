@@ -1,9 +1,10 @@
-"""Build libmoe_nvfp4.so in-tree with nvcc for sm_103a.
+"""Build libmoe_nvfp4.so in-tree with nvcc for sm_103a, and the Python
+binding of the training operators (_binding.so) with the host compiler.
 
 Each .cu file compiles in parallel to an object, then nvcc links the shared
 library (CUDA runtime linked statically, so the library needs only the
-driver at run time).  Rebuilds only when a source or header is newer than
-the library.
+driver at run time).  The binding links against it and against the installed
+torch.  Rebuilds only when a source or header is newer than the results.
 """
 from __future__ import annotations
 
@@ -12,11 +13,14 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "libmoe_nvfp4.so")
+BINDING = os.path.join(PKG, "_binding.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 BUILD_DIR = os.path.join(PKG, "_build")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -36,14 +40,14 @@ def sources():
 
 
 def _deps():
-    return sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + \
+    return sources() + [BINDING_SRC] + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + \
         glob.glob(os.path.join(ROOT, "include", "*.h")) + [os.path.abspath(__file__)]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(OUT):
+    if not os.path.exists(OUT) or not os.path.exists(BINDING):
         return False
-    t = os.path.getmtime(OUT)
+    t = min(os.path.getmtime(OUT), os.path.getmtime(BINDING))
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
@@ -62,8 +66,26 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stderr}")
         return obj, r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
+    import torch
+    cxx = os.environ.get("CXX") or shutil.which("g++") or "c++"
+    tdir = os.path.dirname(torch.__file__)
+
+    def compile_binding():
+        obj = os.path.join(BUILD_DIR, "binding.cpp.o")
+        cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(cc))), "include")
+        cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-c", BINDING_SRC, "-o", obj,
+               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+               "-I", sysconfig.get_paths()["include"], "-I", os.path.join(tdir, "include"),
+               "-I", os.path.join(tdir, "include", "torch", "csrc", "api", "include"), "-isystem", cuda]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"{cxx} failed for {BINDING_SRC}:\n{r.stderr}")
+        return obj
+
+    with cf.ThreadPoolExecutor(max_workers=min(16, os.cpu_count() or 4)) as ex:
+        binding = ex.submit(compile_binding)
         results = list(ex.map(compile_one, sources()))
+        binding_obj = binding.result()
     if verbose:
         for _, log in results:
             print(log)
@@ -74,6 +96,13 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, OUT)
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [cxx, "-shared", "-o", tmp, binding_obj, "-Wl,-rpath,$ORIGIN", "-L", PKG, "-l:libmoe_nvfp4.so",
+           "-L", os.path.join(tdir, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stderr}")
+    os.replace(tmp, BINDING)
     return OUT
 
 
