@@ -87,8 +87,7 @@ __device__ __forceinline__ void scale_part(const void* in, void* out, int64_t at
             float w[VEC];
 #pragma unroll
             for (int j = 0; j < VEC; ++j) w[j] = v[j] * scale;
-            // the result is not read again here: it leaves L2 first
-            __stcs(q + i, RV::pack(w));
+            q[i] = RV::pack(w);
         },
         [&](int i) { static_cast<T_*>(out)[at + i] = (T_)((float)static_cast<const T_*>(in)[at + i] * scale); });
 }
@@ -218,7 +217,7 @@ cudaError_t launch_grad_clip(const LaunchCtx& c, int sms, int n, const void* con
                              const int64_t* numels, const int32_t* dtypes, const float* norm, float max_norm,
                              float eps) {
     return for_tables(n, grads, out, numels, dtypes, [&](const GradTable& t) {
-        const int blocks = t.chunks < 4 * sms ? t.chunks : 4 * sms;
+        const int blocks = t.chunks < 8 * sms ? t.chunks : 8 * sms;
         return c.launch(grad_scale_kernel, dim3(blocks), dim3(kClipThreads), 0, t, norm, max_norm, eps);
     });
 }

@@ -47,7 +47,7 @@ moe_status device_state(int* sms, int* device) {
                    setup_gemm_w4a16_swap_kernels() != cudaSuccess ||
                    setup_router_gemm_kernel() != cudaSuccess ||
                    setup_expert_linear_kernels(dev, d.sms) != cudaSuccess ||
-                   setup_layer_norm_kernels() != cudaSuccess) {
+                   setup_layer_norm_kernels() != cudaSuccess || setup_sort_kernels() != cudaSuccess) {
             d.status = MOE_ERR_CUDA;
         } else {
             d.status = MOE_OK;

@@ -159,6 +159,110 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(int64_t routes
     pdl_launch_dependents();
 }
 
+// The same order in one launch, for up to two routes a thread of a block of
+// 1024, or of a cluster of eight of them (`nc` blocks).  A warp counts its routes expert by expert as it ranks
+// them (the rank stays in a register); a thread per expert turns the warps'
+// counts into starts within the block; the blocks read each other's totals
+// through distributed shared memory.
+constexpr int kClusterThreads = 1024;
+constexpr int kClusterWarps = kClusterThreads / 32;
+constexpr int kClusterBlocks = 8;
+
+template <int S>
+__global__ void __launch_bounds__(kClusterThreads, 1)
+    sort_cluster_kernel(int routes, int E, int nc, const int* __restrict__ ids, int* __restrict__ count,
+                        int* __restrict__ offsets, int* __restrict__ row_of_route, int* __restrict__ route_of_row) {
+    extern __shared__ int smem[];
+    int* s_warp = smem;                            // [kClusterWarps][E] counts, then starts within the block
+    int* s_total = smem + kClusterWarps * E;       // [E] this block's routes of an expert
+    __shared__ int s_scan[kClusterWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = nc > 1 ? (int)cluster_cta_rank() : 0;
+    for (int i = tid; i < kClusterWarps * E; i += kClusterThreads) s_warp[i] = 0;
+    pdl_wait();
+    const int r0 = (rank * kClusterThreads + warp * 32) * S + lane;      // S steps of 32 routes a warp
+    int id[S], place[S];
+#pragma unroll
+    for (int i = 0; i < S; ++i) id[i] = r0 + 32 * i < routes ? ids[r0 + 32 * i] : -1;
+    __syncthreads();
+    int* mine = s_warp + warp * E;
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+        if ((unsigned)id[i] >= (unsigned)E) id[i] = -1;
+        const unsigned peers = __match_any_sync(0xffffffffu, id[i]);
+        place[i] = 0;
+        if (id[i] >= 0) place[i] = mine[id[i]] + __popc(peers & ((1u << lane) - 1u));
+        __syncwarp();
+        if (id[i] >= 0 && lane == __ffs(peers) - 1) mine[id[i]] = place[i] + __popc(peers);
+        __syncwarp();
+    }
+    __syncthreads();
+    int total = 0;                                 // expert tid's (E <= 1024 threads)
+    if (tid < E) {
+#pragma unroll 8
+        for (int w = 0; w < kClusterWarps; ++w) {
+            const int c = s_warp[w * E + tid];
+            s_warp[w * E + tid] = total;
+            total += c;
+        }
+        s_total[tid] = total;
+    }
+    int before = 0;                                // its routes in earlier blocks
+    if (nc > 1) {
+        cluster_sync_all();
+        if (tid < E) {
+            int all = 0;
+#pragma unroll
+            for (int b = 0; b < kClusterBlocks; ++b) {
+                int c = 0;
+                if (b < nc)
+                    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(c) : "r"(cluster_map(s_total + tid, b)));
+                before += b < rank ? c : 0;
+                all += c;
+            }
+            total = all;
+        }
+    }
+    // exclusive scan of the totals over the experts
+    int incl = total;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int a = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += a;
+    }
+    if (lane == 31) s_scan[warp] = incl;
+    if (nc > 1) cluster_sync_all();                // the totals have been read: their place may be reused
+    else __syncthreads();
+    const int sum = s_scan[lane];
+    int run = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int a = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += a;
+    }
+    const int used = __shfl_sync(0xffffffffu, run, 31);
+    const int first = __shfl_sync(0xffffffffu, run - sum, warp) + incl - total;
+    if (tid < E) {
+        s_total[tid] = first + before;             // the block's first row of the expert
+        if (rank == 0) {
+            count[tid] = total;
+            offsets[tid] = first;
+        }
+    }
+    if (rank == 0 && tid == 0) offsets[E] = used;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+        const int r = r0 + 32 * i;
+        if (r >= routes) continue;
+        const int row = id[i] >= 0 ? s_total[id[i]] + mine[id[i]] + place[i] : -1;
+        row_of_route[r] = row;
+        if (row >= 0) route_of_row[row] = r;
+        if (r >= used) route_of_row[r] = -1;
+    }
+    pdl_launch_dependents();
+}
+
 // ---- rows -------------------------------------------------------------------
 
 constexpr int kRowThreads = 256;
@@ -372,10 +476,30 @@ size_t sort_workspace_bytes(int T, int E, int K) {
     return align_up(p.blocks > 1 ? (uint64_t)p.blocks * E * 4 : 4, 256);
 }
 
+cudaError_t setup_sort_kernels() {
+    constexpr int most = (kClusterWarps + 1) * 1024 * 4;
+    const cudaError_t e = cudaFuncSetAttribute(sort_cluster_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(sort_cluster_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+}
+
+// Up to 1024 routes: one block of sort_place_kernel, which counts for itself.
+// Up to 16384: one launch of one block or a cluster of eight.  More: a block
+// per 1024 routes and a launch before it for their counts (the match of equal
+// experts takes about 1 us a step of 32 warps on an SM: eight SMs are too few).
+// Measured on GB300 (top-8, 64 experts; us cluster, two launches): 1600 routes
+// 3.6 5.4;  4096 5.1 5.6;  8192 5.2 7.0;  32768 7.6 7.0;  131072 22 10.5.
 cudaError_t launch_sort_routes(const LaunchCtx& c, int T, int E, int K, const int* ids, int* count, int* offsets,
                                int* row_of_route, int* route_of_row, int* workspace) {
     const int64_t routes = (int64_t)T * K;
     const SortPlan p = sort_plan(routes);
+    if (p.blocks > 1 && routes <= 2 * kClusterBlocks * kClusterThreads) {
+        LaunchCtx one = c;
+        one.cluster = routes <= 2 * kClusterThreads ? 1 : kClusterBlocks;
+        auto kernel = routes <= one.cluster * kClusterThreads ? sort_cluster_kernel<1> : sort_cluster_kernel<2>;
+        return one.launch(kernel, dim3(one.cluster), dim3(kClusterThreads), (size_t)(kClusterWarps + 1) * E * 4,
+                          (int)routes, E, one.cluster, ids, count, offsets, row_of_route, route_of_row);
+    }
     LaunchCtx next = c;
     if (p.blocks > 1) {
         const cudaError_t e = c.launch(sort_count_kernel, dim3(p.blocks), dim3(kSortThreads), (size_t)E * 4, routes, E,

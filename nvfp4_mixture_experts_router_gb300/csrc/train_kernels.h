@@ -8,6 +8,7 @@ namespace moe {
 
 // route_rows.cu
 size_t sort_workspace_bytes(int T, int E, int K);
+cudaError_t setup_sort_kernels();
 cudaError_t launch_sort_routes(const LaunchCtx& c, int T, int E, int K, const int* ids, int* count, int* offsets,
                                int* row_of_route, int* route_of_row, int* workspace);
 cudaError_t launch_dispatch(const LaunchCtx& c, int T, int H, int K, int64_t rows, int elem, const void* x,

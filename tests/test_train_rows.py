@@ -65,7 +65,9 @@ def make_ids(T, E, K, seed, kind="random"):
 @pytest.mark.parametrize("T,E,K,kind", [
     (1, 256, 8, "random"), (1, 1, 1, "one"), (3, 5, 5, "mixed"), (33, 40, 3, "random"), (128, 8, 8, "one"),
     (1024, 64, 1, "mixed"), (1025, 64, 1, "mixed"), (511, 64, 6, "random"), (1000, 300, 32, "mixed"),
-    (2049, 1024, 8, "random"), (700, 16, 4, "dropped"), (16384, 256, 8, "random"), (40001, 1000, 7, "mixed")])
+    (2049, 1024, 8, "random"), (700, 16, 4, "dropped"), (16384, 256, 8, "random"),
+    (255, 9, 8, "mixed"), (257, 1024, 8, "random"), (1023, 5, 8, "mixed"), (1500, 1024, 8, "mixed"),
+    (2048, 1000, 8, "one"), (40001, 1000, 7, "mixed")])
 def test_sort_is_the_stable_order(T, E, K, kind):
     ids = make_ids(T, E, K, 100 + T, kind)
     for got, want in zip(sort(ids, E), sort_ref(ids, E)):
