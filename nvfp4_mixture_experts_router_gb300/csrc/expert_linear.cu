@@ -125,19 +125,15 @@ constexpr uint32_t kIdescAMn = 1u << 15, kIdescBMn = 1u << 16;
 
 struct ExpertTile {
     int e, m0, n0;         // expert, first m of the pair's tile, first n
-    int n;                 // columns of D the MMAs compute, a multiple of 32 up to TN
+    int n;                 // columns of D that the MMAs compute, a multiple of 32 up to TN
     int first, count;      // the expert's segment
 };
 
-// Columns of an expert's tiles.  forward / dgrad: the segment in equal parts of
-// at most TN (the MMAs' time follows N, so 300 rows cost two tiles of 160, not
-// of 256).  wgrad: TN, whose stores leave in 64-column boxes.
-template <int TN, bool WGRAD>
-__device__ __forceinline__ int tile_columns(int extent) {
-    if (WGRAD) return TN;
-    const int parts = (extent + TN - 1) / TN;
-    return parts ? min(TN, ((extent + parts - 1) / parts + 31) / 32 * 32) : TN;
-}
+// Tiles of an expert along n.  forward / dgrad: the segment's 32-row units in
+// nearly equal parts of at most TN (the MMAs' time follows N): 1030 rows are
+// 33 units in tiles of 224, 224, 224, 192 and 192 rows.
+template <int TN>
+__device__ __forceinline__ int n_tiles(int extent) { return (extent + TN - 1) / TN; }
 
 // The tile list: experts in order, an expert's tiles in groups of kMGroup m
 // tiles, n outer and m inner, so that the pairs running at a time share both
@@ -158,12 +154,18 @@ __device__ __forceinline__ ExpertTile expert_tile(const ExpertParams& p, int til
     const int local = tile - (lo ? s_end[lo - 1] : 0);
     const int mt = (p.m_extent + 2 * p.half_m - 1) / (2 * p.half_m);
     const int extent = WGRAD ? p.n_extent : t.count;
-    t.n = tile_columns<TN, WGRAD>(extent);
-    const int nt = (extent + t.n - 1) / t.n;
+    const int nt = n_tiles<TN>(extent);
     const int g = local / (kMGroup * nt), in = local % (kMGroup * nt);
     const int gm = min(kMGroup, mt - g * kMGroup);
-    t.n0 = in / gm * t.n;
-    if (WGRAD) t.n = min(TN, (extent - t.n0 + 31) / 32 * 32);
+    const int i = in / gm;
+    if (WGRAD) {
+        t.n0 = i * TN;
+        t.n = min(TN, (extent - t.n0 + 31) / 32 * 32);
+    } else {
+        const int units = (extent + 31) / 32, per = units / nt, more = units % nt;
+        t.n0 = 32 * (i * per + min(i, more));
+        t.n = 32 * (per + (i < more ? 1 : 0));
+    }
     t.m0 = (g * kMGroup + in % gm) * 2 * p.half_m;
     return t;
 }
@@ -228,8 +230,7 @@ __global__ void __launch_bounds__(ExpertCfg<PRODUCT, TN, DEPTH>::kThreads, 1)
             }
             s_first[e] = (int)first;
             s_count[e] = (int)n;
-            const int extent = kWgrad ? p.n_extent : (int)n, cols = tile_columns<TN, kWgrad>(extent);
-            s_end[e] = mt * ((extent + cols - 1) / cols);
+            s_end[e] = mt * n_tiles<TN>(kWgrad ? p.n_extent : (int)n);
         }
         __syncthreads();
         if (warp == 0) {
