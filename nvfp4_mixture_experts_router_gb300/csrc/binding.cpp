@@ -9,6 +9,7 @@
 // for it.  TypeError: a wrong element type or device; ValueError: a wrong shape.
 #include <Python.h>
 
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/version.h>
@@ -39,6 +40,7 @@ const at::Tensor& tensor(PyObject* o, const char* name) {
     if (!THPVariable_Check(o)) wrong_type(std::string(name) + " must be a tensor");
     const at::Tensor& t = THPVariable_Unpack(o);
     if (!t.is_cuda()) wrong_type(std::string(name) + " must be a CUDA tensor");
+    if (t.get_device() != c10::cuda::current_device()) wrong_value(std::string(name) + " is not on the current device");
     return t;
 }
 

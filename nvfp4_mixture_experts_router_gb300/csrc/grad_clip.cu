@@ -192,11 +192,11 @@ cudaError_t for_tables(int n, const void* const* in, void* const* out, const int
 
 }  // namespace
 
-// A launch holds kListMax tensors at least (or fewer, when 2^30 chunks are
-// full: one launch more for each 2^40 elements, so a launch per tensor and one
-// per kListMax bound their number).
+// Partial sums of every launch: a launch takes kListMax tensors, or fewer if
+// they fill its 2^30 chunks (sixteen tensors of the largest size do).
 size_t grad_norm_workspace_bytes(int n) {
-    return align_up((uint64_t)(n < 1 ? 1 : n) * kNormBlocks * 4, 256);
+    const uint64_t launches = (uint64_t)n / kListMax + (uint64_t)n / 16 + 2;
+    return align_up(launches * kNormBlocks * 4, 256);
 }
 
 cudaError_t launch_grad_norm(const LaunchCtx& c, int sms, int n, const void* const* grads, const int64_t* numels,

@@ -480,29 +480,48 @@ __global__ void __launch_bounds__(512, 1)
     pdl_launch_dependents();
 }
 
-// dgamma and dbeta from `parts` partial sums [parts][2][H]: 32 columns a block,
-// a warp per 32nd of the parts.
+// dgamma and dbeta from `parts` partial sums [parts][2][H]: 32 VEC columns a
+// block, a 32nd of the parts a warp, then the warps' sums in order.
+template <int VEC>
 __global__ void __launch_bounds__(1024) norm_reduce_kernel(int H, int parts, const float* part, float* dgamma,
-                                                           float* dbeta) {
-    __shared__ float s[32][33];
+                                                                   float* dbeta) {
+    using RV = RowVec<float, VEC>;
+    constexpr int kWarps = 32;
+    __shared__ float s[kWarps][32 * VEC];
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int h = blockIdx.x * 32 + lane;
-    const size_t at = blockIdx.y ? H : 0;
-    float v = 0.0f;
-    if (h < H)
+    const int n = H / VEC, c = blockIdx.x * 32 + lane;
+    float v[VEC];
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) v[k] = 0.0f;
+    if (c < n) {
+        const typename RV::Raw* p = reinterpret_cast<const typename RV::Raw*>(part) + (blockIdx.y ? n : 0) + c;
 #pragma unroll 4
-        for (int p = warp; p < parts; p += 32) v += part[(size_t)p * 2 * H + at + h];
-    s[warp][lane] = v;
+        for (int q = warp; q < parts; q += kWarps) {
+            float u[VEC];
+            RV::unpack(p[(size_t)q * 2 * n], u);
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) v[k] += u[k];
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) s[warp][lane * VEC + k] = v[k];
     __syncthreads();
-    // warp w sums column w's 32 partial sums
-    v = warp_sum(s[lane][warp]);
-    const int col = blockIdx.x * 32 + warp;
-    if (lane == 0 && col < H) {
-        if (blockIdx.y == 0) dgamma[col] = v;
-        else dbeta[col] = v;
+    const int h = blockIdx.x * 32 * VEC + (int)threadIdx.x;
+    if (threadIdx.x < 32 * VEC && h < H) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) sum += s[w][threadIdx.x];
+        (blockIdx.y ? dbeta : dgamma)[h] = sum;
     }
     pdl_launch_dependents();
+}
+
+cudaError_t launch_reduce(const LaunchCtx& c, int H, int parts, const float* part, float* dgamma, float* dbeta) {
+    const int wide = H % 4 == 0 ? 4 : 1;
+    const dim3 grid((unsigned)((H / wide + 31) / 32), dbeta ? 2 : 1);
+    return c.launch(wide == 4 ? norm_reduce_kernel<4> : norm_reduce_kernel<1>, grid, dim3(1024), 0, H, parts,
+                    part, dgamma, dbeta);
 }
 
 // ---- rows of more than kRowColumns columns -------------------------------------
@@ -748,14 +767,13 @@ cudaError_t launch_layer_norm_backward(const LaunchCtx& c, int T, int H, int ele
                                        float* workspace) {
     const int bytes = row_vec_bytes(
         H, elem, row_at(x, x_stride, elem) | row_at(dy, dy_stride, elem) | row_at(dx, dx_stride, elem));
-    const dim3 reduce((unsigned)((H + 31) / 32), dbeta ? 2 : 1);
     cudaError_t e;
     if (H <= kRowColumns) {
         int blocks = 0;
         e = launch_backward_rows(c, bytes, T, H, elem, dy, dy_stride, x, x_stride, gamma, mean, rstd, dx, dx_stride,
                                  workspace, &blocks);
         if (e != cudaSuccess) return e;
-        return c.launch(norm_reduce_kernel, reduce, dim3(1024), 0, H, blocks, (const float*)workspace, dgamma, dbeta);
+        return launch_reduce(c, H, blocks, workspace, dgamma, dbeta);
     }
     // the column sums first: dx may overwrite dy or x
     const dim3 parts((unsigned)((H + kNormThreads - 1) / kNormThreads), kNormParts);
@@ -768,7 +786,7 @@ cudaError_t launch_layer_norm_backward(const LaunchCtx& c, int T, int H, int ele
                      static_cast<const uint32_t*>(dy), dy_stride, static_cast<const uint32_t*>(x), x_stride, mean,
                      rstd, workspace);
     if (e != cudaSuccess) return e;
-    e = c.launch(norm_reduce_kernel, reduce, dim3(1024), 0, H, kNormParts, (const float*)workspace, dgamma, dbeta);
+    e = launch_reduce(c, H, kNormParts, workspace, dgamma, dbeta);
     if (e != cudaSuccess || T == 0) return e;
     return launch_dx(c, bytes, T, H, elem, dy, dy_stride, x, x_stride, gamma, mean, rstd, dx, dx_stride);
 }

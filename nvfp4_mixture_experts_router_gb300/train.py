@@ -20,6 +20,7 @@ from dataclasses import dataclass
 from typing import Iterable, Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import api
 
@@ -69,6 +70,7 @@ class _LayerNorm(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, gamma, mean, rstd = ctx.saved_tensors
         dy = dy.contiguous()
@@ -95,6 +97,7 @@ class _Dispatch(torch.autograd.Function):
         return rows
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, drows):
         dx = torch.empty(ctx.shape, dtype=drows.dtype, device=drows.device)
         api.moe_nvfp4_dispatch_backward(drows.contiguous(), ctx.routes.row_of_route, dx)
@@ -116,6 +119,7 @@ class _Combine(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         o_rows, topk_w = ctx.saved_tensors
         do, dw = torch.empty_like(o_rows), torch.empty_like(topk_w)
@@ -139,6 +143,7 @@ class _ExpertLinear(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x_rows, w = ctx.saved_tensors
         r, dy = ctx.routes, dy.contiguous()
