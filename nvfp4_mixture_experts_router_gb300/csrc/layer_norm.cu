@@ -224,6 +224,107 @@ __global__ void __launch_bounds__(MAXT) norm_rows_kernel(int T, int H, int W, co
     pdl_launch_dependents();
 }
 
+// The same for many rows of more than kRingMin columns in 16-byte vectors:
+// persistent blocks of up to 512 threads, two an SM where their shared memory
+// allows, with gamma and beta in shared memory and the rows ahead in a ring of
+// bulk copies, so that a row's two reductions overlap the copies of the next
+// rows and the other block's arithmetic.  A stage is free once the first
+// reduction has passed its barrier.  Waits as in the backward ring below.
+template <typename T_, int VEC>
+__global__ void __launch_bounds__(512, 2)
+    norm_ring_kernel(int T, int H, int S, const typename RowVec<T_, VEC>::Raw* x, int64_t x_stride,
+                     const float* gamma, const float* beta, float eps, typename RowVec<T_, VEC>::Raw* y,
+                     int64_t y_stride, float* mean_out, float* rstd_out, bool wide_params) {
+    using Raw = typename RowVec<T_, VEC>::Raw;
+    constexpr int C = kRingCols, V = C / VEC, P = C / 2;
+    __shared__ float s_red[2][16];
+    __shared__ uint64_t s_full[kRingMax];
+    extern __shared__ __align__(16) uint8_t s_ring[];      // gamma, beta [P][threads] float2 each, then [S][n] vectors
+    pdl_wait();
+    const int lanes = blockDim.x, j = threadIdx.x, lane = j & 31, warp = j >> 5, W = lanes >> 5;
+    const int n = H / VEC;
+    float2* s_gamma = reinterpret_cast<float2*>(s_ring);
+    float2* s_beta = s_gamma + P * lanes;
+    Raw* s_rows = reinterpret_cast<Raw*>(s_ring + (size_t)lanes * C * 8);
+    const uint32_t row_bytes = (uint32_t)n * 16u;
+    const int64_t step = gridDim.x, first = blockIdx.x;
+    uint64_t policy = 0;
+    auto fetch = [&](int64_t t, int stage) {               // thread 0
+        mbar_arrive_expect_tx(&s_full[stage], row_bytes);
+        bulk_load(s_rows + (size_t)stage * n, x + t * x_stride, row_bytes, &s_full[stage], policy);
+    };
+    if (j == 0) {
+        policy = policy_evict_first();                     // x is read once
+        for (int q = 0; q < S; ++q) mbar_init(&s_full[q], 1);
+        fence_mbar_init();
+        for (int q = 0; q < S; ++q)
+            if (first + q * step < T) fetch(first + q * step, q);
+    }
+    {
+        float2 p[P];
+        load_params<VEC, C>(gamma, j, lanes, n, wide_params, p);
+#pragma unroll
+        for (int q = 0; q < P; ++q) s_gamma[q * lanes + j] = p[q];     // read by this thread alone, as beta
+#pragma unroll
+        for (int q = 0; q < P; ++q) p[q] = both(0.0f);
+        if (beta) load_params<VEC, C>(beta, j, lanes, n, wide_params, p);
+#pragma unroll
+        for (int q = 0; q < P; ++q) s_beta[q * lanes + j] = p[q];
+    }
+    __syncthreads();
+    const float inv = 1.0f / (float)H;
+    int stage = 0;
+    uint32_t parity = 0;
+    y += first * y_stride + j;
+    const int64_t y_step = step * y_stride;
+    volatile int never = 0;
+    for (int64_t t = first; t < T; t += step) {
+        const bool landed = mbar_wait(&s_full[stage], parity, &never, nullptr, 0);
+        float2 v[P];
+        {
+            const Raw* at = s_rows + (size_t)stage * n + j;
+            Raw r[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) r[i] = j + i * lanes < n ? at[i * lanes] : Raw{};
+            unpack_cols<T_, VEC, C>(r, v);
+        }
+        float2 sum = v[0];
+#pragma unroll
+        for (int q = 1; q < P; ++q) sum = add2(sum, v[q]);
+        const float a = warp_sum(sum.x + sum.y);
+        if (lane == 0) s_red[0][warp] = a;
+        if (__syncthreads_or(!landed)) {
+            for (int i = 0; i < 100; ++i) __nanosleep(10000);   // copies in flight land before the block leaves
+            break;
+        }
+        if (j == 0 && t + S * step < T) fetch(t + S * step, stage);
+        const float mean = warp_sum(lane < W ? s_red[0][lane & 15] : 0.0f) * inv;
+        float2 sq = both(0.0f);
+#pragma unroll
+        for (int q = 0; q < P; ++q) {
+            v[q] = add2(v[q], both(-mean));
+            // columns past the row's end do not count (VEC is even: a pair is of one vector)
+            if (j + 2 * q / VEC * lanes < n) sq = fma2(v[q], v[q], sq);
+        }
+        const float b = warp_sum(sq.x + sq.y);
+        if (lane == 0) s_red[1][warp] = b;
+        __syncthreads();
+        const float rstd = 1.0f / sqrtf(warp_sum(lane < W ? s_red[1][lane & 15] : 0.0f) * inv + eps);
+#pragma unroll
+        for (int q = 0; q < P; ++q) v[q] = fma2(mul2(v[q], both(rstd)), s_gamma[q * lanes + j], s_beta[q * lanes + j]);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (j + i * lanes < n) y[i * lanes] = pack_cols<T_, VEC, C>(v, i);
+        if (j == 0 && mean_out) {
+            mean_out[t] = mean;
+            rstd_out[t] = rstd;
+        }
+        y += y_step;
+        if (++stage == S) { stage = 0; parity ^= 1u; }
+    }
+    pdl_launch_dependents();
+}
+
 // A row of dy and x in flight.
 template <typename Raw, int V>
 struct NormRow {
@@ -643,6 +744,14 @@ __global__ void __launch_bounds__(kNormThreads)
     }
 }
 
+// Resident blocks of the ring kernel on an SM (its shared memory leaves two
+// stages to each: the longest FP32 rows of a share take 16 KB of gamma and 64
+// KB a stage, or a quarter of it).
+int ring_blocks(int H) {
+    const int share = (H + 32 * kRingCols - 1) / (32 * kRingCols);   // warps, of 16
+    return share <= 4 ? 4 : share <= 8 ? 2 : 1;
+}
+
 template <typename T_, int VEC>
 cudaError_t forward_any(const LaunchCtx& c, int T, int H, const void* x, int64_t x_stride, const float* gamma,
                         const float* beta, float eps, void* y, int64_t y_stride, float* mean, float* rstd) {
@@ -653,6 +762,19 @@ cudaError_t forward_any(const LaunchCtx& c, int T, int H, const void* x, int64_t
         return c.launch(layer_norm_kernel<T_, VEC>, dim3(T), dim3(kNormThreads), 0, H, xv, x_stride / VEC, gamma, beta,
                         eps, yv, y_stride / VEC, mean, rstd);
     const bool wide_params = (row_at(gamma) | row_at(beta)) % 16 == 0;
+    if constexpr (sizeof(Raw) == 16) {
+        if (H > kRingMin && T > 4 * kNormSms) {
+            const int threads = (H + 32 * kRingCols - 1) / (32 * kRingCols) * 32;
+            const int held = threads * kRingCols * 8, row = H * (int)sizeof(T_);
+            int per_sm = ring_blocks(H) < 2 ? 2 : ring_blocks(H);
+            if (kRingBytes / per_sm < held + 2 * row) per_sm = 1;
+            const int fit = (kRingBytes / per_sm - held) / row;
+            const int S = fit > kRingMax ? kRingMax : fit;
+            return c.launch(norm_ring_kernel<T_, VEC>, dim3(per_sm * kNormSms), dim3(threads),
+                            (size_t)held + (size_t)S * row, T, H, S, xv, x_stride / VEC, gamma, beta, eps, yv,
+                            y_stride / VEC, mean, rstd, wide_params);
+        }
+    }
     // long rows, enough of them to fill the SMs: 32 columns a thread, so that
     // several rows share an SM and overlap their loads with their reductions
     const bool many = H > 32 * 8 * kCols && T > 152;
@@ -673,14 +795,6 @@ cudaError_t dx_any(const LaunchCtx& c, int T, int H, const void* dy, int64_t dy_
     return c.launch(layer_norm_dx_kernel<T_, VEC>, dim3(T), dim3(kNormThreads), 0, H, static_cast<const Raw*>(dy),
                     dy_stride / VEC, static_cast<const Raw*>(x), x_stride / VEC, gamma, mean, rstd,
                     static_cast<Raw*>(dx), dx_stride / VEC);
-}
-
-// Resident blocks of the ring kernel on an SM (its shared memory leaves two
-// stages to each: the longest FP32 rows of a share take 16 KB of gamma and 64
-// KB a stage, or a quarter of it).
-int ring_blocks(int H) {
-    const int share = (H + 32 * kRingCols - 1) / (32 * kRingCols);   // warps, of 16
-    return share <= 4 ? 4 : share <= 8 ? 2 : 1;
 }
 
 // Blocks of a persistent backward kernel with `rows` rows at a time: the
@@ -734,6 +848,10 @@ cudaError_t launch_layer_norm(const LaunchCtx& c, int T, int H, int elem, const 
 cudaError_t setup_layer_norm_kernels() {
     static_assert(512 * kRingCols * 4 + 2 * 2 * kRowColumns * 4 <= kRingBytes, "two stages of the longest rows");
     cudaError_t e;
+    if ((e = cudaFuncSetAttribute(norm_ring_kernel<__nv_bfloat16, 8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  kRingBytes)) ||
+        (e = cudaFuncSetAttribute(norm_ring_kernel<float, 4>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes)))
+        return e;
     if ((e = cudaFuncSetAttribute(norm_ring_backward_kernel<__nv_bfloat16, 8>,
                                   cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes)))
         return e;

@@ -88,7 +88,8 @@ def data(T, H, dt, seed=0, offset=0.3):
 
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("T,H", [(1, 1), (1, 7168), (2, 8), (3, 33), (7, 255), (16, 256), (33, 1001), (130, 2048),
-                                 (5, 4104), (4, 8192), (3, 16384), (2, 65536), (2, 65535), (1000, 64), (700, 7168)])
+                                 (5, 4104), (4, 8192), (3, 16384), (2, 65536), (2, 65535), (1000, 64), (700, 7168),
+                                 (1300, 1032), (611, 8192), (2000, 2048), (900, 3001)])
 def test_forward_and_backward(T, H, dt):
     x, gamma, beta, dy = data(T, H, dt)
     got = forward(x, gamma, beta)
