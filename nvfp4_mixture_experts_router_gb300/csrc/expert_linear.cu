@@ -543,13 +543,16 @@ constexpr int kWgradDeepRows = 300;
 // eight rows, with the least work for the busiest pair if every busy expert
 // has one tile of rows.  8 experts of 4096 rows on 76 pairs: 16 tiles of 256
 // rows each are 128 tiles, two rounds of 128 rows per CTA; 19 tiles of 224
-// are 152, two rounds of 112.
-int tile_height(int m_extent, int64_t busy, int pairs) {
+// are 152, two rounds of 112 (4096 x 7168: 88 -> 76 us).  A tile costs about a
+// microsecond besides, the copies of kTileCost elements: 45 experts of 6520 x
+// 416 took 77 us in 32 rounds of 64 rows.
+constexpr int kTileCost = 22000;
+int tile_height(int m_extent, int depth, int64_t busy, int pairs) {
     int best = kHalfM;
     int64_t best_work = INT64_MAX;
     for (int h = kHalfM; h >= 64; h -= 8) {
         const int64_t tiles = busy * ((m_extent + 2 * h - 1) / (2 * h));
-        const int64_t work = (tiles + pairs - 1) / pairs * h;
+        const int64_t work = (tiles + pairs - 1) / pairs * ((int64_t)h * depth + kTileCost);
         if (work < best_work) {
             best = h;
             best_work = work;
@@ -611,7 +614,7 @@ cudaError_t launch_expert_linear(const LaunchCtx& c, int product, int device, co
     } else {
         const bool fwd = product == kExpertForward;
         const cuuint64_t dw[3] = {K, N, (cuuint64_t)a.E}, sw[2] = {K * 2, N * K * 2};
-        if (fwd && tn < 256) p.half_m = tile_height(a.N, busy, grid / 2);
+        if (fwd && tn < 256) p.half_m = tile_height(a.N, a.K, busy, grid / 2);
         // no more rows than there are: the copies of one token's rows are short
         p.box_n = (int)(a.rows < tn / 2 ? (a.rows + 7) / 8 * 8 : tn / 2);
         const cuuint32_t boxw[3] = {64, fwd ? (cuuint32_t)p.half_m : 128u, 1};
