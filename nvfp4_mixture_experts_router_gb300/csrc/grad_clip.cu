@@ -6,8 +6,9 @@
 //
 // The list travels as a kernel argument (pointers, sizes, types), a launch per
 // kListMax tensors: nothing is copied to the device beforehand, and a captured
-// graph replays it.  Tensors are cut into chunks of kChunk elements that the
-// blocks take in turn.  HBM is the bound: one read for the norm, one read and
+// graph replays it.  Tensors are cut into chunks of kChunkMost elements, or of
+// fewer where the whole list would not give every block one, that the blocks
+// take in turn.  HBM is the bound: one read for the norm, one read and
 // one write for the scaling.
 #include "row_vec.cuh"
 #include "train_kernels.h"
@@ -18,8 +19,9 @@ namespace {
 
 constexpr int kClipThreads = 512;
 constexpr int kListMax = 96;
-constexpr int kChunk = 16384;
-constexpr int kInFlight = 4;          // 16-byte loads of a thread: a chunk of BF16 at once
+constexpr int kChunkMost = 16384;     // elements: a thread's kInFlight loads of BF16
+constexpr int kChunkLeast = 4096;
+constexpr int kInFlight = 4;          // 16-byte loads of a thread
 constexpr int kNormBlocks = 608;      // partial sums per launch: four blocks an SM
 
 struct GradEntry {
@@ -32,6 +34,7 @@ struct GradEntry {
 struct GradTable {
     int n;
     int chunks;
+    int chunk;            // elements of a chunk
     GradEntry e[kListMax];
 };
 
@@ -103,8 +106,8 @@ __global__ void __launch_bounds__(kClipThreads) grad_square_kernel(const __grid_
     for (int c = blockIdx.x; c < t.chunks; c += gridDim.x) {
         while (c >= t.e[i].last_chunk) ++i;
         const GradEntry& e = t.e[i];
-        const int64_t at = (int64_t)(c - first_chunk(t, i)) * kChunk;
-        const int count = (int)min((int64_t)kChunk, e.numel - at);
+        const int64_t at = (int64_t)(c - first_chunk(t, i)) * t.chunk;
+        const int count = (int)min((int64_t)t.chunk, e.numel - at);
         const bool wide = reinterpret_cast<uintptr_t>(e.in) % 16 == 0;
         if (e.elem == 2)
             sum += wide ? square_part<__nv_bfloat16, 8>(e.in, at, count) : square_part<__nv_bfloat16, 1>(e.in, at, count);
@@ -147,8 +150,8 @@ __global__ void __launch_bounds__(kClipThreads) grad_scale_kernel(const __grid_c
         while (c < first_chunk(t, i)) --i;
         const GradEntry& e = t.e[i];
         if (scale == 1.0f && e.in == e.out) continue;
-        const int64_t at = (int64_t)(c - first_chunk(t, i)) * kChunk;
-        const int count = (int)min((int64_t)kChunk, e.numel - at);
+        const int64_t at = (int64_t)(c - first_chunk(t, i)) * t.chunk;
+        const int count = (int)min((int64_t)t.chunk, e.numel - at);
         const bool wide = (reinterpret_cast<uintptr_t>(e.in) | reinterpret_cast<uintptr_t>(e.out)) % 16 == 0;
         if (e.elem == 2) {
             if (wide) scale_part<__nv_bfloat16, 8>(e.in, e.out, at, count, scale);
@@ -166,6 +169,12 @@ template <typename F>
 cudaError_t for_tables(int n, const void* const* in, void* const* out, const int64_t* numels, const int32_t* dtypes,
                        F f) {
     GradTable t;
+    int64_t total = 0;
+    for (int i = 0; i < n; ++i) total += numels[i];
+    // a chunk for every block (1.5 million FP32 elements: norm and clip 6.9 -> 6.0
+    // us; chunks of 2048 take 7.7)
+    t.chunk = kChunkMost;
+    while (t.chunk > kChunkLeast && total < (int64_t)t.chunk * kNormBlocks) t.chunk /= 2;
     int64_t chunks = 0;
     t.n = 0;
     auto flush = [&]() {
@@ -178,7 +187,7 @@ cudaError_t for_tables(int n, const void* const* in, void* const* out, const int
     };
     for (int i = 0; i < n; ++i) {
         if (numels[i] == 0) continue;
-        const int64_t c = (numels[i] + kChunk - 1) / kChunk;
+        const int64_t c = (numels[i] + t.chunk - 1) / t.chunk;
         if (t.n == kListMax || chunks + c > (1 << 30)) {
             const cudaError_t e = flush();
             if (e != cudaSuccess) return e;
