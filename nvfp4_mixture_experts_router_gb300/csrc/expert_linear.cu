@@ -258,6 +258,12 @@ __global__ void __launch_bounds__(ExpertCfg<PRODUCT, TN, DEPTH>::kThreads, 1)
     tc_fence_after();
     const uint32_t tmem_base = *tmem_holder;
     const int total = s_end[p.E - 1];
+    // The tiles of wgrad are short (as deep as a segment has rows): its producer
+    // and MMA issuer work out the next tile's place while a stage of the current
+    // one is queued (64 ragged experts 77 -> 72 us; no gain for the others).
+    auto tile_or_none = [&](int tile) {
+        return tile < total ? expert_tile<TN, kWgrad>(p, tile, s_end, s_first, s_count) : ExpertTile{};
+    };
 
     if (warp == 0) {
         if (lane == 0) {
@@ -266,9 +272,12 @@ __global__ void __launch_bounds__(ExpertCfg<PRODUCT, TN, DEPTH>::kThreads, 1)
             const uint32_t landed_own = cluster_map(landed, rank);
             int stage = 0;
             uint32_t phase = 0;
+            ExpertTile next{};
+            if (kWgrad) next = tile_or_none(slot);
             for (int tile = slot; tile < total; tile += slots) {
-                const ExpertTile t = expert_tile<TN, kWgrad>(p, tile, s_end, s_first, s_count);
+                const ExpertTile t = kWgrad ? next : tile_or_none(tile);
                 const int depth = kWgrad ? t.count : p.depth;
+                if (kWgrad && depth == 0) next = tile_or_none(tile + slots);
                 const int m0 = t.m0 + (int)rank * p.half_m, n0 = t.n0 + (int)rank * (t.n / 2);
                 // forward, dgrad: a half of B with no row of the segment is
                 // left as it is (its columns of D are not stored)
@@ -308,6 +317,7 @@ __global__ void __launch_bounds__(ExpertCfg<PRODUCT, TN, DEPTH>::kThreads, 1)
                             tma_load_2d_pair(b_dst + c * (C::kTileB / 2), &tmB, bar, d + 64 * c, t.first + n0, pol);
                     }
                     if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
+                    if (kWgrad && d == 0) next = tile_or_none(tile + slots);
                 }
             }
         }
@@ -316,10 +326,15 @@ __global__ void __launch_bounds__(ExpertCfg<PRODUCT, TN, DEPTH>::kThreads, 1)
             constexpr uint32_t kMajor = (kAMn ? kIdescAMn : 0u) | (kWgrad ? kIdescBMn : 0u);
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
+            ExpertTile next{};
+            if (kWgrad) next = tile_or_none(slot);
             for (int tile = slot; tile < total; tile += slots) {
-                const ExpertTile t = expert_tile<TN, kWgrad>(p, tile, s_end, s_first, s_count);
+                const ExpertTile t = kWgrad ? next : tile_or_none(tile);
                 const int depth = kWgrad ? t.count : p.depth;
-                if (depth == 0) continue;
+                if (depth == 0) {
+                    next = tile_or_none(tile + slots);
+                    continue;
+                }
                 if (!mbar_wait<true>(&acc_empty[acc], acc_phase ^ 1u, abort, p.status, kStatusTimeoutMma)) goto done;
                 tc_fence_after();
                 const uint32_t idesc = idesc_bf16(256, t.n) | kMajor;
@@ -342,6 +357,7 @@ __global__ void __launch_bounds__(ExpertCfg<PRODUCT, TN, DEPTH>::kThreads, 1)
                     }
                     tc_commit_pair_mc(&empty[stage], 0x3);
                     if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
+                    if (kWgrad && d == 0) next = tile_or_none(tile + slots);
                 }
                 tc_commit_pair_mc(&acc_full[acc], 0x3);
                 acc ^= 1;
