@@ -534,21 +534,30 @@ cudaError_t launch_dispatch(const LaunchCtx& c, int T, int H, int K, int64_t row
 #undef MOE_DISPATCH
 }
 
-template <typename T_, int VEC>
-static cudaError_t combine_any(const LaunchCtx& c, int T, int H, int K, int64_t rows, const void* o,
-                               const int* row_of_route, const float* w, void* y, int64_t y_stride) {
+template <typename T_, int VEC, int V, int KB>
+static cudaError_t combine_shape(const LaunchCtx& c, int T, int H, int K, int64_t rows, const void* o,
+                                 const int* row_of_route, const float* w, void* y, int64_t y_stride) {
     using Raw = typename RowVec<T_, VEC>::Raw;
-    // 16-byte vectors: one a thread, eight rows in flight; narrower ones: four
-    // a thread, four rows in flight
-    constexpr int V = sizeof(Raw) == 16 ? 1 : 4, KB = sizeof(Raw) == 16 ? 8 : 4;
     const int n = H / VEC;
     const int lanes = lanes_for((n + V - 1) / V);
     const dim3 grid(token_blocks(T, lanes), (unsigned)((n + lanes * V - 1) / (lanes * V)));
-    if (w)
-        return c.launch(combine_kernel<T_, VEC, V, KB, true>, grid, dim3(kRowThreads), 0, T, n, K, rows,
-                        static_cast<const Raw*>(o), row_of_route, w, static_cast<Raw*>(y), y_stride / VEC, lanes);
-    return c.launch(combine_kernel<T_, VEC, V, KB, false>, grid, dim3(kRowThreads), 0, T, n, K, rows,
-                    static_cast<const Raw*>(o), row_of_route, w, static_cast<Raw*>(y), y_stride / VEC, lanes);
+    auto kernel = w ? combine_kernel<T_, VEC, V, KB, true> : combine_kernel<T_, VEC, V, KB, false>;
+    return c.launch(kernel, grid, dim3(kRowThreads), 0, T, n, K, rows, static_cast<const Raw*>(o), row_of_route, w,
+                    static_cast<Raw*>(y), y_stride / VEC, lanes);
+}
+
+// Loads in flight: of 16-byte vectors one of eight routes, or two of four
+// (11639 FP32 tokens, top-3, 1392: 59 -> 42 us; top-6 is faster with eight: 74
+// against 77); of narrower ones four of four.
+template <typename T_, int VEC>
+static cudaError_t combine_any(const LaunchCtx& c, int T, int H, int K, int64_t rows, const void* o,
+                               const int* row_of_route, const float* w, void* y, int64_t y_stride) {
+    if constexpr (sizeof(typename RowVec<T_, VEC>::Raw) == 16) {
+        return K <= 4 ? combine_shape<T_, VEC, 2, 4>(c, T, H, K, rows, o, row_of_route, w, y, y_stride)
+                      : combine_shape<T_, VEC, 1, 8>(c, T, H, K, rows, o, row_of_route, w, y, y_stride);
+    } else {
+        return combine_shape<T_, VEC, 4, 4>(c, T, H, K, rows, o, row_of_route, w, y, y_stride);
+    }
 }
 
 cudaError_t launch_combine(const LaunchCtx& c, int T, int H, int K, int64_t rows, int elem, const void* o,
@@ -557,23 +566,29 @@ cudaError_t launch_combine(const LaunchCtx& c, int T, int H, int K, int64_t rows
     MOE_ROW_VEC(elem, bytes, combine_any, c, T, H, K, rows, o, row_of_route, w, y, y_stride);
 }
 
+template <typename T_, int VEC, int V, int kK>
+static cudaError_t combine_backward_shape(const LaunchCtx& c, int T, int H, int K, int64_t rows, const void* dy,
+                                          int64_t dy_stride, const void* o, const int* row_of_route, const float* w,
+                                          const int* rows_used, void* d_o, float* dw) {
+    using Raw = typename RowVec<T_, VEC>::Raw;
+    const int n = H / VEC;
+    const int lanes = lanes_for((n + V - 1) / V);
+    return c.launch(combine_backward_kernel<T_, VEC, V, kK>, dim3(token_blocks(T, lanes)), dim3(kRowThreads), 0, T, n, K,
+                    rows, static_cast<const Raw*>(dy), dy_stride / VEC, static_cast<const Raw*>(o), row_of_route, w,
+                    rows_used, static_cast<Raw*>(d_o), dw, lanes);
+}
+
+// Routes at a time: eight, or four with few of them (11639 FP32 tokens, top-3,
+// 1392: 78 -> 72 us; two narrower vectors each: 1001 BF16, 27.9 -> 27.3).
 template <typename T_, int VEC>
 static cudaError_t combine_backward_any(const LaunchCtx& c, int T, int H, int K, int64_t rows, const void* dy,
                                         int64_t dy_stride, const void* o, const int* row_of_route, const float* w,
                                         const int* rows_used, void* d_o, float* dw) {
-    using Raw = typename RowVec<T_, VEC>::Raw;
-    const int n = H / VEC;
-    // eight loads of o in flight: a vector of eight routes, or two of four
-    if (K <= 4) {
-        const int lanes = lanes_for((n + 1) / 2);
-        return c.launch(combine_backward_kernel<T_, VEC, 2, 4>, dim3(token_blocks(T, lanes)), dim3(kRowThreads), 0, T, n,
-                        K, rows, static_cast<const Raw*>(dy), dy_stride / VEC, static_cast<const Raw*>(o), row_of_route,
-                        w, rows_used, static_cast<Raw*>(d_o), dw, lanes);
-    }
-    const int lanes = lanes_for(n);
-    return c.launch(combine_backward_kernel<T_, VEC, 1, 8>, dim3(token_blocks(T, lanes)), dim3(kRowThreads), 0, T, n, K,
-                    rows, static_cast<const Raw*>(dy), dy_stride / VEC, static_cast<const Raw*>(o), row_of_route, w,
-                    rows_used, static_cast<Raw*>(d_o), dw, lanes);
+    constexpr int V = sizeof(typename RowVec<T_, VEC>::Raw) == 16 ? 1 : 2;
+    return K <= 4 ? combine_backward_shape<T_, VEC, V, 4>(c, T, H, K, rows, dy, dy_stride, o, row_of_route, w, rows_used,
+                                                          d_o, dw)
+                  : combine_backward_shape<T_, VEC, 1, 8>(c, T, H, K, rows, dy, dy_stride, o, row_of_route, w, rows_used,
+                                                          d_o, dw);
 }
 
 cudaError_t launch_combine_backward(const LaunchCtx& c, int T, int H, int K, int64_t rows, int elem, const void* dy,
