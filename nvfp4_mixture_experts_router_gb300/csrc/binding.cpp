@@ -65,7 +65,7 @@ float* flat_f32(PyObject* o, const char* name, std::initializer_list<int64_t> sh
 uint32_t* word(PyObject* o, const char* name) {
     if (o == Py_None) return nullptr;
     const at::Tensor& t = tensor(o, name);
-    if (t.element_size() != 4 || t.is_floating_point() || t.numel() != 1)
+    if (t.element_size() != 4 || c10::isFloatingType(t.scalar_type()) || t.numel() != 1)
         wrong_value(std::string(name) + " must be one 32-bit integer");
     return static_cast<uint32_t*>(t.data_ptr());
 }
