@@ -33,6 +33,7 @@
 // leave the device.  Every wait is bounded (1 s); a timeout sets a status bit,
 // marks both CTAs aborted, and all roles drain to the final pair barrier.
 #include <cudaTypedefs.h>
+#include <math.h>
 
 #include "common.cuh"
 #include "host.h"
@@ -547,11 +548,18 @@ cudaError_t launch_rows(const LaunchCtx& c, int tn, int grid, const CUtensorMap&
 // GB300 (dgrad, 16 experts of 4096 x 7168; us at TN = 32, 64, 128, 256):
 //   4 rows 138 138 139 186;  16 rows 147 140 141 152;  32 rows 186 147 143 149;
 //   64 rows 316 195 151 150;  128 rows 542 300 194 161.
-int tile_rows(double mean) { return mean <= 8 ? 32 : mean <= 20 ? 64 : mean <= 80 ? 128 : 256; }
+// Half of that for as long as the tiles (`m_tiles` times those of the segments)
+// leave pairs idle: the time is then one tile's, whose stages follow TN.
+int tile_rows(double mean, int64_t busy, int m_tiles, int pairs) {
+    int tn = mean <= 8 ? 32 : mean <= 20 ? 64 : mean <= 80 ? 128 : 256;
+    while (tn > 32 && busy * m_tiles * (int64_t)ceil(mean / (tn / 2)) <= pairs) tn /= 2;
+    return tn;
+}
 
 // Rows per busy expert from which wgrad takes the deep stages.  Measured on GB300
 // (16 experts of 4096 x 7168; us shallow, deep): 4 rows 143 181;  128 rows 171
-// 189;  256 rows 240 239;  384 rows 330 317;  1024 rows 665 652.
+// 189;  256 rows 240 239;  384 rows 330 317;  1024 rows 665 652.  Also where the
+// tiles leave pairs idle.
 constexpr int kWgradDeepRows = 300;
 
 // D rows per CTA (forward with narrow tiles, where the weights' bytes bound the
@@ -563,11 +571,11 @@ constexpr int kWgradDeepRows = 300;
 // microsecond besides, the copies of kTileCost elements: 45 experts of 6520 x
 // 416 took 77 us in 32 rounds of 64 rows.
 constexpr int kTileCost = 22000;
-int tile_height(int m_extent, int depth, int64_t busy, int pairs) {
+int tile_height(int m_extent, int depth, int64_t row_tiles, int pairs) {
     int best = kHalfM;
     int64_t best_work = INT64_MAX;
     for (int h = kHalfM; h >= 64; h -= 8) {
-        const int64_t tiles = busy * ((m_extent + 2 * h - 1) / (2 * h));
+        const int64_t tiles = row_tiles * ((m_extent + 2 * h - 1) / (2 * h));
         const int64_t work = (tiles + pairs - 1) / pairs * ((int64_t)h * depth + kTileCost);
         if (work < best_work) {
             best = h;
@@ -612,9 +620,11 @@ cudaError_t launch_expert_linear(const LaunchCtx& c, int product, int device, co
         return cudaMemsetAsync(a.out, 0, (size_t)a.E * a.N * a.K * 2, c.stream);
     const cuuint64_t N = (cuuint64_t)a.N, K = (cuuint64_t)a.K, R = (cuuint64_t)a.rows;
     const int64_t busy = a.rows < a.E ? a.rows : a.E;
-    const int tn = product == kExpertWgrad ? 256 : tile_rows((double)a.rows / (double)busy);
-    const bool wgrad_deep = a.rows >= kWgradDeepRows * busy;
-    const int grid = g_expert_grid[device];
+    const double mean = (double)a.rows / (double)busy;
+    const int grid = g_expert_grid[device], pairs = grid / 2;
+    const int m_tiles = ((product == kExpertDgrad ? a.K : a.N) + 255) / 256;
+    const int tn = product == kExpertWgrad ? 256 : tile_rows(mean, busy, m_tiles, pairs);
+    const bool wgrad_deep = mean >= kWgradDeepRows || busy * m_tiles * ((a.K + 255) / 256) <= pairs;
     ExpertParams p{};
     p.half_m = kHalfM;
     CUtensorMap ta, tb, td;
@@ -630,7 +640,7 @@ cudaError_t launch_expert_linear(const LaunchCtx& c, int product, int device, co
     } else {
         const bool fwd = product == kExpertForward;
         const cuuint64_t dw[3] = {K, N, (cuuint64_t)a.E}, sw[2] = {K * 2, N * K * 2};
-        if (fwd && tn < 256) p.half_m = tile_height(a.N, a.K, busy, grid / 2);
+        if (fwd && tn < 256) p.half_m = tile_height(a.N, a.K, busy * (int64_t)ceil(mean / tn), pairs);
         // no more rows than there are: the copies of one token's rows are short
         p.box_n = (int)(a.rows < tn / 2 ? (a.rows + 7) / 8 * 8 : tn / 2);
         const cuuint32_t boxw[3] = {64, fwd ? (cuuint32_t)p.half_m : 128u, 1};

@@ -5,8 +5,8 @@
 //   out_ij = g_ij s,  s = min(1, max_norm / (norm + eps)), NaN if it is one
 //
 // The list travels as a kernel argument (pointers, sizes, types), a launch per
-// kListMax tensors: nothing is copied to the device beforehand, and a captured
-// graph replays it.  Tensors are cut into chunks of kChunkMost elements, or of
+// 960 tensors: nothing is copied to the device beforehand, and a captured graph
+// replays it.  Shorter lists take a smaller argument.  Tensors are cut into chunks of kChunkMost elements, or of
 // fewer where the whole list would not give every block one, that the blocks
 // take in turn.  HBM is the bound: one read for the norm, one read and
 // one write for the scaling.
@@ -18,7 +18,7 @@ namespace moe {
 namespace {
 
 constexpr int kClipThreads = 512;
-constexpr int kListMax = 96;
+constexpr int kListMax = 960;         // tensors of a launch: 30 KB of its 32 KB of arguments
 constexpr int kChunkMost = 16384;     // elements: a thread's kInFlight loads of BF16
 constexpr int kChunkLeast = 4096;
 constexpr int kInFlight = 4;          // 16-byte loads of a thread
@@ -31,11 +31,12 @@ struct GradEntry {
     int32_t last_chunk;   // one past this tensor's last chunk in the launch
     int32_t elem;         // bytes of an element
 };
+template <int MAX>
 struct GradTable {
     int n;
     int chunks;
     int chunk;            // elements of a chunk
-    GradEntry e[kListMax];
+    GradEntry e[MAX];
 };
 
 // A chunk [at, at + count) of a tensor as vectors of VEC, kInFlight of them
@@ -96,15 +97,31 @@ __device__ __forceinline__ void scale_part(const void* in, void* out, int64_t at
 }
 
 // First chunk of entry i.
-__device__ __forceinline__ int first_chunk(const GradTable& t, int i) { return i ? t.e[i - 1].last_chunk : 0; }
+template <int MAX>
+__device__ __forceinline__ int first_chunk(const GradTable<MAX>& t, int i) {
+    return i ? t.e[i - 1].last_chunk : 0;
+}
 
-__global__ void __launch_bounds__(kClipThreads) grad_square_kernel(const __grid_constant__ GradTable t, float* part) {
+// The entry of chunk c, which lies in entries lo..hi.
+template <int MAX>
+__device__ __forceinline__ int entry_of(const GradTable<MAX>& t, int c, int lo, int hi) {
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (c < t.e[mid].last_chunk) hi = mid;
+        else lo = mid + 1;
+    }
+    return lo;
+}
+
+template <int MAX>
+__global__ void __launch_bounds__(kClipThreads) grad_square_kernel(const __grid_constant__ GradTable<MAX> t,
+                                                                   float* part) {
     __shared__ float s_part[kClipThreads / 32];
     pdl_wait();
     float sum = 0.0f;
     int i = 0;
     for (int c = blockIdx.x; c < t.chunks; c += gridDim.x) {
-        while (c >= t.e[i].last_chunk) ++i;
+        if (c >= t.e[i].last_chunk) i = entry_of(t, c, i + 1, t.n - 1);
         const GradEntry& e = t.e[i];
         const int64_t at = (int64_t)(c - first_chunk(t, i)) * t.chunk;
         const int count = (int)min((int64_t)t.chunk, e.numel - at);
@@ -139,7 +156,8 @@ __global__ void __launch_bounds__(1024) grad_norm_kernel(int n, const float* par
     pdl_launch_dependents();
 }
 
-__global__ void __launch_bounds__(kClipThreads) grad_scale_kernel(const __grid_constant__ GradTable t,
+template <int MAX>
+__global__ void __launch_bounds__(kClipThreads) grad_scale_kernel(const __grid_constant__ GradTable<MAX> t,
                                                                   const float* norm, float max_norm, float eps) {
     pdl_wait();
     const float q = max_norm / (norm[0] + eps);
@@ -147,7 +165,7 @@ __global__ void __launch_bounds__(kClipThreads) grad_scale_kernel(const __grid_c
     // from the list's end: what the norm's pass has read last may still be in L2
     int i = t.n - 1;
     for (int c = t.chunks - 1 - (int)blockIdx.x; c >= 0; c -= gridDim.x) {
-        while (c < first_chunk(t, i)) --i;
+        if (c < first_chunk(t, i)) i = entry_of(t, c, 0, i - 1);
         const GradEntry& e = t.e[i];
         if (scale == 1.0f && e.in == e.out) continue;
         const int64_t at = (int64_t)(c - first_chunk(t, i)) * t.chunk;
@@ -163,12 +181,27 @@ __global__ void __launch_bounds__(kClipThreads) grad_scale_kernel(const __grid_c
     }
 }
 
-// Calls f(table) for every launch's share of the list: at most kListMax
-// tensors and 2^30 chunks; tensors without elements are left out.
-template <typename F>
-cudaError_t for_tables(int n, const void* const* in, void* const* out, const int64_t* numels, const int32_t* dtypes,
-                       F f) {
-    GradTable t;
+// Launches a kernel on a table without copying it on the way.
+template <typename... KArgs>
+cudaError_t launch_table(const LaunchCtx& c, void (*kernel)(KArgs...), int blocks, void** args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(kClipThreads);
+    cfg.stream = c.stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = c.pdl ? 1 : 0;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(kernel), args);
+}
+
+// Calls f(table) for every launch's share of the list: at most MAX tensors and
+// 2^30 chunks; tensors without elements are left out.
+template <int MAX, typename F>
+cudaError_t for_tables_of(int n, const void* const* in, void* const* out, const int64_t* numels, const int32_t* dtypes,
+                          F f) {
+    GradTable<MAX> t;
     int64_t total = 0;
     for (int i = 0; i < n; ++i) total += numels[i];
     // a chunk for every block (1.5 million FP32 elements: norm and clip 6.9 -> 6.0
@@ -188,7 +221,7 @@ cudaError_t for_tables(int n, const void* const* in, void* const* out, const int
     for (int i = 0; i < n; ++i) {
         if (numels[i] == 0) continue;
         const int64_t c = (numels[i] + t.chunk - 1) / t.chunk;
-        if (t.n == kListMax || chunks + c > (1 << 30)) {
+        if (t.n == MAX || chunks + c > (1 << 30)) {
             const cudaError_t e = flush();
             if (e != cudaSuccess) return e;
         }
@@ -197,6 +230,15 @@ cudaError_t for_tables(int n, const void* const* in, void* const* out, const int
                                dtypes[i] == MOE_DTYPE_F32 ? 4 : 2};
     }
     return flush();
+}
+
+// With the smallest table that holds the list.
+template <typename F>
+cudaError_t for_tables(int n, const void* const* in, void* const* out, const int64_t* numels, const int32_t* dtypes,
+                       F f) {
+    if (n <= 32) return for_tables_of<32>(n, in, out, numels, dtypes, f);
+    if (n <= 160) return for_tables_of<160>(n, in, out, numels, dtypes, f);
+    return for_tables_of<kListMax>(n, in, out, numels, dtypes, f);
 }
 
 }  // namespace
@@ -212,11 +254,12 @@ cudaError_t launch_grad_norm(const LaunchCtx& c, int sms, int n, const void* con
                              const int32_t* dtypes, float* norm, float* workspace) {
     (void)sms;
     int used = 0;
-    cudaError_t e = for_tables(n, grads, nullptr, numels, dtypes, [&](const GradTable& t) {
+    cudaError_t e = for_tables(n, grads, nullptr, numels, dtypes, [&](auto& t) {
         const int blocks = t.chunks < kNormBlocks ? t.chunks : kNormBlocks;
         float* part = workspace + used;
         used += blocks;
-        return c.launch(grad_square_kernel, dim3(blocks), dim3(kClipThreads), 0, t, part);
+        void* args[] = {&t, &part};
+        return launch_table(c, grad_square_kernel<sizeof(t.e) / sizeof(GradEntry)>, blocks, args);
     });
     if (e != cudaSuccess) return e;
     return c.launch(grad_norm_kernel, dim3(1), dim3(1024), 0, used, (const float*)workspace, norm);
@@ -225,9 +268,10 @@ cudaError_t launch_grad_norm(const LaunchCtx& c, int sms, int n, const void* con
 cudaError_t launch_grad_clip(const LaunchCtx& c, int sms, int n, const void* const* grads, void* const* out,
                              const int64_t* numels, const int32_t* dtypes, const float* norm, float max_norm,
                              float eps) {
-    return for_tables(n, grads, out, numels, dtypes, [&](const GradTable& t) {
+    return for_tables(n, grads, out, numels, dtypes, [&](auto& t) {
         const int blocks = t.chunks < 8 * sms ? t.chunks : 8 * sms;
-        return c.launch(grad_scale_kernel, dim3(blocks), dim3(kClipThreads), 0, t, norm, max_norm, eps);
+        void* args[] = {&t, &norm, &max_norm, &eps};
+        return launch_table(c, grad_scale_kernel<sizeof(t.e) / sizeof(GradEntry)>, blocks, args);
     });
 }
 

@@ -469,6 +469,16 @@ int lanes_for(int n) {
     return best;
 }
 
+// The same where a token's threads walk its whole row: with few tokens as many
+// threads as there are items (23 FP32 tokens of 2688, top-8: 19 -> 5 us).
+constexpr int kFewTokens = 608;
+int walk_lanes(int n, int T) {
+    if (T > kFewTokens) return lanes_for(n);
+    int lanes = 32;
+    while (lanes < kRowThreads && lanes < n) lanes *= 2;
+    return lanes;
+}
+
 }  // namespace
 
 size_t sort_workspace_bytes(int T, int E, int K) {
@@ -552,6 +562,8 @@ static cudaError_t combine_shape(const LaunchCtx& c, int T, int H, int K, int64_
 template <typename T_, int VEC>
 static cudaError_t combine_any(const LaunchCtx& c, int T, int H, int K, int64_t rows, const void* o,
                                const int* row_of_route, const float* w, void* y, int64_t y_stride) {
+    if (K == 1) return combine_shape<T_, VEC, 4, 1>(c, T, H, K, rows, o, row_of_route, w, y, y_stride);
+    if (K == 2) return combine_shape<T_, VEC, 4, 2>(c, T, H, K, rows, o, row_of_route, w, y, y_stride);
     if constexpr (sizeof(typename RowVec<T_, VEC>::Raw) == 16) {
         return K <= 4 ? combine_shape<T_, VEC, 2, 4>(c, T, H, K, rows, o, row_of_route, w, y, y_stride)
                       : combine_shape<T_, VEC, 1, 8>(c, T, H, K, rows, o, row_of_route, w, y, y_stride);
@@ -572,7 +584,7 @@ static cudaError_t combine_backward_shape(const LaunchCtx& c, int T, int H, int 
                                           const int* rows_used, void* d_o, float* dw) {
     using Raw = typename RowVec<T_, VEC>::Raw;
     const int n = H / VEC;
-    const int lanes = lanes_for((n + V - 1) / V);
+    const int lanes = walk_lanes((n + V - 1) / V, T);
     return c.launch(combine_backward_kernel<T_, VEC, V, kK>, dim3(token_blocks(T, lanes)), dim3(kRowThreads), 0, T, n, K,
                     rows, static_cast<const Raw*>(dy), dy_stride / VEC, static_cast<const Raw*>(o), row_of_route, w,
                     rows_used, static_cast<Raw*>(d_o), dw, lanes);
@@ -585,6 +597,12 @@ static cudaError_t combine_backward_any(const LaunchCtx& c, int T, int H, int K,
                                         int64_t dy_stride, const void* o, const int* row_of_route, const float* w,
                                         const int* rows_used, void* d_o, float* dw) {
     constexpr int V = sizeof(typename RowVec<T_, VEC>::Raw) == 16 ? 1 : 2;
+    if (K == 1)
+        return combine_backward_shape<T_, VEC, 4, 1>(c, T, H, K, rows, dy, dy_stride, o, row_of_route, w, rows_used, d_o,
+                                                     dw);
+    if (K == 2)
+        return combine_backward_shape<T_, VEC, 2, 2>(c, T, H, K, rows, dy, dy_stride, o, row_of_route, w, rows_used, d_o,
+                                                     dw);
     return K <= 4 ? combine_backward_shape<T_, VEC, V, 4>(c, T, H, K, rows, dy, dy_stride, o, row_of_route, w, rows_used,
                                                           d_o, dw)
                   : combine_backward_shape<T_, VEC, 1, 8>(c, T, H, K, rows, dy, dy_stride, o, row_of_route, w, rows_used,
