@@ -59,6 +59,7 @@ struct ExpertParams {
     unsigned int* status;  // may be null
     int half_m;            // D rows per CTA of a tile, up to kHalfM
     int box_n;             // forward, dgrad: B rows per copy
+    int stages;            // of the ring: what fits of half_m rows of A and TN / 2 of B
 };
 
 // DEPTH: reduction elements per stage.  Deep stages (64 KB a CTA at TN = 256)
@@ -78,7 +79,9 @@ struct ExpertCfg {
     static constexpr int kEpiWarps = TN >= 64 ? 8 : 4;
     static constexpr int kThreads = (4 + kEpiWarps) * 32;
     static constexpr uint32_t kTmemCols = 2 * TN;
-    static constexpr int kBars = 3 * kStages + 5;
+    // forward: more stages where the tiles are lower than kHalfM
+    static constexpr int kMaxStages = PRODUCT == kExpertForward ? 10 : kStages;
+    static constexpr int kBars = 3 * kMaxStages + 5;
     static constexpr int kOut = kWgrad ? kEpiWarps * kOutBytes : 0;
     static constexpr int kSmemBytes =
         1024 + kStages * (kTileA + kTileB) + kOut + 3 * kMaxExperts * 4 + kBars * 8 + 64;
@@ -96,10 +99,10 @@ __device__ __forceinline__ uint64_t sdesc_mnmajor_sw128(uint32_t saddr, uint32_t
 
 // Descriptor offset (16-byte units) of a stage's j-th 16 reduction elements:
 // 16 rows of 128 bytes further in every chunk (MN-major), or 32 bytes further
-// in the rows of the 64-element chunk j / 4 (K-major, TILE bytes in two chunks).
-template <bool MN, int TILE>
-__device__ __forceinline__ uint64_t operand_step(int j) {
-    return MN ? (uint64_t)j * 128 : (uint64_t)((j >> 2) * (TILE / 2 / 16) + (j & 3) * 2);
+// in the rows of the 64-element chunk j / 4 (K-major, `tile` bytes in two chunks).
+template <bool MN>
+__device__ __forceinline__ uint64_t operand_step(int j, int tile) {
+    return MN ? (uint64_t)j * 128 : (uint64_t)((j >> 2) * (tile / 2 / 16) + (j & 3) * 2);
 }
 
 // Place of 16-byte chunk c of row r in a store buffer of COLS columns: the 128-
@@ -181,12 +184,15 @@ __global__ void __launch_bounds__(ExpertCfg<PRODUCT, TN, DEPTH>::kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* s_a = base;
-    uint8_t* s_b = s_a + C::kStages * C::kTileA;
-    uint8_t* s_out = s_b + C::kStages * C::kTileB;
+    // bytes of a stage's A: its rows, in 128-byte chunks, or the full tile
+    const int a_tile = kAMn ? C::kTileA : p.half_m * DEPTH * 2;
+    const int stages = kAMn ? C::kStages : p.stages;
+    uint8_t* s_b = s_a + stages * a_tile;
+    uint8_t* s_out = s_a + C::kStages * (C::kTileA + C::kTileB);
     uint64_t* full = reinterpret_cast<uint64_t*>(s_out + C::kOut);                // rank 0: a stage of both CTAs
-    uint64_t* empty = full + C::kStages;                                          // both: the stage's MMAs are done
-    uint64_t* landed = empty + C::kStages;                                        // own copies of a stage to be cut
-    uint64_t* acc_full = landed + C::kStages;
+    uint64_t* empty = full + C::kMaxStages;                                       // both: the stage's MMAs are done
+    uint64_t* landed = empty + C::kMaxStages;                                     // own copies of a stage to be cut
+    uint64_t* acc_full = landed + C::kMaxStages;
     uint64_t* acc_empty = acc_full + 2;                                           // rank 0
     uint64_t* drain = acc_empty + 2;
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
@@ -200,7 +206,7 @@ __global__ void __launch_bounds__(ExpertCfg<PRODUCT, TN, DEPTH>::kThreads, 1)
     volatile int no_abort = 0;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < C::kStages; ++i) {
+        for (int i = 0; i < C::kMaxStages; ++i) {
             mbar_init(&full[i], 2);        // one arrival per CTA
             mbar_init(&empty[i], 1);
             mbar_init(&landed[i], 1);
@@ -287,7 +293,7 @@ __global__ void __launch_bounds__(ExpertCfg<PRODUCT, TN, DEPTH>::kThreads, 1)
                 for (int d = 0; d < depth; d += DEPTH) {
                     // completed by rank 0's commit: acquire at cluster scope
                     if (!mbar_wait<true>(&empty[stage], phase ^ 1u, abort, p.status, kStatusTimeoutProducer)) goto done;
-                    uint8_t* a_dst = s_a + stage * C::kTileA;
+                    uint8_t* a_dst = s_a + stage * a_tile;
                     uint8_t* b_dst = s_b + stage * C::kTileB;
                     // a stage to be cut: counted on this CTA's own barrier,
                     // and warp 3 announces it
@@ -307,7 +313,7 @@ __global__ void __launch_bounds__(ExpertCfg<PRODUCT, TN, DEPTH>::kThreads, 1)
                         }
                     } else {
                         for (int c = 0; c < chunks; ++c)
-                            tma_load_3d_pair(a_dst + c * (C::kTileA / 2), &tmA, bar, d + 64 * c, m0, t.e, pol);
+                            tma_load_3d_pair(a_dst + c * (a_tile / 2), &tmA, bar, d + 64 * c, m0, t.e, pol);
                     }
                     if (kWgrad) {
 #pragma unroll
@@ -317,7 +323,7 @@ __global__ void __launch_bounds__(ExpertCfg<PRODUCT, TN, DEPTH>::kThreads, 1)
                         for (int c = 0; c < chunks; ++c)
                             tma_load_2d_pair(b_dst + c * (C::kTileB / 2), &tmB, bar, d + 64 * c, t.first + n0, pol);
                     }
-                    if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
+                    if (++stage == stages) { stage = 0; phase ^= 1u; }
                     if (kWgrad && d == 0) next = tile_or_none(tile + slots);
                 }
             }
@@ -343,21 +349,21 @@ __global__ void __launch_bounds__(ExpertCfg<PRODUCT, TN, DEPTH>::kThreads, 1)
                 for (int d = 0; d < depth; d += DEPTH) {
                     if (!mbar_wait<true>(&full[stage], phase, abort, p.status, kStatusTimeoutMma)) goto done;
                     tc_fence_after();
-                    const uint32_t a_s = smem_u32(s_a + stage * C::kTileA), b_s = smem_u32(s_b + stage * C::kTileB);
+                    const uint32_t a_s = smem_u32(s_a + stage * a_tile), b_s = smem_u32(s_b + stage * C::kTileB);
                     const uint64_t adesc = kAMn ? sdesc_mnmajor_sw128(a_s, C::kChunkMn) : sdesc_kmajor_sw128(a_s);
                     const uint64_t bdesc = kWgrad ? sdesc_mnmajor_sw128(b_s, C::kChunkMn) : sdesc_kmajor_sw128(b_s);
                     if (depth - d >= DEPTH) {
 #pragma unroll
                         for (int j = 0; j < DEPTH / 16; ++j)
-                            tc_mma_bf16_pair(d_tmem, adesc + operand_step<kAMn, C::kTileA>(j),
-                                             bdesc + operand_step<kWgrad, C::kTileB>(j), idesc, (d | j) != 0);
+                            tc_mma_bf16_pair(d_tmem, adesc + operand_step<kAMn>(j, a_tile),
+                                             bdesc + operand_step<kWgrad>(j, C::kTileB), idesc, (d | j) != 0);
                     } else {
                         for (int j = 0; j < (depth - d + 15) / 16; ++j)
-                            tc_mma_bf16_pair(d_tmem, adesc + operand_step<kAMn, C::kTileA>(j),
-                                             bdesc + operand_step<kWgrad, C::kTileB>(j), idesc, (d | j) != 0);
+                            tc_mma_bf16_pair(d_tmem, adesc + operand_step<kAMn>(j, a_tile),
+                                             bdesc + operand_step<kWgrad>(j, C::kTileB), idesc, (d | j) != 0);
                     }
                     tc_commit_pair_mc(&empty[stage], 0x3);
-                    if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
+                    if (++stage == stages) { stage = 0; phase ^= 1u; }
                     if (kWgrad && d == 0) next = tile_or_none(tile + slots);
                 }
                 tc_commit_pair_mc(&acc_full[acc], 0x3);
@@ -522,7 +528,11 @@ int g_expert_grid[64] = {};
 
 template <int PRODUCT, int TN, int DEPTH>
 cudaError_t launch_tiles(const LaunchCtx& c, int grid, const CUtensorMap& a, const CUtensorMap& b,
-                         const CUtensorMap& d, const ExpertParams& p) {
+                         const CUtensorMap& d, ExpertParams p) {
+    // A's last chunk is read as 128 rows: what lies past its own is B's ring
+    using C = ExpertCfg<PRODUCT, TN, DEPTH>;
+    const int fit = C::kStages * (C::kTileA + C::kTileB) / (p.half_m * DEPTH * 2 + C::kTileB);
+    p.stages = fit < C::kMaxStages ? fit : C::kMaxStages;
     return c.launch(expert_linear_kernel<PRODUCT, TN, DEPTH>, dim3((unsigned)grid), dim3(ExpertCfg<PRODUCT, TN, DEPTH>::kThreads),
                     (size_t)ExpertCfg<PRODUCT, TN, DEPTH>::kSmemBytes, a, b, d, p);
 }
