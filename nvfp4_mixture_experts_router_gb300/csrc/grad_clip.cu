@@ -6,10 +6,11 @@
 //
 // The list travels as a kernel argument (pointers, sizes, types), a launch per
 // 960 tensors: nothing is copied to the device beforehand, and a captured graph
-// replays it.  Shorter lists take a smaller argument.  Tensors are cut into chunks of kChunkMost elements, or of
-// fewer where the whole list would not give every block one, that the blocks
-// take in turn.  HBM is the bound: one read for the norm, one read and
-// one write for the scaling.
+// replays it.  Shorter lists take a smaller argument.  Tensors are cut into
+// chunks of kChunkMost elements, or of fewer where the whole list would not
+// give every block one, that the blocks take in turn.  HBM is the bound: one
+// read for the norm, one read and one write for the scaling.  Measured on GB300
+// (302 million BF16 in 131 tensors): norm 95 us (6.4 TB/s), scaling 182 (6.6).
 #include "row_vec.cuh"
 #include "train_kernels.h"
 
