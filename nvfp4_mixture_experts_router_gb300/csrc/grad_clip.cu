@@ -7,10 +7,13 @@
 // The list travels as a kernel argument (pointers, sizes, types), a launch per
 // 960 tensors: nothing is copied to the device beforehand, and a captured graph
 // replays it.  Shorter lists take a smaller argument.  Tensors are cut into
-// chunks of kChunkMost elements, or of fewer where the whole list would not
-// give every block one, that the blocks take in turn.  HBM is the bound: one
-// read for the norm, one read and one write for the scaling.  Measured on GB300
-// (302 million BF16 in 131 tensors): norm 95 us (6.4 TB/s), scaling 182 (6.6).
+// chunks of kChunkMost elements, or of fewer where the whole list fits one round
+// of the blocks, that the blocks take in turn; the argument names the entry of
+// each block's first chunk, so that a short call does not wait for a search of
+// cold constants (249 tensors, 5 million BF16: norm and scaling 16.6 -> 7.8 us).
+// HBM is the bound: one read for the norm, one read and one write for the
+// scaling.  Measured on GB300 (302 million BF16 in 131 tensors): norm 93 us (6.5
+// TB/s), scaling 182 (6.6); 0.77 million FP32 in 19 tensors 3.3 and 2.3.
 #include "row_vec.cuh"
 #include "train_kernels.h"
 
@@ -22,6 +25,7 @@ constexpr int kClipThreads = 512;
 constexpr int kListMax = 960;         // tensors of a launch: 30 KB of its 32 KB of arguments
 constexpr int kChunkMost = 16384;     // elements: a thread's kInFlight loads of BF16
 constexpr int kChunkLeast = 4096;
+constexpr int kChunkStep = 2048;
 constexpr int kInFlight = 4;          // 16-byte loads of a thread
 constexpr int kNormBlocks = 608;      // partial sums per launch: four blocks an SM
 
@@ -34,9 +38,12 @@ struct GradEntry {
 };
 template <int MAX>
 struct GradTable {
+    static constexpr bool kStart = MAX > 32;
     int n;
     int chunks;
     int chunk;            // elements of a chunk
+    // entry of a block's first chunk (a short list is searched: five steps)
+    uint16_t start[kStart ? kNormBlocks : 1];
     GradEntry e[MAX];
 };
 
@@ -114,13 +121,20 @@ __device__ __forceinline__ int entry_of(const GradTable<MAX>& t, int c, int lo, 
     return lo;
 }
 
+// The entry of this block's first chunk c.
+template <int MAX>
+__device__ __forceinline__ int first_entry(const GradTable<MAX>& t, int c) {
+    if (GradTable<MAX>::kStart && blockIdx.x < kNormBlocks) return t.start[blockIdx.x];
+    return c < t.e[0].last_chunk ? 0 : entry_of(t, c, 1, t.n - 1);
+}
+
 template <int MAX>
 __global__ void __launch_bounds__(kClipThreads) grad_square_kernel(const __grid_constant__ GradTable<MAX> t,
                                                                    float* part) {
     __shared__ float s_part[kClipThreads / 32];
+    int i = first_entry(t, blockIdx.x);
     pdl_wait();
     float sum = 0.0f;
-    int i = 0;
     for (int c = blockIdx.x; c < t.chunks; c += gridDim.x) {
         if (c >= t.e[i].last_chunk) i = entry_of(t, c, i + 1, t.n - 1);
         const GradEntry& e = t.e[i];
@@ -160,11 +174,11 @@ __global__ void __launch_bounds__(1024) grad_norm_kernel(int n, const float* par
 template <int MAX>
 __global__ void __launch_bounds__(kClipThreads) grad_scale_kernel(const __grid_constant__ GradTable<MAX> t,
                                                                   const float* norm, float max_norm, float eps) {
+    // from the list's end: what the norm's pass has read last may still be in L2
+    int i = first_entry(t, t.chunks - 1 - (int)blockIdx.x);
     pdl_wait();
     const float q = max_norm / (norm[0] + eps);
     const float scale = q > 1.0f ? 1.0f : q;      // NaN stays NaN
-    // from the list's end: what the norm's pass has read last may still be in L2
-    int i = t.n - 1;
     for (int c = t.chunks - 1 - (int)blockIdx.x; c >= 0; c -= gridDim.x) {
         if (c < first_chunk(t, i)) i = entry_of(t, c, 0, i - 1);
         const GradEntry& e = t.e[i];
@@ -198,22 +212,33 @@ cudaError_t launch_table(const LaunchCtx& c, void (*kernel)(KArgs...), int block
 }
 
 // Calls f(table) for every launch's share of the list: at most MAX tensors and
-// 2^30 chunks; tensors without elements are left out.
+// 2^30 chunks; tensors without elements are left out.  `backward`: the blocks
+// take the chunks from the last one on.
 template <int MAX, typename F>
 cudaError_t for_tables_of(int n, const void* const* in, void* const* out, const int64_t* numels, const int32_t* dtypes,
-                          F f) {
+                          bool backward, F f) {
     GradTable<MAX> t;
     int64_t total = 0;
     for (int i = 0; i < n; ++i) total += numels[i];
-    // a chunk for every block (1.5 million FP32 elements: norm and clip 6.9 -> 6.0
-    // us; chunks of 2048 take 7.7)
-    t.chunk = kChunkMost;
-    while (t.chunk > kChunkLeast && total < (int64_t)t.chunk * kNormBlocks) t.chunk /= 2;
+    // a chunk for every block, in one round: total / chunk + n chunks at most
+    const int64_t share = total / (n < kNormBlocks / 2 ? kNormBlocks - n : kNormBlocks / 2);
+    // (0.77 million FP32 elements: chunks of 4096 6.0 us, of 16384 6.9, of 2048 7.7)
+    t.chunk = share >= kChunkMost    ? kChunkMost
+              : share <= kChunkLeast ? kChunkLeast
+                                     : (int)((share + kChunkStep) / kChunkStep * kChunkStep);
     int64_t chunks = 0;
     t.n = 0;
     auto flush = [&]() {
         if (t.n == 0) return cudaSuccess;
         t.chunks = (int)chunks;
+        if constexpr (GradTable<MAX>::kStart) {
+            const int blocks = chunks < kNormBlocks ? (int)chunks : kNormBlocks;
+            for (int b = 0, k = backward ? t.n - 1 : 0; b < blocks; ++b) {
+                while (backward && k > 0 && chunks - 1 - b < t.e[k - 1].last_chunk) --k;
+                while (!backward && b >= t.e[k].last_chunk) ++k;
+                t.start[b] = (uint16_t)k;
+            }
+        }
         const cudaError_t e = f(t);
         t.n = 0;
         chunks = 0;
@@ -236,10 +261,10 @@ cudaError_t for_tables_of(int n, const void* const* in, void* const* out, const 
 // With the smallest table that holds the list.
 template <typename F>
 cudaError_t for_tables(int n, const void* const* in, void* const* out, const int64_t* numels, const int32_t* dtypes,
-                       F f) {
-    if (n <= 32) return for_tables_of<32>(n, in, out, numels, dtypes, f);
-    if (n <= 160) return for_tables_of<160>(n, in, out, numels, dtypes, f);
-    return for_tables_of<kListMax>(n, in, out, numels, dtypes, f);
+                       bool backward, F f) {
+    if (n <= 32) return for_tables_of<32>(n, in, out, numels, dtypes, backward, f);
+    if (n <= 160) return for_tables_of<160>(n, in, out, numels, dtypes, backward, f);
+    return for_tables_of<kListMax>(n, in, out, numels, dtypes, backward, f);
 }
 
 }  // namespace
@@ -255,7 +280,7 @@ cudaError_t launch_grad_norm(const LaunchCtx& c, int sms, int n, const void* con
                              const int32_t* dtypes, float* norm, float* workspace) {
     (void)sms;
     int used = 0;
-    cudaError_t e = for_tables(n, grads, nullptr, numels, dtypes, [&](auto& t) {
+    cudaError_t e = for_tables(n, grads, nullptr, numels, dtypes, false, [&](auto& t) {
         const int blocks = t.chunks < kNormBlocks ? t.chunks : kNormBlocks;
         float* part = workspace + used;
         used += blocks;
@@ -269,7 +294,7 @@ cudaError_t launch_grad_norm(const LaunchCtx& c, int sms, int n, const void* con
 cudaError_t launch_grad_clip(const LaunchCtx& c, int sms, int n, const void* const* grads, void* const* out,
                              const int64_t* numels, const int32_t* dtypes, const float* norm, float max_norm,
                              float eps) {
-    return for_tables(n, grads, out, numels, dtypes, [&](auto& t) {
+    return for_tables(n, grads, out, numels, dtypes, true, [&](auto& t) {
         const int blocks = t.chunks < 8 * sms ? t.chunks : 8 * sms;
         void* args[] = {&t, &norm, &max_norm, &eps};
         return launch_table(c, grad_scale_kernel<sizeof(t.e) / sizeof(GradEntry)>, blocks, args);
