@@ -33,10 +33,15 @@
 // leave the device.  Every wait is bounded (1 s); a timeout sets a status bit,
 // marks both CTAs aborted, and all roles drain to the final pair barrier.
 //
+// Few tiles of a long depth (SPLIT): a cluster of two or four pairs per tile,
+// each pair with its part of the depth.  The parts' FP32 sums are left in their
+// CTAs' shared memory and every pair adds up and stores a share of the columns,
+// the parts in order: no workspace, no atomics, the same result each time.
+//
 // Bound by HBM while the experts have few rows, by the tensor cores under the
 // power limit with many.  Measured on GB300 (BF16, 6.8 TB/s copied, 1.7 PFLOP/s
 // sustained by cuBLAS): 8 rows of 8 experts of 4096 x 7168 forward 72-75 us
-// (6.3-6.5 TB/s); 2999 rows of 60 experts of 1536 x 2048 dgrad 67 (6.0 TB/s),
+// (6.3-6.5 TB/s); 2999 rows of 60 experts of 1536 x 2048 dgrad 65 (6.2 TB/s),
 // wgrad 72 (5.6 TB/s of gradients written); 16384 rows of 16 experts of
 // 4096 x 7168 forward 600-640 us, dgrad 575-625, wgrad 625-650 (1.5-1.65
 // PFLOP/s; equal segments on cuBLAS 510-545, 560-570, 550-570).
@@ -68,6 +73,7 @@ struct ExpertParams {
     int half_m;            // D rows per CTA of a tile, up to kHalfM
     int box_n;             // forward, dgrad: B rows per copy
     int stages;            // of the ring: what fits of half_m rows of A and TN / 2 of B
+    int split;             // pairs of a cluster that share a tile's depth: 1, 2 or 4
 };
 
 // DEPTH: reduction elements per stage.  Deep stages (64 KB a CTA at TN = 256)
@@ -83,14 +89,15 @@ struct ExpertCfg {
     static constexpr int kChunkMn = DEPTH * 128;                   // bytes of an MN-major chunk
     static constexpr int kStages = DEPTH == 64 ? 5 : TN == 256 ? 3 : TN == 128 ? 4 : 5;
     static constexpr int kOutCols = DEPTH == 64 ? 64 : 32;         // wgrad: columns a warp stores at a time
-    static constexpr int kOutBytes = 32 * kOutCols * 2;
+    static constexpr int kOutRows = TN == 64 ? 16 : 32;            // forward, dgrad: rows a warp stores at a time
+    static constexpr int kOutBytes = kWgrad ? 32 * kOutCols * 2 : kOutRows * 64;
     static constexpr int kEpiWarps = TN >= 64 ? 8 : 4;
     static constexpr int kThreads = (4 + kEpiWarps) * 32;
     static constexpr uint32_t kTmemCols = 2 * TN;
     // forward: more stages where the tiles are lower than kHalfM
     static constexpr int kMaxStages = PRODUCT == kExpertForward ? 10 : kStages;
     static constexpr int kBars = 3 * kMaxStages + 5;
-    static constexpr int kOut = kWgrad ? kEpiWarps * kOutBytes : 0;
+    static constexpr int kOut = kEpiWarps * kOutBytes;
     static constexpr int kSmemBytes =
         1024 + kStages * (kTileA + kTileB) + kOut + 3 * kMaxExperts * 4 + kBars * 8 + 64;
     static_assert(kSmemBytes <= 232448, "shared memory budget");
@@ -131,6 +138,15 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void*
 }
 __device__ __forceinline__ void tma_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void tma_store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t cluster_addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(cluster_addr)
+                 : "memory");
+    return v;
+}
 
 // Bits 15 / 16 of the instruction descriptor: A / B is MN-major.
 constexpr uint32_t kIdescAMn = 1u << 15, kIdescBMn = 1u << 16;
@@ -182,7 +198,8 @@ __device__ __forceinline__ ExpertTile expert_tile(const ExpertParams& p, int til
     return t;
 }
 
-template <int PRODUCT, int TN, int DEPTH>
+// SPLIT: a cluster of p.split pairs per tile, the depth divided.
+template <int PRODUCT, int TN, int DEPTH, bool SPLIT>
 __global__ void __launch_bounds__(ExpertCfg<PRODUCT, TN, DEPTH>::kThreads, 1)
     expert_linear_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                          const __grid_constant__ CUtensorMap tmC, const ExpertParams p) {
@@ -209,8 +226,10 @@ __global__ void __launch_bounds__(ExpertCfg<PRODUCT, TN, DEPTH>::kThreads, 1)
     int* s_first = s_end + kMaxExperts;
     int* s_count = s_first + kMaxExperts;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_cta_rank();
-    const int slot = blockIdx.x >> 1, slots = gridDim.x >> 1;
+    const uint32_t cta = cluster_cta_rank();
+    const uint32_t rank = SPLIT ? cta & 1 : cta, leader = SPLIT ? cta & ~1u : 0;   // rank: in the pair
+    const int slot = SPLIT ? blockIdx.x / (2 * p.split) : blockIdx.x >> 1;
+    const int slots = SPLIT ? gridDim.x / (2 * p.split) : gridDim.x >> 1;
     volatile int no_abort = 0;
 
     if (threadIdx.x == 0) {
@@ -272,7 +291,21 @@ __global__ void __launch_bounds__(ExpertCfg<PRODUCT, TN, DEPTH>::kThreads, 1)
     cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_holder;
-    const int total = s_end[p.E - 1];
+    // a cluster that splits the depth has one tile at most (its ring holds the
+    // sums then): the grid has room for every tile of counts that add up to rows
+    const int total = SPLIT ? min(s_end[p.E - 1], slots) : s_end[p.E - 1];
+    if (SPLIT && total < s_end[p.E - 1] && p.status && blockIdx.x == 0 && threadIdx.x == 0)
+        atomicOr(p.status, kStatusBadRow);
+    // this pair's part of a tile's depth, in whole stages
+    auto part_of = [&](int depth, int& d0, int& d1) {
+        d0 = 0;
+        d1 = depth;
+        if (SPLIT) {
+            const int blocks = (depth + DEPTH - 1) / DEPTH, part = (int)cta >> 1;
+            d0 = min(depth, blocks * part / p.split * DEPTH);
+            d1 = min(depth, blocks * (part + 1) / p.split * DEPTH);
+        }
+    };
     // The tiles of wgrad are short (as deep as a segment has rows): its producer
     // and MMA issuer work out the next tile's place while a stage of the current
     // one is queued (64 ragged experts 77 -> 72 us; no gain for the others).
@@ -280,11 +313,55 @@ __global__ void __launch_bounds__(ExpertCfg<PRODUCT, TN, DEPTH>::kThreads, 1)
         return tile < total ? expert_tile<TN, kWgrad>(p, tile, s_end, s_first, s_count) : ExpertTile{};
     };
 
+    // the epilogue warps' parts of a tile
+    const int q = warp & 3;                            // tensor-memory lane quadrant
+    constexpr int kGroups = C::kEpiWarps / 4;
+    constexpr int kCols = TN / kGroups;                // accumulator columns per warp
+    const int group = (warp - 4) >> 2, col0 = group * kCols;
+    auto row_of = [&](const ExpertTile& t) { return t.m0 + (int)rank * p.half_m + q * 32; };   // the warp's first D row
+    auto limit_of = [&](const ExpertTile& t) {         // columns that exist
+        return min(t.n, (kWgrad ? p.n_extent : t.count) - t.n0);
+    };
+    // wgrad: lane = row of dw[e], columns contiguous: kOutCols of them at a time
+    // through shared memory, so that whole sectors or lines leave; the map's
+    // extents cut what lies past N or K
+    auto put_wgrad = [&](const ExpertTile& t, int c, int mw, auto fetch) {
+        uint8_t* out = s_out + (warp - 4) * C::kOutBytes;
+#pragma unroll
+        for (int h = 0; h < C::kOutCols; h += 32) {
+            float v[32];
+            fetch(c + h, v);
+            if (h == 0) {
+                if (lane == 0) tma_store_wait_read();  // the buffer's last store has read it
+                __syncwarp();
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float w[8] = {v[8 * j],     v[8 * j + 1], v[8 * j + 2], v[8 * j + 3],
+                                    v[8 * j + 4], v[8 * j + 5], v[8 * j + 6], v[8 * j + 7]};
+                *reinterpret_cast<uint4*>(out + out_chunk<C::kOutCols>(lane, h / 8 + j)) = pack_bf16x8(w);
+            }
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) tma_store_3d(&tmC, out, t.n0 + c, mw, t.e);
+    };
+    // forward, dgrad: lane = output column, accumulator column = row of the segment
+    auto put_rows = [&](const ExpertTile& t, int c, int mw, int limit, bool m_there, const auto& v) {
+        constexpr int kCount = sizeof(v) / sizeof(float);
+        __nv_bfloat16* o = p.out + (size_t)(t.first + t.n0 + c) * p.m_extent + mw + lane;
+        if (m_there) {
+#pragma unroll
+            for (int j = 0; j < kCount; ++j)
+                if (c + j < limit) o[(size_t)j * p.m_extent] = __float2bfloat16_rn(v[j]);
+        }
+    };
+
     if (warp == 0) {
         if (lane == 0) {
             const uint64_t pol = policy_evict_normal();
-            const uint32_t full0 = cluster_map(full, 0);
-            const uint32_t landed_own = cluster_map(landed, rank);
+            const uint32_t full0 = cluster_map(full, leader);
+            const uint32_t landed_own = cluster_map(landed, cta);
             int stage = 0;
             uint32_t phase = 0;
             ExpertTile next{};
@@ -292,13 +369,19 @@ __global__ void __launch_bounds__(ExpertCfg<PRODUCT, TN, DEPTH>::kThreads, 1)
             for (int tile = slot; tile < total; tile += slots) {
                 const ExpertTile t = kWgrad ? next : tile_or_none(tile);
                 const int depth = kWgrad ? t.count : p.depth;
-                if (kWgrad && depth == 0) next = tile_or_none(tile + slots);
+                int d0, d1;
+                part_of(depth, d0, d1);
+                if (kWgrad && d0 >= d1) next = tile_or_none(tile + slots);
                 const int m0 = t.m0 + (int)rank * p.half_m, n0 = t.n0 + (int)rank * (t.n / 2);
                 // forward, dgrad: a half of B with no row of the segment is
                 // left as it is (its columns of D are not stored)
                 const bool b1 = kWgrad || t.n0 + t.n / 2 < t.count;
                 const bool b_mine = rank == 0 || b1;
-                for (int d = 0; d < depth; d += DEPTH) {
+                // MN-major chunks that hold an m (or n) of the tile; the others are left too
+                const int a_pair = min(2 * (kHalfM / 64), (p.m_extent - t.m0 + 63) / 64);
+                const int a_mine = max(0, min(kHalfM / 64, a_pair - (int)rank * (kHalfM / 64)));
+                const int b_chunks = (t.n / 2 + 63) / 64;
+                for (int d = d0; d < d1; d += DEPTH) {
                     // completed by rank 0's commit: acquire at cluster scope
                     if (!mbar_wait<true>(&empty[stage], phase ^ 1u, abort, p.status, kStatusTimeoutProducer)) goto done;
                     uint8_t* a_dst = s_a + stage * a_tile;
@@ -307,15 +390,16 @@ __global__ void __launch_bounds__(ExpertCfg<PRODUCT, TN, DEPTH>::kThreads, 1)
                     // and warp 3 announces it
                     const bool cut = kWgrad && depth - d < DEPTH && (depth & 15) != 0;
                     const int chunks = depth - d > 64 ? 2 : 1;             // of K-major rows
-                    const uint32_t a_bytes = kAMn ? C::kTileA : (uint32_t)(chunks * p.half_m * 128);
-                    const uint32_t b_bytes = kWgrad ? C::kTileB : (uint32_t)(chunks * p.box_n * 128);
+                    const uint32_t a_both = kAMn ? a_pair * C::kChunkMn : 2 * chunks * p.half_m * 128;
+                    const uint32_t b_bytes = kWgrad ? b_chunks * C::kChunkMn : chunks * p.box_n * 128;
                     const uint32_t bar = (cut ? landed_own : full0) + (uint32_t)stage * 8u;
-                    if (cut) mbar_arrive_expect_tx(&landed[stage], a_bytes + b_bytes);
-                    else if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2u * a_bytes + (b1 ? 2u : 1u) * b_bytes);
+                    if (cut) mbar_arrive_expect_tx(&landed[stage], a_mine * C::kChunkMn + b_bytes);
+                    else if (rank == 0) mbar_arrive_expect_tx(&full[stage], a_both + (b1 ? 2u : 1u) * b_bytes);
                     else mbar_arrive_cluster(full0 + (uint32_t)stage * 8u);
                     if (kAMn) {
 #pragma unroll
                         for (int j = 0; j < kHalfM / 64; ++j) {
+                            if (j >= a_mine) break;
                             if (kWgrad) tma_load_2d_pair(a_dst + j * C::kChunkMn, &tmA, bar, m0 + 64 * j, t.first + d, pol);
                             else tma_load_3d_pair(a_dst + j * C::kChunkMn, &tmA, bar, m0 + 64 * j, d, t.e, pol);
                         }
@@ -326,13 +410,13 @@ __global__ void __launch_bounds__(ExpertCfg<PRODUCT, TN, DEPTH>::kThreads, 1)
                     if (kWgrad) {
 #pragma unroll
                         for (int j = 0; j < C::kHalfN / 64; ++j)
-                            tma_load_2d_pair(b_dst + j * C::kChunkMn, &tmB, bar, n0 + 64 * j, t.first + d, pol);
+                            if (j < b_chunks) tma_load_2d_pair(b_dst + j * C::kChunkMn, &tmB, bar, n0 + 64 * j, t.first + d, pol);
                     } else if (b_mine) {
                         for (int c = 0; c < chunks; ++c)
                             tma_load_2d_pair(b_dst + c * (C::kTileB / 2), &tmB, bar, d + 64 * c, t.first + n0, pol);
                     }
                     if (++stage == stages) { stage = 0; phase ^= 1u; }
-                    if (kWgrad && d == 0) next = tile_or_none(tile + slots);
+                    if (kWgrad && d == d0) next = tile_or_none(tile + slots);
                 }
             }
         }
@@ -346,15 +430,17 @@ __global__ void __launch_bounds__(ExpertCfg<PRODUCT, TN, DEPTH>::kThreads, 1)
             for (int tile = slot; tile < total; tile += slots) {
                 const ExpertTile t = kWgrad ? next : tile_or_none(tile);
                 const int depth = kWgrad ? t.count : p.depth;
-                if (depth == 0) {
-                    next = tile_or_none(tile + slots);
+                int d0, d1;
+                part_of(depth, d0, d1);
+                if (d0 >= d1) {
+                    if (kWgrad) next = tile_or_none(tile + slots);
                     continue;
                 }
                 if (!mbar_wait<true>(&acc_empty[acc], acc_phase ^ 1u, abort, p.status, kStatusTimeoutMma)) goto done;
                 tc_fence_after();
                 const uint32_t idesc = idesc_bf16(256, t.n) | kMajor;
                 const uint32_t d_tmem = tmem_base + (uint32_t)acc * TN;
-                for (int d = 0; d < depth; d += DEPTH) {
+                for (int d = d0; d < d1; d += DEPTH) {
                     if (!mbar_wait<true>(&full[stage], phase, abort, p.status, kStatusTimeoutMma)) goto done;
                     tc_fence_after();
                     const uint32_t a_s = smem_u32(s_a + stage * a_tile), b_s = smem_u32(s_b + stage * C::kTileB);
@@ -364,17 +450,17 @@ __global__ void __launch_bounds__(ExpertCfg<PRODUCT, TN, DEPTH>::kThreads, 1)
 #pragma unroll
                         for (int j = 0; j < DEPTH / 16; ++j)
                             tc_mma_bf16_pair(d_tmem, adesc + operand_step<kAMn>(j, a_tile),
-                                             bdesc + operand_step<kWgrad>(j, C::kTileB), idesc, (d | j) != 0);
+                                             bdesc + operand_step<kWgrad>(j, C::kTileB), idesc, ((d - d0) | j) != 0);
                     } else {
                         for (int j = 0; j < (depth - d + 15) / 16; ++j)
                             tc_mma_bf16_pair(d_tmem, adesc + operand_step<kAMn>(j, a_tile),
-                                             bdesc + operand_step<kWgrad>(j, C::kTileB), idesc, (d | j) != 0);
+                                             bdesc + operand_step<kWgrad>(j, C::kTileB), idesc, ((d - d0) | j) != 0);
                     }
-                    tc_commit_pair_mc(&empty[stage], 0x3);
+                    tc_commit_pair_mc(&empty[stage], (uint16_t)(0x3 << leader));
                     if (++stage == stages) { stage = 0; phase ^= 1u; }
-                    if (kWgrad && d == 0) next = tile_or_none(tile + slots);
+                    if (kWgrad && d == d0) next = tile_or_none(tile + slots);
                 }
-                tc_commit_pair_mc(&acc_full[acc], 0x3);
+                tc_commit_pair_mc(&acc_full[acc], (uint16_t)(0x3 << leader));
                 acc ^= 1;
                 if (acc == 0) acc_phase ^= 1u;
             }
@@ -383,19 +469,21 @@ __global__ void __launch_bounds__(ExpertCfg<PRODUCT, TN, DEPTH>::kThreads, 1)
         if (kWgrad) {
             // the ragged ends: zeros from the segment's end to the end of its
             // last 16-row step, in this CTA's halves of both operands
-            const uint32_t full0 = cluster_map(full, 0);
+            const uint32_t full0 = cluster_map(full, leader);
             int stage = 0;
             uint32_t phases = 0;           // bit s: parity of landed[s]
             for (int tile = slot; tile < total; tile += slots) {
                 const ExpertTile t = expert_tile<TN, kWgrad>(p, tile, s_end, s_first, s_count);
-                const int blocks = (t.count + DEPTH - 1) / DEPTH;
-                if ((t.count & 15) != 0) {
+                int d0, d1;
+                part_of(t.count, d0, d1);
+                const int blocks = (d1 - d0 + DEPTH - 1) / DEPTH;
+                if ((t.count & 15) != 0 && d1 == t.count && d0 < d1) {
                     const int s = (stage + blocks - 1) % C::kStages;
                     if (!__all_sync(0xffffffffu, mbar_wait(&landed[s], (phases >> s) & 1u, abort, p.status,
                                                            kStatusTimeoutProducer)))
                         goto done;
                     phases ^= 1u << s;
-                    const int r0 = t.count - (blocks - 1) * DEPTH, r1 = (r0 + 15) / 16 * 16;
+                    const int r0 = t.count - d0 - (blocks - 1) * DEPTH, r1 = (r0 + 15) / 16 * 16;
                     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
                     // a row of a chunk is 128 bytes (the swizzle permutes within it)
                     for (int r = r0 + (lane >> 3); r < r1; r += 4) {
@@ -417,17 +505,15 @@ __global__ void __launch_bounds__(ExpertCfg<PRODUCT, TN, DEPTH>::kThreads, 1)
             }
         }
     } else if (warp >= 4) {
-        const int q = warp & 3;                            // tensor-memory lane quadrant
-        constexpr int kCols = TN / (C::kEpiWarps / 4);     // accumulator columns per warp
-        const int col0 = ((warp - 4) >> 2) * kCols;
-        const uint32_t release0 = cluster_map(acc_empty, 0);
+        const uint32_t release0 = cluster_map(acc_empty, leader);
         int acc = 0;
         uint32_t acc_phase = 0;
         for (int tile = slot; tile < total; tile += slots) {
             const ExpertTile t = expert_tile<TN, kWgrad>(p, tile, s_end, s_first, s_count);
-            const int mw = t.m0 + (int)rank * p.half_m + q * 32;     // the warp's first D row
-            const bool m_there = q * 32 + lane < p.half_m && mw + lane < p.m_extent;
-            const bool nothing = kWgrad && t.count == 0;   // no rows: zeros, no accumulator
+            int d0, d1;
+            part_of(kWgrad ? t.count : p.depth, d0, d1);
+            const int mw = row_of(t), limit = limit_of(t);
+            const bool nothing = (kWgrad || SPLIT) && d0 >= d1;      // zeros, no accumulator
             if (!nothing) {
                 // warp-uniform outcome: tcgen05.ld below is a warp-collective instruction
                 if (!__all_sync(0xffffffffu, mbar_wait<true>(&acc_full[acc], acc_phase, abort, p.status,
@@ -435,56 +521,61 @@ __global__ void __launch_bounds__(ExpertCfg<PRODUCT, TN, DEPTH>::kThreads, 1)
                     break;
                 tc_fence_after();
             }
-            const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)acc * TN + (uint32_t)col0;
-            const int limit = min(t.n, (kWgrad ? p.n_extent : t.count) - t.n0);   // columns that exist
-            if (kWgrad) {
-                // lane = row of dw[e], columns contiguous: kOutCols of them at a
-                // time through shared memory, so that whole sectors or lines
-                // leave; the map's extents cut what lies past N or K
-                uint8_t* out = s_out + (warp - 4) * C::kOutBytes;
+            const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)acc * TN;
+            auto fetch = [&](int col, float (&v)[32]) {
+                if (nothing) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+                } else {
+                    tmem_ld32(taddr + (uint32_t)col, v);
+                    tmem_ld_wait();
+                }
+            };
+            if constexpr (SPLIT) {
+                // the sums of this part, [column / 4][row][4], over the ring: its
+                // last stage has been read
+                for (int c = col0; c < col0 + kCols && c < t.n; c += 32) {
+                    float v[32];
+                    fetch(c, v);
+                    float4* sums = reinterpret_cast<float4*>(s_a) + c / 4 * kHalfM + q * 32 + lane;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        sums[j * kHalfM] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                }
+            } else if constexpr (kWgrad) {
 #pragma unroll 1
                 for (int c = 0; c < kCols; c += C::kOutCols) {
                     if (col0 + c >= limit || mw >= p.m_extent) break;      // warp-uniform
-#pragma unroll
-                    for (int h = 0; h < C::kOutCols; h += 32) {
-                        float v[32];
-                        if (nothing) {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) v[j] = 0.0f;
-                        } else {
-                            tmem_ld32(taddr + c + h, v);
-                            tmem_ld_wait();
-                        }
-                        if (h == 0) {
-                            if (lane == 0) tma_store_wait_read();          // the buffer's last store has read it
-                            __syncwarp();
-                        }
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float w[8] = {v[8 * j],     v[8 * j + 1], v[8 * j + 2], v[8 * j + 3],
-                                                v[8 * j + 4], v[8 * j + 5], v[8 * j + 6], v[8 * j + 7]};
-                            *reinterpret_cast<uint4*>(out + out_chunk<C::kOutCols>(lane, h / 8 + j)) = pack_bf16x8(w);
-                        }
-                    }
-                    fence_proxy_async();
-                    __syncwarp();
-                    if (lane == 0) tma_store_3d(&tmC, out, t.n0 + col0 + c, mw, t.e);
+                    put_wgrad(t, col0 + c, mw, fetch);
                 }
             } else {
 #pragma unroll 1
                 for (int c = 0; c < kCols; c += 32) {
                     if (col0 + c >= limit) break;          // warp-uniform
                     float v[32];
-                    tmem_ld32(taddr + c, v);
+                    tmem_ld32(taddr + (uint32_t)(col0 + c), v);
                     tmem_ld_wait();
-                    // lane = output column, accumulator column = row of the segment
-                    __nv_bfloat16* o = p.out + (size_t)(t.first + t.n0 + col0 + c) * p.m_extent + mw + lane;
-                    if (m_there) {
+                    // lane = output column, accumulator column = row of the segment:
+                    // 32 columns of a row side by side, and 16 bytes of it a lane
+                    // (8729 rows of 4152 x 640: 42.6 -> 39.3 us; 2047 of 760 x 96: 10.7 -> 7.9)
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (col0 + c + j < limit) o[(size_t)j * p.m_extent] = __float2bfloat16_rn(v[j]);
+                    for (int h = 0; h < 32; h += C::kOutRows) {
+                        uint8_t* out = s_out + (warp - 4) * C::kOutBytes;
+#pragma unroll
+                        for (int j = 0; j < C::kOutRows; ++j)
+                            *reinterpret_cast<__nv_bfloat16*>(out + j * 64 + lane * 2) = __float2bfloat16_rn(v[h + j]);
+                        __syncwarp();
+                        const int at = (lane & 3) * 8;
+                        const bool there = q * 32 + at < p.half_m && mw + at < p.m_extent;
+#pragma unroll
+                        for (int i = 0; i < C::kOutRows; i += 8) {
+                            const int n = col0 + c + h + i + (lane >> 2);
+                            if (there && n < limit)
+                                *reinterpret_cast<uint4*>(p.out + (size_t)(t.first + t.n0 + n) * p.m_extent + mw + at) =
+                                    *reinterpret_cast<const uint4*>(out + (i + (lane >> 2)) * 64 + at * 2);
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
                 }
             }
             if (!nothing) {
@@ -504,16 +595,58 @@ done:
     if (*abort) {
         // tell the other CTA, let in-flight copies land and retire every
         // issued MMA before the memories go away
-        st_cluster_u32(cluster_map((const void*)abort, rank ^ 1u), 1u);
+        st_cluster_u32(cluster_map((const void*)abort, cta ^ 1u), 1u);
         if (warp == 1 && lane == 0 && rank == 0) {
             tc_commit_pair(drain);
             mbar_wait(drain, 0, &no_abort, p.status, kStatusTimeoutMma);
         }
         for (int i = 0; i < 100; ++i) __nanosleep(10000);
     }
+    if constexpr (SPLIT) {
+        // all parts' sums lie in their CTAs' shared memory: each pair adds up and
+        // stores its share of the columns, the parts in order
+        __syncthreads();
+        cluster_sync_all();
+        if (warp >= 4 && slot < total) {
+            const ExpertTile t = expert_tile<TN, kWgrad>(p, slot, s_end, s_first, s_count);
+            auto fetch = [&](int col, auto& v) {
+                constexpr int kCount = sizeof(v) / sizeof(float);
+#pragma unroll
+                for (int j = 0; j < kCount; ++j) v[j] = 0.0f;
+#pragma unroll
+                for (uint32_t s = 0; s < 4; ++s)
+                    if (s < (uint32_t)p.split) {
+                        const uint32_t from = cluster_map(s_a, 2 * s + rank) + (uint32_t)(col / 4 * kHalfM + q * 32 + lane) * 16u;
+#pragma unroll
+                        for (int j = 0; j < kCount / 4; ++j) {
+                            const float4 w = ld_cluster_f32x4(from + (uint32_t)(j * kHalfM * 16));
+                            v[4 * j] += w.x;
+                            v[4 * j + 1] += w.y;
+                            v[4 * j + 2] += w.z;
+                            v[4 * j + 3] += w.w;
+                        }
+                    }
+            };
+            constexpr int kUnit = kWgrad ? C::kOutCols : 8;
+            const int mw = row_of(t), limit = limit_of(t);
+            const bool m_there = q * 32 + lane < p.half_m && mw + lane < p.m_extent;
+            const int unit0 = ((int)cta >> 1) * kGroups + group;
+#pragma unroll 1
+            for (int c = unit0 * kUnit; c < limit; c += p.split * kGroups * kUnit) {
+                if constexpr (kWgrad) {
+                    if (mw < p.m_extent) put_wgrad(t, c, mw, fetch);
+                } else {
+                    float v[kUnit];
+                    fetch(c, v);
+                    put_rows(t, c, mw, limit, m_there, v);
+                }
+            }
+            if (kWgrad && lane == 0) tma_store_wait();
+        }
+    }
     tc_fence_before();
     __syncthreads();
-    // neither CTA frees tensor memory or leaves before both are done
+    // no CTA frees tensor memory or leaves before all are done
     cluster_sync_all();
     pdl_launch_dependents();
     if (warp == 1) {
@@ -533,6 +666,7 @@ bool encode_bf16_map(CUtensorMap* map, const void* base, int rank, const cuuint6
 }
 
 int g_expert_grid[64] = {};
+int g_expert_clusters[64][3] = {};     // clusters of 1, 2 and 4 pairs that run at a time
 
 template <int PRODUCT, int TN, int DEPTH>
 cudaError_t launch_tiles(const LaunchCtx& c, int grid, const CUtensorMap& a, const CUtensorMap& b,
@@ -541,14 +675,24 @@ cudaError_t launch_tiles(const LaunchCtx& c, int grid, const CUtensorMap& a, con
     using C = ExpertCfg<PRODUCT, TN, DEPTH>;
     const int fit = C::kStages * (C::kTileA + C::kTileB) / (p.half_m * DEPTH * 2 + C::kTileB);
     p.stages = fit < C::kMaxStages ? fit : C::kMaxStages;
-    return c.launch(expert_linear_kernel<PRODUCT, TN, DEPTH>, dim3((unsigned)grid), dim3(ExpertCfg<PRODUCT, TN, DEPTH>::kThreads),
-                    (size_t)ExpertCfg<PRODUCT, TN, DEPTH>::kSmemBytes, a, b, d, p);
+    // the shallow wgrad is not split: the deep one has the few tiles
+    const auto kernel = p.split > 1 ? expert_linear_kernel<PRODUCT, TN, DEPTH, DEPTH == 128>
+                                    : expert_linear_kernel<PRODUCT, TN, DEPTH, false>;
+    return c.launch(kernel, dim3((unsigned)grid), dim3(C::kThreads), (size_t)C::kSmemBytes, a, b, d, p);
 }
 
-template <int PRODUCT, int TN, int DEPTH>
+template <int PRODUCT, int TN, int DEPTH, bool SPLIT>
 cudaError_t set_tiles() {
-    return cudaFuncSetAttribute(expert_linear_kernel<PRODUCT, TN, DEPTH>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                ExpertCfg<PRODUCT, TN, DEPTH>::kSmemBytes);
+    return cudaFuncSetAttribute(expert_linear_kernel<PRODUCT, TN, DEPTH, SPLIT>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, ExpertCfg<PRODUCT, TN, DEPTH>::kSmemBytes);
+}
+template <int PRODUCT, bool SPLIT>
+cudaError_t set_rows() {
+    cudaError_t e;
+    if ((e = set_tiles<PRODUCT, 32, 128, SPLIT>()) || (e = set_tiles<PRODUCT, 64, 128, SPLIT>()) ||
+        (e = set_tiles<PRODUCT, 128, 128, SPLIT>()) || (e = set_tiles<PRODUCT, 256, 128, SPLIT>()))
+        return e;
+    return cudaSuccess;
 }
 
 template <int PRODUCT>
@@ -566,12 +710,46 @@ cudaError_t launch_rows(const LaunchCtx& c, int tn, int grid, const CUtensorMap&
 // GB300 (dgrad, 16 experts of 4096 x 7168; us at TN = 32, 64, 128, 256):
 //   4 rows 138 138 139 186;  16 rows 147 140 141 152;  32 rows 186 147 143 149;
 //   64 rows 316 195 151 150;  128 rows 542 300 194 161.
-// Half of that for as long as the tiles (`m_tiles` times those of the segments)
-// leave pairs idle: the time is then one tile's, whose stages follow TN.
-int tile_rows(double mean, int64_t busy, int m_tiles, int pairs) {
-    int tn = mean <= 8 ? 32 : mean <= 20 ? 64 : mean <= 80 ? 128 : 256;
-    while (tn > 32 && busy * m_tiles * (int64_t)ceil(mean / (tn / 2)) <= pairs) tn /= 2;
-    return tn;
+// Where the tiles leave pairs idle see Split.
+int tile_rows(double mean) { return mean <= 8 ? 32 : mean <= 20 ? 64 : mean <= 80 ? 128 : 256; }
+
+// Few tiles: their rows, and the pairs that share a tile's depth (1: none do).
+struct Split {
+    int tn, pairs;
+};
+
+// While the tiles leave pairs idle the time is one tile's: 5 us and then 0.44 us
+// a stage of 128 (0.6 at 256 rows).  Lower tiles, and a cluster of two or four
+// pairs for each, the depth divided, take what pairs there are; the join costs
+// 1.5 us and more for the sums that cross the cluster.  The least of the times
+// by these measured figures.  Measured on GB300 (us for 1, 2 and 4 pairs):
+//   forward 64 rows of 1024 x 7168: 29.9 19.0 12.8;  2 x 291 rows of 120 x 3680:
+//   17.8 13.3 11.0;  34 rows of 88 x 688: 7.4 7.7 7.1;  dgrad 64 rows of 7168 x
+//   1024: 28.8 18.4 12.3;  wgrad 16384 rows of 256 x 256: 73 43 28;  2 x 912 rows
+//   of 176 x 168: 11.1 11.3 12.0.
+Split split_of(bool wgrad, int tn, int n_extent, double mean, int64_t rows, int64_t busy, int E, int m_tiles, int depth,
+               const int* clusters) {
+    Split best{tn, 1};
+    double best_us = 1e30;
+    const double stages = ceil(depth / 128.0);
+    for (int i = 0; i < 3; ++i)
+        for (int t = tn; t >= (wgrad ? 256 : 32); t /= 2) {
+            // a split tile has a cluster of its own: as many as there can be
+            const int64_t tiles = m_tiles * (wgrad ? E * (int64_t)((n_extent + 255) / 256)
+                                             : i   ? busy + (rows - busy) / t
+                                                   : busy * (int64_t)ceil(mean / t));
+            if (tiles > clusters[i]) continue;
+            const int width = wgrad && n_extent < 256 ? n_extent : t;
+            double us = 0.44 + (width > 64 ? 0.0009 * (width - 64) : 0.0);
+            if (t == 32 && i == 0 && tiles > clusters[0] / 2) us += 0.02;      // more copies of the weights at a time
+            us *= ceil(stages / (1 << i));
+            if (i) us += 1.4 + (wgrad ? 0.0045 * (1 << i) : 0.007) * width;
+            if (us < best_us || (us == best_us && i == 0)) {
+                best = Split{t, 1 << i};
+                best_us = us;
+            }
+        }
+    return best;
 }
 
 // Rows per busy expert from which wgrad takes the deep stages.  Measured on GB300
@@ -607,28 +785,33 @@ int tile_height(int m_extent, int depth, int64_t row_tiles, int pairs) {
 
 cudaError_t setup_expert_linear_kernels(int device, int num_sms) {
     cudaError_t e;
-    if ((e = set_tiles<kExpertForward, 32, 128>()) || (e = set_tiles<kExpertForward, 64, 128>()) ||
-        (e = set_tiles<kExpertForward, 128, 128>()) || (e = set_tiles<kExpertForward, 256, 128>()) ||
-        (e = set_tiles<kExpertDgrad, 32, 128>()) || (e = set_tiles<kExpertDgrad, 64, 128>()) ||
-        (e = set_tiles<kExpertDgrad, 128, 128>()) || (e = set_tiles<kExpertDgrad, 256, 128>()) ||
-        (e = set_tiles<kExpertWgrad, 256, 128>()) || (e = set_tiles<kExpertWgrad, 256, 64>()))
+    if ((e = set_rows<kExpertForward, false>()) || (e = set_rows<kExpertForward, true>()) ||
+        (e = set_rows<kExpertDgrad, false>()) || (e = set_rows<kExpertDgrad, true>()) ||
+        (e = set_tiles<kExpertWgrad, 256, 128, false>()) || (e = set_tiles<kExpertWgrad, 256, 128, true>()) ||
+        (e = set_tiles<kExpertWgrad, 256, 64, false>()))
         return e;
     // persistent grid: as many CTA pairs as can be resident at once
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(num_sms / 2 * 2));
-    cfg.blockDim = dim3(ExpertCfg<kExpertForward, 64, 128>::kThreads);
-    cfg.dynamicSmemBytes = ExpertCfg<kExpertForward, 64, 128>::kSmemBytes;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int clusters = 0;
-    if ((e = cudaOccupancyMaxActiveClusters(&clusters, expert_linear_kernel<kExpertForward, 64, 128>, &cfg))) return e;
-    if (clusters < 1) return cudaErrorInvalidConfiguration;
-    if (device >= 0 && device < 64) g_expert_grid[device] = 2 * (clusters < num_sms / 2 ? clusters : num_sms / 2);
+    if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
+    for (int i = 0; i < 3; ++i) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(num_sms / (2 << i) * (2 << i)));
+        cfg.blockDim = dim3(ExpertCfg<kExpertForward, 64, 128>::kThreads);
+        cfg.dynamicSmemBytes = ExpertCfg<kExpertForward, 64, 128>::kSmemBytes;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2 << i;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int clusters = 0;
+        if ((e = cudaOccupancyMaxActiveClusters(
+                 &clusters, i ? expert_linear_kernel<kExpertForward, 64, 128, true>
+                              : expert_linear_kernel<kExpertForward, 64, 128, false>, &cfg))) return e;
+        g_expert_clusters[device][i] = clusters < num_sms / (2 << i) ? clusters : num_sms / (2 << i);
+    }
+    if (g_expert_clusters[device][0] < 1) return cudaErrorInvalidConfiguration;
+    g_expert_grid[device] = 2 * g_expert_clusters[device][0];
     return cudaSuccess;
 }
 
@@ -639,9 +822,12 @@ cudaError_t launch_expert_linear(const LaunchCtx& c, int product, int device, co
     const cuuint64_t N = (cuuint64_t)a.N, K = (cuuint64_t)a.K, R = (cuuint64_t)a.rows;
     const int64_t busy = a.rows < a.E ? a.rows : a.E;
     const double mean = (double)a.rows / (double)busy;
-    const int grid = g_expert_grid[device], pairs = grid / 2;
+    const int pairs = g_expert_grid[device] / 2;
     const int m_tiles = ((product == kExpertDgrad ? a.K : a.N) + 255) / 256;
-    const int tn = product == kExpertWgrad ? 256 : tile_rows(mean, busy, m_tiles, pairs);
+    const bool is_wgrad = product == kExpertWgrad;
+    const Split sp = split_of(is_wgrad, is_wgrad ? 256 : tile_rows(mean), a.K, mean, a.rows, busy, a.E, m_tiles,
+                              is_wgrad ? (int)ceil(mean) : product == kExpertDgrad ? a.N : a.K, g_expert_clusters[device]);
+    const int tn = sp.tn;
     const bool wgrad_deep = mean >= kWgradDeepRows || busy * m_tiles * ((a.K + 255) / 256) <= pairs;
     ExpertParams p{};
     p.half_m = kHalfM;
@@ -658,7 +844,8 @@ cudaError_t launch_expert_linear(const LaunchCtx& c, int product, int device, co
     } else {
         const bool fwd = product == kExpertForward;
         const cuuint64_t dw[3] = {K, N, (cuuint64_t)a.E}, sw[2] = {K * 2, N * K * 2};
-        if (fwd && tn < 256) p.half_m = tile_height(a.N, a.K, busy * (int64_t)ceil(mean / tn), pairs);
+        if (fwd && sp.pairs > 1) p.half_m = (a.N + 16 * m_tiles - 1) / (16 * m_tiles) * 8;
+        else if (fwd && tn < 256) p.half_m = tile_height(a.N, a.K, busy * (int64_t)ceil(mean / tn), pairs);
         // no more rows than there are: the copies of one token's rows are short
         p.box_n = (int)(a.rows < tn / 2 ? (a.rows + 7) / 8 * 8 : tn / 2);
         const cuuint32_t boxw[3] = {64, fwd ? (cuuint32_t)p.half_m : 128u, 1};
@@ -676,8 +863,13 @@ cudaError_t launch_expert_linear(const LaunchCtx& c, int product, int device, co
     p.offsets = a.offsets;
     p.out = static_cast<__nv_bfloat16*>(a.out);
     p.status = a.status;
+    p.split = sp.pairs;
     LaunchCtx cc = c;
-    cc.cluster = 2;
+    cc.cluster = 2 * sp.pairs;
+    // a split tile has a cluster of its own
+    const int64_t tiles = (int64_t)((p.m_extent + 2 * p.half_m - 1) / (2 * p.half_m)) *
+                          (is_wgrad ? a.E * (int64_t)((a.K + 255) / 256) : busy + (a.rows - busy) / tn);
+    const int grid = sp.pairs > 1 ? (int)(2 * sp.pairs * tiles) : g_expert_grid[device];
     if (product == kExpertForward) return launch_rows<kExpertForward>(cc, tn, grid, ta, tb, p);
     if (product == kExpertDgrad) return launch_rows<kExpertDgrad>(cc, tn, grid, ta, tb, p);
     return wgrad_deep ? launch_tiles<kExpertWgrad, 256, 128>(cc, grid, ta, tb, td, p)

@@ -90,6 +90,31 @@ def test_products_larger(counts, N, K):
     run_all(counts, N, K, seed=3)
 
 
+# depths that the pairs of a cluster divide: whole and ragged stages, parts
+# without a stage, odd heights, ragged ends of the summed rows, empty experts
+@pytest.mark.parametrize("counts,N,K", [
+    ([64], 1024, 2048), ([3], 128, 4096), ([290, 0, 291], 120, 3680), ([1], 8, 2056), ([70], 2056, 8),
+    ([5003], 256, 256), ([0, 1, 2047], 64, 72), ([4096, 3], 136, 264), ([640], 40, 1160), ([33], 7168, 136),
+    ([600, 601], 1032, 120), ([129, 0, 0, 1, 300], 256, 1000), ([2000], 264, 24), ([17], 520, 520), ([8191], 72, 8)])
+def test_few_tiles_share_the_depth(counts, N, K):
+    first = run_all(counts, N, K, seed=5)
+    again = run_all(counts, N, K, seed=5)
+    for x, y in zip(first[5:], again[5:]):
+        assert torch.equal(x, y)
+    run_all(counts, N, K, gaps=5, seed=6)
+
+
+def test_segments_of_more_rows_than_there_are():
+    """Overlapping segments are not allowed; here they end with an error or as written twice."""
+    x, w = torch.randn(64, 2048, device="cuda").bfloat16(), torch.randn(6, 64, 2048, device="cuda").bfloat16()
+    i32 = dict(dtype=torch.int32, device="cuda")
+    count, offsets = torch.full((6,), 64, **i32), torch.zeros(6, **i32)
+    y = torch.zeros(64, 64, dtype=x.dtype, device="cuda")
+    status = torch.zeros(64, dtype=torch.int32, device="cuda")
+    api.moe_nvfp4_expert_linear(x, w, count, offsets, y, status[:1])
+    assert api.moe_nvfp4_last_device_status(status) in (0, api.MOE_ERR_INVALID_ARG)
+
+
 def test_a_neighbours_nan_stays_its_own():
     x, dy, w, count, offsets, y, dx, dw = run_all([30, 40, 50], 128, 192, poison=False)
     keep = (y.clone(), dx.clone(), dw.clone())
