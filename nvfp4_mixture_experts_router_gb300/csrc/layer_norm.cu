@@ -15,15 +15,17 @@
 // each thread keeps the dgamma / dbeta sums of its columns in registers until
 // the end, so that dy and x are read once for both gradients; the blocks' sums
 // go through the workspace to a reduction in a fixed order.  Rows of up to 1024
-// columns, or that start off 16-byte boundaries, go through registers (row
-// kernels), the others through a ring of bulk copies in shared memory (ring
-// kernels).  Longer rows are walked three times (forward) or twice (dx), the
-// re-reads served by the caches, and the column sums are a pass of their own.
+// columns and calls of few rows go through registers (row kernels), the others
+// through a ring of bulk copies in shared memory (ring kernels).  Longer rows
+// are walked three times (forward) or twice (dx), the re-reads served by the
+// caches, and the column sums are a pass of their own.
 //
 // Measured on GB300 (BF16, 8191 rows; copy rate 6.8 TB/s): 7168 columns
-// forward 46 us (5.1 TB/s), backward 67 (5.3); 256 columns 4.0 and 6.5; 1001
-// (single elements) 21 and 21; 2000 rows of 16384 75 and 129.  FP32, 7168:
-// forward 72 (6.5 TB/s), backward 107 (6.6).  One row of 7168 BF16: 3.1.
+// forward 46 us (5.1 TB/s), backward 67 (5.3); 7167 (rows off 16-byte blocks,
+// single elements in and out of the ring) 72 and 123, in registers 202 and 222;
+// 256 columns 4.0 and 6.5; 1001 13.6 and 21; 2000 rows of 16384 75 and 129.
+// FP32, 7168: forward 72 (6.5 TB/s), backward 107 (6.6); 7167 99 and 118.  One
+// row of 7168 BF16: 3.1.
 #include "row_vec.cuh"
 #include "train_kernels.h"
 
@@ -37,7 +39,10 @@ constexpr int kNormSms = 152;       // the persistent backward kernels' grids ar
 constexpr int kCols = 8;            // columns per thread of the row kernels
 constexpr int kRowColumns = 32 * 32 * kCols;
 constexpr int kRingCols = 16;       // columns per thread of the ring kernel
-constexpr int kRingMin = 1024;      // columns
+// Columns of a row from which the ring kernels take it; rows off 16-byte
+// boundaries go there earlier (forward, 8191 rows of 1001 BF16: 21.9 -> 13.6 us,
+// of 601 14.8 -> 12.7, of 300 7.2 against 8.3; backward 21 against 25)
+constexpr int kRingMin = 1024, kRingMinOdd = 512;
 constexpr int kRingMax = 4;         // stages in flight in shared memory (at most)
 constexpr int kRingBytes = 200 * 1024;
 
@@ -229,7 +234,52 @@ __global__ void __launch_bounds__(MAXT) norm_rows_kernel(int T, int H, int W, co
     pdl_launch_dependents();
 }
 
-// The same for many rows of more than kRingMin columns in 16-byte vectors:
+// A row of the rings below in shared memory.  Rows of whole 16-byte vectors are
+// one bulk copy.  Other rows keep their place within 16 bytes: a copy of the
+// whole 16-byte blocks inside the row, and the elements before and after it (a
+// lane of half a warp each) through a register, stored a turn later, before that
+// turn's barrier: a turn ahead of their use at least, as S >= 2.
+template <typename T_, bool WHOLE>
+struct RingRow {
+    static constexpr uint32_t kElem = sizeof(T_);
+    using One = typename RowVec<T_, 1>::Raw;
+    static __host__ __device__ uint32_t slot(uint32_t bytes) { return WHOLE ? bytes : (bytes + 31) & ~15u; }
+    static __device__ __forceinline__ uint32_t offset(const void* row) {
+        return WHOLE ? 0u : (uint32_t)reinterpret_cast<uintptr_t>(row) & 15u;
+    }
+    // [lead, lead + copied(...)) of the row lies in whole blocks
+    static __device__ __forceinline__ uint32_t lead(const void* row) {
+        return WHOLE ? 0u : (16u - offset(row)) & 15u;
+    }
+    static __device__ __forceinline__ uint32_t copied(const void* row, uint32_t bytes) {
+        return WHOLE ? bytes : (bytes - lead(row)) & ~15u;
+    }
+    static __device__ __forceinline__ void copy(uint8_t* slot, const void* row, uint32_t bytes, uint64_t* bar,
+                                                uint64_t policy) {
+        const uint32_t l = lead(row);
+        bulk_load(slot + offset(row) + l, static_cast<const uint8_t*>(row) + l, copied(row, bytes), bar, policy);
+    }
+    One value;
+    uint8_t* to = nullptr;
+    // lane k of sixteen: an element before the copy (k < 8) or after it
+    __device__ __forceinline__ void load(uint8_t* slot, const void* row, uint32_t bytes, int k) {
+        const uint32_t l = lead(row);
+        const uint32_t at = k < 8 ? k * kElem : l + copied(row, bytes) + (k - 8) * kElem;
+        if (at < (k < 8 ? l : bytes)) {
+            value = *reinterpret_cast<const One*>(static_cast<const uint8_t*>(row) + at);
+            to = slot + offset(row) + at;
+        }
+    }
+    __device__ __forceinline__ void store() {
+        if (to) {
+            *reinterpret_cast<One*>(to) = value;
+            to = nullptr;
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // a later copy may write here
+        }
+    }
+};
+
+// The same for many rows of more than kRingMin columns:
 // persistent blocks of up to 512 threads, two an SM where their shared memory
 // allows, with gamma and beta in shared memory and the rows ahead in a ring of
 // bulk copies, so that a row's two reductions overlap the copies of the next
@@ -242,6 +292,8 @@ __global__ void __launch_bounds__(512, 2)
                      int64_t y_stride, float* mean_out, float* rstd_out, bool wide_params) {
     using Raw = typename RowVec<T_, VEC>::Raw;
     constexpr int C = kRingCols, V = C / VEC, P = C / 2;
+    constexpr bool kWhole = sizeof(Raw) == 16;
+    using Row = RingRow<T_, kWhole>;
     __shared__ float s_red[2][16];
     __shared__ uint64_t s_full[kRingMax];
     extern __shared__ __align__(16) uint8_t s_ring[];      // gamma, beta [P][threads] float2 each, then [S][n] vectors
@@ -250,14 +302,16 @@ __global__ void __launch_bounds__(512, 2)
     const int n = H / VEC;
     float2* s_gamma = reinterpret_cast<float2*>(s_ring);
     float2* s_beta = s_gamma + P * lanes;
-    Raw* s_rows = reinterpret_cast<Raw*>(s_ring + (size_t)lanes * C * 8);
-    const uint32_t row_bytes = (uint32_t)n * 16u;
+    uint8_t* s_rows = s_ring + (size_t)lanes * C * 8;
+    const uint32_t row_bytes = (uint32_t)n * (uint32_t)sizeof(Raw), slot = Row::slot(row_bytes);
     const int64_t step = gridDim.x, first = blockIdx.x;
     uint64_t policy = 0;
     auto fetch = [&](int64_t t, int stage) {               // thread 0
-        mbar_arrive_expect_tx(&s_full[stage], row_bytes);
-        bulk_load(s_rows + (size_t)stage * n, x + t * x_stride, row_bytes, &s_full[stage], policy);
+        const Raw* row = x + t * x_stride;
+        mbar_arrive_expect_tx(&s_full[stage], Row::copied(row, row_bytes));
+        Row::copy(s_rows + stage * slot, row, row_bytes, &s_full[stage], policy);
     };
+    Row edge;
     if (j == 0) {
         policy = policy_evict_first();                     // x is read once
         for (int q = 0; q < S; ++q) mbar_init(&s_full[q], 1);
@@ -265,6 +319,12 @@ __global__ void __launch_bounds__(512, 2)
         for (int q = 0; q < S; ++q)
             if (first + q * step < T) fetch(first + q * step, q);
     }
+    if (!kWhole && j < 16)
+        for (int q = 0; q < S; ++q)
+            if (first + q * step < T) {
+                edge.load(s_rows + q * slot, x + (first + q * step) * x_stride, row_bytes, j);
+                edge.store();
+            }
     {
         float2 p[P];
         load_params<VEC, C>(gamma, j, lanes, n, wide_params, p);
@@ -287,7 +347,7 @@ __global__ void __launch_bounds__(512, 2)
         const bool landed = mbar_wait(&s_full[stage], parity, &never, nullptr, 0);
         float2 v[P];
         {
-            const Raw* at = s_rows + (size_t)stage * n + j;
+            const Raw* at = reinterpret_cast<const Raw*>(s_rows + stage * slot + Row::offset(x + t * x_stride)) + j;
             Raw r[V];
 #pragma unroll
             for (int i = 0; i < V; ++i) r[i] = j + i * lanes < n ? at[i * lanes] : Raw{};
@@ -298,17 +358,22 @@ __global__ void __launch_bounds__(512, 2)
         for (int q = 1; q < P; ++q) sum = add2(sum, v[q]);
         const float a = warp_sum(sum.x + sum.y);
         if (lane == 0) s_red[0][warp] = a;
+        if (!kWhole) edge.store();
         if (__syncthreads_or(!landed)) {
             for (int i = 0; i < 100; ++i) __nanosleep(10000);   // copies in flight land before the block leaves
             break;
         }
-        if (j == 0 && t + S * step < T) fetch(t + S * step, stage);
+        if (t + S * step < T) {
+            if (j == 0) fetch(t + S * step, stage);
+            if (!kWhole && j < 16) edge.load(s_rows + stage * slot, x + (t + S * step) * x_stride, row_bytes, j);
+        }
         const float mean = warp_sum(lane < W ? s_red[0][lane & 15] : 0.0f) * inv;
         float2 sq = both(0.0f);
 #pragma unroll
         for (int q = 0; q < P; ++q) {
             v[q] = add2(v[q], both(-mean));
-            // columns past the row's end do not count (VEC is even: a pair is of one vector)
+            // columns past the row's end do not count (a pair is of one vector, or of two of one element)
+            if (VEC == 1 && j + (2 * q + 1) * lanes >= n) v[q].y = 0.0f;
             if (j + 2 * q / VEC * lanes < n) sq = fma2(v[q], v[q], sq);
         }
         const float b = warp_sum(sq.x + sq.y);
@@ -337,22 +402,22 @@ struct NormRow {
     float mean, rstd;
 };
 
-// D rows in flight beyond the current one, in registers.  Bound by the loads in
-// flight and, a row, the two reductions' latency.  Blocks of more than 256 threads
-// (64 registers a thread) keep gamma in shared memory.  FULL: the threads'
-// columns are the row's, no guards.  Columns past the row's end have dy = 0
-// and so add nothing to any sum.
-template <typename T_, int VEC, int MAXT, int D, bool FULL>
-__global__ void __launch_bounds__(MAXT)
+// Rows of up to kRingMin columns: four warps a row at most, two rows or more a
+// block, and kAhead of each group's rows in flight beyond the current one, in
+// registers.  Bound by the loads in flight and, a row, the two reductions'
+// latency.  FULL: the threads' columns are the row's, no guards.  Columns past
+// the row's end have dy = 0 and so add nothing to any sum.
+constexpr int kAhead = 2;
+template <typename T_, int VEC, bool FULL>
+__global__ void __launch_bounds__(kNormThreads)
     norm_rows_backward_kernel(int T, int H, int W, const typename RowVec<T_, VEC>::Raw* dy, int64_t dy_stride,
                               const typename RowVec<T_, VEC>::Raw* x, int64_t x_stride, const float* gamma,
                               const float* mean, const float* rstd, typename RowVec<T_, VEC>::Raw* dx,
                               int64_t dx_stride, float* part, bool wide_params) {
     using Raw = typename RowVec<T_, VEC>::Raw;
-    constexpr int V = kCols / VEC;
-    constexpr bool kHeld = MAXT <= 256;
+    constexpr int V = kCols / VEC, D = kAhead;
     __shared__ float2 s_red[2][32];
-    extern __shared__ float2 s_dyn[];        // G > 1: [G][2][W * 128] sums; else gamma [4][MAXT]
+    extern __shared__ float2 s_dyn[];        // [G][2][W * 128] sums
     pdl_wait();
     const int lanes = W * 32, j = threadIdx.x % lanes, G = blockDim.x / lanes, g = threadIdx.x / lanes;
     const int n = H / VEC;
@@ -360,10 +425,7 @@ __global__ void __launch_bounds__(MAXT)
     float2 ga[kPairs], dg[kPairs], db[kPairs];
     load_params<VEC, kCols>(gamma, j, lanes, n, wide_params, ga);
 #pragma unroll
-    for (int q = 0; q < kPairs; ++q) {
-        dg[q] = db[q] = both(0.0f);
-        if (!kHeld) s_dyn[q * MAXT + threadIdx.x] = ga[q];           // read by this thread alone
-    }
+    for (int q = 0; q < kPairs; ++q) dg[q] = db[q] = both(0.0f);
     const int64_t first = (int64_t)blockIdx.x * G + g;
     dy += first * dy_stride + j;
     x += first * x_stride + j;
@@ -395,7 +457,7 @@ __global__ void __launch_bounds__(MAXT)
 #pragma unroll
         for (int u = 0; u < D; ++u) {
             const int64_t t = tb + u * step;
-            if (D > 1 && t - g >= T) break;
+            if (t - g >= T) break;
             const float2 m = both(-ahead[u].mean), r = both(ahead[u].rstd);
             float2 d[kPairs], hat[kPairs];
             unpack_cols<T_, VEC, kCols>(ahead[u].dy, d);
@@ -407,7 +469,7 @@ __global__ void __launch_bounds__(MAXT)
                 hat[q] = mul2(add2(hat[q], m), r);
                 dg[q] = fma2(d[q], hat[q], dg[q]);
                 db[q] = add2(db[q], d[q]);
-                d[q] = mul2(d[q], kHeld ? ga[q] : s_dyn[q * MAXT + threadIdx.x]);
+                d[q] = mul2(d[q], ga[q]);
                 sg = add2(sg, d[q]);
                 sgx = fma2(d[q], hat[q], sgx);
             }
@@ -427,49 +489,28 @@ __global__ void __launch_bounds__(MAXT)
     // this block's sums: its rows' groups in order.  Column of pair q's first
     // element: eight columns in V vectors
     float* out = part + (size_t)blockIdx.x * 2 * H;
-    if (G > 1) {
-        float* sums = reinterpret_cast<float*>(s_dyn);
-        const int cols = lanes * kCols;
+    float* sums = reinterpret_cast<float*>(s_dyn);
+    const int cols = lanes * kCols;
 #pragma unroll
-        for (int q = 0; q < kCols; ++q) {
-            const int h = (j + q / VEC * lanes) * VEC + q % VEC;
-            sums[(g * 2) * cols + h] = q & 1 ? dg[q >> 1].y : dg[q >> 1].x;
-            sums[(g * 2 + 1) * cols + h] = q & 1 ? db[q >> 1].y : db[q >> 1].x;
+    for (int q = 0; q < kCols; ++q) {
+        const int h = (j + q / VEC * lanes) * VEC + q % VEC;
+        sums[(g * 2) * cols + h] = q & 1 ? dg[q >> 1].y : dg[q >> 1].x;
+        sums[(g * 2 + 1) * cols + h] = q & 1 ? db[q >> 1].y : db[q >> 1].x;
+    }
+    __syncthreads();
+    for (int h = threadIdx.x; h < H; h += blockDim.x) {
+        float a = 0.0f, b = 0.0f;
+        for (int q = 0; q < G; ++q) {
+            a += sums[(q * 2) * cols + h];
+            b += sums[(q * 2 + 1) * cols + h];
         }
-        __syncthreads();
-        for (int h = threadIdx.x; h < H; h += blockDim.x) {
-            float a = 0.0f, b = 0.0f;
-            for (int q = 0; q < G; ++q) {
-                a += sums[(q * 2) * cols + h];
-                b += sums[(q * 2 + 1) * cols + h];
-            }
-            out[h] = a;
-            out[H + h] = b;
-        }
-    } else if constexpr (VEC % 4 == 0) {
-        // 16-byte stores: H is a multiple of VEC, part 256-byte aligned
-#pragma unroll
-        for (int q = 0; q < kPairs; q += 2) {
-            const int h = (j + 2 * q / VEC * lanes) * VEC + 2 * q % VEC;
-            if (h < H) {
-                *reinterpret_cast<float4*>(out + h) = make_float4(dg[q].x, dg[q].y, dg[q + 1].x, dg[q + 1].y);
-                *reinterpret_cast<float4*>(out + H + h) = make_float4(db[q].x, db[q].y, db[q + 1].x, db[q + 1].y);
-            }
-        }
-    } else {
-#pragma unroll
-        for (int q = 0; q < kCols; ++q) {
-            const int h = (j + q / VEC * lanes) * VEC + q % VEC;
-            if (h < H) {
-                out[h] = q & 1 ? dg[q >> 1].y : dg[q >> 1].x;
-                out[H + h] = q & 1 ? db[q >> 1].y : db[q >> 1].x;
-            }
-        }
+        out[h] = a;
+        out[H + h] = b;
     }
     pdl_launch_dependents();
 }
 
-// The same for rows of more than kRingMin columns in 16-byte vectors: sixteen
+// The same for rows of more than kRingMin columns: sixteen
 // columns a thread, 512 threads an SM (one block of 512 or up to four of 128).  The rows ahead
 // wait in shared memory (the copy engine's bulk copies, a ring of S rows of dy
 // and x) instead of registers, which the column sums and the row at hand fill.
@@ -484,6 +525,8 @@ __global__ void __launch_bounds__(512, 1)
                               int64_t dx_stride, float* part, bool wide_params) {
     using Raw = typename RowVec<T_, VEC>::Raw;
     constexpr int C = kRingCols, V = C / VEC, P = C / 2;
+    constexpr bool kWhole = sizeof(Raw) == 16;
+    using Row = RingRow<T_, kWhole>;
     __shared__ float2 s_red[2][16];
     __shared__ uint64_t s_full[kRingMax];
     extern __shared__ __align__(16) uint8_t s_ring[];      // gamma [P][threads] float2, then [S][dy, x][n] vectors
@@ -491,15 +534,21 @@ __global__ void __launch_bounds__(512, 1)
     const int lanes = blockDim.x, j = threadIdx.x, lane = j & 31, warp = j >> 5, W = lanes >> 5;
     const int n = H / VEC;
     float2* s_gamma = reinterpret_cast<float2*>(s_ring);
-    Raw* s_rows = reinterpret_cast<Raw*>(s_ring + (size_t)lanes * C * 4);
-    const uint32_t row_bytes = (uint32_t)n * 16u;
+    uint8_t* s_rows = s_ring + (size_t)lanes * C * 4;
+    const uint32_t row_bytes = (uint32_t)n * (uint32_t)sizeof(Raw), slot = Row::slot(row_bytes);
     const int64_t step = gridDim.x, first = blockIdx.x;
     uint64_t policy = 0;
     auto fetch = [&](int64_t t, int stage) {               // thread 0
-        Raw* to = s_rows + (size_t)stage * 2 * n;
-        mbar_arrive_expect_tx(&s_full[stage], 2u * row_bytes);
-        bulk_load(to, dy + t * dy_stride, row_bytes, &s_full[stage], policy);
-        bulk_load(to + n, x + t * x_stride, row_bytes, &s_full[stage], policy);
+        uint8_t* to = s_rows + stage * 2 * slot;
+        const Raw *row_d = dy + t * dy_stride, *row_x = x + t * x_stride;
+        mbar_arrive_expect_tx(&s_full[stage], Row::copied(row_d, row_bytes) + Row::copied(row_x, row_bytes));
+        Row::copy(to, row_d, row_bytes, &s_full[stage], policy);
+        Row::copy(to + slot, row_x, row_bytes, &s_full[stage], policy);
+    };
+    Row edge;
+    auto load_edge = [&](int64_t t, int stage) {           // the first 32 threads
+        const Raw* row = j < 16 ? dy + t * dy_stride : x + t * x_stride;
+        edge.load(s_rows + (stage * 2 + (j >> 4)) * slot, row, row_bytes, j & 15);
     };
     if (j == 0) {
         policy = policy_evict_first();                     // dy and x are read once
@@ -508,6 +557,12 @@ __global__ void __launch_bounds__(512, 1)
         for (int q = 0; q < S; ++q)
             if (first + q * step < T) fetch(first + q * step, q);
     }
+    if (!kWhole && j < 32)
+        for (int q = 0; q < S; ++q)
+            if (first + q * step < T) {
+                load_edge(first + q * step, q);
+                edge.store();
+            }
     float2 dg[P], db[P];
     {
         float2 ga[P];
@@ -535,13 +590,15 @@ __global__ void __launch_bounds__(512, 1)
         const bool landed = mbar_wait(&s_full[stage], parity, &never, nullptr, 0);
         float2 d[P], hat[P];
         {
-            const Raw* at = s_rows + (size_t)stage * 2 * n + j;
+            const uint8_t* at = s_rows + stage * 2 * slot;
+            const Raw* at_d = reinterpret_cast<const Raw*>(at + Row::offset(dy + t * dy_stride)) + j;
+            const Raw* at_x = reinterpret_cast<const Raw*>(at + slot + Row::offset(x + t * x_stride)) + j;
             Raw rd[V], rx[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const bool there = j + v * lanes < n;
-                rd[v] = there ? at[v * lanes] : Raw{};
-                rx[v] = there ? at[n + v * lanes] : Raw{};
+                rd[v] = there ? at_d[v * lanes] : Raw{};
+                rx[v] = there ? at_x[v * lanes] : Raw{};
             }
             unpack_cols<T_, VEC, C>(rd, d);
             unpack_cols<T_, VEC, C>(rx, hat);
@@ -558,11 +615,15 @@ __global__ void __launch_bounds__(512, 1)
         }
         const float wa = warp_sum(sg.x + sg.y), wb = warp_sum(sgx.x + sgx.y);
         if (lane == 0) s_red[turn][warp] = make_float2(wa, wb);
+        if (!kWhole) edge.store();
         if (__syncthreads_or(!landed)) {
             for (int i = 0; i < 100; ++i) __nanosleep(10000);   // copies in flight land before the block leaves
             break;
         }
-        if (j == 0 && t + S * step < T) fetch(t + S * step, stage);
+        if (t + S * step < T) {
+            if (j == 0) fetch(t + S * step, stage);
+            if (!kWhole && j < 32) load_edge(t + S * step, stage);
+        }
         const float2 w = lane < W ? s_red[turn][lane & 15] : both(0.0f);
         const float2 a = both(-(warp_sum(w.x) * inv)), b = both(-(warp_sum(w.y) * inv));
 #pragma unroll
@@ -574,14 +635,25 @@ __global__ void __launch_bounds__(512, 1)
         dx += dx_step;
         if (++stage == S) { stage = 0; parity ^= 1u; }
     }
-    // 16-byte stores: H is a multiple of VEC (4 or 8), part 256-byte aligned
     float* out = part + (size_t)blockIdx.x * 2 * H;
+    if constexpr (VEC % 4 == 0) {
+        // 16-byte stores: H is a multiple of VEC, part 256-byte aligned
 #pragma unroll
-    for (int q = 0; q < P; q += 2) {
-        const int v = j + 2 * q / VEC * lanes, h = v * VEC + 2 * q % VEC;
-        if (v < n) {
-            *reinterpret_cast<float4*>(out + h) = make_float4(dg[q].x, dg[q].y, dg[q + 1].x, dg[q + 1].y);
-            *reinterpret_cast<float4*>(out + H + h) = make_float4(db[q].x, db[q].y, db[q + 1].x, db[q + 1].y);
+        for (int q = 0; q < P; q += 2) {
+            const int v = j + 2 * q / VEC * lanes, h = v * VEC + 2 * q % VEC;
+            if (v < n) {
+                *reinterpret_cast<float4*>(out + h) = make_float4(dg[q].x, dg[q].y, dg[q + 1].x, dg[q + 1].y);
+                *reinterpret_cast<float4*>(out + H + h) = make_float4(db[q].x, db[q].y, db[q + 1].x, db[q + 1].y);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int q = 0; q < C; ++q) {
+            const int v = j + q / VEC * lanes, h = v * VEC + q % VEC;
+            if (v < n) {
+                out[h] = q & 1 ? dg[q >> 1].y : dg[q >> 1].x;
+                out[H + h] = q & 1 ? db[q >> 1].y : db[q >> 1].x;
+            }
         }
     }
     pdl_launch_dependents();
@@ -768,18 +840,17 @@ cudaError_t forward_any(const LaunchCtx& c, int T, int H, const void* x, int64_t
         return c.launch(layer_norm_kernel<T_, VEC>, dim3(T), dim3(kNormThreads), 0, H, xv, x_stride / VEC, gamma, beta,
                         eps, yv, y_stride / VEC, mean, rstd);
     const bool wide_params = (row_at(gamma) | row_at(beta)) % 16 == 0;
-    if constexpr (sizeof(Raw) == 16) {
-        if (H > kRingMin && T > 4 * kNormSms) {
-            const int threads = (H + 32 * kRingCols - 1) / (32 * kRingCols) * 32;
-            const int held = threads * kRingCols * 8, row = H * (int)sizeof(T_);
-            int per_sm = ring_blocks(H) < 2 ? 2 : ring_blocks(H);
-            if (kRingBytes / per_sm < held + 2 * row) per_sm = 1;
-            const int fit = (kRingBytes / per_sm - held) / row;
-            const int S = fit > kRingMax ? kRingMax : fit;
-            return c.launch(norm_ring_kernel<T_, VEC>, dim3(per_sm * kNormSms), dim3(threads),
-                            (size_t)held + (size_t)S * row, T, H, S, xv, x_stride / VEC, gamma, beta, eps, yv,
-                            y_stride / VEC, mean, rstd, wide_params);
-        }
+    constexpr bool kWhole = sizeof(Raw) == 16;
+    if (H > (kWhole ? kRingMin : kRingMinOdd) && T > 4 * kNormSms) {
+        const int threads = (H + 32 * kRingCols - 1) / (32 * kRingCols) * 32;
+        const int held = threads * kRingCols * 8, row = (int)RingRow<T_, kWhole>::slot(H * sizeof(T_));
+        int per_sm = threads <= 64 ? 12 : ring_blocks(H) < 2 ? 2 : ring_blocks(H);
+        if (kRingBytes / per_sm < held + 2 * row) per_sm = 1;
+        const int fit = (kRingBytes / per_sm - held) / row;
+        const int S = fit > kRingMax ? kRingMax : fit;
+        return c.launch(norm_ring_kernel<T_, VEC>, dim3(per_sm * kNormSms), dim3(threads),
+                        (size_t)held + (size_t)S * row, T, H, S, xv, x_stride / VEC, gamma, beta, eps, yv,
+                        y_stride / VEC, mean, rstd, wide_params);
     }
     // long rows, enough of them to fill the SMs: 32 columns a thread, so that
     // several rows share an SM and overlap their loads with their reductions
@@ -817,26 +888,23 @@ cudaError_t backward_rows_any(const LaunchCtx& c, int T, int H, const void* dy, 
     using Raw = typename RowVec<T_, VEC>::Raw;
     const bool wide_params = row_at(gamma) % 16 == 0;
     const NormShape s = norm_shape(H);
-    if constexpr (sizeof(Raw) == 16) {
-        if (H > kRingMin) {
-            const int threads = (H + 32 * kRingCols - 1) / (32 * kRingCols) * 32;
-            const int per_sm = ring_blocks(H);
-            const int held = threads * kRingCols * 4, stage = 2 * H * (int)sizeof(T_);
-            const int fit = (kRingBytes / per_sm - held) / stage;
-            const int S = fit > kRingMax ? kRingMax : fit;
-            *blocks = backward_blocks(T, 1, per_sm * kNormSms);
-            return c.launch(norm_ring_backward_kernel<T_, VEC>, dim3(*blocks), dim3(threads),
-                            (size_t)held + (size_t)S * stage, T, H, S, static_cast<const Raw*>(dy), dy_stride / VEC,
-                            static_cast<const Raw*>(x), x_stride / VEC, gamma, mean, rstd, static_cast<Raw*>(dx),
-                            dx_stride / VEC, part, wide_params);
-        }
+    if (H > kRingMin) {
+        const int threads = (H + 32 * kRingCols - 1) / (32 * kRingCols) * 32;
+        const int per_sm = ring_blocks(H);
+        const int held = threads * kRingCols * 4;
+        const int stage = 2 * (int)RingRow<T_, sizeof(Raw) == 16>::slot(H * sizeof(T_));
+        const int fit = (kRingBytes / per_sm - held) / stage;
+        const int S = fit > kRingMax ? kRingMax : fit;
+        *blocks = backward_blocks(T, 1, per_sm * kNormSms);
+        return c.launch(norm_ring_backward_kernel<T_, VEC>, dim3(*blocks), dim3(threads),
+                        (size_t)held + (size_t)S * stage, T, H, S, static_cast<const Raw*>(dy), dy_stride / VEC,
+                        static_cast<const Raw*>(x), x_stride / VEC, gamma, mean, rstd, static_cast<Raw*>(dx),
+                        dx_stride / VEC, part, wide_params);
     }
     const bool full = s.W * 32 * kCols == H;
-    auto kernel = s.threads() <= 256 ? (full ? norm_rows_backward_kernel<T_, VEC, 256, 2, true>
-                                             : norm_rows_backward_kernel<T_, VEC, 256, 2, false>)
-                                     : norm_rows_backward_kernel<T_, VEC, 1024, 1, false>;
-    const size_t smem = s.threads() > 256 ? (size_t)kCols * 1024 * 4 : s.G > 1 ? (size_t)s.G * 2 * s.W * 32 * kCols * 4 : 0;
-    *blocks = backward_blocks(T, s.G, (s.threads() > 512 ? 1 : 2) * kNormSms);
+    auto kernel = full ? norm_rows_backward_kernel<T_, VEC, true> : norm_rows_backward_kernel<T_, VEC, false>;
+    const size_t smem = (size_t)s.G * 2 * s.W * 32 * kCols * 4;
+    *blocks = backward_blocks(T, s.G, 2 * kNormSms);
     return c.launch(kernel, dim3(*blocks), dim3(s.threads()), smem, T, H, s.W, static_cast<const Raw*>(dy),
                     dy_stride / VEC, static_cast<const Raw*>(x), x_stride / VEC, gamma, mean, rstd,
                     static_cast<Raw*>(dx), dx_stride / VEC, part, wide_params);
@@ -852,17 +920,28 @@ cudaError_t launch_layer_norm(const LaunchCtx& c, int T, int H, int elem, const 
 }
 
 cudaError_t setup_layer_norm_kernels() {
-    static_assert(512 * kRingCols * 4 + 2 * 2 * kRowColumns * 4 <= kRingBytes, "two stages of the longest rows");
-    cudaError_t e;
-    if ((e = cudaFuncSetAttribute(norm_ring_kernel<__nv_bfloat16, 8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  kRingBytes)) ||
-        (e = cudaFuncSetAttribute(norm_ring_kernel<float, 4>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes)))
-        return e;
-    if ((e = cudaFuncSetAttribute(norm_ring_backward_kernel<__nv_bfloat16, 8>,
-                                  cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes)))
-        return e;
-    return cudaFuncSetAttribute(norm_ring_backward_kernel<float, 4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                kRingBytes);
+    static_assert(512 * kRingCols * 8 + 2 * (kRowColumns * 4 + 32) <= kRingBytes &&
+                      512 * kRingCols * 4 + 2 * 2 * (kRowColumns * 4 + 32) <= kRingBytes,
+                  "two stages of the longest rows");
+    cudaError_t e = cudaSuccess;
+    auto allow = [&](auto kernel) {
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+    };
+    allow(norm_ring_kernel<__nv_bfloat16, 8>);
+    allow(norm_ring_kernel<__nv_bfloat16, 4>);
+    allow(norm_ring_kernel<__nv_bfloat16, 2>);
+    allow(norm_ring_kernel<__nv_bfloat16, 1>);
+    allow(norm_ring_kernel<float, 4>);
+    allow(norm_ring_kernel<float, 2>);
+    allow(norm_ring_kernel<float, 1>);
+    allow(norm_ring_backward_kernel<__nv_bfloat16, 8>);
+    allow(norm_ring_backward_kernel<__nv_bfloat16, 4>);
+    allow(norm_ring_backward_kernel<__nv_bfloat16, 2>);
+    allow(norm_ring_backward_kernel<__nv_bfloat16, 1>);
+    allow(norm_ring_backward_kernel<float, 4>);
+    allow(norm_ring_backward_kernel<float, 2>);
+    allow(norm_ring_backward_kernel<float, 1>);
+    return e;
 }
 
 size_t layer_norm_workspace_bytes(int T, int H) {

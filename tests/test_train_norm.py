@@ -158,6 +158,45 @@ def test_strides_shifts_and_in_place(dt, H, pad, shift):
         check_backward(dy, x, gamma, mean, rstd, got)
 
 
+# rows that start anywhere within 16 bytes, enough of them for several turns of
+# every block; what lies between the rows stays as it is
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,H,pads,shifts", [
+    (613, 513, (0, 0, 0), (0, 0, 0)), (4001, 601, (0, 0, 0), (0, 0, 0)), (7000, 1001, (3, 0, 1), (1, 2, 3)),
+    (2500, 1023, (0, 1, 5), (0, 0, 0)), (1300, 1025, (0, 0, 0), (0, 0, 0)), (1300, 1026, (0, 2, 4), (2, 0, 6)),
+    (900, 2047, (1, 0, 2), (0, 5, 0)), (700, 4097, (0, 0, 0), (7, 7, 7)), (800, 7167, (0, 0, 0), (0, 0, 0)),
+    (650, 8191, (4, 1, 0), (3, 1, 0)), (700, 8190, (0, 0, 0), (0, 0, 0)), (700, 8188, (0, 0, 0), (0, 0, 0)),
+    (700, 4096, (1, 8, 0), (0, 0, 1)), (1, 4099, (0, 0, 0), (1, 1, 1)), (160, 1537, (0, 0, 0), (0, 0, 0))])
+def test_rows_off_16_byte_blocks(T, H, pads, shifts, dt):
+    x, gamma, beta, dy = data(T, H, dt)
+
+    def placed(t, pad, shift):
+        buf = torch.full((T * (H + pad) + shift + 16,), 7.0, dtype=dt, device="cuda")
+        rows = buf[shift:].as_strided((T, H), (H + pad, 1))
+        rows.copy_(t)
+        return buf, rows
+
+    def between(buf, pad, shift):
+        left = torch.ones_like(buf, dtype=torch.bool)
+        left[shift:].as_strided((T, H), (H + pad, 1)).fill_(False)
+        return bool((buf[left] == 7.0).all())
+
+    (_, xs), (_, ds), (ybuf, ys) = (placed(t, pads[i], shifts[i]) for i, t in enumerate((x, dy, torch.zeros_like(x))))
+    mean, rstd = (torch.full((T,), float("nan"), device="cuda") for _ in range(2))
+    api.moe_nvfp4_layer_norm(xs, gamma, beta, EPS, ys, mean, rstd)
+    check_forward(x, gamma, beta, (ys, mean, rstd))
+    assert between(ybuf, pads[2], shifts[2])
+    got = backward(ds, xs, gamma, mean, rstd, dx=ys)
+    check_backward(dy, x, gamma, mean, rstd, got)
+    assert between(ybuf, pads[2], shifts[2])
+    again = backward(ds, xs, gamma, mean, rstd)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+    for over in (ds, xs):
+        keep = over.clone()
+        assert torch.equal(backward(ds, xs, gamma, mean, rstd, dx=over)[0], got[0])
+        over.copy_(keep)
+
+
 def test_gradient_against_differences():
     """L = <c, layer_norm(x)> in 64 bits; central differences of step h along v
     are off by O(h^2) of the third derivative."""
