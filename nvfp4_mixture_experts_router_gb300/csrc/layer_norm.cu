@@ -661,7 +661,7 @@ __global__ void __launch_bounds__(512, 1)
 
 // dgamma and dbeta from `parts` partial sums [parts][2][H]: 32 VEC columns a
 // block, a 32nd of the parts a warp, then the warps' sums in order.
-template <int VEC>
+template <int VEC, int UNROLL>
 __global__ void __launch_bounds__(1024) norm_reduce_kernel(int H, int parts, const float* part, float* dgamma,
                                                                    float* dbeta) {
     using RV = RowVec<float, VEC>;
@@ -675,7 +675,7 @@ __global__ void __launch_bounds__(1024) norm_reduce_kernel(int H, int parts, con
     for (int k = 0; k < VEC; ++k) v[k] = 0.0f;
     if (c < n) {
         const typename RV::Raw* p = reinterpret_cast<const typename RV::Raw*>(part) + (blockIdx.y ? n : 0) + c;
-#pragma unroll 4
+#pragma unroll UNROLL
         for (int q = warp; q < parts; q += kWarps) {
             float u[VEC];
             RV::unpack(p[(size_t)q * 2 * n], u);
@@ -697,9 +697,12 @@ __global__ void __launch_bounds__(1024) norm_reduce_kernel(int H, int parts, con
 }
 
 cudaError_t launch_reduce(const LaunchCtx& c, int H, int parts, const float* part, float* dgamma, float* dbeta) {
-    const int wide = H % 4 == 0 ? 4 : 1;
+    // short rows: more blocks and more loads in flight (5453 rows of 1624,
+    // backward, us for vectors of 4, 2 and 1: 19.0 17.8 17.1; 8191 of 7168: 67.4
+    // 67.1 69.5)
+    const int wide = H % 2 == 0 && H > 2048 ? 2 : 1;
     const dim3 grid((unsigned)((H / wide + 31) / 32), dbeta ? 2 : 1);
-    return c.launch(wide == 4 ? norm_reduce_kernel<4> : norm_reduce_kernel<1>, grid, dim3(1024), 0, H, parts,
+    return c.launch(wide == 2 ? norm_reduce_kernel<2, 4> : norm_reduce_kernel<1, 8>, grid, dim3(1024), 0, H, parts,
                     part, dgamma, dbeta);
 }
 

@@ -560,7 +560,8 @@ static cudaError_t combine_shape(const LaunchCtx& c, int T, int H, int K, int64_
 
 // Loads in flight: of 16-byte vectors one of eight routes, or two of four
 // (11639 FP32 tokens, top-3, 1392: 59 -> 42 us; top-6 is faster with eight: 74
-// against 77); of narrower ones four of four.
+// against 77); of narrower ones four of four, of single BF16 elements eight of
+// two (4096 tokens, top-4, 7167: 91.6 -> 84.5 us; 36 tokens of 393, top-4: no).
 template <typename T_, int VEC>
 static cudaError_t combine_any(const LaunchCtx& c, int T, int H, int K, int64_t rows, const void* o,
                                const int* row_of_route, const float* w, void* y, int64_t y_stride) {
@@ -570,6 +571,8 @@ static cudaError_t combine_any(const LaunchCtx& c, int T, int H, int K, int64_t 
         return K <= 4 ? combine_shape<T_, VEC, 2, 4>(c, T, H, K, rows, o, row_of_route, w, y, y_stride)
                       : combine_shape<T_, VEC, 1, 8>(c, T, H, K, rows, o, row_of_route, w, y, y_stride);
     } else {
+        if constexpr (sizeof(typename RowVec<T_, VEC>::Raw) == 2)
+            if (T >= 64) return combine_shape<T_, VEC, 8, 2>(c, T, H, K, rows, o, row_of_route, w, y, y_stride);
         return combine_shape<T_, VEC, 4, 4>(c, T, H, K, rows, o, row_of_route, w, y, y_stride);
     }
 }
