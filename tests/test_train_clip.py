@@ -60,6 +60,18 @@ def test_norm_and_clip(sizes, dts, max_norm):
     check(tensors, max_norm)                               # in place
 
 
+# lists that take one round of the blocks and several, every size of the
+# argument, and more tensors than one launch holds; empty tensors between
+@pytest.mark.parametrize("sizes", [[20001, 1, 0] * 80, [40000] * 400, [5000, 1, 30000] * 400, [4096] * 608, [4097] * 609,
+                                   [0] * 1000 + [77, 0, 200000], [17, 3000000, 9] * 12, [250001] * 33, [1] * 1921])
+@pytest.mark.parametrize("dts", [[BF], [F32, BF, BF]])
+def test_many_tensors(sizes, dts):
+    tensors = normal(sizes, dts, seed=1)
+    first = check(tensors, 0.5, [torch.full_like(t, float("nan")) for t in tensors])
+    again = norm_of(api.GradList(tensors, None))
+    assert torch.equal(first, again)
+
+
 def test_shifted_pointers():
     base = normal([40000], [BF])[0]
     tensors = [base[1:20000], base[20001:20009], base[20010:39999]]
