@@ -398,10 +398,11 @@ _DTYPES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_F32}
 
 
 class GradList:
-    """A list of gradients (contiguous CUDA tensors, bfloat16 or float32) and
-    where their clipped values go (``out``; the gradients themselves without
-    it).  Built once for buffers that stay where they are; it holds the tensors
-    and their addresses."""
+    """A list of gradients (contiguous CUDA tensors of one device, bfloat16 or
+    float32) and where their clipped values go (``out``; the gradients themselves
+    without it).  Built once for buffers that stay where they are; it holds the
+    tensors and their addresses.  Gradients of several devices take a list each,
+    and their norms are joined between the two calls."""
 
     def __init__(self, grads, out=None):
         self.grads = list(grads)
@@ -413,6 +414,9 @@ class GradList:
                 raise TypeError("gradients must be bfloat16 or float32 CUDA tensors, each output of its gradient's type")
             if o.numel() != g.numel() or not (g.is_contiguous() and o.is_contiguous()):
                 raise ValueError("gradients and outputs must be contiguous and of the same size")
+        self.device = self.grads[0].device if self.grads else None
+        if any(t.device != self.device for ts in (self.grads, self.out) for t in ts):
+            raise ValueError("gradients and outputs must be on one device")
         n = self.n = len(self.grads)
         # the host arrays of the C calls, and their addresses
         self._arrays = ((ctypes.c_void_p * n)(*[g.data_ptr() for g in self.grads]),
@@ -426,8 +430,16 @@ def moe_nvfp4_grad_norm_workspace_bytes(n: int) -> int:
     return int(lib().moe_nvfp4_grad_norm_workspace_bytes(n))
 
 
+def _on_device_of(norm: torch.Tensor, grads: GradList) -> None:
+    """The list reaches the library as addresses: its device is compared with
+    the norm's here, and the norm's with the current one in _binding.so."""
+    if grads.n and norm.device != grads.device:
+        raise ValueError(f"the gradients are on {grads.device}, not on the norm's device {norm.device}")
+
+
 def moe_nvfp4_grad_norm(grads: GradList, norm: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
     """norm[0] (float32) = sqrt of the sum of the squares of every gradient's elements."""
+    _on_device_of(norm, grads)
     _check("moe_nvfp4_grad_norm", (_native or native()).grad_norm(
         grads.n, grads._grads, grads._numels, grads._dtypes, norm, workspace, stream))
 
@@ -435,6 +447,7 @@ def moe_nvfp4_grad_norm(grads: GradList, norm: torch.Tensor, workspace: torch.Te
 def moe_nvfp4_grad_clip(grads: GradList, norm: torch.Tensor, max_norm: float, eps: float = 1e-6,
                         stream=None) -> None:
     """out = gradient * min(1, max_norm / (norm + eps)) for every gradient of the list."""
+    _on_device_of(norm, grads)
     _check("moe_nvfp4_grad_clip", (_native or native()).grad_clip(
         grads.n, grads._grads, grads._out, grads._numels, grads._dtypes, norm, max_norm, eps, stream))
 
