@@ -432,8 +432,9 @@ def moe_nvfp4_grad_norm_workspace_bytes(n: int) -> int:
 
 def _on_device_of(norm: torch.Tensor, grads: GradList) -> None:
     """The list reaches the library as addresses: its device is compared with
-    the norm's here, and the norm's with the current one in _binding.so."""
-    if grads.n and norm.device != grads.device:
+    the norm's here, and the norm's with the current one in _binding.so (which
+    also refuses a norm that is no CUDA tensor)."""
+    if grads.n and getattr(norm, "is_cuda", False) and norm.device != grads.device:
         raise ValueError(f"the gradients are on {grads.device}, not on the norm's device {norm.device}")
 
 
