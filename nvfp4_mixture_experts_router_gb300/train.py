@@ -17,7 +17,7 @@ examples/moe_block.py trains one.
 from __future__ import annotations
 
 from dataclasses import dataclass
-from typing import Iterable, Optional
+from typing import Iterable, Optional, Union
 
 import torch
 from torch.autograd.function import once_differentiable
@@ -163,10 +163,14 @@ def expert_linear(x_rows: torch.Tensor, w: torch.Tensor, routes: Routes) -> torc
     return _ExpertLinear.apply(x_rows.contiguous(), w, routes)
 
 
-def clip_grad_norm_(parameters: Iterable[torch.Tensor], max_norm: float, eps: float = 1e-6) -> torch.Tensor:
-    """Scales the gradients of ``parameters`` in place to a global norm of at
-    most max_norm; returns the norm before (one device float32).  A training
-    loop whose gradients keep their buffers builds an api.GradList once instead."""
+def clip_grad_norm_(parameters: Union[torch.Tensor, Iterable[torch.Tensor]], max_norm: float,
+                    eps: float = 1e-6) -> torch.Tensor:
+    """Scales the gradients of ``parameters`` (or of one tensor) in place to a
+    global norm of at most max_norm; returns the norm before (one device
+    float32).  A training loop whose gradients keep their buffers builds an
+    api.GradList once instead."""
+    if isinstance(parameters, torch.Tensor):
+        parameters = [parameters]
     grads = [p.grad for p in parameters if p.grad is not None]
     if not grads:
         return torch.zeros(1)

@@ -3,7 +3,7 @@ buffers of another size, odd gradients, and errors found on the device."""
 import pytest
 import torch
 
-from nvfp4_mixture_experts_router_gb300 import api, build
+from nvfp4_mixture_experts_router_gb300 import api, build, train
 
 pytestmark = pytest.mark.gpu
 
@@ -21,3 +21,15 @@ def test_a_norm_that_is_no_cuda_tensor_is_a_type_error(norm):
         api.moe_nvfp4_grad_norm(grads, norm, torch.zeros(256, device="cuda"))
     with pytest.raises(TypeError):
         api.moe_nvfp4_grad_clip(grads, norm, 1.0)
+
+
+def param(grad):
+    p = torch.nn.Parameter(torch.zeros(grad.shape, dtype=grad.dtype, device=grad.device))
+    p.grad = grad
+    return p
+
+
+def test_clip_takes_one_tensor():
+    p = param(torch.full((10,), 3.0, device="cuda"))
+    assert abs(float(train.clip_grad_norm_(p, 1.0)) - 90.0 ** 0.5) < 1e-5
+    assert abs(float(p.grad.norm()) - 1.0) < 1e-5
