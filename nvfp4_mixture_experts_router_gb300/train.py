@@ -171,9 +171,10 @@ def clip_grad_norm_(parameters: Union[torch.Tensor, Iterable[torch.Tensor]], max
     api.GradList once instead."""
     if isinstance(parameters, torch.Tensor):
         parameters = [parameters]
+    parameters = list(parameters)
     grads = [p.grad for p in parameters if p.grad is not None]
     if not grads:
-        return torch.zeros(1)
+        return torch.zeros(1, dtype=torch.float32, device=parameters[0].device if parameters else "cuda")
     device = grads[0].device
     norm = torch.empty(1, dtype=torch.float32, device=device)
     ws = torch.empty(api.moe_nvfp4_grad_norm_workspace_bytes(len(grads)), dtype=torch.uint8, device=device)

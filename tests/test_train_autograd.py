@@ -33,3 +33,10 @@ def test_clip_takes_one_tensor():
     p = param(torch.full((10,), 3.0, device="cuda"))
     assert abs(float(train.clip_grad_norm_(p, 1.0)) - 90.0 ** 0.5) < 1e-5
     assert abs(float(p.grad.norm()) - 1.0) < 1e-5
+
+
+def test_clip_without_gradients_stays_on_the_device():
+    p = torch.nn.Parameter(torch.zeros(4, device="cuda"))
+    for arg in (p, [p], []):
+        norm = train.clip_grad_norm_(arg, 1.0)
+        assert norm.is_cuda and norm.dtype == torch.float32 and norm.shape == (1,) and float(norm) == 0.0
