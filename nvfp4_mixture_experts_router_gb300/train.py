@@ -163,11 +163,13 @@ def expert_linear(x_rows: torch.Tensor, w: torch.Tensor, routes: Routes) -> torc
     return _ExpertLinear.apply(x_rows.contiguous(), w, routes)
 
 
+@torch.no_grad()
 def clip_grad_norm_(parameters: Union[torch.Tensor, Iterable[torch.Tensor]], max_norm: float,
                     eps: float = 1e-6) -> torch.Tensor:
     """Scales the gradients of ``parameters`` (or of one tensor) in place to a
     global norm of at most max_norm; returns the norm before (one device
-    float32).  A training loop whose gradients keep their buffers builds an
+    float32).  Gradients that are not contiguous are scaled in a copy and copied
+    back.  A training loop whose gradients keep their buffers builds an
     api.GradList once instead."""
     if isinstance(parameters, torch.Tensor):
         parameters = [parameters]
@@ -178,7 +180,11 @@ def clip_grad_norm_(parameters: Union[torch.Tensor, Iterable[torch.Tensor]], max
     device = grads[0].device
     norm = torch.empty(1, dtype=torch.float32, device=device)
     ws = torch.empty(api.moe_nvfp4_grad_norm_workspace_bytes(len(grads)), dtype=torch.uint8, device=device)
-    gl = api.GradList(grads)
+    packed = [g if g.is_contiguous() else g.contiguous() for g in grads]
+    gl = api.GradList(packed)
     api.moe_nvfp4_grad_norm(gl, norm, ws)
     api.moe_nvfp4_grad_clip(gl, norm, max_norm, eps)
+    for g, c in zip(grads, packed):
+        if g is not c:
+            g.copy_(c)
     return norm

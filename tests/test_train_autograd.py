@@ -40,3 +40,23 @@ def test_clip_without_gradients_stays_on_the_device():
     for arg in (p, [p], []):
         norm = train.clip_grad_norm_(arg, 1.0)
         assert norm.is_cuda and norm.dtype == torch.float32 and norm.shape == (1,) and float(norm) == 0.0
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_clip_of_gradients_in_other_orders(dt):
+    """Transposed and strided gradients (relative bound: a sum of 500 squares and the scaling, three
+    roundings of 2^-24 and one of the type)."""
+    g = torch.Generator("cuda").manual_seed(3)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").to(dt)
+    wide = r(16, 24)
+    grads = [r(12, 20).t(), wide[:, ::2], r(9), r(4, 3, 5).permute(2, 0, 1)]
+    rest = wide[:, 1::2].clone()
+    want = [v.double() for v in grads]
+    total = float(sum(v.square().sum() for v in want).sqrt())
+    norm = float(train.clip_grad_norm_([param(v) for v in grads], 1.0))
+    assert abs(norm - total) <= 600 * 2.0 ** -24 * total
+    half = 2.0 ** -8 if dt == torch.bfloat16 else 2.0 ** -24
+    for v, w in zip(grads, want):
+        w = w / (norm + 1e-6)
+        assert bool(((v.double() - w).abs() <= (half + 4 * 2.0 ** -24) * w.abs() + 1e-38).all())
+    assert torch.equal(wide[:, 1::2], rest)
