@@ -58,6 +58,13 @@ def sort_routes(topk_ids: torch.Tensor, E: int) -> Routes:
     return r
 
 
+def _check_rows(rows: torch.Tensor, routes: Routes, name: str) -> None:
+    """The library takes a route outside its buffer for a dropped one, and a
+    segment outside it for an empty one."""
+    if rows.shape[0] < routes.rows:
+        raise ValueError(f"{name} has {rows.shape[0]} rows for {routes.rows} routes")
+
+
 class _LayerNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, gamma, beta, eps):
@@ -130,6 +137,7 @@ class _Combine(torch.autograd.Function):
 
 def combine(o_rows: torch.Tensor, routes: Routes, topk_w: torch.Tensor) -> torch.Tensor:
     """The tokens' sums of their routes' rows times topk_w [T, K] FP32."""
+    _check_rows(o_rows, routes, "o_rows")
     return _Combine.apply(o_rows.contiguous(), routes, topk_w.contiguous())
 
 
@@ -160,6 +168,7 @@ class _ExpertLinear(torch.autograd.Function):
 def expert_linear(x_rows: torch.Tensor, w: torch.Tensor, routes: Routes) -> torch.Tensor:
     """Every expert's rows times its matrix: x_rows [rows, K], w [E, N, K], BF16.
     Rows past the kept routes are not computed; no other function here reads them."""
+    _check_rows(x_rows, routes, "x_rows")
     return _ExpertLinear.apply(x_rows.contiguous(), w, routes)
 
 

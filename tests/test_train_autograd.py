@@ -60,3 +60,25 @@ def test_clip_of_gradients_in_other_orders(dt):
         w = w / (norm + 1e-6)
         assert bool(((v.double() - w).abs() <= (half + 4 * 2.0 ** -24) * w.abs() + 1e-38).all())
     assert torch.equal(wide[:, 1::2], rest)
+
+
+def routes_of(T, E, K, drop, seed=5):
+    g = torch.Generator("cuda").manual_seed(seed)
+    ids = torch.randint(0, E, (T, K), generator=g, device="cuda", dtype=torch.int32)
+    ids[torch.rand(T, K, generator=g, device="cuda") < drop] = -1
+    return ids, train.sort_routes(ids, E)
+
+
+def test_row_buffers_smaller_than_the_routes_are_refused():
+    ids, routes = routes_of(30, 4, 2, 0.0)
+    w = torch.randn(4, 32, 64, device="cuda").bfloat16()
+    x = torch.randn(60, 64, device="cuda").bfloat16()
+    s = torch.rand(30, 2, device="cuda")
+    with pytest.raises(ValueError):
+        train.expert_linear(x[:59], w, routes)
+    with pytest.raises(ValueError):
+        train.combine(x[:59], routes, s)
+    # more rows than routes: the rest belongs to no route
+    more = torch.cat([x, x[:3]])
+    assert torch.equal(train.expert_linear(more, w, routes)[:60], train.expert_linear(x, w, routes))
+    assert torch.equal(train.combine(more, routes, s), train.combine(x, routes, s))
