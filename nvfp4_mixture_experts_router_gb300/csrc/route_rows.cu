@@ -528,12 +528,16 @@ cudaError_t launch_dispatch(const LaunchCtx& c, int T, int H, int K, int64_t row
     const int bytes = row_vec_bytes(H, elem, row_at(x, x_stride, elem) | row_at(x_rows));
     const int per = bytes / elem;
     const int n = H / per;
+    // groups of threads: a token each, and of the rows to clear 32 each at most
+    // (as many as a token has routes: more groups than tokens only where the
+    // buffer is larger than the routes, as in a call that clears and copies none)
+    const int groups = rows_used && T < rows / 32 ? (int)(rows / 32) : T;
     // few tokens: a vector a thread over more blocks; else four, so that a
     // thread has four loads in flight
-    const bool few = T < 64;
+    const bool few = groups < 64;
     const int lanes = lanes_for(few ? n : (n + 3) / 4);
     const int slice = lanes * (few ? 1 : 4);
-    const dim3 grid(token_blocks(T, lanes), (unsigned)((n + slice - 1) / slice));
+    const dim3 grid(token_blocks(groups, lanes), (unsigned)((n + slice - 1) / slice));
 #define MOE_DISPATCH(RAW, V)                                                                                   \
     c.launch(dispatch_kernel<RAW, V>, grid, dim3(kRowThreads), 0, T, n, K, rows, static_cast<const RAW*>(x),    \
              x_stride / per, row_of_route, rows_used, static_cast<RAW*>(x_rows), lanes)

@@ -65,6 +65,12 @@ def _check_rows(rows: torch.Tensor, routes: Routes, name: str) -> None:
         raise ValueError(f"{name} has {rows.shape[0]} rows for {routes.rows} routes")
 
 
+def _clear_tail(rows: torch.Tensor, routes: Routes) -> torch.Tensor:
+    """Zeros in the rows past the kept routes (a dispatch of no tokens)."""
+    api.moe_nvfp4_dispatch(rows[:0], routes.row_of_route[:0], routes.used, rows)
+    return rows
+
+
 class _LayerNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, gamma, beta, eps):
@@ -148,7 +154,7 @@ class _ExpertLinear(torch.autograd.Function):
         ctx.save_for_backward(x_rows, w)
         y = torch.empty(x_rows.shape[0], w.shape[1], dtype=w.dtype, device=w.device)
         api.moe_nvfp4_expert_linear(x_rows, w, routes.count, routes.offsets, y)
-        return y
+        return _clear_tail(y, routes)
 
     @staticmethod
     @once_differentiable
@@ -159,6 +165,7 @@ class _ExpertLinear(torch.autograd.Function):
         if ctx.needs_input_grad[0]:
             dx = torch.empty_like(x_rows)
             api.moe_nvfp4_expert_linear_dgrad(dy, w, r.count, r.offsets, dx)
+            _clear_tail(dx, r)
         if ctx.needs_input_grad[1]:
             dw = torch.empty_like(w)
             api.moe_nvfp4_expert_linear_wgrad(dy, x_rows, r.count, r.offsets, dw)
@@ -166,8 +173,9 @@ class _ExpertLinear(torch.autograd.Function):
 
 
 def expert_linear(x_rows: torch.Tensor, w: torch.Tensor, routes: Routes) -> torch.Tensor:
-    """Every expert's rows times its matrix: x_rows [rows, K], w [E, N, K], BF16.
-    Rows past the kept routes are not computed; no other function here reads them."""
+    """Every expert's rows times its matrix: x_rows [rows, K], w [E, N, K], BF16;
+    zeros past the kept routes, in the gradient of x_rows too, so that sums over
+    all rows (of a bias after it, say) count the routes alone."""
     _check_rows(x_rows, routes, "x_rows")
     return _ExpertLinear.apply(x_rows.contiguous(), w, routes)
 

@@ -2,6 +2,7 @@
 buffers of another size, odd gradients, and errors found on the device."""
 import pytest
 import torch
+import torch.nn.functional as F
 
 from nvfp4_mixture_experts_router_gb300 import api, build, train
 
@@ -82,3 +83,54 @@ def test_row_buffers_smaller_than_the_routes_are_refused():
     more = torch.cat([x, x[:3]])
     assert torch.equal(train.expert_linear(more, w, routes)[:60], train.expert_linear(x, w, routes))
     assert torch.equal(train.combine(more, routes, s), train.combine(x, routes, s))
+
+
+@pytest.mark.parametrize("T,drop", [(40, 0.3), (300, 0.9), (7, 1.0), (64, 0.0)])
+def test_parameters_between_products_with_dropped_routes(monkeypatch, T, drop):
+    """A scale and a bias per channel between two products, every buffer full
+    of NaN before it is written: the rows that no route owns are zeros and add
+    nothing to their gradients.  Bound: z, the activation, do and da are
+    rounded to BF16 once each (half an ulp is 2^-8), the rest is FP32."""
+    empty, empty_like = torch.empty, torch.empty_like
+    spoil = lambda t: t.fill_(float("nan")) if t.is_floating_point() else t
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: spoil(empty(*a, **k)))
+    monkeypatch.setattr(torch, "empty_like", lambda *a, **k: spoil(empty_like(*a, **k)))
+    H, N, E, K = 64, 96, 5, 3
+    ids, routes = routes_of(T, E, K, drop)
+    g = torch.Generator("cuda").manual_seed(T)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    x = r(T, H).bfloat16().requires_grad_(True)
+    w1 = (r(E, N, H) * H ** -0.5).bfloat16().requires_grad_(True)
+    w2 = (r(E, H, N) * N ** -0.5).bfloat16().requires_grad_(True)
+    scale, bias = (1.0 + 0.2 * r(N)).requires_grad_(True), (0.1 * r(N)).requires_grad_(True)
+    s = torch.rand(T, K, generator=g, device="cuda").requires_grad_(True)
+    z = train.expert_linear(train.dispatch(x, routes), w1, routes)
+    z.retain_grad()
+    a = F.silu(z.float() * scale + bias).bfloat16()
+    a.retain_grad()
+    o = train.expert_linear(a, w2, routes)
+    y = train.combine(o, routes, s)
+    c = r(T, H).bfloat16()
+    y.backward(c)
+    used = int(routes.used)
+    for t in (z, o, a.grad):
+        assert not t[used:].any()
+    x2, w1_2, w2_2, sc2, b2, s2 = (v.detach().double().requires_grad_(True) for v in (x, w1, w2, scale, bias, s))
+    e = ids.clamp(min=0).long()
+    z2 = torch.einsum("th,tknh->tkn", x2, w1_2[e])
+    o2 = torch.einsum("tkn,tkhn->tkh", F.silu(z2 * sc2 + b2), w2_2[e])
+    (o2 * torch.where(ids >= 0, s2, 0.0)[..., None]).sum(1).backward(c.double())
+    for got, want in ((x, x2), (w1, w1_2), (w2, w2_2), (scale, sc2), (bias, b2), (s, s2)):
+        err = float((got.grad.double() - want.grad).norm())
+        assert err <= 5 * 2.0 ** -8 * float(want.grad.norm()), err
+
+
+@pytest.mark.parametrize("rows,used,H,dt", [(1, 0, 8, torch.bfloat16), (31, 4, 33, torch.float32), (5000, 3, 72, torch.bfloat16),
+                                            (4097, 4096, 1001, torch.bfloat16), (70001, 11, 260, torch.float32),
+                                            (2100, -5, 7168, torch.bfloat16), (40, 40, 64, torch.float32)])
+def test_a_dispatch_of_no_tokens_clears_rows(rows, used, H, dt):
+    out = torch.full((rows, H), 7.0, dtype=dt, device="cuda")
+    none = torch.empty(0, 3, dtype=torch.int32, device="cuda")
+    api.moe_nvfp4_dispatch(out[:0], none, torch.tensor([used], dtype=torch.int32, device="cuda"), out)
+    used = max(used, 0)
+    assert bool((out[:used] == 7.0).all()) and not out[used:].any()
