@@ -37,7 +37,7 @@ class MoEBlock(torch.nn.Module):
     def forward(self, x):
         h = train.layer_norm(x, self.gamma, self.beta)
         ids, w = self.route(h)
-        routes = train.sort_routes(ids, self.E)
+        routes = self.routes = train.sort_routes(ids, self.E)
         z = train.expert_linear(train.dispatch(h, routes), self.w1, routes)
         gate, up = z.chunk(2, dim=1)
         o = train.expert_linear(F.silu(gate) * up, self.w2, routes)
@@ -59,6 +59,7 @@ def train_block(tokens=512, hidden=256, inter=128, experts=8, topk=2, steps=20, 
         norm = train.clip_grad_norm_(block.parameters(), max_norm)
         opt.step()
         losses.append((float(loss.detach()), float(norm)))
+        block.routes.check()        # errors found on the device (it waits, as the two reads before it do)
     return losses
 
 

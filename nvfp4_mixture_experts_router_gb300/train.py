@@ -33,6 +33,7 @@ class Routes:
     offsets: torch.Tensor       # int32 [E + 1]
     row_of_route: torch.Tensor  # int32 [T, K], -1: dropped
     route_of_row: torch.Tensor  # int32 [T * K], -1: no route
+    status: Optional[torch.Tensor] = None   # int32 [1]: errors that the experts' products found on the device
 
     @property
     def rows(self) -> int:
@@ -43,13 +44,24 @@ class Routes:
         """The number of kept routes, one device int32."""
         return self.offsets[self.E:]
 
+    def check(self) -> None:
+        """Waits for the current stream and raises MoEError if a product on these
+        routes, or a gradient of one, found a segment outside its rows
+        (MOE_ERR_INVALID_ARG) or gave up a wait (MOE_ERR_TIMEOUT: its output is
+        undefined).  An error is raised once."""
+        if self.status is not None:
+            code = api.moe_nvfp4_last_device_status(self.status)
+            if code != api.MOE_OK:
+                raise api.MoEError("an experts' product", code)
+
 
 def sort_routes(topk_ids: torch.Tensor, E: int) -> Routes:
-    """Routes of topk_ids [T, K] (int32; ids outside [0, E) are dropped)."""
+    """Routes of topk_ids [T, K] (int32; ids outside [0, E) are dropped).  Errors
+    that the experts' products find on the device are read with Routes.check."""
     T, K = topk_ids.shape
     i32 = dict(dtype=torch.int32, device=topk_ids.device)
     r = Routes(E, torch.empty(E, **i32), torch.empty(E + 1, **i32), torch.empty(T, K, **i32),
-               torch.empty(T * K, **i32))
+               torch.empty(T * K, **i32), torch.zeros(1, **i32))
     nbytes = api.moe_nvfp4_sort_workspace_bytes(T, E, K)
     if nbytes == 0:
         raise api.MoEError("moe_nvfp4_sort_workspace_bytes", api.MOE_ERR_INVALID_ARG)
@@ -153,7 +165,7 @@ class _ExpertLinear(torch.autograd.Function):
         ctx.routes = routes
         ctx.save_for_backward(x_rows, w)
         y = torch.empty(x_rows.shape[0], w.shape[1], dtype=w.dtype, device=w.device)
-        api.moe_nvfp4_expert_linear(x_rows, w, routes.count, routes.offsets, y)
+        api.moe_nvfp4_expert_linear(x_rows, w, routes.count, routes.offsets, y, routes.status)
         return _clear_tail(y, routes)
 
     @staticmethod
@@ -164,11 +176,11 @@ class _ExpertLinear(torch.autograd.Function):
         dx = dw = None
         if ctx.needs_input_grad[0]:
             dx = torch.empty_like(x_rows)
-            api.moe_nvfp4_expert_linear_dgrad(dy, w, r.count, r.offsets, dx)
+            api.moe_nvfp4_expert_linear_dgrad(dy, w, r.count, r.offsets, dx, r.status)
             _clear_tail(dx, r)
         if ctx.needs_input_grad[1]:
             dw = torch.empty_like(w)
-            api.moe_nvfp4_expert_linear_wgrad(dy, x_rows, r.count, r.offsets, dw)
+            api.moe_nvfp4_expert_linear_wgrad(dy, x_rows, r.count, r.offsets, dw, r.status)
         return dx, dw, None
 
 

@@ -134,3 +134,24 @@ def test_a_dispatch_of_no_tokens_clears_rows(rows, used, H, dt):
     api.moe_nvfp4_dispatch(out[:0], none, torch.tensor([used], dtype=torch.int32, device="cuda"), out)
     used = max(used, 0)
     assert bool((out[:used] == 7.0).all()) and not out[used:].any()
+
+
+def test_bad_segments_are_reported():
+    ids, routes = routes_of(30, 4, 2, 0.0)
+    x = torch.randn(60, 64, device="cuda").bfloat16().requires_grad_(True)
+    w = torch.randn(4, 32, 64, device="cuda").bfloat16().requires_grad_(True)
+    y = train.expert_linear(x, w, routes)
+    routes.check()
+    keep = routes.count.clone()
+    routes.count[3] += 1000                     # past the buffer's end
+    for call in (lambda: train.expert_linear(x, w, routes),
+                 lambda: torch.autograd.grad(y, x, torch.ones_like(y), retain_graph=True),
+                 lambda: torch.autograd.grad(y, w, torch.ones_like(y), retain_graph=True)):
+        call()
+        with pytest.raises(api.MoEError) as err:
+            routes.check()
+        assert err.value.code == api.MOE_ERR_INVALID_ARG
+        routes.check()                          # reported once
+    routes.count.copy_(keep)
+    y.sum().backward()
+    routes.check()
