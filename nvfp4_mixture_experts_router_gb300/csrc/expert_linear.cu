@@ -655,6 +655,18 @@ done:
     }
 }
 
+// No rows at all: a segment with some, or one that starts elsewhere than at 0,
+// is reported as by the kernel above.
+__global__ void __launch_bounds__(256) segment_check_kernel(int E, const int* count, const int* offsets,
+                                                            unsigned int* status) {
+    pdl_wait();
+    for (int e = threadIdx.x; e < E; e += 256) {
+        const int64_t first = offsets[e], n = count[e];
+        if (n < 0 || first < 0 || first + n > 0) atomicOr(status, kStatusBadRow);
+    }
+    pdl_launch_dependents();
+}
+
 // Tensor map of a BF16 array: dims[0] contiguous, byte strides of the others,
 // boxes as wide as the swizzle.
 bool encode_bf16_map(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
@@ -817,8 +829,13 @@ cudaError_t setup_expert_linear_kernels(int device, int num_sms) {
 
 cudaError_t launch_expert_linear(const LaunchCtx& c, int product, int device, const ExpertArgs& a) {
     if (device < 0 || device >= 64 || g_expert_grid[device] < 2) return cudaErrorInvalidValue;
-    if (a.rows == 0)   // wgrad only: no rows, a gradient of zeros
-        return cudaMemsetAsync(a.out, 0, (size_t)a.E * a.N * a.K * 2, c.stream);
+    if (a.rows == 0) {
+        cudaError_t e = cudaSuccess;
+        if (a.status) e = c.launch(segment_check_kernel, dim3(1), dim3(256), 0, a.E, a.count, a.offsets, a.status);
+        if (e == cudaSuccess && product == kExpertWgrad)    // a gradient of zeros
+            e = cudaMemsetAsync(a.out, 0, (size_t)a.E * a.N * a.K * 2, c.stream);
+        return e;
+    }
     const cuuint64_t N = (cuuint64_t)a.N, K = (cuuint64_t)a.K, R = (cuuint64_t)a.rows;
     const int64_t busy = a.rows < a.E ? a.rows : a.E;
     const double mean = (double)a.rows / (double)busy;

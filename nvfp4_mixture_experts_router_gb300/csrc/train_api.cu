@@ -176,7 +176,7 @@ static moe_status expert_product(int product, int64_t rows, int N, int K, int E,
                       {out, fwd ? yb : wg ? wb : xb, true}};
     const uintptr_t al[] = {16, 16, 4, 4, 4, 16};
     if (!spans_ok(s, 6, al)) return MOE_ERR_INVALID_ARG;
-    if (rows == 0 && !wg) return MOE_OK;
+    if (rows == 0 && !wg && !status) return MOE_OK;
     LaunchCtx c;
     int sms = 0, device = 0;
     const moe_status st = begin(stream, &c, &sms, &device);
