@@ -9,7 +9,8 @@
  * checked on the host before anything is launched, `stream` is a
  * cudaStream_t (NULL = legacy default stream).  Also:
  *   - No output may overlap an input or another output unless its comment
- *     says so (MOE_ERR_INVALID_ARG).
+ *     says so (MOE_ERR_INVALID_ARG).  Token rows of one stride may lie side by
+ *     side in one buffer; other ranges that cross count as overlapping.
  *   - An empty call (T = 0, rows = 0, no elements) is valid; operands of no
  *     elements may be NULL.
  *   - Sums, statistics and accumulators are FP32; each output is rounded

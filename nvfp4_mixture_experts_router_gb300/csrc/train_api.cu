@@ -19,16 +19,30 @@ bool dtype_ok(int d) { return d == MOE_DTYPE_BF16 || d == MOE_DTYPE_F32; }
 int elem_of(int d) { return d == MOE_DTYPE_F32 ? 4 : 2; }
 bool routes_ok(int T, int K) { return tokens_ok(T) && K >= 1 && K <= 32 && (int64_t)T * K <= (1 << 26); }
 
-// A range of device memory an argument covers.
+// A range of device memory an argument covers: `bytes` from p on; of rows
+// `stride` bytes apart (0: one run) only the first `width` bytes each.
 struct Span {
     const void* p;
     size_t bytes;
     bool out;
+    size_t stride = 0, width = 0;
 };
 
-// Bytes from the first element of a [rows][width] buffer to past its last.
-size_t rows_bytes(int64_t rows, int64_t stride, int64_t width, int elem) {
-    return rows > 0 ? (size_t)((rows - 1) * stride + width) * elem : 0;
+// The rows of a [rows][width] buffer, `stride` elements apart.
+Span rows_span(const void* p, int64_t rows, int64_t stride, int64_t width, int elem, bool out) {
+    const size_t bytes = rows > 0 ? (size_t)((rows - 1) * stride + width) * elem : 0;
+    return Span{p, bytes, out, (size_t)stride * elem, (size_t)width * elem};
+}
+
+// Do two spans share a byte?  Rows of one stride share none where their columns,
+// taken modulo the stride, lie side by side; other ranges that cross count as
+// shared.
+bool shared(const Span& a, const Span& b) {
+    if (!overlaps(a.p, a.bytes, b.p, b.bytes)) return false;
+    if (a.stride == 0 || a.stride != b.stride) return true;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    const size_t after = y >= x ? (y - x) % a.stride : (a.stride - (x - y) % a.stride) % a.stride;   // b's column from a's
+    return after < a.width || after + b.width > a.stride;
 }
 
 bool stride_ok(int64_t stride, int64_t width) { return stride >= width && stride <= (1ll << 40); }
@@ -40,9 +54,7 @@ bool spans_ok(const Span* s, int n, const uintptr_t* align) {
         if (s[i].bytes && (!s[i].p || !aligned(s[i].p, align[i]))) return false;
     for (int i = 0; i < n; ++i)
         for (int j = 0; j < n; ++j)
-            if (i != j && s[i].out && s[i].bytes && s[j].bytes &&
-                overlaps(s[i].p, s[i].bytes, s[j].p, s[j].bytes))
-                return false;
+            if (i != j && s[i].out && s[i].bytes && s[j].bytes && shared(s[i], s[j])) return false;
     return true;
 }
 
@@ -92,7 +104,7 @@ moe_status moe_nvfp4_dispatch(int T, int H, int K, int64_t rows, int dtype, cons
                               const int32_t* row_of_route, const int32_t* rows_used, void* x_rows, void* stream) {
     if (!row_args_ok(T, H, K, rows, dtype, x_stride)) return MOE_ERR_INVALID_ARG;
     const int el = elem_of(dtype);
-    const Span s[] = {{x, rows_bytes(T, x_stride, H, el), false},
+    const Span s[] = {rows_span(x, T, x_stride, H, el, false),
                       {row_of_route, (size_t)T * K * 4, false},
                       {rows_used, rows_used ? 4u : 0u, false},
                       {x_rows, (size_t)rows * H * el, true}};
@@ -114,7 +126,7 @@ static moe_status gather_sum(int T, int H, int K, int64_t rows, int dtype, const
     const Span s[] = {{in, (size_t)rows * H * el, false},
                       {row_of_route, (size_t)T * K * 4, false},
                       {w, weighted ? (size_t)T * K * 4 : 0, false},
-                      {out, rows_bytes(T, out_stride, H, el), true}};
+                      rows_span(out, T, out_stride, H, el, true)};
     const uintptr_t al[] = {(uintptr_t)el, 4, 4, (uintptr_t)el};
     if (!spans_ok(s, 4, al)) return MOE_ERR_INVALID_ARG;
     if (T == 0) return MOE_OK;
@@ -142,7 +154,7 @@ moe_status moe_nvfp4_combine_backward(int T, int H, int K, int64_t rows, int dty
     if (!row_args_ok(T, H, K, rows, dtype, dy_stride)) return MOE_ERR_INVALID_ARG;
     const int el = elem_of(dtype);
     const size_t rb = (size_t)T * K * 4;
-    const Span s[] = {{dy, rows_bytes(T, dy_stride, H, el), false},
+    const Span s[] = {rows_span(dy, T, dy_stride, H, el, false),
                       {o_rows, (size_t)rows * H * el, false},
                       {row_of_route, rb, false},
                       {topk_w, rb, false},
@@ -212,10 +224,10 @@ moe_status moe_nvfp4_layer_norm(int T, int H, int dtype, const void* x, int64_t 
     const int el = elem_of(dtype);
     const bool in_place = y == x && y_stride == x_stride;
     const size_t sb = mean ? (size_t)T * 4 : 0;
-    const Span s[] = {{x, in_place ? 0 : rows_bytes(T, x_stride, H, el), false},
+    const Span s[] = {rows_span(x, in_place ? 0 : T, x_stride, H, el, false),
                       {gamma, (size_t)H * 4, false},
                       {beta, beta ? (size_t)H * 4 : 0, false},
-                      {y, rows_bytes(T, y_stride, H, el), true},
+                      rows_span(y, T, y_stride, H, el, true),
                       {mean, sb, true},
                       {rstd, sb, true}};
     const uintptr_t al[] = {(uintptr_t)el, 4, 4, (uintptr_t)el, 4, 4};
@@ -242,12 +254,12 @@ moe_status moe_nvfp4_layer_norm_backward(int T, int H, int dtype, const void* dy
     const int el = elem_of(dtype);
     const size_t need = layer_norm_workspace_bytes(T, H);
     const bool over_dy = dx == dy && dx_stride == dy_stride, over_x = dx == x && dx_stride == x_stride;
-    const Span s[] = {{dy, over_dy ? 0 : rows_bytes(T, dy_stride, H, el), false},
-                      {x, over_x ? 0 : rows_bytes(T, x_stride, H, el), false},
+    const Span s[] = {rows_span(dy, over_dy ? 0 : T, dy_stride, H, el, false),
+                      rows_span(x, over_x ? 0 : T, x_stride, H, el, false),
                       {gamma, (size_t)H * 4, false},
                       {mean, (size_t)T * 4, false},
                       {rstd, (size_t)T * 4, false},
-                      {dx, rows_bytes(T, dx_stride, H, el), true},
+                      rows_span(dx, T, dx_stride, H, el, true),
                       {dgamma, (size_t)H * 4, true},
                       {dbeta, dbeta ? (size_t)H * 4 : 0, true},
                       {workspace, need, true}};

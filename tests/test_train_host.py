@@ -1,10 +1,14 @@
-"""Training operators without a GPU: lists of gradients on several devices."""
+"""Training operators without a GPU: lists of gradients on several devices and
+overlaps of strided rows."""
+import ctypes
 import types
 
 import pytest
 import torch
 
-from nvfp4_mixture_experts_router_gb300 import api
+from nvfp4_mixture_experts_router_gb300 import api, build
+
+BAD = api.MOE_ERR_INVALID_ARG
 
 
 class FakeGrad:
@@ -53,3 +57,19 @@ def test_a_list_of_another_device_than_the_norm_is_refused(monkeypatch):
     api.moe_nvfp4_grad_clip(grads, there, 1.0)
     api.moe_nvfp4_grad_norm(api.GradList([]), here, None)      # an empty list is on no device
     assert len(launched) == 3
+
+
+def test_overlapping_strided_rows_are_refused():
+    """Rows of one stride side by side in a buffer: refused where the columns
+    meet, where a row reaches into the next one, and at another stride."""
+    build.build()
+    L = api.lib()
+    at = lambda i, off=0: ctypes.c_void_p((i << 36) + off)
+    f = lambda off, ys=128, H=64: L.moe_nvfp4_layer_norm(9, H, api.MOE_DTYPE_F32, at(1, 4096), 128, at(2), at(3), 1e-5,
+                                                         at(1, 4096 + off), ys, None, None, None)
+    for columns in (1, 63, -1, -63, 65, 127, -65, 128, -128, 256, 128 * 8 + 63):
+        assert f(4 * columns) == BAD, columns
+    assert f(4 * 64, ys=129) == BAD and f(4 * 64, ys=127) == BAD and f(4 * 64, ys=256) == BAD
+    # statistics (one run of memory) inside the gaps of the rows
+    assert L.moe_nvfp4_layer_norm(9, 64, api.MOE_DTYPE_F32, at(1), 128, at(2), at(3), 1e-5, at(4), 64, at(1, 256),
+                                  at(5), None) == BAD
