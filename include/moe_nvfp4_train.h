@@ -131,7 +131,13 @@ MOE_API moe_status moe_nvfp4_expert_linear_wgrad(int64_t rows, int N, int K, int
  *   dgamma = sum_t dy * xhat,  dbeta = sum_t dy   (FP32 [H]; dbeta may be NULL)
  * dx may be dy or x itself (same pointer and stride).  workspace:
  * moe_nvfp4_layer_norm_workspace_bytes(T, H) (0 if invalid), 256-byte
- * aligned.  With T = 0, dgamma and dbeta are zero. */
+ * aligned.  With T = 0, dgamma and dbeta are zero.
+ * Rows that are copied ahead (calls of many tokens) are waited for 1 s at most:
+ * a row whose copy does not land, and the later rows of its block, leave NaN in
+ * y or dx and in the statistics, and dgamma and dbeta become NaN.
+ * MOE_DEBUG_NORM_SKIP_COPY, added to dtype, is a test hook: the copy of row
+ * T / 2 is left out where rows are copied ahead. */
+#define MOE_DEBUG_NORM_SKIP_COPY 0x100
 MOE_API moe_status moe_nvfp4_layer_norm(int T, int H, int dtype, const void* x, int64_t x_stride,
                                         const float* gamma, const float* beta, float eps,
                                         void* y, int64_t y_stride, float* mean, float* rstd,

@@ -41,6 +41,7 @@ MOE_ROUTER_GEMM = 1 << 14
 MOE_W8A8_MXFP8 = 3 << 2
 
 MOE_DTYPE_BF16, MOE_DTYPE_F32 = 0, 1
+MOE_DEBUG_NORM_SKIP_COPY = 0x100
 
 
 class MoEError(RuntimeError):

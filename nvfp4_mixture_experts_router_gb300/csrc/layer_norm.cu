@@ -26,6 +26,8 @@
 // 256 columns 4.0 and 6.5; 1001 13.6 and 21; 2000 rows of 16384 75 and 129.
 // FP32, 7168: forward 72 (6.5 TB/s), backward 107 (6.6); 7167 99 and 118.  One
 // row of 7168 BF16: 3.1.
+#include <math.h>
+
 #include "row_vec.cuh"
 #include "train_kernels.h"
 
@@ -279,17 +281,29 @@ struct RingRow {
     }
 };
 
+// NaN in the vectors of a row from `at` on, `lanes` apart; thread j's is the j-th of n.
+template <typename T_, int VEC>
+__device__ __forceinline__ void put_nan_row(typename RowVec<T_, VEC>::Raw* at, int j, int lanes, int n) {
+    float u[VEC];
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) u[k] = NAN;
+    const typename RowVec<T_, VEC>::Raw nan = RowVec<T_, VEC>::pack(u);
+#pragma unroll 1
+    for (int i = 0; j + i < n; i += lanes) at[i] = nan;
+}
+
 // The same for many rows of more than kRingMin columns:
 // persistent blocks of up to 512 threads, two an SM where their shared memory
 // allows, with gamma and beta in shared memory and the rows ahead in a ring of
 // bulk copies, so that a row's two reductions overlap the copies of the next
 // rows and the other block's arithmetic.  A stage is free once the first
 // reduction has passed its barrier.  Waits as in the backward ring below.
+// skip_row: a row whose copy is left out (tests of the wait's limit), or -1.
 template <typename T_, int VEC>
 __global__ void __launch_bounds__(512, 2)
     norm_ring_kernel(int T, int H, int S, const typename RowVec<T_, VEC>::Raw* x, int64_t x_stride,
                      const float* gamma, const float* beta, float eps, typename RowVec<T_, VEC>::Raw* y,
-                     int64_t y_stride, float* mean_out, float* rstd_out, bool wide_params) {
+                     int64_t y_stride, float* mean_out, float* rstd_out, bool wide_params, int skip_row) {
     using Raw = typename RowVec<T_, VEC>::Raw;
     constexpr int C = kRingCols, V = C / VEC, P = C / 2;
     constexpr bool kWhole = sizeof(Raw) == 16;
@@ -307,6 +321,7 @@ __global__ void __launch_bounds__(512, 2)
     const int64_t step = gridDim.x, first = blockIdx.x;
     uint64_t policy = 0;
     auto fetch = [&](int64_t t, int stage) {               // thread 0
+        if (t == skip_row) return;
         const Raw* row = x + t * x_stride;
         mbar_arrive_expect_tx(&s_full[stage], Row::copied(row, row_bytes));
         Row::copy(s_rows + stage * slot, row, row_bytes, &s_full[stage], policy);
@@ -343,7 +358,8 @@ __global__ void __launch_bounds__(512, 2)
     y += first * y_stride + j;
     const int64_t y_step = step * y_stride;
     volatile int never = 0;
-    for (int64_t t = first; t < T; t += step) {
+    int64_t t = first;
+    for (; t < T; t += step) {
         const bool landed = mbar_wait(&s_full[stage], parity, &never, nullptr, 0);
         float2 v[P];
         {
@@ -391,6 +407,12 @@ __global__ void __launch_bounds__(512, 2)
         }
         y += y_step;
         if (++stage == S) { stage = 0; parity ^= 1u; }
+    }
+    // gave up: no result for row t and the block's later ones
+    for (; t < T; t += step) {
+        put_nan_row<T_, VEC>(y, j, lanes, n);
+        if (j == 0 && mean_out) mean_out[t] = rstd_out[t] = NAN;
+        y += y_step;
     }
     pdl_launch_dependents();
 }
@@ -516,13 +538,14 @@ __global__ void __launch_bounds__(kNormThreads)
 // and x) instead of registers, which the column sums and the row at hand fill.
 // A stage is free once the row's reduction has passed its barrier: every
 // thread has read its columns by then.  The wait for a copy is bounded (1 s);
-// a block that gave up stops at the barrier, all its threads together.
+// a block that gave up stops at the barrier, all its threads together, and
+// leaves NaN where its results belong.
 template <typename T_, int VEC>
 __global__ void __launch_bounds__(512, 1)
     norm_ring_backward_kernel(int T, int H, int S, const typename RowVec<T_, VEC>::Raw* dy, int64_t dy_stride,
                               const typename RowVec<T_, VEC>::Raw* x, int64_t x_stride, const float* gamma,
                               const float* mean, const float* rstd, typename RowVec<T_, VEC>::Raw* dx,
-                              int64_t dx_stride, float* part, bool wide_params) {
+                              int64_t dx_stride, float* part, bool wide_params, int skip_row) {
     using Raw = typename RowVec<T_, VEC>::Raw;
     constexpr int C = kRingCols, V = C / VEC, P = C / 2;
     constexpr bool kWhole = sizeof(Raw) == 16;
@@ -539,6 +562,7 @@ __global__ void __launch_bounds__(512, 1)
     const int64_t step = gridDim.x, first = blockIdx.x;
     uint64_t policy = 0;
     auto fetch = [&](int64_t t, int stage) {               // thread 0
+        if (t == skip_row) return;
         uint8_t* to = s_rows + stage * 2 * slot;
         const Raw *row_d = dy + t * dy_stride, *row_x = x + t * x_stride;
         mbar_arrive_expect_tx(&s_full[stage], Row::copied(row_d, row_bytes) + Row::copied(row_x, row_bytes));
@@ -581,7 +605,8 @@ __global__ void __launch_bounds__(512, 1)
     dx += first * dx_stride + j;
     const int64_t dx_step = step * dx_stride;
     volatile int never = 0;
-    for (int64_t t = first; t < T; t += step) {
+    int64_t t = first;
+    for (; t < T; t += step) {
         const float2 m = both(-next_mean), r = both(next_rstd);
         if (t + step < T) {
             next_mean = mean[t + step];
@@ -634,6 +659,11 @@ __global__ void __launch_bounds__(512, 1)
         turn ^= 1;
         dx += dx_step;
         if (++stage == S) { stage = 0; parity ^= 1u; }
+    }
+    if (t < T) {      // gave up: no result for row t and the block's later ones, nor for the column sums
+#pragma unroll
+        for (int q = 0; q < P; ++q) dg[q] = db[q] = both(NAN);
+        for (; t < T; t += step, dx += dx_step) put_nan_row<T_, VEC>(dx, j, lanes, n);
     }
     float* out = part + (size_t)blockIdx.x * 2 * H;
     if constexpr (VEC % 4 == 0) {
@@ -835,7 +865,8 @@ int ring_blocks(int H) {
 
 template <typename T_, int VEC>
 cudaError_t forward_any(const LaunchCtx& c, int T, int H, const void* x, int64_t x_stride, const float* gamma,
-                        const float* beta, float eps, void* y, int64_t y_stride, float* mean, float* rstd) {
+                        const float* beta, float eps, void* y, int64_t y_stride, float* mean, float* rstd,
+                        int skip_row) {
     using Raw = typename RowVec<T_, VEC>::Raw;
     const Raw* xv = static_cast<const Raw*>(x);
     Raw* yv = static_cast<Raw*>(y);
@@ -853,7 +884,7 @@ cudaError_t forward_any(const LaunchCtx& c, int T, int H, const void* x, int64_t
         const int S = fit > kRingMax ? kRingMax : fit;
         return c.launch(norm_ring_kernel<T_, VEC>, dim3(per_sm * kNormSms), dim3(threads),
                         (size_t)held + (size_t)S * row, T, H, S, xv, x_stride / VEC, gamma, beta, eps, yv,
-                        y_stride / VEC, mean, rstd, wide_params);
+                        y_stride / VEC, mean, rstd, wide_params, skip_row);
     }
     // long rows, enough of them to fill the SMs: 32 columns a thread, so that
     // several rows share an SM and overlap their loads with their reductions
@@ -887,7 +918,7 @@ int backward_blocks(int T, int rows, int resident) {
 template <typename T_, int VEC>
 cudaError_t backward_rows_any(const LaunchCtx& c, int T, int H, const void* dy, int64_t dy_stride, const void* x,
                               int64_t x_stride, const float* gamma, const float* mean, const float* rstd, void* dx,
-                              int64_t dx_stride, float* part, int* blocks) {
+                              int64_t dx_stride, float* part, int* blocks, int skip_row) {
     using Raw = typename RowVec<T_, VEC>::Raw;
     const bool wide_params = row_at(gamma) % 16 == 0;
     const NormShape s = norm_shape(H);
@@ -902,7 +933,7 @@ cudaError_t backward_rows_any(const LaunchCtx& c, int T, int H, const void* dy, 
         return c.launch(norm_ring_backward_kernel<T_, VEC>, dim3(*blocks), dim3(threads),
                         (size_t)held + (size_t)S * stage, T, H, S, static_cast<const Raw*>(dy), dy_stride / VEC,
                         static_cast<const Raw*>(x), x_stride / VEC, gamma, mean, rstd, static_cast<Raw*>(dx),
-                        dx_stride / VEC, part, wide_params);
+                        dx_stride / VEC, part, wide_params, skip_row);
     }
     const bool full = s.W * 32 * kCols == H;
     auto kernel = full ? norm_rows_backward_kernel<T_, VEC, true> : norm_rows_backward_kernel<T_, VEC, false>;
@@ -917,9 +948,9 @@ cudaError_t backward_rows_any(const LaunchCtx& c, int T, int H, const void* dy, 
 
 cudaError_t launch_layer_norm(const LaunchCtx& c, int T, int H, int elem, const void* x, int64_t x_stride,
                               const float* gamma, const float* beta, float eps, void* y, int64_t y_stride, float* mean,
-                              float* rstd) {
+                              float* rstd, int skip_row) {
     const int bytes = row_vec_bytes(H, elem, row_at(x, x_stride, elem) | row_at(y, y_stride, elem));
-    MOE_ROW_VEC(elem, bytes, forward_any, c, T, H, x, x_stride, gamma, beta, eps, y, y_stride, mean, rstd);
+    MOE_ROW_VEC(elem, bytes, forward_any, c, T, H, x, x_stride, gamma, beta, eps, y, y_stride, mean, rstd, skip_row);
 }
 
 cudaError_t setup_layer_norm_kernels() {
@@ -962,22 +993,22 @@ static cudaError_t launch_dx(const LaunchCtx& c, int bytes, int T, int H, int el
 static cudaError_t launch_backward_rows(const LaunchCtx& c, int bytes, int T, int H, int elem, const void* dy,
                                         int64_t dy_stride, const void* x, int64_t x_stride, const float* gamma,
                                         const float* mean, const float* rstd, void* dx, int64_t dx_stride,
-                                        float* part, int* blocks) {
+                                        float* part, int* blocks, int skip_row) {
     MOE_ROW_VEC(elem, bytes, backward_rows_any, c, T, H, dy, dy_stride, x, x_stride, gamma, mean, rstd, dx, dx_stride,
-                part, blocks);
+                part, blocks, skip_row);
 }
 
 cudaError_t launch_layer_norm_backward(const LaunchCtx& c, int T, int H, int elem, const void* dy, int64_t dy_stride,
                                        const void* x, int64_t x_stride, const float* gamma, const float* mean,
                                        const float* rstd, void* dx, int64_t dx_stride, float* dgamma, float* dbeta,
-                                       float* workspace) {
+                                       float* workspace, int skip_row) {
     const int bytes = row_vec_bytes(
         H, elem, row_at(x, x_stride, elem) | row_at(dy, dy_stride, elem) | row_at(dx, dx_stride, elem));
     cudaError_t e;
     if (H <= kRowColumns) {
         int blocks = 0;
         e = launch_backward_rows(c, bytes, T, H, elem, dy, dy_stride, x, x_stride, gamma, mean, rstd, dx, dx_stride,
-                                 workspace, &blocks);
+                                 workspace, &blocks, skip_row);
         if (e != cudaSuccess) return e;
         return launch_reduce(c, H, blocks, workspace, dgamma, dbeta);
     }

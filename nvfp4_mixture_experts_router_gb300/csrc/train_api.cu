@@ -72,6 +72,14 @@ bool row_args_ok(int T, int H, int K, int64_t rows, int dtype, int64_t stride) {
     return routes_ok(T, K) && width_ok(H) && dtype_ok(dtype) && rows >= 0 && rows <= kMaxRows && stride_ok(stride, H);
 }
 
+// The row that MOE_DEBUG_NORM_SKIP_COPY in a layer norm's dtype leaves out, or
+// -1; takes the flag out of the dtype.
+int skipped_row(int T, int* dtype) {
+    if (*dtype < 0 || !(*dtype & MOE_DEBUG_NORM_SKIP_COPY)) return -1;
+    *dtype &= ~MOE_DEBUG_NORM_SKIP_COPY;
+    return T / 2;
+}
+
 }  // namespace
 
 extern "C" {
@@ -218,6 +226,7 @@ moe_status moe_nvfp4_expert_linear_wgrad(int64_t rows, int N, int K, int E, cons
 moe_status moe_nvfp4_layer_norm(int T, int H, int dtype, const void* x, int64_t x_stride, const float* gamma,
                                 const float* beta, float eps, void* y, int64_t y_stride, float* mean, float* rstd,
                                 void* stream) {
+    const int skip_row = skipped_row(T, &dtype);
     if (!tokens_ok(T) || !width_ok(H) || !dtype_ok(dtype) || !stride_ok(x_stride, H) || !stride_ok(y_stride, H))
         return MOE_ERR_INVALID_ARG;
     if (!(eps >= 0.0f) || isinf(eps) || (mean == nullptr) != (rstd == nullptr)) return MOE_ERR_INVALID_ARG;
@@ -237,7 +246,8 @@ moe_status moe_nvfp4_layer_norm(int T, int H, int dtype, const void* x, int64_t 
     int sms = 0;
     const moe_status st = begin(stream, &c, &sms);
     if (st != MOE_OK) return st;
-    return cuda_status(launch_layer_norm(c, T, H, el, x, x_stride, gamma, beta, eps, y, y_stride, mean, rstd));
+    return cuda_status(launch_layer_norm(c, T, H, el, x, x_stride, gamma, beta, eps, y, y_stride, mean, rstd,
+                                         skip_row));
 }
 
 size_t moe_nvfp4_layer_norm_workspace_bytes(int T, int H) {
@@ -249,6 +259,7 @@ moe_status moe_nvfp4_layer_norm_backward(int T, int H, int dtype, const void* dy
                                          int64_t x_stride, const float* gamma, const float* mean, const float* rstd,
                                          void* dx, int64_t dx_stride, float* dgamma, float* dbeta, void* workspace,
                                          size_t workspace_bytes, void* stream) {
+    const int skip_row = skipped_row(T, &dtype);
     if (!tokens_ok(T) || !width_ok(H) || !dtype_ok(dtype)) return MOE_ERR_INVALID_ARG;
     if (!stride_ok(dy_stride, H) || !stride_ok(x_stride, H) || !stride_ok(dx_stride, H)) return MOE_ERR_INVALID_ARG;
     const int el = elem_of(dtype);
@@ -271,7 +282,7 @@ moe_status moe_nvfp4_layer_norm_backward(int T, int H, int dtype, const void* dy
     const moe_status st = begin(stream, &c, &sms);
     if (st != MOE_OK) return st;
     return cuda_status(launch_layer_norm_backward(c, T, H, el, dy, dy_stride, x, x_stride, gamma, mean, rstd, dx,
-                                                  dx_stride, dgamma, dbeta, static_cast<float*>(workspace)));
+                                                  dx_stride, dgamma, dbeta, static_cast<float*>(workspace), skip_row));
 }
 
 size_t moe_nvfp4_grad_norm_workspace_bytes(int n) {

@@ -20,16 +20,17 @@ cudaError_t launch_combine_backward(const LaunchCtx& c, int T, int H, int K, int
                                     int64_t dy_stride, const void* o, const int* row_of_route, const float* w,
                                     const int* rows_used, void* d_o, float* dw);
 
-// layer_norm.cu (x and y may be the same rows; workspace of layer_norm_workspace_bytes)
+// layer_norm.cu (x and y may be the same rows; workspace of layer_norm_workspace_bytes;
+// skip_row: a row that a ring kernel never copies, for tests, or -1)
 cudaError_t launch_layer_norm(const LaunchCtx& c, int T, int H, int elem, const void* x, int64_t x_stride,
                               const float* gamma, const float* beta, float eps, void* y, int64_t y_stride, float* mean,
-                              float* rstd);
+                              float* rstd, int skip_row);
 cudaError_t setup_layer_norm_kernels();
 size_t layer_norm_workspace_bytes(int T, int H);
 cudaError_t launch_layer_norm_backward(const LaunchCtx& c, int T, int H, int elem, const void* dy, int64_t dy_stride,
                                        const void* x, int64_t x_stride, const float* gamma, const float* mean,
                                        const float* rstd, void* dx, int64_t dx_stride, float* dgamma, float* dbeta,
-                                       float* workspace);
+                                       float* workspace, int skip_row);
 
 // grad_clip.cu
 size_t grad_norm_workspace_bytes(int n);
