@@ -4,7 +4,9 @@ binding of the training operators (_binding.so) with the host compiler.
 Each .cu file compiles in parallel to an object, then nvcc links the shared
 library (CUDA runtime linked statically, so the library needs only the
 driver at run time).  The binding links against it and against the installed
-torch.  Rebuilds only when a source or header is newer than the results.
+torch; without Python's or torch's headers the library is built all the same,
+and the error raised after it.  Rebuilds only when a source or header is newer
+than the results.
 """
 from __future__ import annotations
 
@@ -66,11 +68,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stderr}")
         return obj, r.stderr
 
-    import torch
     cxx = os.environ.get("CXX") or shutil.which("g++") or "c++"
-    tdir = os.path.dirname(torch.__file__)
 
     def compile_binding():
+        import torch
+        tdir = os.path.dirname(torch.__file__)
         obj = os.path.join(BUILD_DIR, "binding.cpp.o")
         cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(cc))), "include")
         cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-c", BINDING_SRC, "-o", obj,
@@ -80,12 +82,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"{cxx} failed for {BINDING_SRC}:\n{r.stderr}")
-        return obj
+        return obj, tdir
 
     with cf.ThreadPoolExecutor(max_workers=min(16, os.cpu_count() or 4)) as ex:
         binding = ex.submit(compile_binding)
         results = list(ex.map(compile_one, sources()))
-        binding_obj = binding.result()
     if verbose:
         for _, log in results:
             print(log)
@@ -96,6 +97,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, OUT)
+    binding_obj, tdir = binding.result()
     tmp = BINDING + f".tmp{os.getpid()}"
     cmd = [cxx, "-shared", "-o", tmp, binding_obj, "-Wl,-rpath,$ORIGIN", "-L", PKG, "-l:libmoe_nvfp4.so",
            "-L", os.path.join(tdir, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
