@@ -418,6 +418,7 @@ class GradList:
         self.device = self.grads[0].device if self.grads else None
         if any(t.device != self.device for ts in (self.grads, self.out) for t in ts):
             raise ValueError("gradients and outputs must be on one device")
+        self.index = self.device.index if self.grads else None
         n = self.n = len(self.grads)
         # the host arrays of the C calls, and their addresses
         self._arrays = ((ctypes.c_void_p * n)(*[g.data_ptr() for g in self.grads]),
@@ -431,7 +432,7 @@ def moe_nvfp4_grad_norm_workspace_bytes(n: int) -> int:
     return int(lib().moe_nvfp4_grad_norm_workspace_bytes(n))
 
 
-def _on_device_of(norm: torch.Tensor, grads: GradList) -> None:
+def _refuse_device(norm, grads: GradList) -> None:
     """The list reaches the library as addresses: its device is compared with
     the norm's here, and the norm's with the current one in _binding.so (which
     also refuses a norm that is no CUDA tensor)."""
@@ -441,7 +442,8 @@ def _on_device_of(norm: torch.Tensor, grads: GradList) -> None:
 
 def moe_nvfp4_grad_norm(grads: GradList, norm: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
     """norm[0] (float32) = sqrt of the sum of the squares of every gradient's elements."""
-    _on_device_of(norm, grads)
+    if not isinstance(norm, torch.Tensor) or norm.get_device() != grads.index:
+        _refuse_device(norm, grads)
     _check("moe_nvfp4_grad_norm", (_native or native()).grad_norm(
         grads.n, grads._grads, grads._numels, grads._dtypes, norm, workspace, stream))
 
@@ -449,7 +451,8 @@ def moe_nvfp4_grad_norm(grads: GradList, norm: torch.Tensor, workspace: torch.Te
 def moe_nvfp4_grad_clip(grads: GradList, norm: torch.Tensor, max_norm: float, eps: float = 1e-6,
                         stream=None) -> None:
     """out = gradient * min(1, max_norm / (norm + eps)) for every gradient of the list."""
-    _on_device_of(norm, grads)
+    if not isinstance(norm, torch.Tensor) or norm.get_device() != grads.index:
+        _refuse_device(norm, grads)
     _check("moe_nvfp4_grad_clip", (_native or native()).grad_clip(
         grads.n, grads._grads, grads._out, grads._numels, grads._dtypes, norm, max_norm, eps, stream))
 
