@@ -416,7 +416,7 @@ class GradList:
             if o.numel() != g.numel() or not (g.is_contiguous() and o.is_contiguous()):
                 raise ValueError("gradients and outputs must be contiguous and of the same size")
         self.device = self.grads[0].device if self.grads else None
-        if any(t.device != self.device for ts in (self.grads, self.out) for t in ts):
+        if any(t.device != self.device for t in (self.grads if out is None else self.grads + self.out)):
             raise ValueError("gradients and outputs must be on one device")
         self.index = self.device.index if self.grads else None
         n = self.n = len(self.grads)
