@@ -163,43 +163,53 @@ RowArgs row_args(PyObject* tokens, const char* name, PyObject* rows, PyObject* r
     return a;
 }
 
+// The C entry, without the interpreter's lock: a launch may wait for room in the
+// device's queue, and other threads run meanwhile (0.1 us a call).
+template <typename... P, typename... A>
+int call(moe_status (*f)(P...), const A&... a) {
+    PyThreadState* const thread = PyEval_SaveThread();
+    const int status = f(static_cast<P>(a)...);      // the C entries throw nothing
+    PyEval_RestoreThread(thread);
+    return status;
+}
+
 int sort_routes(PyObject* const* a) {
     const int E = small(integer(a[0], "E"), "E");
     const at::Tensor& ids = tensor(a[1], "topk_ids");
     if (ids.dim() != 2) wrong_value("topk_ids must be [T, K]");
     const int64_t T = ids.size(0), K = ids.size(1);
     const Space ws = workspace(a[6]);
-    return moe_nvfp4_sort_routes(small(T, "T"), E, small(K, "K"), flat_i32(a[1], "topk_ids", {T, K}),
-                                 flat_i32(a[2], "count", {E}), flat_i32(a[3], "offsets", {(int64_t)E + 1}),
-                                 flat_i32(a[4], "row_of_route", {T, K}), flat_i32(a[5], "route_of_row", {T * K}), ws.p,
-                                 ws.bytes, handle(a[7]));
+    return call(moe_nvfp4_sort_routes, small(T, "T"), E, small(K, "K"), flat_i32(a[1], "topk_ids", {T, K}),
+                flat_i32(a[2], "count", {E}), flat_i32(a[3], "offsets", {(int64_t)E + 1}),
+                flat_i32(a[4], "row_of_route", {T, K}), flat_i32(a[5], "route_of_row", {T * K}), ws.p, ws.bytes,
+                handle(a[7]));
 }
 
 int dispatch(PyObject* const* a) {
     const RowArgs r = row_args(a[0], "x", a[3], a[1]);
-    return moe_nvfp4_dispatch(r.tokens.T, r.tokens.H, r.K, r.count, r.tokens.dtype, r.tokens.p, r.tokens.stride,
-                              r.row_of_route, reinterpret_cast<int32_t*>(word(a[2], "rows_used")), r.rows, handle(a[4]));
+    return call(moe_nvfp4_dispatch, r.tokens.T, r.tokens.H, r.K, r.count, r.tokens.dtype, r.tokens.p, r.tokens.stride,
+                r.row_of_route, reinterpret_cast<int32_t*>(word(a[2], "rows_used")), r.rows, handle(a[4]));
 }
 
 int dispatch_backward(PyObject* const* a) {
     const RowArgs r = row_args(a[2], "dx", a[0], a[1]);
-    return moe_nvfp4_dispatch_backward(r.tokens.T, r.tokens.H, r.K, r.count, r.tokens.dtype, r.rows, r.row_of_route,
-                                       r.tokens.p, r.tokens.stride, handle(a[3]));
+    return call(moe_nvfp4_dispatch_backward, r.tokens.T, r.tokens.H, r.K, r.count, r.tokens.dtype, r.rows,
+                r.row_of_route, r.tokens.p, r.tokens.stride, handle(a[3]));
 }
 
 int combine(PyObject* const* a) {
     const RowArgs r = row_args(a[3], "y", a[0], a[1]);
-    return moe_nvfp4_combine(r.tokens.T, r.tokens.H, r.K, r.count, r.tokens.dtype, r.rows, r.row_of_route,
-                             flat_f32(a[2], "topk_w", {r.tokens.T, r.K}), r.tokens.p, r.tokens.stride, handle(a[4]));
+    return call(moe_nvfp4_combine, r.tokens.T, r.tokens.H, r.K, r.count, r.tokens.dtype, r.rows, r.row_of_route,
+                flat_f32(a[2], "topk_w", {r.tokens.T, r.K}), r.tokens.p, r.tokens.stride, handle(a[4]));
 }
 
 int combine_backward(PyObject* const* a) {
     const RowArgs r = row_args(a[0], "dy", a[1], a[2]);
-    return moe_nvfp4_combine_backward(
-        r.tokens.T, r.tokens.H, r.K, r.count, r.tokens.dtype, r.tokens.p, r.tokens.stride, r.rows, r.row_of_route,
-        flat_f32(a[3], "topk_w", {r.tokens.T, r.K}), reinterpret_cast<int32_t*>(word(a[4], "rows_used")),
-        flat(a[5], "do_rows", r.tokens.type, {r.count, r.tokens.H}), flat_f32(a[6], "dw", {r.tokens.T, r.K}),
-        handle(a[7]));
+    return call(moe_nvfp4_combine_backward, r.tokens.T, r.tokens.H, r.K, r.count, r.tokens.dtype, r.tokens.p,
+                r.tokens.stride, r.rows, r.row_of_route, flat_f32(a[3], "topk_w", {r.tokens.T, r.K}),
+                reinterpret_cast<int32_t*>(word(a[4], "rows_used")),
+                flat(a[5], "do_rows", r.tokens.type, {r.count, r.tokens.H}), flat_f32(a[6], "dw", {r.tokens.T, r.K}),
+                handle(a[7]));
 }
 
 using ExpertEntry = moe_status (*)(int64_t, int, int, int, const void*, const void*, const int32_t*, const int32_t*,
@@ -227,8 +237,8 @@ int expert_product(PyObject* const* a, int weights, ExpertEntry entry, bool firs
     if (offsets.scalar_type() != at::kInt) wrong_type("offsets must be Int");
     if (offsets.dim() != 1 || offsets.size(0) < E || !offsets.is_contiguous())
         wrong_value("offsets must be contiguous [E] or longer");
-    return entry(R, small(N, "N"), small(K, "K"), small(E, "E"), first, second, flat_i32(a[2], "count", {E}),
-                 static_cast<const int32_t*>(offsets.data_ptr()), out, word(a[5], "status"), handle(a[6]));
+    return call(entry, R, small(N, "N"), small(K, "K"), small(E, "E"), first, second, flat_i32(a[2], "count", {E}),
+                static_cast<const int32_t*>(offsets.data_ptr()), out, word(a[5], "status"), handle(a[6]));
 }
 
 int expert_linear(PyObject* const* a) {
@@ -253,19 +263,18 @@ Rows same_rows(PyObject* o, const char* name, const Rows& x) {
 
 int layer_norm(PyObject* const* a) {
     const Rows x = rows2d(a[0], "x"), y = same_rows(a[4], "y", x);
-    return moe_nvfp4_layer_norm(x.T, x.H, x.dtype, x.p, x.stride, flat_f32(a[1], "gamma", {x.H}),
-                                flat_f32(a[2], "beta", {x.H}, true), (float)number(a[3], "eps"), y.p, y.stride,
-                                flat_f32(a[5], "mean", {x.T}, true), flat_f32(a[6], "rstd", {x.T}, true), handle(a[7]));
+    return call(moe_nvfp4_layer_norm, x.T, x.H, x.dtype, x.p, x.stride, flat_f32(a[1], "gamma", {x.H}),
+                flat_f32(a[2], "beta", {x.H}, true), (float)number(a[3], "eps"), y.p, y.stride,
+                flat_f32(a[5], "mean", {x.T}, true), flat_f32(a[6], "rstd", {x.T}, true), handle(a[7]));
 }
 
 int layer_norm_backward(PyObject* const* a) {
     const Rows x = rows2d(a[1], "x"), dy = same_rows(a[0], "dy", x), dx = same_rows(a[5], "dx", x);
     const Space ws = workspace(a[8]);
-    return moe_nvfp4_layer_norm_backward(x.T, x.H, x.dtype, dy.p, dy.stride, x.p, x.stride,
-                                         flat_f32(a[2], "gamma", {x.H}), flat_f32(a[3], "mean", {x.T}),
-                                         flat_f32(a[4], "rstd", {x.T}), dx.p, dx.stride,
-                                         flat_f32(a[6], "dgamma", {x.H}), flat_f32(a[7], "dbeta", {x.H}, true), ws.p,
-                                         ws.bytes, handle(a[9]));
+    return call(moe_nvfp4_layer_norm_backward, x.T, x.H, x.dtype, dy.p, dy.stride, x.p, x.stride,
+                flat_f32(a[2], "gamma", {x.H}), flat_f32(a[3], "mean", {x.T}), flat_f32(a[4], "rstd", {x.T}), dx.p,
+                dx.stride, flat_f32(a[6], "dgamma", {x.H}), flat_f32(a[7], "dbeta", {x.H}, true), ws.p, ws.bytes,
+                handle(a[9]));
 }
 
 template <typename T>
@@ -276,16 +285,16 @@ T* address(PyObject* o) {
 // The list's host arrays, as addresses, then the norm.
 int grad_norm(PyObject* const* a) {
     const Space ws = workspace(a[5]);
-    return moe_nvfp4_grad_norm(small(integer(a[0], "n"), "n"), address<const void* const>(a[1]),
-                               address<const int64_t>(a[2]), address<const int32_t>(a[3]), flat_f32(a[4], "norm", {1}),
-                               ws.p, ws.bytes, handle(a[6]));
+    return call(moe_nvfp4_grad_norm, small(integer(a[0], "n"), "n"), address<const void* const>(a[1]),
+                address<const int64_t>(a[2]), address<const int32_t>(a[3]), flat_f32(a[4], "norm", {1}), ws.p,
+                ws.bytes, handle(a[6]));
 }
 
 int grad_clip(PyObject* const* a) {
-    return moe_nvfp4_grad_clip(small(integer(a[0], "n"), "n"), address<const void* const>(a[1]),
-                               address<void* const>(a[2]), address<const int64_t>(a[3]), address<const int32_t>(a[4]),
-                               flat_f32(a[5], "norm", {1}), (float)number(a[6], "max_norm"),
-                               (float)number(a[7], "eps"), handle(a[8]));
+    return call(moe_nvfp4_grad_clip, small(integer(a[0], "n"), "n"), address<const void* const>(a[1]),
+                address<void* const>(a[2]), address<const int64_t>(a[3]), address<const int32_t>(a[4]),
+                flat_f32(a[5], "norm", {1}), (float)number(a[6], "max_norm"), (float)number(a[7], "eps"),
+                handle(a[8]));
 }
 
 // Runs one of the functions above on n arguments; no C++ exception leaves.

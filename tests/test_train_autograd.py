@@ -1,5 +1,8 @@
 """train.py beside the block: what its functions do with dropped routes, row
 buffers of another size, odd gradients, and errors found on the device."""
+import threading
+import time
+
 import pytest
 import torch
 import torch.nn.functional as F
@@ -155,3 +158,33 @@ def test_bad_segments_are_reported():
     routes.count.copy_(keep)
     y.sum().backward()
     routes.check()
+
+
+def test_other_threads_run_while_a_launch_waits():
+    """A launch into a full queue waits for the device; the interpreter is free
+    meanwhile.  The queue fills behind a kernel of half a second and more."""
+    x, gamma = torch.zeros(4, 64, device="cuda"), torch.ones(64, device="cuda")
+    y, side = torch.empty_like(x), torch.cuda.Stream()
+    api.moe_nvfp4_layer_norm(x, gamma, None, 1e-5, y)
+    torch.cuda.synchronize()
+    took = []
+
+    def work():
+        t0 = time.perf_counter()
+        for _ in range(6000):
+            api.moe_nvfp4_layer_norm(x, gamma, None, 1e-5, y, None, None, side)
+        took.append(time.perf_counter() - t0)
+
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(2_000_000_000)
+    worker = threading.Thread(target=work)
+    longest, last = 0.0, time.perf_counter()
+    worker.start()             # may come back only once the worker's launch does
+    while worker.is_alive():
+        time.sleep(0.001)
+        now = time.perf_counter()
+        longest, last = max(longest, now - last), now
+    worker.join()
+    torch.cuda.synchronize()
+    assert took[0] > 0.3, "the queue never filled"
+    assert longest < 0.5 * took[0], (longest, took[0])
