@@ -188,3 +188,16 @@ def test_other_threads_run_while_a_launch_waits():
     torch.cuda.synchronize()
     assert took[0] > 0.3, "the queue never filled"
     assert longest < 0.5 * took[0], (longest, took[0])
+
+
+def test_transforms_without_a_rule_raise():
+    gamma = torch.ones(64, device="cuda")
+    x = torch.randn(3, 5, 64, device="cuda")
+    with pytest.raises(RuntimeError):
+        torch.func.vmap(lambda v: train.layer_norm(v, gamma))(x)
+    with pytest.raises((RuntimeError, NotImplementedError)):
+        torch.func.jvp(lambda v: train.layer_norm(v, gamma), (x[0],), (x[1],))
+    v = x[1].clone().requires_grad_(True)
+    (d,) = torch.autograd.grad(train.layer_norm(v, gamma).square().sum(), v, create_graph=True)
+    with pytest.raises(RuntimeError):
+        d.sum().backward()
