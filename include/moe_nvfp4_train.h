@@ -160,8 +160,10 @@ MOE_API moe_status moe_nvfp4_layer_norm_backward(int T, int H, int dtype,
  *              NaN if the quotient is
  * Two calls, so that norms of several devices can be joined between them.
  * out[i] has grads[i]'s type and may be grads[i] itself; in place with s = 1
- * nothing is written.  The squares are FP32: an element beyond 1.8e19 in
- * magnitude makes the norm infinite, one below 1e-23 adds nothing.
+ * nothing is written.  The squares and their sum are FP32: a norm above 1.8e19
+ * is infinite, although every element may be smaller (s is 0 then), elements
+ * below 1e-19 in magnitude lose digits and those below 1e-23 add nothing.  The
+ * tensors are on the current device.
  * 0 <= n <= 65536, 0 <= numel < 2^40, each pointer aligned to its element;
  * a tensor of no elements may be NULL.  Sizes and pointers are not compared
  * for overlaps: the outputs must not overlap each other or another input.
