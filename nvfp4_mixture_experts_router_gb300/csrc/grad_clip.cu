@@ -27,7 +27,9 @@ constexpr int kChunkMost = 16384;     // elements: a thread's kInFlight loads of
 constexpr int kChunkLeast = 4096;
 constexpr int kChunkStep = 2048;
 constexpr int kInFlight = 4;          // 16-byte loads of a thread
-constexpr int kNormBlocks = 608;      // partial sums per launch: four blocks an SM
+// Partial sums per launch, four blocks on each of 152 SMs: a constant, as the
+// workspace's size is asked for without a device and the sums' order follows it
+constexpr int kNormBlocks = 608;
 
 struct GradEntry {
     const void* in;
@@ -276,9 +278,8 @@ size_t grad_norm_workspace_bytes(int n) {
     return align_up(launches * kNormBlocks * 4, 256);
 }
 
-cudaError_t launch_grad_norm(const LaunchCtx& c, int sms, int n, const void* const* grads, const int64_t* numels,
+cudaError_t launch_grad_norm(const LaunchCtx& c, int n, const void* const* grads, const int64_t* numels,
                              const int32_t* dtypes, float* norm, float* workspace) {
-    (void)sms;
     int used = 0;
     cudaError_t e = for_tables(n, grads, nullptr, numels, dtypes, false, [&](auto& t) {
         const int blocks = t.chunks < kNormBlocks ? t.chunks : kNormBlocks;

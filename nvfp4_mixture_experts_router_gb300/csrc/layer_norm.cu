@@ -37,7 +37,9 @@ namespace {
 
 constexpr int kNormThreads = 256;
 constexpr int kNormParts = 64;      // row groups of the column sums, long rows
-constexpr int kNormSms = 152;       // the persistent backward kernels' grids are multiples of this
+// The persistent kernels' grids are multiples of this.  A constant: the backward's
+// workspace, a partial sum a block, is sized without a device
+constexpr int kNormSms = 152;
 constexpr int kCols = 8;            // columns per thread of the row kernels
 constexpr int kRowColumns = 32 * 32 * kCols;
 constexpr int kRingCols = 16;       // columns per thread of the ring kernel

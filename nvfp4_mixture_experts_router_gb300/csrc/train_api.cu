@@ -310,7 +310,7 @@ moe_status moe_nvfp4_grad_norm(int n, const void* const* grads, const int64_t* n
     int sms = 0;
     const moe_status st = begin(stream, &c, &sms);
     if (st != MOE_OK) return st;
-    return cuda_status(launch_grad_norm(c, sms, n, grads, numels, dtypes, norm, static_cast<float*>(workspace)));
+    return cuda_status(launch_grad_norm(c, n, grads, numels, dtypes, norm, static_cast<float*>(workspace)));
 }
 
 moe_status moe_nvfp4_grad_clip(int n, const void* const* grads, void* const* out, const int64_t* numels,

@@ -34,7 +34,7 @@ cudaError_t launch_layer_norm_backward(const LaunchCtx& c, int T, int H, int ele
 
 // grad_clip.cu
 size_t grad_norm_workspace_bytes(int n);
-cudaError_t launch_grad_norm(const LaunchCtx& c, int sms, int n, const void* const* grads, const int64_t* numels,
+cudaError_t launch_grad_norm(const LaunchCtx& c, int n, const void* const* grads, const int64_t* numels,
                              const int32_t* dtypes, float* norm, float* workspace);
 cudaError_t launch_grad_clip(const LaunchCtx& c, int sms, int n, const void* const* grads, void* const* out,
                              const int64_t* numels, const int32_t* dtypes, const float* norm, float max_norm,
