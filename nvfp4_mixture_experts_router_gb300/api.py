@@ -324,10 +324,10 @@ def moe_nvfp4_sort_routes(E: int, topk_ids: torch.Tensor, count: torch.Tensor, o
         E, topk_ids, count, offsets, row_of_route, route_of_row, workspace, stream))
 
 
-def moe_nvfp4_dispatch(x: torch.Tensor, row_of_route: torch.Tensor, rows_used: Optional[torch.Tensor],
-                       x_rows: torch.Tensor, stream=None) -> None:
+def moe_nvfp4_dispatch(x: Optional[torch.Tensor], row_of_route: Optional[torch.Tensor],
+                       rows_used: Optional[torch.Tensor], x_rows: torch.Tensor, stream=None) -> None:
     """x_rows[row_of_route[t, k]] = x[t]; rows from rows_used (one device int32,
-    None: none) on are set to zero."""
+    None: none) on are set to zero.  x and row_of_route None: no tokens."""
     _check("moe_nvfp4_dispatch", (_native or native()).dispatch(x, row_of_route, rows_used, x_rows, stream))
 
 

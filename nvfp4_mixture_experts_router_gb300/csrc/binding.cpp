@@ -186,6 +186,12 @@ int sort_routes(PyObject* const* a) {
 }
 
 int dispatch(PyObject* const* a) {
+    if (a[0] == Py_None && a[1] == Py_None) {        // no tokens
+        const Rows r = rows2d(a[3], "the expert-ordered rows");
+        void* p = flat(a[3], "the expert-ordered rows", r.type, {r.T, r.H});
+        return call(moe_nvfp4_dispatch, 0, r.H, 1, r.T, r.dtype, nullptr, r.H, nullptr,
+                    reinterpret_cast<int32_t*>(word(a[2], "rows_used")), p, handle(a[4]));
+    }
     const RowArgs r = row_args(a[0], "x", a[3], a[1]);
     return call(moe_nvfp4_dispatch, r.tokens.T, r.tokens.H, r.K, r.count, r.tokens.dtype, r.tokens.p, r.tokens.stride,
                 r.row_of_route, reinterpret_cast<int32_t*>(word(a[2], "rows_used")), r.rows, handle(a[4]));

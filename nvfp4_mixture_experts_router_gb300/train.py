@@ -17,6 +17,7 @@ examples/moe_block.py trains one.
 from __future__ import annotations
 
 from dataclasses import dataclass
+from functools import cached_property
 from typing import Iterable, Optional, Union
 
 import torch
@@ -39,7 +40,7 @@ class Routes:
     def rows(self) -> int:
         return self.route_of_row.shape[0]
 
-    @property
+    @cached_property
     def used(self) -> torch.Tensor:
         """The number of kept routes, one device int32."""
         return self.offsets[self.E:]
@@ -79,7 +80,7 @@ def _check_rows(rows: torch.Tensor, routes: Routes, name: str) -> None:
 
 def _clear_tail(rows: torch.Tensor, routes: Routes) -> torch.Tensor:
     """Zeros in the rows past the kept routes (a dispatch of no tokens)."""
-    api.moe_nvfp4_dispatch(rows[:0], routes.row_of_route[:0], routes.used, rows)
+    api.moe_nvfp4_dispatch(None, None, routes.used, rows)
     return rows
 
 

@@ -135,8 +135,15 @@ def test_a_dispatch_of_no_tokens_clears_rows(rows, used, H, dt):
     out = torch.full((rows, H), 7.0, dtype=dt, device="cuda")
     none = torch.empty(0, 3, dtype=torch.int32, device="cuda")
     api.moe_nvfp4_dispatch(out[:0], none, torch.tensor([used], dtype=torch.int32, device="cuda"), out)
-    used = max(used, 0)
-    assert bool((out[:used] == 7.0).all()) and not out[used:].any()
+    keep = max(used, 0)
+    assert bool((out[:keep] == 7.0).all()) and not out[keep:].any()
+    out.fill_(7.0)
+    api.moe_nvfp4_dispatch(None, None, torch.tensor([used], dtype=torch.int32, device="cuda"), out)
+    assert bool((out[:keep] == 7.0).all()) and not out[keep:].any()
+    with pytest.raises(TypeError):
+        api.moe_nvfp4_dispatch(None, none, None, out)
+    with pytest.raises(TypeError):
+        api.moe_nvfp4_dispatch(out[:0], None, None, out)
 
 
 def test_bad_segments_are_reported():
