@@ -34,7 +34,7 @@ class Routes:
     offsets: torch.Tensor       # int32 [E + 1]
     row_of_route: torch.Tensor  # int32 [T, K], -1: dropped
     route_of_row: torch.Tensor  # int32 [T * K], -1: no route
-    status: Optional[torch.Tensor] = None   # int32 [1]: errors that the experts' products found on the device
+    status: Optional[torch.Tensor] = None   # int32 [1]: errors that the device's products found
 
     @property
     def rows(self) -> int:
@@ -46,14 +46,28 @@ class Routes:
         return self.offsets[self.E:]
 
     def check(self) -> None:
-        """Waits for the current stream and raises MoEError if a product on these
-        routes, or a gradient of one, found a segment outside its rows
-        (MOE_ERR_INVALID_ARG) or gave up a wait (MOE_ERR_TIMEOUT: its output is
-        undefined).  An error is raised once."""
-        if self.status is not None:
-            code = api.moe_nvfp4_last_device_status(self.status)
-            if code != api.MOE_OK:
-                raise api.MoEError("an experts' product", code)
+        """Waits for the current stream and raises MoEError if an experts' product
+        or a gradient of one, on these or other routes of the device, has found a
+        segment outside its rows (MOE_ERR_INVALID_ARG) or given up a wait
+        (MOE_ERR_TIMEOUT: its output is undefined) since the last error was raised."""
+        if self.status is not None and int(self.status) != 0:
+            raise api.MoEError("an experts' product", api.moe_nvfp4_last_device_status(self.status))
+
+
+_status_words = {}
+
+
+def _status_word(device: torch.device) -> torch.Tensor:
+    """The device's status word for the products of this module.  One for all
+    routes: a word each cost the sort a launch to clear it (16 -> 32 us of host
+    time)."""
+    word = _status_words.get(device)
+    if word is None:
+        word = torch.zeros(1, dtype=torch.int32, device=device)
+        if not torch.cuda.is_current_stream_capturing():    # else it is the graph's, cleared by its replays
+            torch.cuda.current_stream(device).synchronize() # other streams use it too
+            word = _status_words.setdefault(device, word)
+    return word
 
 
 def sort_routes(topk_ids: torch.Tensor, E: int) -> Routes:
@@ -62,12 +76,13 @@ def sort_routes(topk_ids: torch.Tensor, E: int) -> Routes:
     T, K = topk_ids.shape
     i32 = dict(dtype=torch.int32, device=topk_ids.device)
     r = Routes(E, torch.empty(E, **i32), torch.empty(E + 1, **i32), torch.empty(T, K, **i32),
-               torch.empty(T * K, **i32), torch.zeros(1, **i32))
+               torch.empty(T * K, **i32))
     nbytes = api.moe_nvfp4_sort_workspace_bytes(T, E, K)
     if nbytes == 0:
         raise api.MoEError("moe_nvfp4_sort_workspace_bytes", api.MOE_ERR_INVALID_ARG)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=topk_ids.device)
     api.moe_nvfp4_sort_routes(E, topk_ids, r.count, r.offsets, r.row_of_route, r.route_of_row, ws)
+    r.status = _status_word(topk_ids.device)
     return r
 
 

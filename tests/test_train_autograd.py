@@ -208,3 +208,26 @@ def test_transforms_without_a_rule_raise():
     (d,) = torch.autograd.grad(train.layer_norm(v, gamma).square().sum(), v, create_graph=True)
     with pytest.raises(RuntimeError):
         d.sum().backward()
+
+
+def test_routes_of_host_tensors_are_a_type_error():
+    with pytest.raises(TypeError):
+        train.sort_routes(torch.zeros(4, 2, dtype=torch.int32), 8)
+
+
+def test_routes_first_sorted_in_a_graph(monkeypatch):
+    """The status word is then the graph's own, cleared by its replays."""
+    monkeypatch.setattr(train, "_status_words", {})
+    ids, _ = routes_of(30, 4, 2, 0.0)
+    monkeypatch.setattr(train, "_status_words", {})
+    x, w = torch.randn(60, 64, device="cuda").bfloat16(), torch.randn(4, 32, 64, device="cuda").bfloat16()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        routes = train.sort_routes(ids, 4)
+        y = train.expert_linear(x, w, routes)
+    graph.replay()
+    routes.check()
+    again = train.sort_routes(ids, 4)
+    assert again.status.data_ptr() != routes.status.data_ptr()
+    assert torch.equal(train.expert_linear(x, w, again), y)
+    again.check()
