@@ -208,7 +208,6 @@ def expert_linear(x_rows: torch.Tensor, w: torch.Tensor, routes: Routes) -> torc
     return _ExpertLinear.apply(x_rows.contiguous(), w, routes)
 
 
-@torch.no_grad()
 def clip_grad_norm_(parameters: Union[torch.Tensor, Iterable[torch.Tensor]], max_norm: float,
                     eps: float = 1e-6) -> torch.Tensor:
     """Scales the gradients of ``parameters`` (or of one tensor) in place to a
@@ -225,11 +224,13 @@ def clip_grad_norm_(parameters: Union[torch.Tensor, Iterable[torch.Tensor]], max
     device = grads[0].device
     norm = torch.empty(1, dtype=torch.float32, device=device)
     ws = torch.empty(api.moe_nvfp4_grad_norm_workspace_bytes(len(grads)), dtype=torch.uint8, device=device)
-    packed = [g if g.is_contiguous() else g.contiguous() for g in grads]
+    strided = [i for i, g in enumerate(grads) if not g.is_contiguous()]
+    packed = list(grads)
+    for i in strided:
+        packed[i] = grads[i].detach().contiguous()
     gl = api.GradList(packed)
     api.moe_nvfp4_grad_norm(gl, norm, ws)
     api.moe_nvfp4_grad_clip(gl, norm, max_norm, eps)
-    for g, c in zip(grads, packed):
-        if g is not c:
-            g.copy_(c)
+    for i in strided:
+        grads[i].detach().copy_(packed[i])
     return norm
