@@ -415,10 +415,10 @@ class GradList:
                 raise TypeError("gradients must be bfloat16 or float32 CUDA tensors, each output of its gradient's type")
             if o.numel() != g.numel() or not (g.is_contiguous() and o.is_contiguous()):
                 raise ValueError("gradients and outputs must be contiguous and of the same size")
-        self.device = self.grads[0].device if self.grads else None
-        if any(t.device != self.device for t in (self.grads if out is None else self.grads + self.out)):
+        device = self.grads[0].device if self.grads else None
+        if any(t.device != device for t in (self.grads if out is None else self.grads + self.out)):
             raise ValueError("gradients and outputs must be on one device")
-        self.index = self.device.index if self.grads else None
+        self.index = device.index if self.grads else 0      # compared with the norm's in _binding.so
         n = self.n = len(self.grads)
         # the host arrays of the C calls, and their addresses
         self._arrays = ((ctypes.c_void_p * n)(*[g.data_ptr() for g in self.grads]),
@@ -432,29 +432,17 @@ def moe_nvfp4_grad_norm_workspace_bytes(n: int) -> int:
     return int(lib().moe_nvfp4_grad_norm_workspace_bytes(n))
 
 
-def _refuse_device(norm, grads: GradList) -> None:
-    """The list reaches the library as addresses: its device is compared with
-    the norm's here, and the norm's with the current one in _binding.so (which
-    also refuses a norm that is no CUDA tensor)."""
-    if grads.n and getattr(norm, "is_cuda", False) and norm.device != grads.device:
-        raise ValueError(f"the gradients are on {grads.device}, not on the norm's device {norm.device}")
-
-
 def moe_nvfp4_grad_norm(grads: GradList, norm: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
     """norm[0] (float32) = sqrt of the sum of the squares of every gradient's elements."""
-    if not isinstance(norm, torch.Tensor) or norm.get_device() != grads.index:
-        _refuse_device(norm, grads)
     _check("moe_nvfp4_grad_norm", (_native or native()).grad_norm(
-        grads.n, grads._grads, grads._numels, grads._dtypes, norm, workspace, stream))
+        grads.n, grads.index, grads._grads, grads._numels, grads._dtypes, norm, workspace, stream))
 
 
 def moe_nvfp4_grad_clip(grads: GradList, norm: torch.Tensor, max_norm: float, eps: float = 1e-6,
                         stream=None) -> None:
     """out = gradient * min(1, max_norm / (norm + eps)) for every gradient of the list."""
-    if not isinstance(norm, torch.Tensor) or norm.get_device() != grads.index:
-        _refuse_device(norm, grads)
     _check("moe_nvfp4_grad_clip", (_native or native()).grad_clip(
-        grads.n, grads._grads, grads._out, grads._numels, grads._dtypes, norm, max_norm, eps, stream))
+        grads.n, grads.index, grads._grads, grads._out, grads._numels, grads._dtypes, norm, max_norm, eps, stream))
 
 
 # ---- convenience ---------------------------------------------------------------

@@ -288,19 +288,27 @@ T* address(PyObject* o) {
     return reinterpret_cast<T*>(integer(o, "an array's address"));
 }
 
-// The list's host arrays, as addresses, then the norm.
+// The list's length and device and its host arrays, as addresses, then the norm,
+// which is on the current device: the list has to be there too.
+int list_length(PyObject* const* a, PyObject* norm) {
+    const int n = small(integer(a[0], "n"), "n");
+    if (n > 0 && tensor(norm, "norm").get_device() != integer(a[1], "the gradients' device"))
+        wrong_value("the gradients are not on the norm's device");
+    return n;
+}
+
 int grad_norm(PyObject* const* a) {
-    const Space ws = workspace(a[5]);
-    return call(moe_nvfp4_grad_norm, small(integer(a[0], "n"), "n"), address<const void* const>(a[1]),
-                address<const int64_t>(a[2]), address<const int32_t>(a[3]), flat_f32(a[4], "norm", {1}), ws.p,
-                ws.bytes, handle(a[6]));
+    const Space ws = workspace(a[6]);
+    return call(moe_nvfp4_grad_norm, list_length(a, a[5]), address<const void* const>(a[2]),
+                address<const int64_t>(a[3]), address<const int32_t>(a[4]), flat_f32(a[5], "norm", {1}), ws.p,
+                ws.bytes, handle(a[7]));
 }
 
 int grad_clip(PyObject* const* a) {
-    return call(moe_nvfp4_grad_clip, small(integer(a[0], "n"), "n"), address<const void* const>(a[1]),
-                address<void* const>(a[2]), address<const int64_t>(a[3]), address<const int32_t>(a[4]),
-                flat_f32(a[5], "norm", {1}), (float)number(a[6], "max_norm"), (float)number(a[7], "eps"),
-                handle(a[8]));
+    return call(moe_nvfp4_grad_clip, list_length(a, a[6]), address<const void* const>(a[2]),
+                address<void* const>(a[3]), address<const int64_t>(a[4]), address<const int32_t>(a[5]),
+                flat_f32(a[6], "norm", {1}), (float)number(a[7], "max_norm"), (float)number(a[8], "eps"),
+                handle(a[9]));
 }
 
 // Runs one of the functions above on n arguments; no C++ exception leaves.
@@ -339,8 +347,8 @@ PyMethodDef g_methods[] = {
     method<expert_linear_wgrad, 7>("expert_linear_wgrad"),
     method<layer_norm, 8>("layer_norm"),
     method<layer_norm_backward, 10>("layer_norm_backward"),
-    method<grad_norm, 7>("grad_norm"),
-    method<grad_clip, 9>("grad_clip"),
+    method<grad_norm, 8>("grad_norm"),
+    method<grad_clip, 10>("grad_clip"),
     {nullptr, nullptr, 0, nullptr},
 };
 

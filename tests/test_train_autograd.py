@@ -27,6 +27,20 @@ def test_a_norm_that_is_no_cuda_tensor_is_a_type_error(norm):
         api.moe_nvfp4_grad_clip(grads, norm, 1.0)
 
 
+def test_a_list_of_another_device_than_the_norm_is_refused():
+    """The list's device is claimed, not real: its tensors stay where they are."""
+    g, norm, ws = torch.ones(8, device="cuda"), torch.full((1,), 7.0, device="cuda"), torch.zeros(256 * 1024, device="cuda")
+    grads = api.GradList([g])
+    assert grads.index == 0
+    grads.index = 1
+    with pytest.raises(ValueError, match="device"):
+        api.moe_nvfp4_grad_norm(grads, norm, ws)
+    with pytest.raises(ValueError, match="device"):
+        api.moe_nvfp4_grad_clip(grads, norm, 1.0)
+    torch.cuda.synchronize()
+    assert float(norm) == 7.0 and bool((g == 1.0).all())
+
+
 def param(grad):
     p = torch.nn.Parameter(torch.zeros(grad.shape, dtype=grad.dtype, device=grad.device))
     p.grad = grad
