@@ -69,8 +69,9 @@ MOE_API moe_status moe_nvfp4_sort_routes(int T, int E, int K, const int32_t* top
  * combine_backward:  do_rows[row(t,k)] = topk_w[t][k] * dy[t]
  *                    dw[t][k] = sum_h dy[t][h] * o_rows[row(t,k)][h]; 0 if dropped
  * topk_w and dw are FP32 [T][K].  rows_used: device int32, rows [rows_used,
- * rows) of x_rows / do_rows are set to zero (offsets + E of the sort);
- * NULL leaves every row that no route owns as it was. */
+ * rows) of x_rows / do_rows are set to zero (offsets + E of the sort), by a
+ * dispatch of T = 0 tokens those alone; NULL leaves every row that no route
+ * owns as it was. */
 MOE_API moe_status moe_nvfp4_dispatch(int T, int H, int K, int64_t rows, int dtype,
                                       const void* x, int64_t x_stride,
                                       const int32_t* row_of_route, const int32_t* rows_used,

@@ -164,7 +164,7 @@ RowArgs row_args(PyObject* tokens, const char* name, PyObject* rows, PyObject* r
 }
 
 // The C entry, without the interpreter's lock: a launch may wait for room in the
-// device's queue, and other threads run meanwhile (0.1 us a call).
+// device's queue, and other threads run meanwhile (0.05 us of a call's 2.2).
 template <typename... P, typename... A>
 int call(moe_status (*f)(P...), const A&... a) {
     PyThreadState* const thread = PyEval_SaveThread();

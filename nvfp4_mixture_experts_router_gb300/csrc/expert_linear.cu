@@ -43,8 +43,9 @@
 // sustained by cuBLAS): 8 rows of 8 experts of 4096 x 7168 forward 72-75 us
 // (6.3-6.5 TB/s); 2999 rows of 60 experts of 1536 x 2048 dgrad 65 (6.2 TB/s),
 // wgrad 72 (5.6 TB/s of gradients written); 16384 rows of 16 experts of
-// 4096 x 7168 forward 600-640 us, dgrad 575-625, wgrad 625-650 (1.5-1.65
-// PFLOP/s; equal segments on cuBLAS 510-545, 560-570, 550-570).
+// 4096 x 7168 forward 585-675 us, dgrad 580-625, wgrad 625-660 (1.43-1.65
+// PFLOP/s, by the box and by what ran before; equal segments 550-580, 540-610 and
+// 600-640, on cuBLAS 500-545, 515-570 and 530-570).
 #include <cudaTypedefs.h>
 #include <math.h>
 

@@ -530,7 +530,8 @@ cudaError_t launch_dispatch(const LaunchCtx& c, int T, int H, int K, int64_t row
     const int n = H / per;
     // groups of threads: a token each, and of the rows to clear 32 each at most
     // (as many as a token has routes: more groups than tokens only where the
-    // buffer is larger than the routes, as in a call that clears and copies none)
+    // buffer is larger than the routes, as in a call that clears and copies none:
+    // half of 131072 rows of 7168 BF16 2037 us with one group, 134 so)
     const int groups = rows_used && T < rows / 32 ? (int)(rows / 32) : T;
     // few tokens: a vector a thread over more blocks; else four, so that a
     // thread has four loads in flight
