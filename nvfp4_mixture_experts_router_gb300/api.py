@@ -11,7 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 from dataclasses import dataclass
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -42,6 +42,10 @@ MOE_W8A8_MXFP8 = 3 << 2
 
 MOE_DTYPE_BF16, MOE_DTYPE_F32 = 0, 1
 MOE_DEBUG_NORM_SKIP_COPY = 0x100
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_GROUP_MAX, MOE_GROUP_TOP2 = 0, 1
+MOE_SCALE_ROW, MOE_SCALE_BLOCK128, MOE_SCALE_MX = 0, 1, 2
+MOE_ADAMW_BLOCK = 256
 
 
 class MoEError(RuntimeError):
@@ -53,6 +57,23 @@ class MoEError(RuntimeError):
 class moe_shape(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int), ("H", ctypes.c_int), ("I", ctypes.c_int), ("E", ctypes.c_int),
                 ("K", ctypes.c_int)]
+
+
+class moe_route_rule(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("groups", ctypes.c_int32), ("topk_groups", ctypes.c_int32),
+                ("group_score", ctypes.c_int32), ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class moe_adamw_tensor(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("param", "grad", "exp_avg", "exp_avg_sq", "exp_avg_scale",
+                                               "exp_avg_sq_scale", "master")] + \
+               [("numel", ctypes.c_int64)] + \
+               [(n, ctypes.c_int32) for n in ("param_dtype", "grad_dtype", "state_bits", "reserved")]
+
+
+class moe_adamw_rule(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps", "weight_decay", "max_norm",
+                                               "clip_eps")] + [("step", ctypes.c_int64)]
 
 
 _LAYOUT_FIELDS = ["rows_cap", "status", "topk_ids", "topk_w", "count", "offsets", "padded_offsets", "meta",
@@ -109,6 +130,12 @@ def lib():
             "moe_nvfp4_layer_norm": (c, [c, c, c, P, i64, P, P, f, P, i64, P, P, P]),
             "moe_nvfp4_layer_norm_workspace_bytes": (sz, [c, c]),
             "moe_nvfp4_layer_norm_backward": (c, [c, c, c, P, i64, P, i64, P, P, P, P, i64, P, P, P, sz, P]),
+            "moe_nvfp4_route_topk": (c, [c, c, c, c, P, i64, P, moe_route_rule, P, P, P]),
+            "moe_nvfp4_route_topk_backward": (c, [c, c, c, c, P, i64, P, P, moe_route_rule, P, i64, P]),
+            "moe_nvfp4_rms_norm": (c, [c, c, c, P, i64, P, i64, P, f, P, i64, P, i64, P, P, c, P, P]),
+            "moe_nvfp4_rms_norm_workspace_bytes": (sz, [c, c]),
+            "moe_nvfp4_rms_norm_backward": (c, [c, c, c, P, i64, P, i64, P, i64, P, P, P, i64, P, P, sz, P]),
+            "moe_nvfp4_adamw": (c, [c, P, moe_adamw_rule, P, P, P]),
             "moe_nvfp4_grad_norm_workspace_bytes": (sz, [c]),
             "moe_nvfp4_grad_norm": (c, [c, P, P, P, P, P, sz, P]),
             "moe_nvfp4_grad_clip": (c, [c, P, P, P, P, P, f, f, P]),
@@ -132,7 +159,9 @@ EXPORTED_TRAIN = ["moe_nvfp4_sort_workspace_bytes", "moe_nvfp4_sort_routes", "mo
                   "moe_nvfp4_dispatch_backward", "moe_nvfp4_combine", "moe_nvfp4_combine_backward",
                   "moe_nvfp4_expert_linear", "moe_nvfp4_expert_linear_dgrad", "moe_nvfp4_expert_linear_wgrad",
                   "moe_nvfp4_layer_norm", "moe_nvfp4_layer_norm_workspace_bytes", "moe_nvfp4_layer_norm_backward",
-                  "moe_nvfp4_grad_norm_workspace_bytes", "moe_nvfp4_grad_norm", "moe_nvfp4_grad_clip"]
+                  "moe_nvfp4_grad_norm_workspace_bytes", "moe_nvfp4_grad_norm", "moe_nvfp4_grad_clip",
+                  "moe_nvfp4_route_topk", "moe_nvfp4_route_topk_backward", "moe_nvfp4_rms_norm",
+                  "moe_nvfp4_rms_norm_workspace_bytes", "moe_nvfp4_rms_norm_backward", "moe_nvfp4_adamw"]
 EXPORTED_TRAIN.sort()
 NUM_STAGE_EVENTS = 8
 STAGES = ["router", "permute", "quantize_x", "fc1", "quantize_h", "fc2", "finalize"]
@@ -310,6 +339,31 @@ def native():
     return _native
 
 
+class RouteRule(NamedTuple):
+    """How experts are chosen (moe_route_rule)."""
+    score: int = MOE_SCORE_SOFTMAX
+    groups: int = 1
+    topk_groups: int = 1
+    group_score: int = MOE_GROUP_MAX
+    renormalize: bool = True
+    scale: float = 1.0
+
+
+def moe_nvfp4_route_topk(logits: torch.Tensor, bias: Optional[torch.Tensor], rule: RouteRule, topk_ids: torch.Tensor,
+                         topk_w: torch.Tensor, stream=None) -> None:
+    """The experts of each token, from logits [T, E] (bfloat16 or float32) and a
+    bias [E] that enters the choice alone (None: 0): topk_ids [T, K] int32, -1
+    where fewer can be chosen, and their weights topk_w [T, K]."""
+    _check("moe_nvfp4_route_topk", (_native or native()).route_topk(logits, bias, rule, topk_ids, topk_w, stream))
+
+
+def moe_nvfp4_route_topk_backward(logits: torch.Tensor, topk_ids: torch.Tensor, dw: torch.Tensor, rule: RouteRule,
+                                  dlogits: torch.Tensor, stream=None) -> None:
+    """dlogits [T, E] of the logits' type, from the gradient dw [T, K] of the weights."""
+    _check("moe_nvfp4_route_topk_backward", (_native or native()).route_topk_backward(
+        logits, topk_ids, dw, rule, dlogits, stream))
+
+
 def moe_nvfp4_sort_workspace_bytes(T: int, E: int, K: int) -> int:
     return int(lib().moe_nvfp4_sort_workspace_bytes(T, E, K))
 
@@ -395,6 +449,31 @@ def moe_nvfp4_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: torc
         dy, x, gamma, mean, rstd, dx, dgamma, dbeta, workspace, stream))
 
 
+def moe_nvfp4_rms_norm(x: torch.Tensor, residual: Optional[torch.Tensor], gamma: torch.Tensor, eps: float,
+                       h: Optional[torch.Tensor], y: Optional[torch.Tensor], q: Optional[torch.Tensor] = None,
+                       scales: Optional[torch.Tensor] = None, rstd: Optional[torch.Tensor] = None,
+                       stream=None) -> None:
+    """h = x + residual (rounded; x without a residual), y = h * rstd * gamma over
+    the rows of x [T, H].  h may be x or the residual.  q [T, H] float8_e4m3fn is y
+    by its scales: float32 [T], a row's; float32 [T, ceil(H / 128)]; or
+    float8_e8m0fnu (or uint8) [T, ceil(H / 32)], powers of two.  gamma [H] and rstd
+    [T] float32.  y or q may be None."""
+    _check("moe_nvfp4_rms_norm", (_native or native()).rms_norm(x, residual, gamma, eps, h, y, q, scales, rstd, stream))
+
+
+def moe_nvfp4_rms_norm_workspace_bytes(T: int, H: int) -> int:
+    return int(lib().moe_nvfp4_rms_norm_workspace_bytes(T, H))
+
+
+def moe_nvfp4_rms_norm_backward(dy: torch.Tensor, dh: Optional[torch.Tensor], h: torch.Tensor, gamma: torch.Tensor,
+                                rstd: torch.Tensor, dx: torch.Tensor, dgamma: torch.Tensor, workspace: torch.Tensor,
+                                stream=None) -> None:
+    """dx [T, H], of x and of the residual alike, and dgamma [H] of the RMS norm, from
+    the forward's h and rstd; dh is the gradient that reaches h from elsewhere."""
+    _check("moe_nvfp4_rms_norm_backward", (_native or native()).rms_norm_backward(
+        dy, dh, h, gamma, rstd, dx, dgamma, workspace, stream))
+
+
 _DTYPES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_F32}
 
 
@@ -443,6 +522,98 @@ def moe_nvfp4_grad_clip(grads: GradList, norm: torch.Tensor, max_norm: float, ep
     """out = gradient * min(1, max_norm / (norm + eps)) for every gradient of the list."""
     _check("moe_nvfp4_grad_clip", (_native or native()).grad_clip(
         grads.n, grads.index, grads._grads, grads._out, grads._numels, grads._dtypes, norm, max_norm, eps, stream))
+
+
+class AdamWRule(NamedTuple):
+    """The numbers of an AdamW step; max_norm and clip_eps count where a norm is given."""
+    lr: float = 1e-3
+    beta1: float = 0.9
+    beta2: float = 0.999
+    eps: float = 1e-8
+    weight_decay: float = 0.01
+    max_norm: float = 1.0
+    clip_eps: float = 1e-6
+
+
+class AdamWList:
+    """Parameters, their gradients and their states for moe_nvfp4_adamw: contiguous
+    CUDA tensors of one device.  exp_avg and exp_avg_sq are float32, or
+    float8_e4m3fn with a float32 scale for each MOE_ADAMW_BLOCK elements (of the
+    second moment's root) in exp_avg_scale and exp_avg_sq_scale; master holds
+    float32 values of bfloat16 parameters.  Entries of the scales and of master may
+    be None, and so may the whole lists.  Built once for buffers that stay where
+    they are (set_grads takes other gradients); it holds the tensors and their
+    addresses."""
+
+    def __init__(self, params, grads, exp_avg, exp_avg_sq, exp_avg_scale=None, exp_avg_sq_scale=None, master=None):
+        none = [None] * len(params)
+        self.params, self.exp_avg, self.exp_avg_sq = list(params), list(exp_avg), list(exp_avg_sq)
+        self.exp_avg_scale = none if exp_avg_scale is None else list(exp_avg_scale)
+        self.exp_avg_sq_scale = none if exp_avg_sq_scale is None else list(exp_avg_sq_scale)
+        self.master = none if master is None else list(master)
+        n = self.n = len(self.params)
+        if any(len(v) != n for v in (self.exp_avg, self.exp_avg_sq, self.exp_avg_scale, self.exp_avg_sq_scale,
+                                     self.master)):
+            raise ValueError("as many states as parameters")
+        device = self.params[0].device if n else None
+        self._array = (moe_adamw_tensor * n)()
+        for e, p, m, v, ms, vs, w in zip(self._array, self.params, self.exp_avg, self.exp_avg_sq, self.exp_avg_scale,
+                                         self.exp_avg_sq_scale, self.master):
+            bits = 8 if m.dtype == torch.float8_e4m3fn else 32
+            if p.dtype not in _DTYPES or m.dtype not in (torch.float32, torch.float8_e4m3fn) or v.dtype != m.dtype:
+                raise TypeError("parameters must be bfloat16 or float32, states float32 or float8_e4m3fn")
+            if w is not None and (p.dtype != torch.bfloat16 or w.dtype != torch.float32):
+                raise TypeError("master values are float32, of bfloat16 parameters")
+            if (ms is None) != (bits == 32) or (vs is None) != (bits == 32):
+                raise ValueError("states of 8 bits have scales, and only they")
+            if bits == 8 and (ms.dtype != torch.float32 or vs.dtype != torch.float32):
+                raise TypeError("scales must be float32")
+            numel, blocks = p.numel(), -(-p.numel() // MOE_ADAMW_BLOCK)
+            for t, size in ((p, numel), (m, numel), (v, numel), (w, numel), (ms, blocks), (vs, blocks)):
+                if t is None:
+                    continue
+                if not t.is_cuda:
+                    raise TypeError("parameters and states must be CUDA tensors")
+                if t.device != device:
+                    raise ValueError("parameters and states must be on one device")
+                if t.numel() != size or not t.is_contiguous():
+                    raise ValueError("parameters and states must be contiguous, and of matching sizes")
+            e.param, e.exp_avg, e.exp_avg_sq = p.data_ptr(), m.data_ptr(), v.data_ptr()
+            e.exp_avg_scale = None if ms is None else ms.data_ptr()
+            e.exp_avg_sq_scale = None if vs is None else vs.data_ptr()
+            e.master = None if w is None else w.data_ptr()
+            e.numel, e.param_dtype, e.state_bits = numel, _DTYPES[p.dtype], bits
+        at = [p.data_ptr() for p in self.params if p.numel()]
+        if len(set(at)) < len(at):
+            raise ValueError("a parameter occurs twice")
+        self.index = device.index if n else 0               # compared with the current device in _binding.so
+        self._tensors = ctypes.addressof(self._array)
+        self.grads = []
+        self.set_grads(grads)
+
+    def set_grads(self, grads) -> None:
+        """Takes other gradients, one for each parameter."""
+        grads = list(grads)
+        if len(grads) != self.n:
+            raise ValueError("as many gradients as parameters")
+        for p, g in zip(self.params, grads):
+            if g.dtype not in _DTYPES or not g.is_cuda:
+                raise TypeError("gradients must be bfloat16 or float32 CUDA tensors")
+            if g.device != p.device or g.numel() != p.numel() or not g.is_contiguous():
+                raise ValueError("gradients must be contiguous, of their parameter's size and device")
+        for e, g in zip(self._array, grads):
+            e.grad, e.grad_dtype = g.data_ptr(), _DTYPES[g.dtype]
+        self.grads = grads
+
+
+def moe_nvfp4_adamw(tensors: AdamWList, rule: AdamWRule, step: int, norm: Optional[torch.Tensor] = None,
+                    lr_step: Optional[torch.Tensor] = None, stream=None) -> None:
+    """One AdamW step, number ``step`` from 1, in place.  norm (device float32 [1]):
+    the gradients count times min(1, max_norm / (norm + clip_eps)).  lr_step
+    (device float32 [2]): the learning rate and the step's number in place of the
+    rule's and ``step``."""
+    _check("moe_nvfp4_adamw", (_native or native()).adamw(tensors.n, tensors.index, tensors._tensors, rule, step, norm,
+                                                          lr_step, stream))
 
 
 # ---- convenience ---------------------------------------------------------------

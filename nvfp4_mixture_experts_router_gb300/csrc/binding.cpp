@@ -218,6 +218,48 @@ int combine_backward(PyObject* const* a) {
                 handle(a[7]));
 }
 
+// A rule is a tuple (api.RouteRule, api.AdamWRule).
+PyObject* item(PyObject* rule, Py_ssize_t i, Py_ssize_t n) {
+    if (!PyTuple_Check(rule) || PyTuple_GET_SIZE(rule) != n)
+        wrong_type("the rule must be a tuple of " + std::to_string(n));
+    return PyTuple_GET_ITEM(rule, i);
+}
+moe_route_rule route_rule(PyObject* o) {
+    moe_route_rule r;
+    r.score = small(integer(item(o, 0, 6), "score"), "score");
+    r.groups = small(integer(item(o, 1, 6), "groups"), "groups");
+    r.topk_groups = small(integer(item(o, 2, 6), "topk_groups"), "topk_groups");
+    r.group_score = small(integer(item(o, 3, 6), "group_score"), "group_score");
+    r.renormalize = small(integer(item(o, 4, 6), "renormalize"), "renormalize");
+    r.scale = (float)number(item(o, 5, 6), "scale");
+    return r;
+}
+
+// [T, K] of a tensor of two dimensions: K.
+int slots(PyObject* o, const char* name) {
+    const at::Tensor& t = tensor(o, name);
+    if (t.dim() != 2) wrong_value(std::string(name) + " must be [T, K]");
+    return small(t.size(1), "K");
+}
+
+int route_topk(PyObject* const* a) {
+    const Rows l = rows2d(a[0], "logits");
+    const int K = slots(a[3], "topk_ids");
+    return call(moe_nvfp4_route_topk, l.T, l.H, K, l.dtype, l.p, l.stride, flat_f32(a[1], "bias", {l.H}, true),
+                route_rule(a[2]), flat_i32(a[3], "topk_ids", {l.T, K}), flat_f32(a[4], "topk_w", {l.T, K}),
+                handle(a[5]));
+}
+
+int route_topk_backward(PyObject* const* a) {
+    const Rows l = rows2d(a[0], "logits"), d = rows2d(a[4], "dlogits");
+    if (d.dtype != l.dtype) wrong_type("dlogits must have the type of the logits");
+    if (d.T != l.T || d.H != l.H) wrong_value("dlogits must have the shape of the logits");
+    const int K = slots(a[1], "topk_ids");
+    return call(moe_nvfp4_route_topk_backward, l.T, l.H, K, l.dtype, l.p, l.stride,
+                flat_i32(a[1], "topk_ids", {l.T, K}), flat_f32(a[2], "dw", {l.T, K}), route_rule(a[3]), d.p, d.stride,
+                handle(a[5]));
+}
+
 using ExpertEntry = moe_status (*)(int64_t, int, int, int, const void*, const void*, const int32_t*, const int32_t*,
                                    void*, uint32_t*, void*);
 
@@ -283,6 +325,49 @@ int layer_norm_backward(PyObject* const* a) {
                 handle(a[9]));
 }
 
+// Rows that may be None.
+Rows rows_or_none(PyObject* o, const char* name, const Rows& x) {
+    if (o != Py_None) return same_rows(o, name, x);
+    Rows r = x;
+    r.p = nullptr;
+    return r;
+}
+
+int rms_norm(PyObject* const* a) {
+    const Rows x = rows2d(a[0], "x"), res = rows_or_none(a[1], "residual", x), h = rows_or_none(a[4], "h", x),
+               y = rows_or_none(a[5], "y", x);
+    void* q = flat(a[6], "q", at::kFloat8_e4m3fn, {x.T, x.H}, true);
+    void* scales = nullptr;
+    int mode = MOE_SCALE_ROW;
+    if (a[7] != Py_None) {
+        const at::Tensor& s = tensor(a[7], "scales");
+        if (s.scalar_type() != at::kFloat) {
+            if (s.scalar_type() != at::kFloat8_e8m0fnu && s.scalar_type() != at::kByte)
+                wrong_type("scales must be float32, float8_e8m0fnu or uint8");
+            mode = MOE_SCALE_MX;
+            scales = flat(a[7], "scales", s.scalar_type(), {x.T, (x.H + 31) / 32});
+        } else if (s.dim() == 1) {
+            scales = flat_f32(a[7], "scales", {x.T});
+        } else {
+            mode = MOE_SCALE_BLOCK128;
+            scales = flat_f32(a[7], "scales", {x.T, (x.H + 127) / 128});
+        }
+    }
+    if (x.T > 0 && (a[6] == Py_None) != (a[7] == Py_None)) wrong_value("q and scales go together");
+    return call(moe_nvfp4_rms_norm, x.T, x.H, x.dtype, x.p, x.stride, res.p, res.stride, flat_f32(a[2], "gamma", {x.H}),
+                (float)number(a[3], "eps"), h.p, h.stride, y.p, y.stride, q, scales, mode,
+                flat_f32(a[8], "rstd", {x.T}, true), handle(a[9]));
+}
+
+int rms_norm_backward(PyObject* const* a) {
+    const Rows h = rows2d(a[2], "h"), dy = same_rows(a[0], "dy", h), dh = rows_or_none(a[1], "dh", h),
+               dx = same_rows(a[5], "dx", h);
+    const Space ws = workspace(a[7]);
+    return call(moe_nvfp4_rms_norm_backward, h.T, h.H, h.dtype, dy.p, dy.stride, dh.p, dh.stride, h.p, h.stride,
+                flat_f32(a[3], "gamma", {h.H}), flat_f32(a[4], "rstd", {h.T}), dx.p, dx.stride,
+                flat_f32(a[6], "dgamma", {h.H}), ws.p, ws.bytes, handle(a[8]));
+}
+
 template <typename T>
 T* address(PyObject* o) {
     return reinterpret_cast<T*>(integer(o, "an array's address"));
@@ -309,6 +394,19 @@ int grad_clip(PyObject* const* a) {
                 address<void* const>(a[3]), address<const int64_t>(a[4]), address<const int32_t>(a[5]),
                 flat_f32(a[6], "norm", {1}), (float)number(a[7], "max_norm"), (float)number(a[8], "eps"),
                 handle(a[9]));
+}
+
+// (n, the list's device, its address, the rule, step, norm, lr_step, stream)
+int adamw(PyObject* const* a) {
+    const int n = small(integer(a[0], "n"), "n");
+    if (n > 0 && integer(a[1], "the tensors' device") != c10::cuda::current_device())
+        wrong_value("the tensors are not on the current device");
+    moe_adamw_rule r;
+    double* const to[] = {&r.lr, &r.beta1, &r.beta2, &r.eps, &r.weight_decay, &r.max_norm, &r.clip_eps};
+    for (int i = 0; i < 7; ++i) *to[i] = number(item(a[3], i, 7), "the rule's entry");
+    r.step = integer(a[4], "step");
+    return call(moe_nvfp4_adamw, n, address<const moe_adamw_tensor>(a[2]), r, flat_f32(a[5], "norm", {1}, true),
+                flat_f32(a[6], "lr_step", {2}, true), handle(a[7]));
 }
 
 // Runs one of the functions above on n arguments; no C++ exception leaves.
@@ -347,6 +445,11 @@ PyMethodDef g_methods[] = {
     method<expert_linear_wgrad, 7>("expert_linear_wgrad"),
     method<layer_norm, 8>("layer_norm"),
     method<layer_norm_backward, 10>("layer_norm_backward"),
+    method<route_topk, 6>("route_topk"),
+    method<route_topk_backward, 6>("route_topk_backward"),
+    method<rms_norm, 10>("rms_norm"),
+    method<rms_norm_backward, 9>("rms_norm_backward"),
+    method<adamw, 8>("adamw"),
     method<grad_norm, 8>("grad_norm"),
     method<grad_clip, 10>("grad_clip"),
     {nullptr, nullptr, 0, nullptr},

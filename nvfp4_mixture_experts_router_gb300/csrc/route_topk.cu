@@ -1,0 +1,581 @@
+// Experts chosen from logits, and the gradient of the logits.
+//
+//   s = softmax(l) or sigmoid(l),  c = s + bias (l without a bias)
+//   group score = max c, or the sum of the two largest s (+ bias)
+//   ids = the K largest c in the topk_groups best groups
+//   w_k = scale s_k, or scale s_k / sum_j s_j
+//
+// A warp has a token: EPL consecutive experts a lane, so that the order of the
+// lanes and of a lane's registers is the order of the experts and ties fall to
+// the lower one.  c is held as an unsigned integer of the same order, 0 for an
+// expert that cannot be chosen; the K largest are K rounds of a warp-wide
+// maximum.
+//
+// The choice has to be that of exact scores: an expert more or less is not a
+// rounding.  Logits compare exactly.  Scores with a bias, and sums of two
+// scores, are computed in FP32 with a bound of their error; where two values
+// that decide are closer than their bounds, the warp computes the ones that may
+// decide in FP64 (about one token in 300 with 256 experts, standard normal
+// logits and a bias), and compares those.
+#include <float.h>
+#include <math.h>
+
+#include "row_vec.cuh"
+#include "train_kernels.h"
+
+namespace moe {
+
+namespace {
+
+constexpr unsigned kAll = 0xffffffffu;
+constexpr int kRouteWarps = 8;      // tokens of a block, at most
+
+struct RouteArgs {
+    int T, E, K;
+    const void* logits;
+    int64_t stride;
+    const float* bias;
+    moe_route_rule rule;
+    int* ids;
+    float* w;
+    bool wide;      // rows in 16-byte loads
+};
+
+// The unsigned integer in the order of a float that is no NaN (zeros alike); not 0.
+__device__ __forceinline__ uint32_t order_of(float v) {
+    const uint32_t b = __float_as_uint(v + 0.0f);
+    return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ float value_of(uint32_t k) {
+    return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
+}
+
+// A logit as it counts: NaN as -infinity, at most the largest FP32 number.
+__device__ __forceinline__ float as_logit(float v) { return v > -INFINITY ? fminf(v, FLT_MAX) : -INFINITY; }
+
+__device__ __forceinline__ float load_logit(const float* p) { return as_logit(*p); }
+__device__ __forceinline__ float load_logit(const __nv_bfloat16* p) { return as_logit(__bfloat162float(*p)); }
+
+// The lane's EPL logits, -infinity past the row's end.
+template <typename T_, int EPL>
+__device__ __forceinline__ void load_row(const T_* row, int E, bool wide, float (&l)[EPL]) {
+    const int e0 = (threadIdx.x & 31) * EPL;
+    constexpr int kMost = 16 / sizeof(T_), VEC = EPL < kMost ? EPL : kMost;
+    if (VEC > 1 && wide) {
+#pragma unroll
+        for (int i = 0; i < EPL; i += VEC) {
+            float u[VEC];
+            if (e0 + i < E) {       // E is a multiple of VEC then
+                RowVec<T_, VEC>::unpack(*reinterpret_cast<const typename RowVec<T_, VEC>::Raw*>(row + e0 + i), u);
+            } else {
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) u[k] = -INFINITY;
+            }
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) l[i + k] = as_logit(u[k]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) l[i] = e0 + i < E ? load_logit(row + e0 + i) : -INFINITY;
+    }
+}
+
+// Scores in FP32.  Of sigmoid the absolute error is below kSigmoidErr: e^-l is
+// off by (3 + 1.18 |l|) 2^-23 of itself at most (__expf's documented bound),
+// which s (1 - s) takes to 0.75 + 0.27 units of 2^-23, and the sum and the
+// division add 2.5.  Of softmax, p = e^x / S with x = l -
+// max, it is below (32 + 1.2 |x|) 2^-23 p: e^x as above, S a sum of at most 32
+// + 5 roundings and of terms each that exact (their mean |x| is at most log E).
+constexpr float kUnit = 1.1920929e-07f;     // 2^-23
+constexpr float kSigmoidErr = 4.0f * kUnit;
+constexpr float kTiny = 7.5e-37f;           // 2^-120, where the approximations flush to zero
+__device__ __forceinline__ float sigmoid_fast(float l) { return __fdividef(1.0f, 1.0f + __expf(-l)); }
+
+struct Softmax {
+    float max, inv;     // of the row; p = e^(l - max) inv
+    __device__ __forceinline__ float of(float l) const { return __expf(l - max) * inv; }
+};
+template <int EPL>
+__device__ __forceinline__ Softmax softmax_of(const float (&l)[EPL]) {
+    float m = l[0], s = 0.0f;
+#pragma unroll
+    for (int i = 1; i < EPL; ++i) m = fmaxf(m, l[i]);
+    m = warp_max(m);
+    if (!(m > -INFINITY)) m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) s += __expf(l[i] - m);
+    s = warp_sum(s);
+    return Softmax{m, s > 0.0f ? __fdividef(1.0f, s) : 0.0f};
+}
+
+// The two largest of a group of lanes' values, a >= b.
+__device__ __forceinline__ void join_top2(float& a, float& b, float a2, float b2) {
+    b = fmaxf(fminf(a, a2), a >= a2 ? b : b2);
+    a = fmaxf(a, a2);
+}
+__device__ __forceinline__ void into_top2(float& a, float& b, float v) {
+    b = fmaxf(b, fminf(a, v));
+    a = fmaxf(a, v);
+}
+
+// ---- the exact choice, for the tokens that FP32 cannot decide --------------------
+
+// A token's scores in FP64: c of expert e, with the warp's S of a softmax.
+template <typename T_>
+struct Exact {
+    const T_* row;
+    const float* bias;
+    bool sigmoid;
+    double max, sum;
+    __device__ double operator()(int e) const {
+        const double l = (double)load_logit(row + e);
+        const double s = sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - max) / sum;
+        return bias ? s + (double)bias[e] : s;
+    }
+};
+template <typename T_, int EPL>
+__device__ __forceinline__ Exact<T_> exact_of(const T_* row, const float* bias, bool sigmoid, int E, float max) {
+    double s = 0.0;
+    if (!sigmoid) {
+        const int e0 = (threadIdx.x & 31) * EPL;
+        for (int i = 0; i < EPL && e0 + i < E; ++i) s += exp((double)load_logit(row + e0 + i) - (double)max);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
+    }
+    return Exact<T_>{row, bias, sigmoid, (double)max, s};
+}
+
+// The topk_groups best groups, as a mask: lane g has group g's score, or NaN
+// for a group that does not exist.
+template <typename F>
+__device__ __forceinline__ uint32_t best_groups(F score, int groups, int take) {
+    const int lane = threadIdx.x & 31;
+    int above = 0;
+    for (int g = 0; g < groups; ++g) {
+        const F v = __shfl_sync(kAll, score, g);
+        above += v > score || (v == score && g < lane);
+    }
+    return __ballot_sync(kAll, lane < groups && above < take);
+}
+
+// The lane's experts in the taken groups of `size`, as a mask.
+template <int EPL>
+__device__ __forceinline__ uint32_t lane_mask(uint32_t taken, int size) {
+    const int e0 = (threadIdx.x & 31) * EPL;
+    int g = e0 / size, r = e0 - g * size;
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+        m |= ((taken >> (g & 31)) & 1u) << i;       // past the last group: no experts
+        if (++r == size) {
+            r = 0;
+            ++g;
+        }
+    }
+    return m;
+}
+
+// The groups by FP64 scores.  s_c: E doubles of this warp.  can: a mask of the
+// lane's experts.
+template <typename T_, int EPL>
+__device__ __noinline__ uint32_t exact_groups(const Exact<T_>& f, int E, const moe_route_rule& rule, uint32_t can,
+                                              double* s_c) {
+    const int lane = threadIdx.x & 31, e0 = lane * EPL, size = E / rule.groups;
+    for (int i = 0; i < EPL && e0 + i < E; ++i) s_c[e0 + i] = (can >> i) & 1u ? f(e0 + i) : -INFINITY;
+    __syncwarp();
+    double a = -INFINITY, b = -INFINITY;
+    if (lane < rule.groups) {
+        for (int i = 0; i < size; ++i) {
+            const double v = s_c[lane * size + i];
+            b = fmax(b, fmin(a, v));
+            a = fmax(a, v);
+        }
+        if (rule.group_score == MOE_GROUP_TOP2 && b > -INFINITY) a += b;
+    }
+    __syncwarp();
+    return best_groups(a, rule.groups, rule.topk_groups);
+}
+
+// The K largest c among the lane's experts `near` (a mask; every expert that may
+// be one of them), in FP64.  Slot k's expert in lane k, or -1.
+template <typename T_, int EPL>
+__device__ __noinline__ int exact_choice(const Exact<T_>& f, int E, int K, uint32_t near, double* s_c) {
+    const int lane = threadIdx.x & 31, e0 = lane * EPL;
+    uint16_t* list = reinterpret_cast<uint16_t*>(s_c + E);
+    for (int i = 0; i < EPL && e0 + i < E; ++i) s_c[e0 + i] = -INFINITY;
+    // the experts to look at, spread over the lanes
+    int n = 0;
+    for (int i = 0; i < EPL; ++i) {
+        const uint32_t who = __ballot_sync(kAll, (near >> i) & 1u);
+        if ((near >> i) & 1u) list[n + __popc(who & ((1u << lane) - 1))] = (uint16_t)(e0 + i);
+        n += __popc(who);
+    }
+    __syncwarp();
+    for (int p = lane; p < n; p += 32) s_c[list[p]] = f(list[p]);
+    __syncwarp();
+    int mine = -1;
+    for (int k = 0; k < K; ++k) {
+        double v = -INFINITY;
+        int e = E;
+        for (int i = 0; i < EPL && e0 + i < E; ++i)
+            if (s_c[e0 + i] > v) {
+                v = s_c[e0 + i];
+                e = e0 + i;
+            }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const double v2 = __shfl_xor_sync(kAll, v, o);
+            const int e2 = __shfl_xor_sync(kAll, e, o);
+            if (v2 > v || (v2 == v && e2 < e)) {
+                v = v2;
+                e = e2;
+            }
+        }
+        if (e == E) break;      // the same in every lane
+        if (lane == k) mine = e;
+        __syncwarp();
+        if (lane == 0) s_c[e] = -INFINITY;
+        __syncwarp();
+    }
+    return mine;
+}
+
+// ---- forward ------------------------------------------------------------------------
+
+template <typename T_, int EPL>
+__global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const RouteArgs a) {
+    extern __shared__ double s_exact[];     // [warps][E] values and E indices, with a bias or sums of two
+    pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.E, K = a.K, e0 = lane * EPL;
+    const int t = blockIdx.x * (blockDim.x >> 5) + warp;
+    if (t >= a.T) return;
+    const T_* row = static_cast<const T_*>(a.logits) + (int64_t)t * a.stride;
+    double* s_c = s_exact + (size_t)warp * (E + (E + 3) / 4);
+    const bool sigmoid = a.rule.score == MOE_SCORE_SIGMOID, grouped = a.rule.topk_groups < a.rule.groups;
+    const bool pair = grouped && a.rule.group_score == MOE_GROUP_TOP2;
+    float l[EPL];
+    load_row<T_, EPL>(row, E, a.wide, l);
+    Softmax soft{0.0f, 0.0f};
+    if (!sigmoid && (a.bias || pair || !a.rule.renormalize)) soft = softmax_of<EPL>(l);
+    // c in order; 0: cannot be chosen
+    uint32_t key[EPL], can = 0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+        const float b = a.bias && e0 + i < E ? a.bias[e0 + i] : 0.0f;
+        const bool ok = l[i] > -INFINITY && b > -INFINITY;
+        const float c = a.bias ? (sigmoid ? sigmoid_fast(l[i]) : soft.of(l[i])) + b : l[i];
+        key[i] = ok ? order_of(c) : 0u;
+        can |= ok ? 1u << i : 0u;
+    }
+    // bounds of the error of any c: its score's, and c's own rounding
+    const float most = sigmoid ? kSigmoidErr : 32.0f * kUnit * soft.inv;
+    auto err_of = [&](float c) { return most + kTiny + 2.0f * kUnit * fabsf(c); };
+
+    if (grouped) {
+        const int size = E / a.rule.groups;
+        float x = -INFINITY, y = -INFINITY;     // lane g: the two largest of group g
+        auto value = [&](int i) {
+            if (!((can >> i) & 1u)) return -INFINITY;
+            return pair && !a.bias ? (sigmoid ? sigmoid_fast(l[i]) : soft.of(l[i])) : value_of(key[i]);
+        };
+        const int span = size / EPL;
+        if (size % EPL == 0 && (span & (span - 1)) == 0) {
+            // a group is 2^n whole lanes
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) into_top2(x, y, value(i));
+            for (int o = 1; o < span; o <<= 1) {
+                const float x2 = __shfl_xor_sync(kAll, x, o), y2 = __shfl_xor_sync(kAll, y, o);
+                join_top2(x, y, x2, y2);
+            }
+            const int src = lane * span & 31;
+            x = __shfl_sync(kAll, x, src);
+            y = __shfl_sync(kAll, y, src);
+        } else {
+            float* s_v = reinterpret_cast<float*>(s_c);
+#pragma unroll
+            for (int i = 0; i < EPL; ++i)
+                if (e0 + i < E) s_v[e0 + i] = value(i);
+            __syncwarp();
+            if (lane < a.rule.groups)
+                for (int i = 0; i < size; ++i) into_top2(x, y, s_v[lane * size + i]);
+            __syncwarp();
+        }
+        const float score = lane >= a.rule.groups ? NAN : pair && y > -INFINITY ? x + y : x;
+        uint32_t taken = best_groups(score, a.rule.groups, a.rule.topk_groups);
+        if (a.bias || pair) {
+            // +-infinity is exact
+            const float err = fabsf(score) < INFINITY ? 2.0f * err_of(score) + 4.0f * kUnit * fabsf(x) : 0.0f;
+            const bool in = (taken >> lane) & 1u, out = !in && score > -INFINITY;
+            const float low = -warp_max(in ? -(score - err) : -INFINITY);
+            const float high = warp_max(out ? score + err : -INFINITY);
+            if (high > -INFINITY && high >= low)
+                taken = exact_groups<T_, EPL>(exact_of<T_, EPL>(row, a.bias, sigmoid, E, soft.max), E, a.rule, can, s_c);
+        }
+        const uint32_t open = lane_mask<EPL>(taken, size);
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+            if (!((open >> i) & 1u)) key[i] = 0u;
+        can &= open;
+    }
+
+    // K rounds; slot k in lane k
+    int mine = -1;
+    uint32_t mine_key = 0;
+    uint32_t best = 0;
+    int at = 0;
+    auto own_best = [&]() {
+        best = key[0];
+        at = 0;
+#pragma unroll
+        for (int i = 1; i < EPL; ++i)
+            if (key[i] > best) {
+                best = key[i];
+                at = i;
+            }
+    };
+    own_best();
+    uint32_t left = (1u << (EPL - 1) << 1) - 1;     // experts of the lane not chosen yet
+    for (int k = 0; k < K; ++k) {
+        const uint32_t m = __reduce_max_sync(kAll, best);
+        if (m == 0) break;
+        const int src = __ffs(__ballot_sync(kAll, best == m)) - 1;
+        const int e = src * EPL + __shfl_sync(kAll, at, src);
+        if (lane == k) {
+            mine = e;
+            mine_key = m;
+        }
+        if (lane == src) {
+            left &= ~(1u << at);
+#pragma unroll
+            for (int i = 0; i < EPL; ++i)
+                if (i == at) key[i] = 0u;
+            own_best();
+        }
+    }
+
+    if (a.bias) {
+        // Is the order of the chosen, and their being the largest, beyond doubt?
+        const float my_l = mine >= 0 ? load_logit(row + mine) : 0.0f, my_b = mine >= 0 ? a.bias[mine] : 0.0f;
+        auto bound = [&](float c, float l_) {
+            const float score_err = sigmoid ? kSigmoidErr : soft.of(l_) * kUnit * (32.0f + 1.2f * (soft.max - l_));
+            return fabsf(c) < INFINITY ? score_err + kTiny + 2.0f * kUnit * fabsf(c) : 0.0f;
+        };
+        const float c = mine >= 0 ? value_of(mine_key) : -INFINITY, e = mine >= 0 ? bound(c, my_l) : 0.0f;
+        const int chosen = __popc(__ballot_sync(kAll, mine >= 0));
+        const float c2 = __shfl_down_sync(kAll, c, 1), e2 = __shfl_down_sync(kAll, e, 1);
+        const float l2 = __shfl_down_sync(kAll, my_l, 1), b2 = __shfl_down_sync(kAll, my_b, 1);
+        // equal inputs are equal exactly, in the lower expert's favour
+        bool doubt = lane + 1 < chosen && !(c - e > c2 + e2) && !(my_l == l2 && my_b == b2);
+        const uint32_t next = __reduce_max_sync(kAll, best);
+        float low = -INFINITY;
+        if (chosen == K && next != 0) {
+            low = -warp_max(mine >= 0 ? e - c : -INFINITY);
+            const float v = value_of(next);
+            if (!(low > v + (fabsf(v) < INFINITY ? err_of(v) : 0.0f))) {
+                const float last_l = __shfl_sync(kAll, my_l, K - 1), last_b = __shfl_sync(kAll, my_b, K - 1);
+#pragma unroll
+                for (int i = 0; i < EPL; ++i)
+                    if (key[i] != 0u) {
+                        const float u = value_of(key[i]);
+                        doubt |= !(low > u + bound(u, l[i])) && !(l[i] == last_l && a.bias[e0 + i] == last_b);
+                    }
+            }
+        }
+        if (__any_sync(kAll, doubt)) {
+            uint32_t near = 0;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                const float u = value_of(key[i]);
+                if (((can >> i) & 1u) && (!((left >> i) & 1u) || !(low > u + bound(u, l[i])))) near |= 1u << i;
+            }
+            mine = exact_choice<T_, EPL>(exact_of<T_, EPL>(row, a.bias, sigmoid, E, soft.max), E, K, near, s_c);
+        }
+    }
+
+    // weights: of renormalized sigmoids the common factor e^-min(max, 0) is left
+    // out, so that they do not underflow together
+    const float my_l = mine >= 0 ? load_logit(row + mine) : -INFINITY;
+    float s;
+    if (a.rule.renormalize) {
+        float m = warp_max(my_l);
+        if (!(m > -INFINITY)) m = 0.0f;
+        s = sigmoid ? expf(fminf(my_l, 0.0f) - fminf(m, 0.0f)) / (1.0f + expf(-fabsf(my_l))) : expf(my_l - m);
+        const float sum = warp_sum(mine >= 0 ? s : 0.0f);
+        s = s / sum;
+    } else if (sigmoid) {
+        s = 1.0f / (1.0f + expf(-my_l));
+    } else {
+        s = expf(my_l - soft.max) * soft.inv;
+    }
+    if (lane < K) {
+        a.ids[(int64_t)t * K + lane] = mine;
+        a.w[(int64_t)t * K + lane] = mine >= 0 ? s * a.rule.scale : 0.0f;
+    }
+    pdl_launch_dependents();
+}
+
+// ---- backward -----------------------------------------------------------------------
+
+struct RouteGradArgs {
+    int T, E, K;
+    const void* logits;
+    int64_t stride;
+    const int* ids;
+    const float* dw;
+    moe_route_rule rule;
+    void* out;
+    int64_t out_stride;
+    bool wide;
+};
+
+template <typename T_>
+__device__ __forceinline__ void put(T_* p, float v) { *p = (T_)v; }
+
+// Lane k has slot k:
+//   softmax, renormalized   w (u - sum w u)                u = scale dw
+//   softmax                 p_e (u_e - sum_k p_k u_k)      over all experts
+//   sigmoid, renormalized   w (1 - s) (u - sum w u)
+//   sigmoid                 u s (1 - s)
+// The row is written as if no expert were chosen, and then the chosen ones, by
+// the same warp.  Bound by the row's bytes.
+template <typename T_, int EPL>
+__global__ void __launch_bounds__(32 * kRouteWarps) route_topk_backward_kernel(const RouteGradArgs a) {
+    pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.E, K = a.K, e0 = lane * EPL;
+    const int t = blockIdx.x * (blockDim.x >> 5) + warp;
+    if (t >= a.T) return;
+    const T_* row = static_cast<const T_*>(a.logits) + (int64_t)t * a.stride;
+    T_* out = static_cast<T_*>(a.out) + (int64_t)t * a.out_stride;
+    const bool sigmoid = a.rule.score == MOE_SCORE_SIGMOID, full = !sigmoid && !a.rule.renormalize;
+    int e = lane < K ? a.ids[(int64_t)t * K + lane] : -1;
+    const float dw = lane < K ? a.dw[(int64_t)t * K + lane] : 0.0f;
+    if (e < 0 || e >= E) e = -1;
+    const float u = e >= 0 ? dw * a.rule.scale : 0.0f;
+    const float my_l = e >= 0 ? load_logit(row + e) : -INFINITY;
+    float d = 0.0f, base = 0.0f;
+    float l[EPL];
+    Softmax soft{0.0f, 0.0f};
+    if (full) {
+        load_row<T_, EPL>(row, E, a.wide, l);
+        soft = softmax_of<EPL>(l);
+        base = -warp_sum(e >= 0 ? soft.of(my_l) * u : 0.0f);
+        d = u;
+    } else if (a.rule.renormalize) {
+        float m = warp_max(my_l);
+        if (!(m > -INFINITY)) m = 0.0f;
+        float w = sigmoid ? expf(fminf(my_l, 0.0f) - fminf(m, 0.0f)) / (1.0f + expf(-fabsf(my_l))) : expf(my_l - m);
+        const float sum = warp_sum(e >= 0 ? w : 0.0f);
+        w = e >= 0 ? w / sum : 0.0f;
+        d = w * (u - warp_sum(w * u));
+        if (sigmoid) d *= 1.0f / (1.0f + expf(my_l));
+    } else {
+        const float x = expf(-fabsf(my_l));
+        d = u * (x / ((1.0f + x) * (1.0f + x)));
+    }
+    // slots of one expert add up
+    float sum = 0.0f;
+    for (int k = 0; k < K; ++k) {
+        const int e2 = __shfl_sync(kAll, e, k);
+        const float d2 = __shfl_sync(kAll, d, k);
+        if (e2 == e) sum += d2;
+    }
+    __syncwarp();       // dlogits may be the logits: every lane has read them
+    constexpr int kMost = 16 / sizeof(T_), VEC = EPL < kMost ? EPL : kMost;
+    if (VEC > 1 && a.wide) {
+#pragma unroll
+        for (int i = 0; i < EPL; i += VEC) {
+            float v[VEC];
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) v[k] = full ? soft.of(l[i + k]) * base : 0.0f;
+            if (e0 + i < E)
+                *reinterpret_cast<typename RowVec<T_, VEC>::Raw*>(out + e0 + i) = RowVec<T_, VEC>::pack(v);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+            if (e0 + i < E) put(out + e0 + i, full ? soft.of(l[i]) * base : 0.0f);
+    }
+    __syncwarp();
+    if (e >= 0) put(out + e, full ? soft.of(my_l) * (sum + base) : sum);
+    pdl_launch_dependents();
+}
+
+// Tokens of a block: as many blocks as SMs first.
+int route_warps(int T) {
+    int w = kRouteWarps;
+    while (w > 1 && T <= 152 * (w / 2)) w /= 2;
+    return w;
+}
+
+// Calls f<EPL>() for the smallest EPL that holds E experts in a warp.
+#define MOE_ROUTE_EPL(E, f, T_, ...)                  \
+    do {                                              \
+        if ((E) <= 32) return f<T_, 1>(__VA_ARGS__);  \
+        if ((E) <= 64) return f<T_, 2>(__VA_ARGS__);  \
+        if ((E) <= 128) return f<T_, 4>(__VA_ARGS__); \
+        if ((E) <= 256) return f<T_, 8>(__VA_ARGS__); \
+        if ((E) <= 512) return f<T_, 16>(__VA_ARGS__);\
+        return f<T_, 32>(__VA_ARGS__);                \
+    } while (0)
+
+template <typename T_, int EPL>
+cudaError_t forward_epl(const LaunchCtx& c, RouteArgs a) {
+    constexpr int kMost = 16 / sizeof(T_), VEC = EPL < kMost ? EPL : kMost;
+    a.wide = a.E % VEC == 0 && row_at(a.logits, a.stride, sizeof(T_)) % (VEC * sizeof(T_)) == 0;
+    const int warps = route_warps(a.T);
+    const bool scratch = a.bias || a.rule.topk_groups < a.rule.groups;
+    const size_t smem = scratch ? (size_t)warps * (a.E + (a.E + 3) / 4) * 8 : 0;
+    return c.launch(route_topk_kernel<T_, EPL>, dim3((unsigned)((a.T + warps - 1) / warps)), dim3(32 * warps), smem, a);
+}
+template <typename T_>
+cudaError_t forward_of(const LaunchCtx& c, const RouteArgs& a) {
+    MOE_ROUTE_EPL(a.E, forward_epl, T_, c, a);
+}
+
+template <typename T_, int EPL>
+cudaError_t backward_epl(const LaunchCtx& c, RouteGradArgs a) {
+    constexpr int kMost = 16 / sizeof(T_), VEC = EPL < kMost ? EPL : kMost;
+    a.wide = a.E % VEC == 0 &&
+             (row_at(a.logits, a.stride, sizeof(T_)) | row_at(a.out, a.out_stride, sizeof(T_))) % (VEC * sizeof(T_)) == 0;
+    const int warps = route_warps(a.T);
+    return c.launch(route_topk_backward_kernel<T_, EPL>, dim3((unsigned)((a.T + warps - 1) / warps)), dim3(32 * warps),
+                    0, a);
+}
+template <typename T_>
+cudaError_t backward_of(const LaunchCtx& c, const RouteGradArgs& a) {
+    MOE_ROUTE_EPL(a.E, backward_epl, T_, c, a);
+}
+
+template <typename T_>
+cudaError_t allow_forward() {
+    cudaError_t e = cudaSuccess;
+    auto allow = [&](auto kernel) {     // 8 warps of 1024 experts: 80 KB
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRouteWarps * 1280 * 8);
+    };
+    allow(route_topk_kernel<T_, 16>);
+    allow(route_topk_kernel<T_, 32>);
+    return e;
+}
+
+}  // namespace
+
+cudaError_t setup_route_topk_kernels() {
+    const cudaError_t e = allow_forward<float>();
+    return e != cudaSuccess ? e : allow_forward<__nv_bfloat16>();
+}
+
+cudaError_t launch_route_topk(const LaunchCtx& c, int T, int E, int K, int elem, const void* logits, int64_t stride,
+                              const float* bias, const moe_route_rule& rule, int* ids, float* w) {
+    const RouteArgs a{T, E, K, logits, stride, bias, rule, ids, w, false};
+    return elem == 2 ? forward_of<__nv_bfloat16>(c, a) : forward_of<float>(c, a);
+}
+
+cudaError_t launch_route_topk_backward(const LaunchCtx& c, int T, int E, int K, int elem, const void* logits,
+                                       int64_t stride, const int* ids, const float* dw, const moe_route_rule& rule,
+                                       void* out, int64_t out_stride) {
+    const RouteGradArgs a{T, E, K, logits, stride, ids, dw, rule, out, out_stride, false};
+    return elem == 2 ? backward_of<__nv_bfloat16>(c, a) : backward_of<float>(c, a);
+}
+
+}  // namespace moe

@@ -84,6 +84,59 @@ int skipped_row(int T, int* dtype) {
 
 extern "C" {
 
+static bool route_rule_ok(int T, int E, int K, int dtype, const moe_route_rule& r) {
+    if (!tokens_ok(T) || E < 1 || E > 1024 || !dtype_ok(dtype)) return false;
+    if (r.score != MOE_SCORE_SOFTMAX && r.score != MOE_SCORE_SIGMOID) return false;
+    if (r.group_score != MOE_GROUP_MAX && r.group_score != MOE_GROUP_TOP2) return false;
+    if (r.groups < 1 || r.groups > 32 || E % r.groups != 0) return false;
+    if (r.topk_groups < 1 || r.topk_groups > r.groups) return false;
+    if (K < 1 || K > 32 || K > E / r.groups * r.topk_groups) return false;
+    return (r.renormalize == 0 || r.renormalize == 1) && isfinite(r.scale);
+}
+
+moe_status moe_nvfp4_route_topk(int T, int E, int K, int dtype, const void* logits, int64_t logits_stride,
+                                const float* bias, moe_route_rule rule, int32_t* topk_ids, float* topk_w,
+                                void* stream) {
+    if (!route_rule_ok(T, E, K, dtype, rule) || !stride_ok(logits_stride, E)) return MOE_ERR_INVALID_ARG;
+    const int el = elem_of(dtype);
+    const size_t rb = (size_t)T * K * 4;
+    const Span s[] = {rows_span(logits, T, logits_stride, E, el, false),
+                      {bias, bias ? (size_t)E * 4 : 0, false},
+                      {topk_ids, rb, true},
+                      {topk_w, rb, true}};
+    const uintptr_t al[] = {(uintptr_t)el, 4, 4, 4};
+    if (!spans_ok(s, 4, al)) return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    LaunchCtx c;
+    int sms = 0;
+    const moe_status st = begin(stream, &c, &sms);
+    if (st != MOE_OK) return st;
+    return cuda_status(launch_route_topk(c, T, E, K, el, logits, logits_stride, bias, rule, topk_ids, topk_w));
+}
+
+moe_status moe_nvfp4_route_topk_backward(int T, int E, int K, int dtype, const void* logits, int64_t logits_stride,
+                                         const int32_t* topk_ids, const float* dw, moe_route_rule rule, void* dlogits,
+                                         int64_t dlogits_stride, void* stream) {
+    if (!route_rule_ok(T, E, K, dtype, rule) || !stride_ok(logits_stride, E) || !stride_ok(dlogits_stride, E))
+        return MOE_ERR_INVALID_ARG;
+    const int el = elem_of(dtype);
+    const size_t rb = (size_t)T * K * 4;
+    const bool in_place = dlogits == logits && dlogits_stride == logits_stride;
+    const Span s[] = {rows_span(logits, in_place ? 0 : T, logits_stride, E, el, false),
+                      {topk_ids, rb, false},
+                      {dw, rb, false},
+                      rows_span(dlogits, T, dlogits_stride, E, el, true)};
+    const uintptr_t al[] = {(uintptr_t)el, 4, 4, (uintptr_t)el};
+    if (!spans_ok(s, 4, al)) return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    LaunchCtx c;
+    int sms = 0;
+    const moe_status st = begin(stream, &c, &sms);
+    if (st != MOE_OK) return st;
+    return cuda_status(launch_route_topk_backward(c, T, E, K, el, logits, logits_stride, topk_ids, dw, rule, dlogits,
+                                                  dlogits_stride));
+}
+
 size_t moe_nvfp4_sort_workspace_bytes(int T, int E, int K) {
     if (!routes_ok(T, K) || E < 1 || E > 1024) return 0;
     return sort_workspace_bytes(T, E, K);
@@ -285,6 +338,80 @@ moe_status moe_nvfp4_layer_norm_backward(int T, int H, int dtype, const void* dy
                                                   dx_stride, dgamma, dbeta, static_cast<float*>(workspace), skip_row));
 }
 
+moe_status moe_nvfp4_rms_norm(int T, int H, int dtype, const void* x, int64_t x_stride, const void* residual,
+                              int64_t residual_stride, const float* gamma, float eps, void* h, int64_t h_stride,
+                              void* y, int64_t y_stride, void* q, void* scales, int scale_mode, float* rstd,
+                              void* stream) {
+    if (!tokens_ok(T) || !width_ok(H) || !dtype_ok(dtype) || !stride_ok(x_stride, H)) return MOE_ERR_INVALID_ARG;
+    if ((residual && !stride_ok(residual_stride, H)) || (h && !stride_ok(h_stride, H)) || (y && !stride_ok(y_stride, H)))
+        return MOE_ERR_INVALID_ARG;
+    if (!(eps >= 0.0f) || isinf(eps) || (h && !residual) || (q == nullptr) != (scales == nullptr))
+        return MOE_ERR_INVALID_ARG;
+    if (q && scale_mode != MOE_SCALE_ROW && scale_mode != MOE_SCALE_BLOCK128 && scale_mode != MOE_SCALE_MX)
+        return MOE_ERR_INVALID_ARG;
+    if (T > 0 && !y && !q) return MOE_ERR_INVALID_ARG;
+    const int el = elem_of(dtype);
+    // h over x or the residual; y over one of them, if h is not
+    auto over = [](const void* a, int64_t as, const void* b, int64_t bs) { return a && a == b && as == bs; };
+    const bool x_out = over(h, h_stride, x, x_stride) || over(y, y_stride, x, x_stride);
+    const bool r_out = over(h, h_stride, residual, residual_stride) || over(y, y_stride, residual, residual_stride);
+    const size_t per = scale_mode == MOE_SCALE_MX ? (size_t)(H + 31) / 32 : scale_mode == MOE_SCALE_BLOCK128 ? (size_t)(H + 127) / 128 * 4 : 4;
+    const uintptr_t sal = scale_mode == MOE_SCALE_MX ? 1 : 4;
+    const Span s[] = {rows_span(x, x_out ? 0 : T, x_stride, H, el, false),
+                      rows_span(residual, !residual || r_out ? 0 : T, residual_stride, H, el, false),
+                      {gamma, (size_t)H * 4, false},
+                      rows_span(h, h ? T : 0, h_stride, H, el, true),
+                      rows_span(y, y ? T : 0, y_stride, H, el, true),
+                      {q, q ? (size_t)T * H : 0, true},
+                      {scales, scales ? (size_t)T * per : 0, true},
+                      {rstd, rstd ? (size_t)T * 4 : 0, true}};
+    const uintptr_t al[] = {(uintptr_t)el, (uintptr_t)el, 4, (uintptr_t)el, (uintptr_t)el, 1, sal, 4};
+    if (!spans_ok(s, 8, al)) return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    LaunchCtx c;
+    int sms = 0;
+    const moe_status st = begin(stream, &c, &sms);
+    if (st != MOE_OK) return st;
+    return cuda_status(launch_rms_norm(c, el, RmsArgs{T, H, x, x_stride, residual, residual_stride, gamma, eps, h,
+                                                      h_stride, y, y_stride, q, scales, scale_mode, rstd}));
+}
+
+size_t moe_nvfp4_rms_norm_workspace_bytes(int T, int H) {
+    if (!tokens_ok(T) || !width_ok(H)) return 0;
+    return rms_norm_workspace_bytes(T, H);
+}
+
+moe_status moe_nvfp4_rms_norm_backward(int T, int H, int dtype, const void* dy, int64_t dy_stride, const void* dh,
+                                       int64_t dh_stride, const void* h, int64_t h_stride, const float* gamma,
+                                       const float* rstd, void* dx, int64_t dx_stride, float* dgamma, void* workspace,
+                                       size_t workspace_bytes, void* stream) {
+    if (!tokens_ok(T) || !width_ok(H) || !dtype_ok(dtype)) return MOE_ERR_INVALID_ARG;
+    if (!stride_ok(dy_stride, H) || !stride_ok(h_stride, H) || !stride_ok(dx_stride, H) ||
+        (dh && !stride_ok(dh_stride, H)))
+        return MOE_ERR_INVALID_ARG;
+    const int el = elem_of(dtype);
+    const size_t need = rms_norm_workspace_bytes(T, H);
+    auto over = [&](const void* p, int64_t stride) { return p == dx && stride == dx_stride; };
+    const Span s[] = {rows_span(dy, over(dy, dy_stride) ? 0 : T, dy_stride, H, el, false),
+                      rows_span(dh, !dh || over(dh, dh_stride) ? 0 : T, dh_stride, H, el, false),
+                      rows_span(h, over(h, h_stride) ? 0 : T, h_stride, H, el, false),
+                      {gamma, (size_t)H * 4, false},
+                      {rstd, (size_t)T * 4, false},
+                      rows_span(dx, T, dx_stride, H, el, true),
+                      {dgamma, (size_t)H * 4, true},
+                      {workspace, need, true}};
+    const uintptr_t al[] = {(uintptr_t)el, (uintptr_t)el, (uintptr_t)el, 4, 4, (uintptr_t)el, 4, 256};
+    if (!spans_ok(s, 8, al)) return MOE_ERR_INVALID_ARG;
+    if (workspace_bytes < need) return MOE_ERR_WORKSPACE;
+    LaunchCtx c;
+    int sms = 0;
+    const moe_status st = begin(stream, &c, &sms);
+    if (st != MOE_OK) return st;
+    return cuda_status(launch_rms_norm_backward(c, el, RmsGradArgs{T, H, dy, dy_stride, dh, dh_stride, h, h_stride,
+                                                                   gamma, rstd, dx, dx_stride, dgamma,
+                                                                   static_cast<float*>(workspace)}));
+}
+
 size_t moe_nvfp4_grad_norm_workspace_bytes(int n) {
     if (n < 0 || n > 65536) return 0;
     return grad_norm_workspace_bytes(n);
@@ -325,6 +452,41 @@ moe_status moe_nvfp4_grad_clip(int n, const void* const* grads, void* const* out
     const moe_status st = begin(stream, &c, &sms);
     if (st != MOE_OK) return st;
     return cuda_status(launch_grad_clip(c, sms, n, grads, out, numels, dtypes, norm, max_norm, eps));
+}
+
+static bool adamw_tensor_ok(const moe_adamw_tensor& t) {
+    if (t.numel < 0 || t.numel >= (1ll << 40) || !dtype_ok(t.param_dtype) || !dtype_ok(t.grad_dtype)) return false;
+    if ((t.state_bits != 32 && t.state_bits != 8) || t.reserved != 0) return false;
+    if (t.master && t.param_dtype != MOE_DTYPE_BF16) return false;
+    const bool scaled = t.state_bits == 8;
+    if (!scaled && (t.exp_avg_scale || t.exp_avg_sq_scale)) return false;
+    if (t.numel == 0) return true;
+    auto ok = [](const void* p, int align) { return p && aligned(p, align); };
+    return ok(t.param, elem_of(t.param_dtype)) && ok(t.grad, elem_of(t.grad_dtype)) && ok(t.exp_avg, scaled ? 1 : 4) &&
+           ok(t.exp_avg_sq, scaled ? 1 : 4) && (!scaled || (ok(t.exp_avg_scale, 4) && ok(t.exp_avg_sq_scale, 4))) &&
+           aligned(t.master, 4);
+}
+
+moe_status moe_nvfp4_adamw(int n, const moe_adamw_tensor* tensors, moe_adamw_rule rule, const float* norm,
+                           const float* lr_step, void* stream) {
+    if (n < 0 || n > 65536 || (n > 0 && !tensors)) return MOE_ERR_INVALID_ARG;
+    auto number = [](double v) { return v >= 0.0 && isfinite((float)v); };
+    if (!number(rule.weight_decay) || !number(rule.eps) || !((float)rule.eps > 0.0f)) return MOE_ERR_INVALID_ARG;
+    if (!(rule.beta1 >= 0.0 && rule.beta1 < 1.0) || !(rule.beta2 >= 0.0 && rule.beta2 < 1.0)) return MOE_ERR_INVALID_ARG;
+    if (!lr_step && (!number(rule.lr) || rule.step < 1)) return MOE_ERR_INVALID_ARG;
+    if (norm && (!number(rule.max_norm) || !number(rule.clip_eps))) return MOE_ERR_INVALID_ARG;
+    if (!aligned(norm, 4) || !aligned(lr_step, 4)) return MOE_ERR_INVALID_ARG;
+    bool any = false;
+    for (int i = 0; i < n; ++i) {
+        if (!adamw_tensor_ok(tensors[i])) return MOE_ERR_INVALID_ARG;
+        any |= tensors[i].numel > 0;
+    }
+    if (!any) return MOE_OK;
+    LaunchCtx c;
+    int sms = 0;
+    const moe_status st = begin(stream, &c, &sms);
+    if (st != MOE_OK) return st;
+    return cuda_status(launch_adamw(c, n, tensors, rule, norm, lr_step));
 }
 
 }  // extern "C"

@@ -20,6 +20,14 @@ cudaError_t launch_combine_backward(const LaunchCtx& c, int T, int H, int K, int
                                     int64_t dy_stride, const void* o, const int* row_of_route, const float* w,
                                     const int* rows_used, void* d_o, float* dw);
 
+// route_topk.cu
+cudaError_t setup_route_topk_kernels();
+cudaError_t launch_route_topk(const LaunchCtx& c, int T, int E, int K, int elem, const void* logits, int64_t stride,
+                              const float* bias, const moe_route_rule& rule, int* ids, float* w);
+cudaError_t launch_route_topk_backward(const LaunchCtx& c, int T, int E, int K, int elem, const void* logits,
+                                       int64_t stride, const int* ids, const float* dw, const moe_route_rule& rule,
+                                       void* out, int64_t out_stride);
+
 // layer_norm.cu (x and y may be the same rows; workspace of layer_norm_workspace_bytes;
 // skip_row: a row that a ring kernel never copies, for tests, or -1)
 cudaError_t launch_layer_norm(const LaunchCtx& c, int T, int H, int elem, const void* x, int64_t x_stride,
@@ -31,6 +39,47 @@ cudaError_t launch_layer_norm_backward(const LaunchCtx& c, int T, int H, int ele
                                        const void* x, int64_t x_stride, const float* gamma, const float* mean,
                                        const float* rstd, void* dx, int64_t dx_stride, float* dgamma, float* dbeta,
                                        float* workspace, int skip_row);
+
+// rms_norm.cu (pointers that may be null: residual, h, y, q, scales, rstd; dh)
+struct RmsArgs {
+    int T, H;
+    const void* x;
+    int64_t x_stride;
+    const void* residual;
+    int64_t residual_stride;
+    const float* gamma;
+    float eps;
+    void* h;
+    int64_t h_stride;
+    void* y;
+    int64_t y_stride;
+    void* q;
+    void* scales;
+    int scale_mode;
+    float* rstd;
+};
+struct RmsGradArgs {
+    int T, H;
+    const void* dy;
+    int64_t dy_stride;
+    const void* dh;
+    int64_t dh_stride;
+    const void* h;
+    int64_t h_stride;
+    const float* gamma;
+    const float* rstd;
+    void* dx;
+    int64_t dx_stride;
+    float* dgamma;
+    float* part;           // workspace of rms_norm_workspace_bytes
+};
+cudaError_t launch_rms_norm(const LaunchCtx& c, int elem, const RmsArgs& a);
+size_t rms_norm_workspace_bytes(int T, int H);
+cudaError_t launch_rms_norm_backward(const LaunchCtx& c, int elem, const RmsGradArgs& a);
+
+// adamw.cu
+cudaError_t launch_adamw(const LaunchCtx& c, int n, const moe_adamw_tensor* tensors, const moe_adamw_rule& rule,
+                         const float* norm, const float* lr_step);
 
 // grad_clip.cu
 size_t grad_norm_workspace_bytes(int n);

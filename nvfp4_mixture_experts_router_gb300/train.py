@@ -3,14 +3,19 @@
 Each function allocates its outputs and workspaces with torch, runs on the
 current stream, and has its gradient from the same library (api.py has the
 calls themselves, on the caller's buffers).  A pre-norm Mixture-of-Experts
-block, with the router and the activation in torch:
+block, with the gate's product and the activation in torch:
 
-    h = train.layer_norm(x, gamma, beta)
-    ids, w = top-K of the router's logits of h          # [T, K]
+    y, h = train.rms_norm(x, gamma, residual)           # or train.layer_norm(x, gamma, beta)
+    ids, w = train.route(gate(y), K, bias, api.RouteRule(...))      # [T, K]
     routes = train.sort_routes(ids, E)
-    z = train.expert_linear(train.dispatch(h, routes), w1, routes)
+    z = train.expert_linear(train.dispatch(y, routes), w1, routes)
     o = train.expert_linear(activation(z), w2, routes)
-    y = x + train.combine(o, routes, w)
+    x = train.combine(o, routes, w)                     # the next block's x, with h as its residual
+
+and its optimizer:
+
+    opt = train.AdamW(parameters, lr=1e-3, state_bits=8)
+    opt.step(norm=train.grad_norm(parameters), max_norm=1.0)
 
 examples/moe_block.py trains one.
 """
@@ -18,7 +23,7 @@ from __future__ import annotations
 
 from dataclasses import dataclass
 from functools import cached_property
-from typing import Iterable, Optional, Union
+from typing import Iterable, Optional, Tuple, Union
 
 import torch
 from torch.autograd.function import once_differentiable
@@ -97,6 +102,67 @@ def _clear_tail(rows: torch.Tensor, routes: Routes) -> torch.Tensor:
     """Zeros in the rows past the kept routes (a dispatch of no tokens)."""
     api.moe_nvfp4_dispatch(None, None, routes.used, rows)
     return rows
+
+
+class _Route(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, K, bias, rule):
+        T = logits.shape[0]
+        ids = torch.empty(T, K, dtype=torch.int32, device=logits.device)
+        w = torch.empty(T, K, dtype=torch.float32, device=logits.device)
+        api.moe_nvfp4_route_topk(logits, bias, rule, ids, w)
+        ctx.rule = rule
+        ctx.save_for_backward(logits, ids)
+        ctx.mark_non_differentiable(ids)
+        return ids, w
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, _, dw):
+        logits, ids = ctx.saved_tensors
+        dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        api.moe_nvfp4_route_topk_backward(logits, ids, dw.contiguous(), ctx.rule, dlogits)
+        return dlogits, None, None, None
+
+
+def route(logits: torch.Tensor, K: int, bias: Optional[torch.Tensor] = None,
+          rule: api.RouteRule = api.RouteRule()) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The K experts of each token and their weights, [T, K] int32 and FP32, from
+    logits [T, E] (BF16 or FP32).  The bias [E] FP32 enters the choice alone and has
+    no gradient: a training loop moves it against the experts' load (Routes.count)."""
+    return _Route.apply(logits, K, None if bias is None else bias.detach(), rule)
+
+
+class _RmsNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, gamma, eps):
+        new = lambda: torch.empty(x.shape, dtype=x.dtype, device=x.device)      # noqa: E731
+        y, h = new(), None if residual is None else new()
+        rstd = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
+        api.moe_nvfp4_rms_norm(x, residual, gamma, eps, h, y, None, None, rstd)
+        ctx.save_for_backward(x if h is None else h, gamma, rstd)
+        ctx.with_residual = h is not None
+        ctx.set_materialize_grads(False)
+        return y if h is None else (y, h)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dh=None):
+        h, gamma, rstd = ctx.saved_tensors
+        if dy is None:      # only h was used
+            return dh, dh if ctx.with_residual else None, None, None
+        dx = torch.empty(h.shape, dtype=h.dtype, device=h.device)
+        dgamma = torch.empty_like(gamma)
+        ws = torch.empty(api.moe_nvfp4_rms_norm_workspace_bytes(*h.shape), dtype=torch.uint8, device=h.device)
+        api.moe_nvfp4_rms_norm_backward(dy.contiguous(), None if dh is None else dh.contiguous(), h, gamma, rstd, dx,
+                                        dgamma, ws)
+        return dx, dx if ctx.with_residual else None, dgamma, None
+
+
+def rms_norm(x: torch.Tensor, gamma: torch.Tensor, residual: Optional[torch.Tensor] = None, eps: float = 1e-6):
+    """RMS norm of h = x + residual, [T, H] (BF16 or FP32), gamma [H] FP32.  Returns y
+    and h, or y alone without a residual (h is x then)."""
+    return _RmsNorm.apply(x, residual, gamma, eps)
 
 
 class _LayerNorm(torch.autograd.Function):
@@ -206,6 +272,103 @@ def expert_linear(x_rows: torch.Tensor, w: torch.Tensor, routes: Routes) -> torc
     all rows (of a bias after it, say) count the routes alone."""
     _check_rows(x_rows, routes, "x_rows")
     return _ExpertLinear.apply(x_rows.contiguous(), w, routes)
+
+
+def grad_norm(parameters: Union[torch.Tensor, Iterable[torch.Tensor]]) -> torch.Tensor:
+    """The global norm of the gradients of ``parameters`` (one device float32), for
+    AdamW.step, which clips on its way; the gradients stay as they are."""
+    grads = [p.grad for p in ([parameters] if isinstance(parameters, torch.Tensor) else parameters)
+             if p.grad is not None]
+    device = grads[0].device if grads else "cuda"
+    norm = torch.empty(1, dtype=torch.float32, device=device)
+    ws = torch.empty(api.moe_nvfp4_grad_norm_workspace_bytes(len(grads)), dtype=torch.uint8, device=device)
+    api.moe_nvfp4_grad_norm(api.GradList([g.detach().contiguous() for g in grads]), norm, ws)
+    return norm
+
+
+class AdamW:
+    """AdamW over parameters (BF16 or FP32, contiguous, on one device), a launch for
+    each kind of states and 384 tensors (moe_nvfp4_adamw).
+
+    state_bits 8 keeps both moments in E4M3 with a scale for each 256 elements, of
+    tensors from min_8bit elements on; master keeps FP32 values of BF16
+    parameters, from which these are rounded.  Parameters without a gradient are
+    left as they are.  capturable: the learning rate and the number of the step
+    are read on the device (self.lr_step), so that a step captured into a CUDA
+    graph counts on when it is replayed; run one step before the capture."""
+
+    def __init__(self, params: Iterable[torch.Tensor], lr: float = 1e-3, betas: Tuple[float, float] = (0.9, 0.999),
+                 eps: float = 1e-8, weight_decay: float = 0.01, state_bits: int = 32, master: bool = True,
+                 min_8bit: int = 4096, capturable: bool = False):
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits must be 8 or 32")
+        self.params = list(params)
+        self.lr, self.betas, self.eps, self.weight_decay = lr, betas, eps, weight_decay
+        self.steps = 0
+        self.state = []
+        for p in self.params:
+            n, s, dev = p.numel(), {}, dict(device=p.device)
+            small = state_bits == 32 or n < min_8bit
+            for name in ("exp_avg", "exp_avg_sq"):
+                if small:
+                    s[name] = torch.zeros(n, dtype=torch.float32, **dev)
+                else:
+                    s[name] = torch.zeros(n, dtype=torch.uint8, **dev).view(torch.float8_e4m3fn)
+                    s[name + "_scale"] = torch.zeros(-(-n // api.MOE_ADAMW_BLOCK), dtype=torch.float32, **dev)
+            if master and p.dtype == torch.bfloat16:
+                s["master"] = p.detach().float().reshape(-1)
+            self.state.append(s)
+        self.lr_step = None
+        if capturable and self.params:
+            self.lr_step = torch.tensor([lr, 0.0], dtype=torch.float32, device=self.params[0].device)
+            self._device_lr = lr
+        self._list, self._of = None, None
+
+    def zero_grad(self, set_to_none: bool = True) -> None:
+        for p in self.params:
+            if set_to_none or p.grad is None:
+                p.grad = None
+            else:
+                p.grad.zero_()
+
+    @torch.no_grad()
+    def step(self, norm: Optional[torch.Tensor] = None, max_norm: float = 1.0, clip_eps: float = 1e-6) -> None:
+        """One step.  norm: the gradients' global norm (grad_norm), by which they are
+        clipped to max_norm on the way."""
+        used = [i for i, p in enumerate(self.params) if p.grad is not None]
+        of = [(i, self.params[i].data_ptr()) for i in used]
+        grads = [self.params[i].grad.contiguous() for i in used]
+        if of != self._of:
+            get = lambda name: [self.state[i].get(name) for i in used]      # noqa: E731
+            self._list = api.AdamWList([self.params[i] for i in used], grads, get("exp_avg"), get("exp_avg_sq"),
+                                       get("exp_avg_scale"), get("exp_avg_sq_scale"), get("master"))
+            self._of = of
+        else:
+            self._list.set_grads(grads)
+        self.steps += 1
+        if self.lr_step is not None:
+            if self._device_lr != self.lr and not torch.cuda.is_current_stream_capturing():
+                self.lr_step[0].fill_(self.lr)
+                self._device_lr = self.lr
+            self.lr_step[1].add_(1.0)
+        rule = api.AdamWRule(self.lr, *self.betas, self.eps, self.weight_decay, max_norm, clip_eps)
+        api.moe_nvfp4_adamw(self._list, rule, self.steps, norm, self.lr_step)
+        self._list.grads = []       # the gradients may go
+
+    def state_dict(self) -> dict:
+        return {"steps": self.steps if self.lr_step is None else int(self.lr_step[1]), "state": self.state}
+
+    def load_state_dict(self, saved: dict) -> None:
+        """Copies the states of an optimizer of the same parameters and kind."""
+        if [{k: (v.shape, v.dtype) for k, v in s.items()} for s in saved["state"]] != \
+                [{k: (v.shape, v.dtype) for k, v in s.items()} for s in self.state]:
+            raise ValueError("the states are of other parameters, or of another kind")
+        for mine, theirs in zip(self.state, saved["state"]):
+            for k, v in theirs.items():
+                mine[k].copy_(v)
+        self.steps = saved["steps"]
+        if self.lr_step is not None:
+            self.lr_step[1].fill_(self.steps)
 
 
 def clip_grad_norm_(parameters: Union[torch.Tensor, Iterable[torch.Tensor]], max_norm: float,
