@@ -297,7 +297,7 @@ MOE_API moe_status moe_nvfp4_grad_clip(int n, const void* const* grads, void* co
  *      8: E4M3 bytes of m and of sqrt(v), each block of MOE_ADAMW_BLOCK elements
  *         (the last may be shorter) with an FP32 scale, [ceil(numel / block)] in
  *         exp_avg_scale and exp_avg_sq_scale: value = byte * scale.  Written
- *         with the scale largest magnitude / 448, rounded to nearest even; a
+ *         with the scale largest magnitude * (1 / 448), rounded to nearest even; a
  *         block whose largest magnitude is below 2^-100 becomes zeros with
  *         scale 0, and no other sqrt(v) > 0 rounds to zero (its byte is 1 at
  *         least).  A block with a value that is not finite becomes NaN.  The
@@ -308,10 +308,10 @@ MOE_API moe_status moe_nvfp4_grad_clip(int n, const void* const* grads, void* co
  * [2]: lr and t, a whole number up to 2^24) these replace rule.lr and rule.step,
  * so that a captured graph can be replayed with other ones; the corrections
  * are FP32 then.
- * A gradient below 1e-23 in magnitude adds nothing to v: its square is FP32.
+ * Squares and v are FP32; v below 2^-126 counts as zero.
  * 0 <= n <= 65536, 0 <= numel < 2^40; pointers aligned to their element; a
  * tensor of no elements may have NULL pointers.  lr and weight_decay >= 0,
- * 0 <= beta < 1, eps > 0, max_norm and clip_eps >= 0, all finite; step >= 1
+ * 0 <= beta < 1, eps >= 2^-126, max_norm and clip_eps >= 0, all finite; step >= 1
  * (not looked at with lr_step).  The tensors are on the current device; no
  * buffer may overlap another one of the call (not compared). */
 #define MOE_ADAMW_BLOCK 256

@@ -62,6 +62,13 @@ __device__ __forceinline__ float e4m3_to_f32(uint32_t code) {
     return __half2float(__ushort_as_half(static_cast<unsigned short>(r & 0xFFFFu)));
 }
 
+// Exact float values of two E4M3 codes, of the low 16 bits.
+__device__ __forceinline__ float2 e4m3x2_to_f32x2(uint32_t codes) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((unsigned short)codes));
+    return __half22float2(*reinterpret_cast<const __half2*>(&r));
+}
+
 // Two E2M1 codes in one byte: `lo` -> bits 0-3, `hi` -> bits 4-7.
 __device__ __forceinline__ uint32_t f32x2_to_e2m1x2(float lo, float hi) {
     uint32_t r;

@@ -471,7 +471,7 @@ moe_status moe_nvfp4_adamw(int n, const moe_adamw_tensor* tensors, moe_adamw_rul
                            const float* lr_step, void* stream) {
     if (n < 0 || n > 65536 || (n > 0 && !tensors)) return MOE_ERR_INVALID_ARG;
     auto number = [](double v) { return v >= 0.0 && isfinite((float)v); };
-    if (!number(rule.weight_decay) || !number(rule.eps) || !((float)rule.eps > 0.0f)) return MOE_ERR_INVALID_ARG;
+    if (!number(rule.weight_decay) || !number(rule.eps) || !((float)rule.eps >= 1.17549435e-38f)) return MOE_ERR_INVALID_ARG;
     if (!(rule.beta1 >= 0.0 && rule.beta1 < 1.0) || !(rule.beta2 >= 0.0 && rule.beta2 < 1.0)) return MOE_ERR_INVALID_ARG;
     if (!lr_step && (!number(rule.lr) || rule.step < 1)) return MOE_ERR_INVALID_ARG;
     if (norm && (!number(rule.max_norm) || !number(rule.clip_eps))) return MOE_ERR_INVALID_ARG;
