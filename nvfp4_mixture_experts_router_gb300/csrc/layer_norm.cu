@@ -106,29 +106,6 @@ __device__ __forceinline__ typename RowVec<T_, VEC>::Raw pack_cols(const float2 
     return RowVec<T_, VEC>::pack(u);
 }
 
-// VEC consecutive parameters, of vector c of the row.  `wide`: 16-byte loads
-// (an aligned array; vectors of four or eight).
-template <int VEC>
-__device__ __forceinline__ void load_vector(const float* p, int c, bool wide, float2 (&v)[(VEC + 1) / 2]) {
-    p += (size_t)c * VEC;
-    if constexpr (VEC % 4 == 0) {
-        if (wide) {
-#pragma unroll
-            for (int k = 0; k < VEC / 4; ++k) {
-                const float4 w = reinterpret_cast<const float4*>(p)[k];
-                v[2 * k] = make_float2(w.x, w.y);
-                v[2 * k + 1] = make_float2(w.z, w.w);
-            }
-            return;
-        }
-    }
-#pragma unroll
-    for (int k = 0; k < VEC; ++k) {
-        if (k & 1) v[k >> 1].y = p[k];
-        else v[k >> 1] = make_float2(p[k], 0.0f);
-    }
-}
-
 // The parameters of the thread's C columns (0 past the row's end).
 template <int VEC, int C>
 __device__ __forceinline__ void load_params(const float* p, int j, int lanes, int n, bool wide, float2 (&v)[C / 2]) {

@@ -9,6 +9,7 @@
 // HBM is the bound: every input read once, every output written once.
 #include <math.h>
 
+#include "f32x2.cuh"
 #include "row_vec.cuh"
 #include "train_kernels.h"
 
@@ -24,6 +25,341 @@ __device__ __forceinline__ float linear_scale(float amax) {
     return amax == 0.0f ? 1.0f : fmaxf(amax / kE4M3Max, 1.17549435e-38f);
 }
 
+// A vector's values in pairs (a single one with 0).
+template <typename T_, int VEC>
+__device__ __forceinline__ void unpack_pairs(const typename RowVec<T_, VEC>::Raw& r, float2 (&v)[(VEC + 1) / 2]) {
+    float u[VEC];
+    RowVec<T_, VEC>::unpack(r, u);
+#pragma unroll
+    for (int k = 0; k < (VEC + 1) / 2; ++k) v[k] = make_float2(u[2 * k], VEC > 1 ? u[(2 * k + 1) % VEC] : 0.0f);
+}
+
+template <typename T_, int VEC>
+__device__ __forceinline__ typename RowVec<T_, VEC>::Raw pack_pairs(const float2 (&v)[(VEC + 1) / 2]) {
+    float u[VEC];
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) u[k] = k & 1 ? v[k >> 1].y : v[k >> 1].x;
+    return RowVec<T_, VEC>::pack(u);
+}
+
+// 1 / sqrt(S / H + eps) as the sum of two FP32 numbers, from S in two.  What is
+// quantized after it sits on borders (of E4M3's steps, of powers of two) that an
+// error of a unit crosses one time in a million; with rstd and h gamma in two
+// numbers y is rounded once.
+struct Rstd {
+    float hi, lo;
+};
+__device__ __forceinline__ float2 two_sum(float a, float b) {       // a + b = x + y
+    const float s = a + b, t = s - a;
+    return make_float2(s, (a - (s - t)) + (b - t));
+}
+__device__ __forceinline__ Rstd rstd_of(float2 sum, float2 inv_h, float eps) {
+    const float v = sum.x * inv_h.x;
+    const float v_lo = fmaf(sum.x, inv_h.x, -v) + fmaf(sum.x, inv_h.y, sum.y * inv_h.x);
+    const float2 t = two_sum(v, eps);
+    const float r = rsqrtf(t.x), w = t.x * r;       // Newton's correction: r (1 - t r^2) / 2
+    const float lo = 0.5f * r * (fmaf(-w, r, 1.0f) - fmaf(t.x, r, -w) * r - (t.y + v_lo) * r * r);
+    return Rstd{r, fabsf(lo) < INFINITY ? lo : 0.0f};
+}
+// h gamma rstd of two elements, rounded once (but for a unit in some hundreds).
+__device__ __forceinline__ float2 scaled(float2 h, float2 gamma, Rstd r) {
+    const float2 p = mul2(h, gamma), p_lo = make_float2(fmaf(h.x, gamma.x, -p.x), fmaf(h.y, gamma.y, -p.y));
+    return fma2(p, both(r.hi), fma2(p, both(r.lo), mul2(p_lo, both(r.hi))));
+}
+
+// Sum over the W warps of a row in two FP32 numbers, and with `most` the row's
+// largest m; every thread gets them.
+struct RowJoin {
+    float2 sum;
+    float most;
+};
+__device__ __forceinline__ RowJoin join_row(float sum, float m, bool most, int W, float2* s) {
+    sum = warp_sum(sum);
+    if (most) m = warp_max(m);
+    float2 v = make_float2(sum, 0.0f);
+    if (W > 1) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        if (lane == 0) s[warp] = make_float2(sum, m);
+        __syncthreads();
+        const float2 u = lane < W ? s[warp / W * W + lane] : make_float2(0.0f, 0.0f);
+        v.x = u.x;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1)
+            if (o < W) {
+                const float2 t = two_sum(v.x, __shfl_xor_sync(0xffffffffu, v.x, o));
+                v = make_float2(t.x, v.y + __shfl_xor_sync(0xffffffffu, v.y, o) + t.y);
+            }
+        // (lanes past the next power of two have not met the row's)
+        v.x = __shfl_sync(0xffffffffu, v.x, 0);
+        v.y = __shfl_sync(0xffffffffu, v.y, 0);
+        if (most) m = warp_max(u.y);
+    }
+    return RowJoin{v, m};
+}
+
+// A scale of `amax` by the mode's rule, stored at `to[i]`, and what y is multiplied by.
+__device__ __forceinline__ float put_scale(int mode, void* to, int64_t i, float amax, bool writes) {
+    if (mode == MOE_SCALE_MX) {
+        // mx_block_exp in the fields of FP32: the code is the exponent's less 8, 0 below that (and of infinity)
+        const int field = (int)(__float_as_uint(amax) >> 23), code = field < 255 ? max(field - 8, 0) : 0;
+        if (writes) static_cast<uint8_t*>(to)[i] = (uint8_t)code;
+        return __uint_as_float((uint32_t)(254 - code) << 23);
+    }
+    const float scale = linear_scale(amax);
+    if (writes) static_cast<float*>(to)[i] = scale;
+    return 1.0f / scale;
+}
+
+// Four E4M3 codes.
+__device__ __forceinline__ uint32_t e4m3x4(float2 a, float2 b) {
+    uint32_t r;
+    asm("{\n .reg .b16 lo, hi;\n cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n"
+        " mov.b32 %0, {lo, hi};\n}" : "=r"(r) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+template <int VEC>
+__device__ __forceinline__ void store_codes(uint8_t* q, float2 (&v)[(VEC + 1) / 2], float inv) {
+#pragma unroll
+    for (int k = 0; k < (VEC + 1) / 2; ++k) v[k] = mul2(v[k], both(inv));
+    if constexpr (VEC == 8) *reinterpret_cast<uint2*>(q) = make_uint2(e4m3x4(v[0], v[1]), e4m3x4(v[2], v[3]));
+    else if constexpr (VEC == 4) *reinterpret_cast<uint32_t*>(q) = e4m3x4(v[0], v[1]);
+    else if constexpr (VEC == 2) *reinterpret_cast<uint16_t*>(q) = (uint16_t)f32x2_to_e4m3x2(v[0].x, v[0].y);
+    else *q = (uint8_t)f32x2_to_e4m3x2(v[0].x, 0.0f);
+}
+// The first `count` codes of a vector, at any address.
+template <int VEC>
+__device__ __forceinline__ void put_codes(uint8_t* q, float2 (&v)[VEC / 2], float inv, int count) {
+#pragma unroll
+    for (int k = 0; k < VEC / 2; ++k) v[k] = mul2(v[k], both(inv));
+    uint32_t w[VEC / 4];
+#pragma unroll
+    for (int k = 0; k < VEC / 4; ++k) w[k] = e4m3x4(v[2 * k], v[2 * k + 1]);
+#pragma unroll
+    for (int k = 0; k < VEC; ++k)
+        if (k < count) q[k] = (uint8_t)(w[k >> 2] >> (8 * (k & 3)));
+}
+// The largest of `m` and the magnitudes of a vector.
+template <int VEC>
+__device__ __forceinline__ float max_of(float m, const float2 (&v)[(VEC + 1) / 2]) {
+#pragma unroll
+    for (int k = 0; k < (VEC + 1) / 2; ++k)
+        asm("{\n .reg .f32 x, y;\n abs.f32 x, %1;\n abs.f32 y, %2;\n max.f32 %0, %0, x, y;\n}" : "+f"(m) : "f"(v[k].x), "f"(v[k].y));
+    return m;
+}
+
+// A row off 16-byte blocks through shared memory: it lies there with its place
+// within 16 bytes, so that its whole blocks move in vectors and its ends alone by
+// elements, and the threads take and put vectors of the row at that offset.
+struct RowSlot {
+    static __host__ __device__ size_t bytes(size_t row) { return (row + 63) & ~(size_t)15; }    // with a vector past the end
+    static __device__ __forceinline__ uint32_t offset(const void* row) { return (uint32_t)reinterpret_cast<uintptr_t>(row) & 15u; }
+    // By `lanes` threads, of which this is the j-th.
+    template <typename One>
+    static __device__ __forceinline__ void move(uint8_t* slot, uint8_t* row, uint32_t bytes, int j, int lanes, bool out) {
+        const uint32_t off = offset(row), lead = min((16u - off) & 15u, bytes), whole = (bytes - lead) & ~15u;
+        uint8_t* in_slot = slot + off;
+        uint4 *a = reinterpret_cast<uint4*>(in_slot + lead), *b = reinterpret_cast<uint4*>(row + lead);
+        for (uint32_t k = j; k < whole / 16; k += lanes) (out ? b : a)[k] = (out ? a : b)[k];
+        // up to 15 bytes before and after
+        for (uint32_t k = j * sizeof(One); k < 32; k += lanes * sizeof(One)) {
+            const uint32_t at = k < 16 ? k : lead + whole + (k - 16);
+            if (at < (k < 16 ? lead : bytes)) {
+                One *c = reinterpret_cast<One*>(in_slot + at), *d = reinterpret_cast<One*>(row + at);
+                *(out ? d : c) = *(out ? c : d);
+            }
+        }
+    }
+    // Vector c of a row at `off`: two blocks, shifted.  Of the last one `count`
+    // elements count, the others become 0.
+    template <typename T_>
+    static __device__ __forceinline__ uint4 take(const uint8_t* slot, uint32_t off, int c, int count) {
+        constexpr int VEC = 16 / sizeof(T_);
+        const uint4 lo = reinterpret_cast<const uint4*>(slot)[c], hi = reinterpret_cast<const uint4*>(slot)[c + 1];
+        uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+        for (int i = 0; i < 6; ++i) w[i] = off & 8u ? w[i + 2] : w[i];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = off & 4u ? w[i + 1] : w[i];
+        if (sizeof(T_) == 2) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], off & 2u ? 16 : 0);
+        }
+        if (count < VEC) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                if (i >= count) w[i * sizeof(T_) / 4] &= sizeof(T_) == 4 ? 0u : i & 1 ? 0xffffu : 0xffff0000u;
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    template <typename T_>
+    static __device__ __forceinline__ void put(uint8_t* slot, uint32_t off, int c, int count, const uint4& v) {
+        constexpr int VEC = 16 / sizeof(T_);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint8_t* to = slot + off + c * 16;
+        if (count == VEC && (off & 3u) == 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) reinterpret_cast<uint32_t*>(to)[i] = w[i];
+        } else if (sizeof(T_) == 2 && count == VEC) {
+            *reinterpret_cast<uint16_t*>(to) = (uint16_t)w[0];
+#pragma unroll
+            for (int i = 0; i < 3; ++i) *reinterpret_cast<uint32_t*>(to + 2 + 4 * i) = __funnelshift_r(w[i], w[i + 1], 16);
+            *reinterpret_cast<uint16_t*>(to + 14) = (uint16_t)(w[3] >> 16);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                if (i < count) {
+                    if (sizeof(T_) == 2) reinterpret_cast<uint16_t*>(to)[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+                    else reinterpret_cast<uint32_t*>(to)[i] = w[i & 3];
+                }
+        }
+    }
+};
+
+// A thread's columns of gamma, of vector c (0 past the row's end).  RAGGED: the last
+// vector may be cut.
+template <int VEC, bool RAGGED>
+__device__ __forceinline__ void gamma_vector(const float* gamma, int H, int c, bool wide, float2 (&ga)[(VEC + 1) / 2]) {
+#pragma unroll
+    for (int k = 0; k < (VEC + 1) / 2; ++k) ga[k] = both(0.0f);
+    if ((c + 1) * VEC <= H) {
+        load_vector<VEC>(gamma, c, wide, ga);
+    } else if (RAGGED) {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k)
+            if (c * VEC + k < H) (k & 1 ? ga[k >> 1].y : ga[k >> 1].x) = gamma[c * VEC + k];
+    }
+}
+
+constexpr int kRowColumns = 8192;   // rows up to here lie in registers
+
+// Rows of up to kRowColumns columns in registers: C columns a thread, V vectors
+// that lie `lanes` vectors apart; W warps a row, eight warps a block or one row.
+// STAGED: the rows pass through shared memory (RowSlot).
+template <typename T_, int VEC, int C, bool RES, bool Q, bool STAGED, int THREADS, int BLOCKS>
+__global__ void __launch_bounds__(THREADS, BLOCKS) rms_rows_kernel(const RmsArgs a, int W, float2 inv_h, bool wide_gamma) {
+    using RV = RowVec<T_, VEC>;
+    using Raw = typename RV::Raw;
+    using One = typename RowVec<T_, 1>::Raw;
+    constexpr int V = C / VEC, P = (VEC + 1) / 2;
+    static_assert(!STAGED || sizeof(Raw) == 16, "staged rows are taken in whole vectors");
+    static_assert(!Q || VEC >= 4, "a block of 128 is a warp's");
+    __shared__ float2 s_red[32];
+    extern __shared__ __align__(16) uint8_t s_mem[];    // STAGED: a group's slots
+    pdl_wait();
+    const int lanes = W * 32, j = threadIdx.x % lanes, g = threadIdx.x / lanes, G = blockDim.x / lanes;
+    const int n = (a.H + VEC - 1) / VEC;                // (not STAGED: H is a multiple)
+    const int64_t t = (int64_t)blockIdx.x * G + g;
+    const bool live = t < a.T;
+    const uint32_t row_bytes = (uint32_t)a.H * sizeof(T_);
+    const size_t slot = RowSlot::bytes(row_bytes);
+    uint8_t *slot0 = s_mem + g * (STAGED ? 2 * slot + RowSlot::bytes(a.H) : 0), *slot1 = slot0 + slot, *slot_q = slot1 + slot;
+    const T_* x = static_cast<const T_*>(a.x) + (live ? t : 0) * a.x_stride;
+    const T_* res = RES ? static_cast<const T_*>(a.residual) + (live ? t : 0) * a.residual_stride : nullptr;
+    T_* out_h = RES && a.h && live ? static_cast<T_*>(a.h) + t * a.h_stride : nullptr;
+    T_* y = a.y && live ? static_cast<T_*>(a.y) + t * a.y_stride : nullptr;
+    uint8_t* q = Q && a.q && live ? static_cast<uint8_t*>(a.q) + t * a.H : nullptr;
+    if constexpr (STAGED) {
+        if (live) RowSlot::move<One>(slot0, (uint8_t*)x, row_bytes, j, lanes, false);
+        if (RES && live) RowSlot::move<One>(slot1, (uint8_t*)res, row_bytes, j, lanes, false);
+        __syncthreads();
+    }
+    auto count_of = [&](int c) { return min(VEC, a.H - c * VEC); };
+    auto load = [&](const T_* row, const uint8_t* at, int c) -> Raw {
+        if (!live || c >= n) return Raw{};
+        if constexpr (STAGED) return RowSlot::take<T_>(at, RowSlot::offset(row), c, count_of(c));
+        else return reinterpret_cast<const Raw*>(row)[c];
+    };
+    auto store = [&](T_* row, uint8_t* at, int c, const Raw& v) {
+        if constexpr (STAGED) RowSlot::put<T_>(at, RowSlot::offset(row), c, count_of(c), v);
+        else reinterpret_cast<Raw*>(row)[c] = v;
+    };
+    Raw h[V];
+    {
+        Raw r[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            h[i] = load(x, slot0, j + i * lanes);
+            if (RES) r[i] = load(res, slot1, j + i * lanes);
+        }
+        if constexpr (RES) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                float2 u[P], v[P];
+                unpack_pairs<T_, VEC>(h[i], u);
+                unpack_pairs<T_, VEC>(r[i], v);
+#pragma unroll
+                for (int k = 0; k < P; ++k) u[k] = add2(u[k], v[k]);
+                h[i] = pack_pairs<T_, VEC>(u);
+                if (!STAGED && out_h && j + i * lanes < n) store(out_h, nullptr, j + i * lanes, h[i]);
+            }
+        }
+    }
+    // gamma of vector c (from L1)
+    auto gamma_of = [&](int c, float2 (&ga)[P]) { gamma_vector<VEC, STAGED>(a.gamma, a.H, c, wide_gamma, ga); };
+    const bool by_row = Q && a.scale_mode == MOE_SCALE_ROW;
+    float2 sq = both(0.0f);
+    float most = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        float2 u[P];
+        unpack_pairs<T_, VEC>(h[i], u);
+#pragma unroll
+        for (int k = 0; k < P; ++k) sq = fma2(u[k], u[k], sq);
+        if (by_row) {
+            float2 ga[P];
+            gamma_of(j + i * lanes, ga);
+#pragma unroll
+            for (int k = 0; k < P; ++k) u[k] = mul2(u[k], ga[k]);
+            most = max_of<VEC>(most, u);
+        }
+    }
+    const RowJoin row = join_row(sq.x + sq.y, most, by_row, W, s_red);
+    const Rstd r = rstd_of(row.sum, inv_h, a.eps);
+    if (a.rstd && live && j == 0) a.rstd[t] = r.hi + r.lo;
+    float inv = 1.0f;
+    if (by_row) inv = put_scale(MOE_SCALE_ROW, a.scales, t, row.most * r.hi, live && j == 0);
+    if constexpr (STAGED)
+        if (W == 1) __syncthreads();        // (else join_row's: every thread has taken its vectors)
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = j + i * lanes;
+        const bool there = live && c < n;
+        float2 u[P], ga[P];
+        if (STAGED && out_h && there) store(out_h, slot0, c, h[i]);
+        unpack_pairs<T_, VEC>(h[i], u);
+        gamma_of(c, ga);
+#pragma unroll
+        for (int k = 0; k < P; ++k) u[k] = scaled(u[k], ga[k], r);
+        if (y && there) store(y, slot1, c, pack_pairs<T_, VEC>(u));
+        if constexpr (Q) {
+            if (!by_row) {
+                const bool mx = a.scale_mode == MOE_SCALE_MX;
+                float m = max_of<VEC>(0.0f, u);
+#pragma unroll
+                for (int o = 1; o < 32 / VEC; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                if (!mx) {
+#pragma unroll
+                    for (int o = 32 / VEC; o < 128 / VEC; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                }
+                const int per = mx ? 32 : 128;
+                inv = put_scale(a.scale_mode, a.scales, t * ((a.H + per - 1) / per) + c * VEC / per, m,
+                                there && c * VEC % per == 0);
+            }
+            if (q && there) {
+                if constexpr (STAGED) put_codes<VEC>(slot_q + RowSlot::offset(q) + c * VEC, u, inv, count_of(c));
+                else store_codes<VEC>(q + (int64_t)c * VEC, u, inv);
+            }
+        }
+    }
+    if constexpr (STAGED) {
+        __syncthreads();
+        if (out_h) RowSlot::move<One>(slot0, reinterpret_cast<uint8_t*>(out_h), row_bytes, j, lanes, true);
+        if (y) RowSlot::move<One>(slot1, reinterpret_cast<uint8_t*>(y), row_bytes, j, lanes, true);
+        if (q) RowSlot::move<uint8_t>(slot_q, q, (uint32_t)a.H, j, lanes, true);
+    }
+    pdl_launch_dependents();
+}
+
 constexpr int kRmsThreads = 512;
 constexpr int kRmsParts = 152;      // row groups of dgamma
 
@@ -37,23 +373,6 @@ __device__ __forceinline__ float block_join(float v, float* s) {
     const int lane = threadIdx.x & 31;
     v = lane < (int)(blockDim.x >> 5) ? s[lane] : 0.0f;
     return MAX ? warp_max(v) : warp_sum(v);
-}
-
-template <typename T_, int VEC>
-__device__ __forceinline__ void store_codes(uint8_t* q, const float (&v)[VEC], float inv) {
-    if constexpr (VEC == 1) {
-        *q = (uint8_t)f32x2_to_e4m3x2(v[0] * inv, 0.0f);
-    } else if constexpr (VEC == 2) {
-        *reinterpret_cast<uint16_t*>(q) = (uint16_t)f32x2_to_e4m3x2(v[0] * inv, v[1] * inv);
-    } else {
-        uint32_t w[VEC / 4];
-#pragma unroll
-        for (int k = 0; k < VEC / 4; ++k)
-            w[k] = f32x2_to_e4m3x2(v[4 * k] * inv, v[4 * k + 1] * inv) |
-                   f32x2_to_e4m3x2(v[4 * k + 2] * inv, v[4 * k + 3] * inv) << 16;
-        if constexpr (VEC == 8) *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
-        else *reinterpret_cast<uint32_t*>(q) = w[0];
-    }
 }
 
 // A block a row, which is walked once for each of its results.
@@ -145,14 +464,248 @@ __global__ void __launch_bounds__(kRmsThreads)
 #pragma unroll
         for (int k = 0; k < VEC; ++k) v[k] = v[k] * rstd * a.gamma[c * VEC + k];
         if (y) y[c] = RV::pack(v);
-        if (q) store_codes<T_, VEC>(q + c * VEC, v, a.scale_mode == MOE_SCALE_ROW ? inv : s_block[c * VEC / 32]);
+        if (q) {
+            float2 u[(VEC + 1) / 2];
+#pragma unroll
+            for (int k = 0; k < (VEC + 1) / 2; ++k) u[k] = make_float2(v[2 * k], VEC > 1 ? v[(2 * k + 1) % VEC] : 0.0f);
+            store_codes<VEC>(q + c * VEC, u, a.scale_mode == MOE_SCALE_ROW ? inv : s_block[c * VEC / 32]);
+        }
     }
     pdl_launch_dependents();
 }
 
 // ---- backward -----------------------------------------------------------------------
 
-// Partial sums of dgamma: a thread per column, a group of rows per blockIdx.y.
+// A block's sums of dgamma, its groups' in order, to the block's row of `part`.
+template <int VEC, int V>
+__device__ __forceinline__ void put_sums(const RmsGradArgs& a, const float2 (&dg)[V][(VEC + 1) / 2], int j, int lanes, int g,
+                                         int G, float* sums) {
+    float* out = a.part + (size_t)blockIdx.x * a.H;
+    if (G > 1) __syncthreads();
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+            const int h = (j + i * lanes) * VEC + k;
+            const float v = k & 1 ? dg[i][k >> 1].y : dg[i][k >> 1].x;
+            if (h < a.H) (G > 1 ? sums + (size_t)g * a.H : out)[h] = v;
+        }
+    if (G > 1) {
+        __syncthreads();
+        for (int h = threadIdx.x; h < a.H; h += blockDim.x) {
+            float v = 0.0f;
+            for (int q = 0; q < G; ++q) v += sums[(size_t)q * a.H + h];
+            out[h] = v;
+        }
+    }
+}
+
+// Rows of up to kRowColumns columns: a block walks rows, W warps a row of C columns
+// a thread (eight warps a block, or one row), and each thread keeps the sums of
+// dgamma for its columns in registers until the end.  The rows wait in a ring of S
+// stages in shared memory, where each thread copies and reads its own vectors
+// alone.  A turn takes the sum of one row's g hhat and writes the row before it,
+// whose sum has met in between: one barrier a turn, and the two rows' reductions
+// overlap.  DH: 0 none, 1 in the ring, 2 loaded when it is needed (FP32: three
+// stages of all three would not fit).
+template <typename T_, int VEC, int C, int DH>
+__global__ void __launch_bounds__(512, 1) rms_ring_backward_kernel(const RmsGradArgs a, int W, int S, float inv_h, bool wide_gamma) {
+    using RV = RowVec<T_, VEC>;
+    using Raw = typename RV::Raw;
+    constexpr int V = C / VEC, P = (VEC + 1) / 2, N = DH == 1 ? 3 : 2;
+    __shared__ float s_red[2][32];
+    extern __shared__ __align__(16) uint8_t s_mem[];    // [S][N][V][threads] vectors; in the end the groups' sums
+    pdl_wait();
+    const int lanes = W * 32, j = threadIdx.x % lanes, g = threadIdx.x / lanes, G = blockDim.x / lanes;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = a.H / VEC;
+    const int64_t step = (int64_t)gridDim.x * G, first = (int64_t)blockIdx.x * G + g;
+    const Raw* rows[3] = {static_cast<const Raw*>(a.dy) + j, static_cast<const Raw*>(a.h) + j, static_cast<const Raw*>(a.dh) + j};
+    const int64_t strides[3] = {a.dy_stride / VEC, a.h_stride / VEC, a.dh_stride / VEC};
+    Raw* dx = static_cast<Raw*>(a.dx) + j;
+    const int64_t dx_stride = a.dx_stride / VEC;
+    Raw* ring = reinterpret_cast<Raw*>(s_mem) + threadIdx.x;
+    auto at = [&](int stage, int k, int i) { return ring + ((stage * N + k) * V + i) * (int)blockDim.x; };
+    auto fetch = [&](int64_t t, int stage) {
+        if (t < a.T)
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const Raw* row = rows[k] + t * strides[k];
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (j + i * lanes < n)
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(at(stage, k, i))),
+                                     "l"(row + i * lanes), "n"(sizeof(Raw)) : "memory");
+            }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    for (int q = 0; q < S; ++q) fetch(first + q * step, q);
+    float2 dg[V][P];
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int k = 0; k < P; ++k) dg[i][k] = both(0.0f);
+    int stage = 0, before = 0, turn = 0;
+    float sum_before = 0.0f, rstd_before = 0.0f, rstd = first < a.T ? a.rstd[first] : 0.0f;
+    // turns: row t's sum and row t - step's result; one more than rows.  Uniform over the block
+    for (int64_t t = first; t - g - step < a.T; t += step) {
+        const bool live = t < a.T, had = t >= step && t - step < a.T && t != first;
+        const float rstd_next = t + step < a.T ? a.rstd[t + step] : 0.0f;
+        // row t's copies; S - 2 later ones may be under way (row t - step's stage is filled below)
+        if (t == first) {
+            if (S == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
+            else asm volatile("cp.async.wait_group 3;" ::: "memory");
+        } else {
+            if (S == 3) asm volatile("cp.async.wait_group 1;" ::: "memory");
+            else asm volatile("cp.async.wait_group 2;" ::: "memory");
+        }
+        Raw e[V];
+        if (DH == 2) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) e[i] = had && j + i * lanes < n ? rows[2][(t - step) * strides[2] + i * lanes] : Raw{};
+        }
+        float2 sum = both(0.0f);
+        if (live) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (j + i * lanes < n) {
+                    float2 d[P], h[P], ga[P];
+                    unpack_pairs<T_, VEC>(*at(stage, 0, i), d);
+                    unpack_pairs<T_, VEC>(*at(stage, 1, i), h);
+                    gamma_vector<VEC, false>(a.gamma, a.H, j + i * lanes, wide_gamma, ga);
+#pragma unroll
+                    for (int k = 0; k < P; ++k) {
+                        const float2 p = mul2(d[k], mul2(h[k], both(rstd)));
+                        dg[i][k] = add2(dg[i][k], p);
+                        sum = fma2(p, ga[k], sum);
+                    }
+                }
+        }
+        float s = warp_sum(sum.x + sum.y);
+        if (W > 1) {
+            if (lane == 0) s_red[turn][warp] = s;
+            if (t != first) sum_before = warp_sum(lane < W ? s_red[turn ^ 1][warp / W * W + lane] : 0.0f);
+        }
+        if (had) {
+            const float mean = sum_before * inv_h * rstd_before;
+            Raw* out = dx + (t - step) * dx_stride;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (j + i * lanes < n) {
+                    float2 d[P], h[P], ga[P], u[P];
+                    unpack_pairs<T_, VEC>(*at(before, 0, i), d);
+                    unpack_pairs<T_, VEC>(*at(before, 1, i), h);
+                    if (DH == 1) unpack_pairs<T_, VEC>(*at(before, N - 1, i), u);
+                    if (DH == 2) unpack_pairs<T_, VEC>(e[i], u);
+                    gamma_vector<VEC, false>(a.gamma, a.H, j + i * lanes, wide_gamma, ga);
+                    // rstd (g - hhat mean) + dh
+#pragma unroll
+                    for (int k = 0; k < P; ++k) {
+                        const float2 w = fma2(h[k], both(-mean), mul2(d[k], ga[k]));
+                        d[k] = DH ? fma2(w, both(rstd_before), u[k]) : mul2(w, both(rstd_before));
+                    }
+                    out[i * lanes] = pack_pairs<T_, VEC>(d);
+                }
+        }
+        if (t != first) fetch(t + (S - 1) * step, before);      // the stage of row t - step is free
+        if (W > 1) __syncthreads();
+        sum_before = s;
+        rstd_before = rstd;
+        rstd = rstd_next;
+        before = stage;
+        if (++stage == S) stage = 0;
+        turn ^= 1;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    put_sums<VEC, V>(a, dg, j, lanes, g, G, reinterpret_cast<float*>(s_mem));
+    pdl_launch_dependents();
+}
+
+// The same for rows off 16-byte blocks, in vectors of two bytes: each row through
+// slots (RowSlot), one after the other.
+template <typename T_, int C, bool DH, int BLOCKS>
+__global__ void __launch_bounds__(512, BLOCKS) rms_slot_backward_kernel(const RmsGradArgs a, int W, float inv_h, bool wide_gamma) {
+    constexpr int VEC = 16 / sizeof(T_);
+    using Raw = typename RowVec<T_, VEC>::Raw;
+    using One = typename RowVec<T_, 1>::Raw;
+    constexpr int V = C / VEC, P = VEC / 2, N = DH ? 3 : 2;
+    __shared__ float s_red[2][32];
+    extern __shared__ __align__(16) uint8_t s_mem[];    // [groups][N] slots; in the end the groups' sums
+    pdl_wait();
+    const int lanes = W * 32, j = threadIdx.x % lanes, g = threadIdx.x / lanes, G = blockDim.x / lanes;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = (a.H + VEC - 1) / VEC;
+    const int64_t step = (int64_t)gridDim.x * G, first = (int64_t)blockIdx.x * G + g;
+    const T_* rows[3] = {static_cast<const T_*>(a.dy), static_cast<const T_*>(a.h), static_cast<const T_*>(a.dh)};
+    const int64_t strides[3] = {a.dy_stride, a.h_stride, a.dh_stride};
+    const uint32_t row_bytes = (uint32_t)a.H * sizeof(T_);
+    const size_t slot = RowSlot::bytes(row_bytes);
+    uint8_t* slots = s_mem + g * N * slot;
+    float2 dg[V][P];
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int k = 0; k < P; ++k) dg[i][k] = both(0.0f);
+    int turn = 0;
+    for (int64_t t = first; t - g < a.T; t += step) {        // uniform over the block
+        const bool live = t < a.T;
+        const float rstd = live ? a.rstd[t] : 0.0f;
+        if (live)
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                RowSlot::move<One>(slots + k * slot, (uint8_t*)(rows[k] + t * strides[k]), row_bytes, j, lanes, false);
+        __syncthreads();
+        Raw r[N][V];
+        float2 sum = both(0.0f);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = j + i * lanes;
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                r[k][i] = live && c < n ? RowSlot::take<T_>(slots + k * slot, RowSlot::offset(rows[k] + t * strides[k]), c,
+                                                            min(VEC, a.H - c * VEC))
+                                        : Raw{};
+            float2 d[P], h[P], ga[P];
+            unpack_pairs<T_, VEC>(r[0][i], d);
+            unpack_pairs<T_, VEC>(r[1][i], h);
+            gamma_vector<VEC, true>(a.gamma, a.H, c, wide_gamma, ga);
+#pragma unroll
+            for (int k = 0; k < P; ++k) {
+                const float2 p = mul2(d[k], mul2(h[k], both(rstd)));
+                dg[i][k] = add2(dg[i][k], p);
+                sum = fma2(p, ga[k], sum);
+            }
+        }
+        float s = warp_sum(sum.x + sum.y);
+        if (lane == 0) s_red[turn][warp] = s;
+        __syncthreads();            // and every thread has taken its vectors
+        if (W > 1) s = warp_sum(lane < W ? s_red[turn][warp / W * W + lane] : 0.0f);
+        turn ^= 1;
+        const float mean = s * inv_h * rstd;
+        T_* out = static_cast<T_*>(a.dx) + (live ? t : 0) * a.dx_stride;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = j + i * lanes;
+            float2 d[P], h[P], ga[P], u[P];
+            unpack_pairs<T_, VEC>(r[0][i], d);
+            unpack_pairs<T_, VEC>(r[1][i], h);
+            if (DH) unpack_pairs<T_, VEC>(r[N - 1][i], u);
+            gamma_vector<VEC, true>(a.gamma, a.H, c, wide_gamma, ga);
+#pragma unroll
+            for (int k = 0; k < P; ++k) {
+                const float2 w = fma2(h[k], both(-mean), mul2(d[k], ga[k]));
+                d[k] = DH ? fma2(w, both(rstd), u[k]) : mul2(w, both(rstd));
+            }
+            if (live && c < n) RowSlot::put<T_>(slots, RowSlot::offset(out), c, min(VEC, a.H - c * VEC), pack_pairs<T_, VEC>(d));
+        }
+        __syncthreads();
+        if (live) RowSlot::move<One>(slots, reinterpret_cast<uint8_t*>(out), row_bytes, j, lanes, true);
+        __syncthreads();
+    }
+    put_sums<VEC, V>(a, dg, j, lanes, g, G, reinterpret_cast<float*>(s_mem));
+    pdl_launch_dependents();
+}
+
+// Partial sums of dgamma for longer rows: a thread per column, a group of rows per
+// blockIdx.y.
 template <typename T_>
 __global__ void __launch_bounds__(256) rms_partial_kernel(const RmsGradArgs a) {
     using RV = RowVec<T_, 1>;
@@ -170,13 +723,22 @@ __global__ void __launch_bounds__(256) rms_partial_kernel(const RmsGradArgs a) {
     a.part[(size_t)blockIdx.y * a.H + c] = sum;
 }
 
-__global__ void __launch_bounds__(256) rms_reduce_kernel(int H, int parts, const float* part, float* dgamma) {
+// dgamma from `parts` partial sums [parts][H]: 32 columns a block, a 32nd of the
+// parts a warp, then the warps' sums in order.
+__global__ void __launch_bounds__(1024) rms_reduce_kernel(int H, int parts, const float* part, float* dgamma) {
+    __shared__ float s[32][33];
     pdl_wait();
-    const int c = blockIdx.x * 256 + threadIdx.x;
-    if (c >= H) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float sum = 0.0f;
-    for (int p = 0; p < parts; ++p) sum += part[(size_t)p * H + c];
-    dgamma[c] = sum;
+    if (c < H) {
+#pragma unroll 8
+        for (int p = warp; p < parts; p += 32) sum += part[(size_t)p * H + c];
+    }
+    s[warp][lane] = sum;
+    __syncthreads();
+    sum = warp_sum(s[lane][warp]);
+    if (lane == 0 && blockIdx.x * 32 + warp < H) dgamma[blockIdx.x * 32 + warp] = sum;
+    pdl_launch_dependents();
 }
 
 template <typename T_, int VEC>
@@ -215,11 +777,91 @@ __global__ void __launch_bounds__(kRmsThreads) rms_dx_kernel(const RmsGradArgs a
     }
 }
 
+// C columns a thread.
+template <typename T_, int VEC, int C, bool Q, bool STAGED, int THREADS, int BLOCKS>
+cudaError_t forward_rows(const LaunchCtx& c, const RmsArgs& a) {
+    const int W = (a.H + 32 * C - 1) / (32 * C), G = W >= 8 ? 1 : 8 / W, threads = W * G * 32;
+    const double inv = 1.0 / a.H;
+    const float2 inv_h = make_float2((float)inv, (float)(inv - (double)(float)inv));
+    const bool wide_gamma = row_at(a.gamma) % 16 == 0;
+    const size_t slots = STAGED ? G * (2 * RowSlot::bytes(a.H * sizeof(T_)) + RowSlot::bytes(a.H)) : 0;
+    auto kernel = a.residual ? rms_rows_kernel<T_, VEC, C, true, Q, STAGED, THREADS, BLOCKS>
+                             : rms_rows_kernel<T_, VEC, C, false, Q, STAGED, THREADS, BLOCKS>;
+    return c.launch(kernel, dim3((unsigned)((a.T + G - 1) / G)), dim3(threads), slots, a, W, inv_h, wide_gamma);
+}
+
+template <typename T_, int VEC, bool Q>
+cudaError_t forward_short(const LaunchCtx& c, const RmsArgs& a) {
+    constexpr int kWhole = 16 / sizeof(T_);
+    if constexpr (VEC < 4 && (sizeof(T_) == 2 || Q)) {
+        // through shared memory, where a vector (or its codes) is less than eight bytes
+        if (sizeof(T_) == 2 && a.H > 4096) return forward_rows<T_, kWhole, 32, Q, true, 256, 4>(c, a);
+        if (a.H > 256) return forward_rows<T_, kWhole, 16, Q, true, 512, 2>(c, a);
+        return forward_rows<T_, kWhole, 8, Q, true, 256, 4>(c, a);
+    } else {
+        if constexpr (sizeof(T_) == 2)
+            if (a.H > 512 && a.T > 2 * 152) return forward_rows<T_, VEC, 32, Q, false, 256, 4>(c, a);
+        if constexpr (VEC >= 2)
+            if (a.H > 256 && a.T > 152) return forward_rows<T_, VEC, 16, Q, false, 512, 2>(c, a);
+        return forward_rows<T_, VEC, 8, Q, false, 1024, 1>(c, a);
+    }
+}
+
 template <typename T_, int VEC>
 cudaError_t forward_any(const LaunchCtx& c, const RmsArgs& a) {
+    if (a.H <= kRowColumns) return a.q ? forward_short<T_, VEC, true>(c, a) : forward_short<T_, VEC, false>(c, a);
     const size_t smem = a.q && a.scale_mode != MOE_SCALE_ROW ? (size_t)(a.H + 31) / 32 * 4 : 0;
     return c.launch(rms_norm_kernel<T_, VEC>, dim3((unsigned)a.T), dim3(kRmsThreads), smem, a);
 }
+// The shape of the backward kernels of short rows: warps a row, rows a block, and
+// blocks on an SM (512 threads, or twice as many for the slots of BF16 rows).
+struct BackwardShape {
+    int C, W, G, threads, per_sm;
+};
+BackwardShape backward_shape(int H, bool many) {
+    BackwardShape s;
+    s.C = H > 256 ? 16 : 8;
+    s.W = (H + 32 * s.C - 1) / (32 * s.C);
+    s.G = s.W >= 8 ? 1 : 8 / s.W;
+    s.threads = s.W * s.G * 32;
+    s.per_sm = (many ? 1024 : 512) / s.threads;
+    return s;
+}
+int backward_blocks(int T, const BackwardShape& s) {
+    const int need = (T + s.G - 1) / s.G, most = 152 * s.per_sm;
+    return need < 1 ? 1 : need < most ? need : most;
+}
+
+constexpr int kBackwardSmem = 216 * 1024;
+template <typename T_, int VEC, int C>
+cudaError_t ring_backward(const LaunchCtx& c, const RmsGradArgs& a, const BackwardShape& s) {
+    constexpr int kDh = sizeof(T_) == 2 ? 1 : 2;
+    auto kernel = a.dh ? rms_ring_backward_kernel<T_, VEC, C, kDh> : rms_ring_backward_kernel<T_, VEC, C, 0>;
+    const int stage = (a.dh && kDh == 1 ? 3 : 2) * s.threads * C * (int)sizeof(T_);
+    const int S = 4 * stage <= kBackwardSmem / s.per_sm ? 4 : 3;     // (three of the longest rows' are 144 KB of BF16, 192 of FP32)
+    const int sums = s.G > 1 ? s.G * a.H * 4 : 0;
+    return c.launch(kernel, dim3(backward_blocks(a.T, s)), dim3(s.threads), S * stage > sums ? S * stage : sums, a, s.W, S,
+                    1.0f / (float)a.H, row_at(a.gamma) % 16 == 0);
+}
+template <typename T_, int C>
+cudaError_t slot_backward(const LaunchCtx& c, const RmsGradArgs& a, const BackwardShape& s) {
+    constexpr int kBlocks = sizeof(T_) == 2 ? 2 : 1;
+    auto kernel = a.dh ? rms_slot_backward_kernel<T_, C, true, kBlocks> : rms_slot_backward_kernel<T_, C, false, kBlocks>;
+    const size_t slots = s.G * (a.dh ? 3 : 2) * RowSlot::bytes(a.H * sizeof(T_)), sums = s.G > 1 ? (size_t)s.G * a.H * 4 : 0;
+    return c.launch(kernel, dim3(backward_blocks(a.T, s)), dim3(s.threads), slots > sums ? slots : sums, a, s.W,
+                    1.0f / (float)a.H, row_at(a.gamma) % 16 == 0);
+}
+// Are rows of these vectors taken through slots?  (Asynchronous copies have four bytes at least.)
+bool in_slots(int elem, int bytes) { return elem == 2 && bytes == 2; }
+template <typename T_, int VEC>
+cudaError_t backward_any(const LaunchCtx& c, const RmsGradArgs& a, const BackwardShape& s) {
+    if constexpr (VEC * sizeof(T_) < 4) return s.C == 16 ? slot_backward<T_, 16>(c, a, s) : slot_backward<T_, 8>(c, a, s);
+    else return s.C == 16 ? ring_backward<T_, VEC, 16>(c, a, s) : ring_backward<T_, VEC, 8>(c, a, s);
+}
+cudaError_t launch_backward_rows(const LaunchCtx& c, int elem, int bytes, const RmsGradArgs& a, const BackwardShape& s) {
+    MOE_ROW_VEC(elem, bytes, backward_any, c, a, s);
+}
+
 template <typename T_, int VEC>
 cudaError_t dx_any(const LaunchCtx& c, const RmsGradArgs& a) {
     return c.launch(rms_dx_kernel<T_, VEC>, dim3((unsigned)a.T), dim3(kRmsThreads), 0, a);
@@ -238,20 +880,75 @@ cudaError_t launch_rms_norm(const LaunchCtx& c, int elem, const RmsArgs& a) {
     MOE_ROW_VEC(elem, bytes, forward_any, c, a);
 }
 
-size_t rms_norm_workspace_bytes(int T, int H) { return align_up((uint64_t)kRmsParts * H * 4, 256); }
+namespace {
+template <typename K>
+void allow(cudaError_t& e, K kernel) {
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBackwardSmem);
+}
+template <typename T_, int C, int THREADS, int BLOCKS>
+void allow_staged(cudaError_t& e) {
+    constexpr int VEC = 16 / sizeof(T_);
+    allow(e, rms_rows_kernel<T_, VEC, C, false, true, true, THREADS, BLOCKS>);
+    allow(e, rms_rows_kernel<T_, VEC, C, true, true, true, THREADS, BLOCKS>);
+    if constexpr (sizeof(T_) == 2) {
+        allow(e, rms_rows_kernel<T_, VEC, C, false, false, true, THREADS, BLOCKS>);
+        allow(e, rms_rows_kernel<T_, VEC, C, true, false, true, THREADS, BLOCKS>);
+    }
+}
+template <typename T_, int VEC>
+void allow_ring(cudaError_t& e) {
+    constexpr int kDh = sizeof(T_) == 2 ? 1 : 2;
+    allow(e, rms_ring_backward_kernel<T_, VEC, 8, 0>);
+    allow(e, rms_ring_backward_kernel<T_, VEC, 8, kDh>);
+    allow(e, rms_ring_backward_kernel<T_, VEC, 16, 0>);
+    allow(e, rms_ring_backward_kernel<T_, VEC, 16, kDh>);
+}
+}  // namespace
+
+cudaError_t setup_rms_norm_kernels() {
+    cudaError_t e = cudaSuccess;
+    allow_staged<__nv_bfloat16, 8, 256, 4>(e);
+    allow_staged<__nv_bfloat16, 16, 512, 2>(e);
+    allow_staged<__nv_bfloat16, 32, 256, 4>(e);
+    allow_staged<float, 8, 256, 4>(e);
+    allow_staged<float, 16, 512, 2>(e);
+    allow_ring<__nv_bfloat16, 8>(e);
+    allow_ring<__nv_bfloat16, 4>(e);
+    allow_ring<__nv_bfloat16, 2>(e);
+    allow_ring<float, 4>(e);
+    allow_ring<float, 2>(e);
+    allow_ring<float, 1>(e);
+    allow(e, rms_slot_backward_kernel<__nv_bfloat16, 8, false, 2>);
+    allow(e, rms_slot_backward_kernel<__nv_bfloat16, 8, true, 2>);
+    allow(e, rms_slot_backward_kernel<__nv_bfloat16, 16, false, 2>);
+    allow(e, rms_slot_backward_kernel<__nv_bfloat16, 16, true, 2>);
+    return e;
+}
+
+// Partial sums of dgamma, a row of H for each block of the backward kernels.
+size_t rms_norm_workspace_bytes(int T, int H) {
+    const int parts = H > kRowColumns ? kRmsParts : backward_blocks(T, backward_shape(H, true));
+    return align_up((uint64_t)parts * H * 4, 256);
+}
 
 cudaError_t launch_rms_norm_backward(const LaunchCtx& c, int elem, const RmsGradArgs& a) {
-    // the column sums first: dx may overwrite dy or h
-    const dim3 parts((unsigned)((a.H + 255) / 256), kRmsParts);
-    cudaError_t e = c.launch(elem == 2 ? rms_partial_kernel<__nv_bfloat16> : rms_partial_kernel<float>, parts, dim3(256),
-                             0, a);
-    if (e != cudaSuccess) return e;
-    e = c.launch(rms_reduce_kernel, dim3((unsigned)((a.H + 255) / 256)), dim3(256), 0, a.H, kRmsParts,
-                 (const float*)a.part, a.dgamma);
-    if (e != cudaSuccess || a.T == 0) return e;
     const int bytes = row_vec_bytes(a.H, elem,
                                     row_at(a.dy, a.dy_stride, elem) | row_at(a.dh, a.dh ? a.dh_stride : 0, elem) |
                                         row_at(a.h, a.h_stride, elem) | row_at(a.dx, a.dx_stride, elem));
+    const bool rows = a.H <= kRowColumns;
+    const BackwardShape s = backward_shape(a.H, in_slots(elem, bytes));
+    cudaError_t e;
+    if (rows) {
+        e = launch_backward_rows(c, elem, bytes, a, s);
+    } else {
+        // the column sums first: dx may overwrite dy or h
+        const dim3 parts((unsigned)((a.H + 255) / 256), kRmsParts);
+        e = c.launch(elem == 2 ? rms_partial_kernel<__nv_bfloat16> : rms_partial_kernel<float>, parts, dim3(256), 0, a);
+    }
+    if (e != cudaSuccess) return e;
+    e = c.launch(rms_reduce_kernel, dim3((unsigned)((a.H + 31) / 32)), dim3(1024), 0, a.H,
+                 rows ? backward_blocks(a.T, s) : kRmsParts, (const float*)a.part, a.dgamma);
+    if (e != cudaSuccess || rows || a.T == 0) return e;
     return launch_dx(c, elem, bytes, a);
 }
 

@@ -2,6 +2,7 @@
 // 8, 4 and 2 bytes that divides a row and that every row starts on.
 #pragma once
 #include "common.cuh"
+#include "f32x2.cuh"
 
 namespace moe {
 
@@ -99,6 +100,29 @@ struct RowVec<float, 1> {
         return __float_as_uint(v[0]);
     }
 };
+
+// VEC consecutive parameters, of vector c of the row.  `wide`: 16-byte loads
+// (an aligned array; vectors of four or eight).
+template <int VEC>
+__device__ __forceinline__ void load_vector(const float* p, int c, bool wide, float2 (&v)[(VEC + 1) / 2]) {
+    p += (size_t)c * VEC;
+    if constexpr (VEC % 4 == 0) {
+        if (wide) {
+#pragma unroll
+            for (int k = 0; k < VEC / 4; ++k) {
+                const float4 w = reinterpret_cast<const float4*>(p)[k];
+                v[2 * k] = make_float2(w.x, w.y);
+                v[2 * k + 1] = make_float2(w.z, w.w);
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) {
+        if (k & 1) v[k >> 1].y = p[k];
+        else v[k >> 1] = make_float2(p[k], 0.0f);
+    }
+}
 
 // Bytes of the widest vector for rows of H elements in buffers whose first
 // elements and row strides (in bytes) are all or'ed into `where`.

@@ -73,6 +73,7 @@ struct RmsGradArgs {
     float* dgamma;
     float* part;           // workspace of rms_norm_workspace_bytes
 };
+cudaError_t setup_rms_norm_kernels();
 cudaError_t launch_rms_norm(const LaunchCtx& c, int elem, const RmsArgs& a);
 size_t rms_norm_workspace_bytes(int T, int H);
 cudaError_t launch_rms_norm_backward(const LaunchCtx& c, int elem, const RmsGradArgs& a);
