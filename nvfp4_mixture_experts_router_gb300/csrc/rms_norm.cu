@@ -476,6 +476,14 @@ __global__ void __launch_bounds__(kRmsThreads)
 
 // ---- backward -----------------------------------------------------------------------
 
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* to, const void* from) {
+    if constexpr (BYTES == 16)      // (past L1)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(to)), "l"(from), "n"(BYTES) : "memory");
+}
+
 // A block's sums of dgamma, its groups' in order, to the block's row of `part`.
 template <int VEC, int V>
 __device__ __forceinline__ void put_sums(const RmsGradArgs& a, const float2 (&dg)[V][(VEC + 1) / 2], int j, int lanes, int g,
@@ -533,17 +541,18 @@ __global__ void __launch_bounds__(512, 1) rms_ring_backward_kernel(const RmsGrad
 #pragma unroll
                 for (int i = 0; i < V; ++i)
                     if (j + i * lanes < n)
-                        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(at(stage, k, i))),
-                                     "l"(row + i * lanes), "n"(sizeof(Raw)) : "memory");
+                        copy_async<sizeof(Raw)>(at(stage, k, i), row + i * lanes);
             }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     for (int q = 0; q < S; ++q) fetch(first + q * step, q);
-    float2 dg[V][P];
+    float2 ga[V][P], dg[V][P];
 #pragma unroll
-    for (int i = 0; i < V; ++i)
+    for (int i = 0; i < V; ++i) {
+        gamma_vector<VEC, false>(a.gamma, a.H, j + i * lanes, wide_gamma, ga[i]);
 #pragma unroll
         for (int k = 0; k < P; ++k) dg[i][k] = both(0.0f);
+    }
     int stage = 0, before = 0, turn = 0;
     float sum_before = 0.0f, rstd_before = 0.0f, rstd = first < a.T ? a.rstd[first] : 0.0f;
     // turns: row t's sum and row t - step's result; one more than rows.  Uniform over the block
@@ -568,15 +577,14 @@ __global__ void __launch_bounds__(512, 1) rms_ring_backward_kernel(const RmsGrad
 #pragma unroll
             for (int i = 0; i < V; ++i)
                 if (j + i * lanes < n) {
-                    float2 d[P], h[P], ga[P];
+                    float2 d[P], h[P];
                     unpack_pairs<T_, VEC>(*at(stage, 0, i), d);
                     unpack_pairs<T_, VEC>(*at(stage, 1, i), h);
-                    gamma_vector<VEC, false>(a.gamma, a.H, j + i * lanes, wide_gamma, ga);
 #pragma unroll
                     for (int k = 0; k < P; ++k) {
                         const float2 p = mul2(d[k], mul2(h[k], both(rstd)));
                         dg[i][k] = add2(dg[i][k], p);
-                        sum = fma2(p, ga[k], sum);
+                        sum = fma2(p, ga[i][k], sum);
                     }
                 }
         }
@@ -591,16 +599,15 @@ __global__ void __launch_bounds__(512, 1) rms_ring_backward_kernel(const RmsGrad
 #pragma unroll
             for (int i = 0; i < V; ++i)
                 if (j + i * lanes < n) {
-                    float2 d[P], h[P], ga[P], u[P];
+                    float2 d[P], h[P], u[P];
                     unpack_pairs<T_, VEC>(*at(before, 0, i), d);
                     unpack_pairs<T_, VEC>(*at(before, 1, i), h);
                     if (DH == 1) unpack_pairs<T_, VEC>(*at(before, N - 1, i), u);
                     if (DH == 2) unpack_pairs<T_, VEC>(e[i], u);
-                    gamma_vector<VEC, false>(a.gamma, a.H, j + i * lanes, wide_gamma, ga);
                     // rstd (g - hhat mean) + dh
 #pragma unroll
                     for (int k = 0; k < P; ++k) {
-                        const float2 w = fma2(h[k], both(-mean), mul2(d[k], ga[k]));
+                        const float2 w = fma2(h[k], both(-mean), mul2(d[k], ga[i][k]));
                         d[k] = DH ? fma2(w, both(rstd_before), u[k]) : mul2(w, both(rstd_before));
                     }
                     out[i * lanes] = pack_pairs<T_, VEC>(d);
@@ -931,23 +938,26 @@ size_t rms_norm_workspace_bytes(int T, int H) {
     return align_up((uint64_t)parts * H * 4, 256);
 }
 
-cudaError_t launch_rms_norm_backward(const LaunchCtx& c, int elem, const RmsGradArgs& a) {
+cudaError_t launch_rms_norm_backward(const LaunchCtx& c, int elem, const RmsGradArgs& args) {
+    RmsGradArgs a = args;
     const int bytes = row_vec_bytes(a.H, elem,
                                     row_at(a.dy, a.dy_stride, elem) | row_at(a.dh, a.dh ? a.dh_stride : 0, elem) |
                                         row_at(a.h, a.h_stride, elem) | row_at(a.dx, a.dx_stride, elem));
     const bool rows = a.H <= kRowColumns;
     const BackwardShape s = backward_shape(a.H, in_slots(elem, bytes));
+    const int parts = rows ? backward_blocks(a.T, s) : kRmsParts;
+    if (parts == 1) a.part = a.dgamma;          // one block's sums are the result
     cudaError_t e;
     if (rows) {
         e = launch_backward_rows(c, elem, bytes, a, s);
     } else {
         // the column sums first: dx may overwrite dy or h
-        const dim3 parts((unsigned)((a.H + 255) / 256), kRmsParts);
-        e = c.launch(elem == 2 ? rms_partial_kernel<__nv_bfloat16> : rms_partial_kernel<float>, parts, dim3(256), 0, a);
+        const dim3 grid((unsigned)((a.H + 255) / 256), kRmsParts);
+        e = c.launch(elem == 2 ? rms_partial_kernel<__nv_bfloat16> : rms_partial_kernel<float>, grid, dim3(256), 0, a);
     }
-    if (e != cudaSuccess) return e;
-    e = c.launch(rms_reduce_kernel, dim3((unsigned)((a.H + 31) / 32)), dim3(1024), 0, a.H,
-                 rows ? backward_blocks(a.T, s) : kRmsParts, (const float*)a.part, a.dgamma);
+    if (e == cudaSuccess && parts > 1)
+        e = c.launch(rms_reduce_kernel, dim3((unsigned)((a.H + 31) / 32)), dim3(1024), 0, a.H, parts, (const float*)a.part,
+                     a.dgamma);
     if (e != cudaSuccess || rows || a.T == 0) return e;
     return launch_dx(c, elem, bytes, a);
 }
