@@ -8,15 +8,18 @@
 // A warp has a token: EPL consecutive experts a lane, so that the order of the
 // lanes and of a lane's registers is the order of the experts and ties fall to
 // the lower one.  c is held as an unsigned integer of the same order, 0 for an
-// expert that cannot be chosen; the K largest are K rounds of a warp-wide
-// maximum.
+// expert that cannot be chosen.  The K-th largest of the lanes' own largest is a
+// border below which none of the K largest lies: the experts above it, few more
+// than K, go to a lane each, which counts those before its own.  (Where they are
+// more than the lanes, many being equal or K large, K rounds of a warp-wide
+// maximum.)
 //
 // The choice has to be that of exact scores: an expert more or less is not a
 // rounding.  Logits compare exactly.  Scores with a bias, and sums of two
-// scores, are computed in FP32 with a bound of their error; where two values
-// that decide are closer than their bounds, the warp computes the ones that may
-// decide in FP64 (about one token in 300 with 256 experts, standard normal
-// logits and a bias), and compares those.
+// scores, are computed in FP32 with a bound of their error, and the border lies
+// lower by twice that; where two values that decide are closer than their bounds,
+// each lane computes its own again in FP64 (about one token in 300 with 256
+// experts, standard normal logits and a bias).
 #include <float.h>
 #include <math.h>
 
@@ -38,20 +41,20 @@ struct RouteArgs {
     moe_route_rule rule;
     int* ids;
     float* w;
-    bool wide;      // rows in 16-byte loads
+    bool wide, wide_bias;      // rows, and the bias, in vectors
 };
 
-// The unsigned integer in the order of a float that is no NaN (zeros alike); not 0.
+// The unsigned integer in the order of a float that is no NaN; not 0.
 __device__ __forceinline__ uint32_t order_of(float v) {
-    const uint32_t b = __float_as_uint(v + 0.0f);
-    return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
+    const int b = __float_as_int(v);
+    return (uint32_t)(b ^ ((b >> 31) | (int)0x80000000));
 }
 __device__ __forceinline__ float value_of(uint32_t k) {
     return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
 }
 
 // A logit as it counts: NaN as -infinity, at most the largest FP32 number.
-__device__ __forceinline__ float as_logit(float v) { return v > -INFINITY ? fminf(v, FLT_MAX) : -INFINITY; }
+__device__ __forceinline__ float as_logit(float v) { return fminf(fmaxf(v, -INFINITY), FLT_MAX); }
 
 __device__ __forceinline__ float load_logit(const float* p) { return as_logit(*p); }
 __device__ __forceinline__ float load_logit(const __nv_bfloat16* p) { return as_logit(__bfloat162float(*p)); }
@@ -81,19 +84,29 @@ __device__ __forceinline__ void load_row(const T_* row, int E, bool wide, float 
 }
 
 // Scores in FP32.  Of sigmoid the absolute error is below kSigmoidErr: e^-l is
-// off by (3 + 1.18 |l|) 2^-23 of itself at most (__expf's documented bound),
-// which s (1 - s) takes to 0.75 + 0.27 units of 2^-23, and the sum and the
-// division add 2.5.  Of softmax, p = e^x / S with x = l -
-// max, it is below (32 + 1.2 |x|) 2^-23 p: e^x as above, S a sum of at most 32
-// + 5 roundings and of terms each that exact (their mean |x| is at most log E).
+// off by (3 + 1.18 |l|) 2^-23 of itself at most (the product with log2 e and ex2's
+// documented 2^-22), which s (1 - s) takes to 0.75 + 0.27 units of 2^-23, and the
+// sum and the reciprocal (documented 2^-23) add 2.5.  Of softmax, p = e^x / S with
+// x = l - max, it is below (32 + 1.2 |x|) 2^-23 p: e^x as above, S a sum of at most
+// 32 + 5 roundings and of terms each that exact (their mean |x| is at most log E);
+// that is largest at p's largest.
 constexpr float kUnit = 1.1920929e-07f;     // 2^-23
 constexpr float kSigmoidErr = 4.0f * kUnit;
 constexpr float kTiny = 7.5e-37f;           // 2^-120, where the approximations flush to zero
-__device__ __forceinline__ float sigmoid_fast(float l) { return __fdividef(1.0f, 1.0f + __expf(-l)); }
+__device__ __forceinline__ float exp_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.44269504f));
+    return r;
+}
+__device__ __forceinline__ float sigmoid_fast(float l) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + exp_fast(-l)));
+    return r;
+}
 
 struct Softmax {
     float max, inv;     // of the row; p = e^(l - max) inv
-    __device__ __forceinline__ float of(float l) const { return __expf(l - max) * inv; }
+    __device__ __forceinline__ float of(float l) const { return exp_fast(l - max) * inv; }
 };
 template <int EPL>
 __device__ __forceinline__ Softmax softmax_of(const float (&l)[EPL]) {
@@ -103,7 +116,7 @@ __device__ __forceinline__ Softmax softmax_of(const float (&l)[EPL]) {
     m = warp_max(m);
     if (!(m > -INFINITY)) m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) s += __expf(l[i] - m);
+    for (int i = 0; i < EPL; ++i) s += exp_fast(l[i] - m);
     s = warp_sum(s);
     return Softmax{m, s > 0.0f ? __fdividef(1.0f, s) : 0.0f};
 }
@@ -118,7 +131,7 @@ __device__ __forceinline__ void into_top2(float& a, float& b, float v) {
     a = fmaxf(a, v);
 }
 
-// ---- the exact choice, for the tokens that FP32 cannot decide --------------------
+// ---- what FP32 cannot decide --------------------------------------------------------
 
 // A token's scores in FP64: c of expert e, with the warp's S of a softmax.
 template <typename T_>
@@ -127,7 +140,7 @@ struct Exact {
     const float* bias;
     bool sigmoid;
     double max, sum;
-    __device__ double operator()(int e) const {
+    __device__ __forceinline__ double operator()(int e) const {
         const double l = (double)load_logit(row + e);
         const double s = sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - max) / sum;
         return bias ? s + (double)bias[e] : s;
@@ -138,6 +151,7 @@ __device__ __forceinline__ Exact<T_> exact_of(const T_* row, const float* bias, 
     double s = 0.0;
     if (!sigmoid) {
         const int e0 = (threadIdx.x & 31) * EPL;
+#pragma unroll 1
         for (int i = 0; i < EPL && e0 + i < E; ++i) s += exp((double)load_logit(row + e0 + i) - (double)max);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
@@ -178,45 +192,58 @@ __device__ __forceinline__ uint32_t lane_mask(uint32_t taken, int size) {
 // The groups by FP64 scores.  s_c: E doubles of this warp.  can: a mask of the
 // lane's experts.
 template <typename T_, int EPL>
-__device__ __noinline__ uint32_t exact_groups(const Exact<T_>& f, int E, const moe_route_rule& rule, uint32_t can,
-                                              double* s_c) {
-    const int lane = threadIdx.x & 31, e0 = lane * EPL, size = E / rule.groups;
+__device__ __noinline__ uint32_t exact_groups(const T_* row, const float* bias, bool sigmoid, int E, float max, int groups,
+                                              int take, bool pair, uint32_t can, double* s_c) {
+    const int lane = threadIdx.x & 31, e0 = lane * EPL, size = E / groups;
+    const Exact<T_> f = exact_of<T_, EPL>(row, bias, sigmoid, E, max);
+#pragma unroll 1
     for (int i = 0; i < EPL && e0 + i < E; ++i) s_c[e0 + i] = (can >> i) & 1u ? f(e0 + i) : -INFINITY;
     __syncwarp();
     double a = -INFINITY, b = -INFINITY;
-    if (lane < rule.groups) {
+    if (lane < groups) {
+#pragma unroll 1
         for (int i = 0; i < size; ++i) {
             const double v = s_c[lane * size + i];
             b = fmax(b, fmin(a, v));
             a = fmax(a, v);
         }
-        if (rule.group_score == MOE_GROUP_TOP2 && b > -INFINITY) a += b;
+        if (pair && b > -INFINITY) a += b;
     }
     __syncwarp();
-    return best_groups(a, rule.groups, rule.topk_groups);
+    return best_groups(a, groups, take);
+}
+
+// The rank of the lane's expert e (-1: none) among the warp's, by FP64.
+template <typename T_, int EPL>
+__device__ __noinline__ int exact_rank(const T_* row, const float* bias, bool sigmoid, int E, float max, int e, int n) {
+    const int lane = threadIdx.x & 31;
+    const Exact<T_> f = exact_of<T_, EPL>(row, bias, sigmoid, E, max);
+    const double c = e >= 0 ? f(e) : -INFINITY;
+    int rank = 0;
+#pragma unroll 1
+    for (int j = 0; j < n; ++j) {
+        const double v = __shfl_sync(kAll, c, j);
+        rank += v > c || (v == c && j < lane);
+    }
+    return rank;
 }
 
 // The K largest c among the lane's experts `near` (a mask; every expert that may
 // be one of them), in FP64.  Slot k's expert in lane k, or -1.
 template <typename T_, int EPL>
-__device__ __noinline__ int exact_choice(const Exact<T_>& f, int E, int K, uint32_t near, double* s_c) {
+__device__ __noinline__ int exact_choice(const T_* row, const float* bias, bool sigmoid, int E, float max, int K, uint32_t near,
+                                         double* s_c) {
     const int lane = threadIdx.x & 31, e0 = lane * EPL;
-    uint16_t* list = reinterpret_cast<uint16_t*>(s_c + E);
-    for (int i = 0; i < EPL && e0 + i < E; ++i) s_c[e0 + i] = -INFINITY;
-    // the experts to look at, spread over the lanes
-    int n = 0;
-    for (int i = 0; i < EPL; ++i) {
-        const uint32_t who = __ballot_sync(kAll, (near >> i) & 1u);
-        if ((near >> i) & 1u) list[n + __popc(who & ((1u << lane) - 1))] = (uint16_t)(e0 + i);
-        n += __popc(who);
-    }
-    __syncwarp();
-    for (int p = lane; p < n; p += 32) s_c[list[p]] = f(list[p]);
+    const Exact<T_> f = exact_of<T_, EPL>(row, bias, sigmoid, E, max);
+#pragma unroll 1
+    for (int i = 0; i < EPL && e0 + i < E; ++i) s_c[e0 + i] = (near >> i) & 1u ? f(e0 + i) : -INFINITY;
     __syncwarp();
     int mine = -1;
+#pragma unroll 1
     for (int k = 0; k < K; ++k) {
         double v = -INFINITY;
         int e = E;
+#pragma unroll 1
         for (int i = 0; i < EPL && e0 + i < E; ++i)
             if (s_c[e0 + i] > v) {
                 v = s_c[e0 + i];
@@ -240,47 +267,76 @@ __device__ __noinline__ int exact_choice(const Exact<T_>& f, int E, int K, uint3
     return mine;
 }
 
+// The K largest of exact keys in K rounds.  Slot k's expert in lane k, or -1.
+template <int EPL>
+__device__ __forceinline__ int rounds_choice(uint32_t (&key)[EPL], int K) {
+    const int lane = threadIdx.x & 31;
+    int mine = -1;
+#pragma unroll 1
+    for (int k = 0; k < K; ++k) {
+        uint32_t best = key[0];
+        int at = 0;
+#pragma unroll
+        for (int i = 1; i < EPL; ++i)
+            if (key[i] > best) {
+                best = key[i];
+                at = i;
+            }
+        const uint32_t m = __reduce_max_sync(kAll, best);
+        if (m == 0) break;
+        const int src = __ffs(__ballot_sync(kAll, best == m)) - 1;
+        const int e = src * EPL + __shfl_sync(kAll, at, src);
+        if (lane == k) mine = e;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+            if (lane == src && i == at) key[i] = 0u;
+    }
+    return mine;
+}
+
 // ---- forward ------------------------------------------------------------------------
 
 template <typename T_, int EPL>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const RouteArgs a) {
-    extern __shared__ double s_exact[];     // [warps][E] values and E indices, with a bias or sums of two
+    __shared__ uint2 s_near[kRouteWarps][33];   // key and expert; then the keys by rank
+    extern __shared__ double s_exact[];         // [warps][E], with a bias or sums of two
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.E, K = a.K, e0 = lane * EPL;
     const int t = blockIdx.x * (blockDim.x >> 5) + warp;
     if (t >= a.T) return;
     const T_* row = static_cast<const T_*>(a.logits) + (int64_t)t * a.stride;
-    double* s_c = s_exact + (size_t)warp * (E + (E + 3) / 4);
+    double* s_c = s_exact + (size_t)warp * E;
     const bool sigmoid = a.rule.score == MOE_SCORE_SIGMOID, grouped = a.rule.topk_groups < a.rule.groups;
-    const bool pair = grouped && a.rule.group_score == MOE_GROUP_TOP2;
-    float l[EPL];
+    const bool pair = grouped && a.rule.group_score == MOE_GROUP_TOP2, biased = a.bias != nullptr;
+    float l[EPL], b[EPL];
     load_row<T_, EPL>(row, E, a.wide, l);
+    if (biased) load_row<float, EPL>(a.bias, E, a.wide_bias, b);    // (of +infinity, the largest number: no c is closer to it)
     Softmax soft{0.0f, 0.0f};
-    if (!sigmoid && (a.bias || pair || !a.rule.renormalize)) soft = softmax_of<EPL>(l);
+    if (!sigmoid && (biased || pair || !a.rule.renormalize)) soft = softmax_of<EPL>(l);
     // c in order; 0: cannot be chosen
-    uint32_t key[EPL], can = 0;
+    uint32_t key[EPL];
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-        const float b = a.bias && e0 + i < E ? a.bias[e0 + i] : 0.0f;
-        const bool ok = l[i] > -INFINITY && b > -INFINITY;
-        const float c = a.bias ? (sigmoid ? sigmoid_fast(l[i]) : soft.of(l[i])) + b : l[i];
-        key[i] = ok ? order_of(c) : 0u;
-        can |= ok ? 1u << i : 0u;
+        if (biased) {
+            const bool ok = fminf(l[i], b[i]) > -INFINITY;
+            key[i] = ok ? order_of((sigmoid ? sigmoid_fast(l[i]) : soft.of(l[i])) + b[i]) : 0u;
+        } else {
+            key[i] = l[i] > -INFINITY ? order_of(l[i] + 0.0f) : 0u;         // zeros alike
+        }
     }
-    // bounds of the error of any c: its score's, and c's own rounding
+    // a bound of the error of c: its score's, and c's own rounding
     const float most = sigmoid ? kSigmoidErr : 32.0f * kUnit * soft.inv;
     auto err_of = [&](float c) { return most + kTiny + 2.0f * kUnit * fabsf(c); };
 
     if (grouped) {
-        const int size = E / a.rule.groups;
+        const int groups = a.rule.groups, size = E / groups, span = size / EPL;
+        const bool whole = size % EPL == 0 && (span & (span - 1)) == 0;     // a group is 2^n whole lanes
         float x = -INFINITY, y = -INFINITY;     // lane g: the two largest of group g
         auto value = [&](int i) {
-            if (!((can >> i) & 1u)) return -INFINITY;
-            return pair && !a.bias ? (sigmoid ? sigmoid_fast(l[i]) : soft.of(l[i])) : value_of(key[i]);
+            if (key[i] == 0u) return -INFINITY;
+            return pair && !biased ? (sigmoid ? sigmoid_fast(l[i]) : soft.of(l[i])) : value_of(key[i]);
         };
-        const int span = size / EPL;
-        if (size % EPL == 0 && (span & (span - 1)) == 0) {
-            // a group is 2^n whole lanes
+        if (whole) {
 #pragma unroll
             for (int i = 0; i < EPL; ++i) into_top2(x, y, value(i));
             for (int o = 1; o < span; o <<= 1) {
@@ -296,100 +352,88 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const Rout
             for (int i = 0; i < EPL; ++i)
                 if (e0 + i < E) s_v[e0 + i] = value(i);
             __syncwarp();
-            if (lane < a.rule.groups)
+            if (lane < groups)
                 for (int i = 0; i < size; ++i) into_top2(x, y, s_v[lane * size + i]);
             __syncwarp();
         }
-        const float score = lane >= a.rule.groups ? NAN : pair && y > -INFINITY ? x + y : x;
-        uint32_t taken = best_groups(score, a.rule.groups, a.rule.topk_groups);
-        if (a.bias || pair) {
-            // +-infinity is exact
-            const float err = fabsf(score) < INFINITY ? 2.0f * err_of(score) + 4.0f * kUnit * fabsf(x) : 0.0f;
+        const float score = lane >= groups ? NAN : pair && y > -INFINITY ? x + y : x;
+        uint32_t taken = best_groups(score, groups, a.rule.topk_groups);
+        if (biased || pair) {
+            const float err = score > -INFINITY ? 2.0f * err_of(score) + 4.0f * kUnit * fabsf(x) : 0.0f;
             const bool in = (taken >> lane) & 1u, out = !in && score > -INFINITY;
             const float low = -warp_max(in ? -(score - err) : -INFINITY);
             const float high = warp_max(out ? score + err : -INFINITY);
-            if (high > -INFINITY && high >= low)
-                taken = exact_groups<T_, EPL>(exact_of<T_, EPL>(row, a.bias, sigmoid, E, soft.max), E, a.rule, can, s_c);
+            if (high > -INFINITY && !(high < low)) {
+                uint32_t can = 0;
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) can |= key[i] != 0u ? 1u << i : 0u;
+                taken = exact_groups<T_, EPL>(row, a.bias, sigmoid, E, soft.max, groups, a.rule.topk_groups, pair, can, s_c);
+            }
         }
-        const uint32_t open = lane_mask<EPL>(taken, size);
+        const uint32_t open = whole ? (taken >> (lane / span & 31)) & 1u ? kAll : 0u : lane_mask<EPL>(taken, size);
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
             if (!((open >> i) & 1u)) key[i] = 0u;
-        can &= open;
     }
 
-    // K rounds; slot k in lane k
-    int mine = -1;
-    uint32_t mine_key = 0;
-    uint32_t best = 0;
-    int at = 0;
-    auto own_best = [&]() {
-        best = key[0];
-        at = 0;
+    // the border: the K-th largest of the lanes' largest (equal ones leave together), lower by the bounds
+    uint32_t mine_best = key[0], border = 0;
 #pragma unroll
-        for (int i = 1; i < EPL; ++i)
-            if (key[i] > best) {
-                best = key[i];
-                at = i;
-            }
-    };
-    own_best();
-    uint32_t left = (1u << (EPL - 1) << 1) - 1;     // experts of the lane not chosen yet
+    for (int i = 1; i < EPL; ++i) mine_best = max(mine_best, key[i]);
     for (int k = 0; k < K; ++k) {
-        const uint32_t m = __reduce_max_sync(kAll, best);
-        if (m == 0) break;
-        const int src = __ffs(__ballot_sync(kAll, best == m)) - 1;
-        const int e = src * EPL + __shfl_sync(kAll, at, src);
-        if (lane == k) {
-            mine = e;
-            mine_key = m;
-        }
-        if (lane == src) {
-            left &= ~(1u << at);
-#pragma unroll
-            for (int i = 0; i < EPL; ++i)
-                if (i == at) key[i] = 0u;
-            own_best();
-        }
+        border = __reduce_max_sync(kAll, mine_best);
+        if (mine_best == border) mine_best = 0u;
     }
-
-    if (a.bias) {
-        // Is the order of the chosen, and their being the largest, beyond doubt?
-        const float my_l = mine >= 0 ? load_logit(row + mine) : 0.0f, my_b = mine >= 0 ? a.bias[mine] : 0.0f;
-        auto bound = [&](float c, float l_) {
-            const float score_err = sigmoid ? kSigmoidErr : soft.of(l_) * kUnit * (32.0f + 1.2f * (soft.max - l_));
-            return fabsf(c) < INFINITY ? score_err + kTiny + 2.0f * kUnit * fabsf(c) : 0.0f;
-        };
-        const float c = mine >= 0 ? value_of(mine_key) : -INFINITY, e = mine >= 0 ? bound(c, my_l) : 0.0f;
-        const int chosen = __popc(__ballot_sync(kAll, mine >= 0));
-        const float c2 = __shfl_down_sync(kAll, c, 1), e2 = __shfl_down_sync(kAll, e, 1);
-        const float l2 = __shfl_down_sync(kAll, my_l, 1), b2 = __shfl_down_sync(kAll, my_b, 1);
-        // equal inputs are equal exactly, in the lower expert's favour
-        bool doubt = lane + 1 < chosen && !(c - e > c2 + e2) && !(my_l == l2 && my_b == b2);
-        const uint32_t next = __reduce_max_sync(kAll, best);
-        float low = -INFINITY;
-        if (chosen == K && next != 0) {
-            low = -warp_max(mine >= 0 ? e - c : -INFINITY);
-            const float v = value_of(next);
-            if (!(low > v + (fabsf(v) < INFINITY ? err_of(v) : 0.0f))) {
-                const float last_l = __shfl_sync(kAll, my_l, K - 1), last_b = __shfl_sync(kAll, my_b, K - 1);
+    if (border != 0u && biased) {
+        const float v = value_of(border);
+        border = order_of(v - 2.1f * err_of(v));
+    }
+    border = max(border, 1u);
+    // the experts from there on, in their order
+    uint32_t near = 0;
 #pragma unroll
-                for (int i = 0; i < EPL; ++i)
-                    if (key[i] != 0u) {
-                        const float u = value_of(key[i]);
-                        doubt |= !(low > u + bound(u, l[i])) && !(l[i] == last_l && a.bias[e0 + i] == last_b);
-                    }
-            }
-        }
-        if (__any_sync(kAll, doubt)) {
-            uint32_t near = 0;
+    for (int i = 0; i < EPL; ++i) near |= key[i] >= border ? 1u << i : 0u;
+    int pos = __popc(near);
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) {
-                const float u = value_of(key[i]);
-                if (((can >> i) & 1u) && (!((left >> i) & 1u) || !(low > u + bound(u, l[i])))) near |= 1u << i;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(kAll, pos, o);
+        if (lane >= o) pos += v;
+    }
+    const int n = __shfl_sync(kAll, pos, 31);
+    int mine = -1, slot = lane;     // this lane's expert and its place
+    if (n <= 32) {
+        pos -= __popc(near);
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+            if ((near >> i) & 1u) s_near[warp][pos++] = make_uint2(key[i], (uint32_t)(e0 + i));
+        __syncwarp();
+        const uint2 own = lane < n ? s_near[warp][lane] : make_uint2(0u, 0u);
+        if (lane < n) mine = (int)own.y;
+        slot = 0;
+        for (int j0 = 0; j0 < n; j0 += 4)
+#pragma unroll
+            for (int j = j0; j < j0 + 4; ++j)       // (0 in the lanes past n - 1)
+                slot += __shfl_sync(kAll, own.x, j) + (j < lane) > own.x;
+        if (biased) {
+            // is the order of the chosen, and of the first that is not, beyond doubt?
+            __syncwarp();
+            if (lane < n) s_near[warp][slot] = own;
+            __syncwarp();
+            bool doubt = false;
+            if (lane < min(n - 1, K)) {
+                const uint2 u = s_near[warp][lane], v = s_near[warp][lane + 1];
+                const float c = value_of(u.x), d = value_of(v.x);
+                // equal inputs are equal exactly, in the lower expert's favour
+                doubt = !(c - d > err_of(c) + err_of(d)) &&
+                        !(load_logit(row + u.y) == load_logit(row + v.y) && as_logit(a.bias[u.y]) == as_logit(a.bias[v.y]));
             }
-            mine = exact_choice<T_, EPL>(exact_of<T_, EPL>(row, a.bias, sigmoid, E, soft.max), E, K, near, s_c);
+            if (__any_sync(kAll, doubt)) slot = exact_rank<T_, EPL>(row, a.bias, sigmoid, E, soft.max, mine, n);
         }
+        if (slot >= K) mine = -1;
+    } else if (biased) {
+        mine = exact_choice<T_, EPL>(row, a.bias, sigmoid, E, soft.max, K, near, s_c);
+    } else {
+        mine = rounds_choice<EPL>(key, K);
     }
 
     // weights: of renormalized sigmoids the common factor e^-min(max, 0) is left
@@ -407,9 +451,16 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const Rout
     } else {
         s = expf(my_l - soft.max) * soft.inv;
     }
-    if (lane < K) {
-        a.ids[(int64_t)t * K + lane] = mine;
-        a.w[(int64_t)t * K + lane] = mine >= 0 ? s * a.rule.scale : 0.0f;
+    int* ids = a.ids + (int64_t)t * K;
+    float* w = a.w + (int64_t)t * K;
+    if (mine >= 0) {
+        ids[slot] = mine;
+        w[slot] = s * a.rule.scale;
+    }
+    const int chosen = __popc(__ballot_sync(kAll, mine >= 0));
+    if (lane >= chosen && lane < K) {
+        ids[lane] = -1;
+        w[lane] = 0.0f;
     }
     pdl_launch_dependents();
 }
@@ -524,7 +575,9 @@ cudaError_t forward_epl(const LaunchCtx& c, RouteArgs a) {
     a.wide = a.E % VEC == 0 && row_at(a.logits, a.stride, sizeof(T_)) % (VEC * sizeof(T_)) == 0;
     const int warps = route_warps(a.T);
     const bool scratch = a.bias || a.rule.topk_groups < a.rule.groups;
-    const size_t smem = scratch ? (size_t)warps * (a.E + (a.E + 3) / 4) * 8 : 0;
+    constexpr int kBias = EPL < 4 ? EPL : 4;
+    a.wide_bias = a.E % kBias == 0 && row_at(a.bias) % (kBias * 4) == 0;
+    const size_t smem = scratch ? (size_t)warps * a.E * 8 : 0;
     return c.launch(route_topk_kernel<T_, EPL>, dim3((unsigned)((a.T + warps - 1) / warps)), dim3(32 * warps), smem, a);
 }
 template <typename T_>
@@ -549,9 +602,9 @@ cudaError_t backward_of(const LaunchCtx& c, const RouteGradArgs& a) {
 template <typename T_>
 cudaError_t allow_forward() {
     cudaError_t e = cudaSuccess;
-    auto allow = [&](auto kernel) {     // 8 warps of 1024 experts: 80 KB
+    auto allow = [&](auto kernel) {     // 8 warps of 1024 experts: 64 KB
         if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRouteWarps * 1280 * 8);
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRouteWarps * 1024 * 8);
     };
     allow(route_topk_kernel<T_, 16>);
     allow(route_topk_kernel<T_, 32>);
@@ -567,7 +620,7 @@ cudaError_t setup_route_topk_kernels() {
 
 cudaError_t launch_route_topk(const LaunchCtx& c, int T, int E, int K, int elem, const void* logits, int64_t stride,
                               const float* bias, const moe_route_rule& rule, int* ids, float* w) {
-    const RouteArgs a{T, E, K, logits, stride, bias, rule, ids, w, false};
+    const RouteArgs a{T, E, K, logits, stride, bias, rule, ids, w, false, false};
     return elem == 2 ? forward_of<__nv_bfloat16>(c, a) : forward_of<float>(c, a);
 }
 
