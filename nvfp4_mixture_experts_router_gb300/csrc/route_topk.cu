@@ -7,8 +7,8 @@
 //
 // A warp has a token: EPL consecutive experts a lane, so that the order of the
 // lanes and of a lane's registers is the order of the experts and ties fall to
-// the lower one.  c is held as an unsigned integer of the same order, 0 for an
-// expert that cannot be chosen.  The K-th largest of the lanes' own largest is a
+// the lower one.  -infinity is an expert that cannot be
+// chosen.  The K-th largest of the lanes' own largest is a
 // border below which none of the K largest lies: the experts above it, few more
 // than K, go to a lane each, which counts those before its own.  (Where they are
 // more than the lanes, many being equal or K large, K rounds of a warp-wide
@@ -42,6 +42,7 @@ struct RouteArgs {
     int* ids;
     float* w;
     bool wide, wide_bias;      // rows, and the bias, in vectors
+    int size, span;            // experts of a group; log2 of its lanes, or -1
 };
 
 // The unsigned integer in the order of a float that is no NaN; not 0.
@@ -121,6 +122,24 @@ __device__ __forceinline__ Softmax softmax_of(const float (&l)[EPL]) {
     return Softmax{m, s > 0.0f ? __fdividef(1.0f, s) : 0.0f};
 }
 
+// The largest over the warp (no NaN).
+__device__ __forceinline__ float warp_largest(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+// The lane's number of `mine` things before its own in the order of the lanes, and of all.
+__device__ __forceinline__ int before_lane(int mine, int* all) {
+    int sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(kAll, sum, o);
+        if ((int)(threadIdx.x & 31) >= o) sum += v;
+    }
+    *all = __shfl_sync(kAll, sum, 31);
+    return sum - mine;
+}
+
 // The two largest of a group of lanes' values, a >= b.
 __device__ __forceinline__ void join_top2(float& a, float& b, float a2, float b2) {
     b = fmaxf(fminf(a, a2), a >= a2 ? b : b2);
@@ -165,10 +184,12 @@ template <typename F>
 __device__ __forceinline__ uint32_t best_groups(F score, int groups, int take) {
     const int lane = threadIdx.x & 31;
     int above = 0;
-    for (int g = 0; g < groups; ++g) {
-        const F v = __shfl_sync(kAll, score, g);
-        above += v > score || (v == score && g < lane);
-    }
+    for (int g0 = 0; g0 < groups; g0 += 4)
+#pragma unroll
+        for (int g = g0; g < g0 + 4; ++g) {         // (NaN past the last group)
+            const F v = __shfl_sync(kAll, score, g);
+            above += v > score || (v == score && g < lane);
+        }
     return __ballot_sync(kAll, lane < groups && above < take);
 }
 
@@ -189,15 +210,22 @@ __device__ __forceinline__ uint32_t lane_mask(uint32_t taken, int size) {
     return m;
 }
 
-// The groups by FP64 scores.  s_c: E doubles of this warp.  can: a mask of the
-// lane's experts.
+// The groups by FP64 scores.  can: a mask of the lane's experts that may be among
+// their group's largest; s_c: E doubles of this warp; s_list: 32 entries.
 template <typename T_, int EPL>
 __device__ __noinline__ uint32_t exact_groups(const T_* row, const float* bias, bool sigmoid, int E, float max, int groups,
-                                              int take, bool pair, uint32_t can, double* s_c) {
+                                              int take, bool pair, uint32_t can, double* s_c, uint2* s_list) {
     const int lane = threadIdx.x & 31, e0 = lane * EPL, size = E / groups;
     const Exact<T_> f = exact_of<T_, EPL>(row, bias, sigmoid, E, max);
+    int n, pos = before_lane(__popc(can), &n);
 #pragma unroll 1
-    for (int i = 0; i < EPL && e0 + i < E; ++i) s_c[e0 + i] = (can >> i) & 1u ? f(e0 + i) : -INFINITY;
+    for (int i = 0; i < EPL && e0 + i < E; ++i) {
+        const bool look = (can >> i) & 1u;
+        s_c[e0 + i] = look && n > 32 ? f(e0 + i) : -INFINITY;
+        if (look && n <= 32) s_list[pos++].x = (uint32_t)(e0 + i);
+    }
+    __syncwarp();
+    if (n <= 32 && lane < n) s_c[s_list[lane].x] = f((int)s_list[lane].x);     // one each
     __syncwarp();
     double a = -INFINITY, b = -INFINITY;
     if (lane < groups) {
@@ -208,6 +236,8 @@ __device__ __noinline__ uint32_t exact_groups(const T_* row, const float* bias, 
             a = fmax(a, v);
         }
         if (pair && b > -INFINITY) a += b;
+    } else {
+        a = NAN;
     }
     __syncwarp();
     return best_groups(a, groups, take);
@@ -267,29 +297,29 @@ __device__ __noinline__ int exact_choice(const T_* row, const float* bias, bool 
     return mine;
 }
 
-// The K largest of exact keys in K rounds.  Slot k's expert in lane k, or -1.
+// The K largest of exact values in K rounds.  Slot k's expert in lane k, or -1.
 template <int EPL>
-__device__ __forceinline__ int rounds_choice(uint32_t (&key)[EPL], int K) {
+__device__ __forceinline__ int rounds_choice(float (&c)[EPL], int K) {
     const int lane = threadIdx.x & 31;
     int mine = -1;
 #pragma unroll 1
     for (int k = 0; k < K; ++k) {
-        uint32_t best = key[0];
+        float best = c[0];
         int at = 0;
 #pragma unroll
         for (int i = 1; i < EPL; ++i)
-            if (key[i] > best) {
-                best = key[i];
+            if (c[i] > best) {
+                best = c[i];
                 at = i;
             }
-        const uint32_t m = __reduce_max_sync(kAll, best);
-        if (m == 0) break;
+        const float m = warp_largest(best);
+        if (!(m > -INFINITY)) break;
         const int src = __ffs(__ballot_sync(kAll, best == m)) - 1;
         const int e = src * EPL + __shfl_sync(kAll, at, src);
         if (lane == k) mine = e;
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
-            if (lane == src && i == at) key[i] = 0u;
+            if (lane == src && i == at) c[i] = -INFINITY;
     }
     return mine;
 }
@@ -313,37 +343,33 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const Rout
     if (biased) load_row<float, EPL>(a.bias, E, a.wide_bias, b);    // (of +infinity, the largest number: no c is closer to it)
     Softmax soft{0.0f, 0.0f};
     if (!sigmoid && (biased || pair || !a.rule.renormalize)) soft = softmax_of<EPL>(l);
-    // c in order; 0: cannot be chosen
-    uint32_t key[EPL];
+    float c[EPL];       // -infinity: cannot be chosen
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-        if (biased) {
-            const bool ok = fminf(l[i], b[i]) > -INFINITY;
-            key[i] = ok ? order_of((sigmoid ? sigmoid_fast(l[i]) : soft.of(l[i])) + b[i]) : 0u;
-        } else {
-            key[i] = l[i] > -INFINITY ? order_of(l[i] + 0.0f) : 0u;         // zeros alike
-        }
+        if (biased) c[i] = fminf(l[i], b[i]) > -INFINITY ? (sigmoid ? sigmoid_fast(l[i]) : soft.of(l[i])) + b[i] : -INFINITY;
+        else c[i] = l[i];
     }
     // a bound of the error of c: its score's, and c's own rounding
     const float most = sigmoid ? kSigmoidErr : 32.0f * kUnit * soft.inv;
-    auto err_of = [&](float c) { return most + kTiny + 2.0f * kUnit * fabsf(c); };
+    auto err_of = [&](float v) { return most + kTiny + 2.0f * kUnit * fabsf(v); };
 
     if (grouped) {
-        const int groups = a.rule.groups, size = E / groups, span = size / EPL;
-        const bool whole = size % EPL == 0 && (span & (span - 1)) == 0;     // a group is 2^n whole lanes
-        float x = -INFINITY, y = -INFINITY;     // lane g: the two largest of group g
+        const int groups = a.rule.groups;
+        const bool whole = a.span >= 0;         // a group is 2^span whole lanes
+        const bool plain = pair && !biased;     // sums of the scores
+        float x = -INFINITY, y = -INFINITY, border = -INFINITY;     // lane g: the two largest of group g
         auto value = [&](int i) {
-            if (key[i] == 0u) return -INFINITY;
-            return pair && !biased ? (sigmoid ? sigmoid_fast(l[i]) : soft.of(l[i])) : value_of(key[i]);
+            return !plain ? c[i] : c[i] > -INFINITY ? (sigmoid ? sigmoid_fast(c[i]) : soft.of(c[i])) : -INFINITY;
         };
         if (whole) {
 #pragma unroll
             for (int i = 0; i < EPL; ++i) into_top2(x, y, value(i));
-            for (int o = 1; o < span; o <<= 1) {
+            for (int o = 1; o < 1 << a.span; o <<= 1) {
                 const float x2 = __shfl_xor_sync(kAll, x, o), y2 = __shfl_xor_sync(kAll, y, o);
                 join_top2(x, y, x2, y2);
             }
-            const int src = lane * span & 31;
+            border = pair ? y : x;              // of the lane's own group
+            const int src = lane << a.span & 31;
             x = __shfl_sync(kAll, x, src);
             y = __shfl_sync(kAll, y, src);
         } else {
@@ -353,62 +379,58 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const Rout
                 if (e0 + i < E) s_v[e0 + i] = value(i);
             __syncwarp();
             if (lane < groups)
-                for (int i = 0; i < size; ++i) into_top2(x, y, s_v[lane * size + i]);
+                for (int i = 0; i < a.size; ++i) into_top2(x, y, s_v[lane * a.size + i]);
             __syncwarp();
         }
         const float score = lane >= groups ? NAN : pair && y > -INFINITY ? x + y : x;
         uint32_t taken = best_groups(score, groups, a.rule.topk_groups);
         if (biased || pair) {
-            const float err = score > -INFINITY ? 2.0f * err_of(score) + 4.0f * kUnit * fabsf(x) : 0.0f;
-            const bool in = (taken >> lane) & 1u, out = !in && score > -INFINITY;
-            const float low = -warp_max(in ? -(score - err) : -INFINITY);
-            const float high = warp_max(out ? score + err : -INFINITY);
+            const float err = 2.0f * err_of(score) + 4.0f * kUnit * fabsf(x);
+            const bool in = (taken >> lane) & 1u && score > -INFINITY, out = !((taken >> lane) & 1u) && score > -INFINITY;
+            const float low = -warp_largest(in ? err - score : -INFINITY);
+            const float high = warp_largest(out ? score + err : -INFINITY);
             if (high > -INFINITY && !(high < low)) {
+                border = fmaxf(border - 2.1f * err_of(border), -FLT_MAX);      // (none: all that can be chosen)
                 uint32_t can = 0;
 #pragma unroll
-                for (int i = 0; i < EPL; ++i) can |= key[i] != 0u ? 1u << i : 0u;
-                taken = exact_groups<T_, EPL>(row, a.bias, sigmoid, E, soft.max, groups, a.rule.topk_groups, pair, can, s_c);
+                for (int i = 0; i < EPL; ++i) can |= value(i) >= border ? 1u << i : 0u;
+                taken = exact_groups<T_, EPL>(row, a.bias, sigmoid, E, soft.max, groups, a.rule.topk_groups, pair, can, s_c,
+                                              s_near[warp]);
             }
         }
-        const uint32_t open = whole ? (taken >> (lane / span & 31)) & 1u ? kAll : 0u : lane_mask<EPL>(taken, size);
+        const uint32_t open = whole ? (taken >> (lane >> a.span)) & 1u ? kAll : 0u : lane_mask<EPL>(taken, a.size);
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
-            if (!((open >> i) & 1u)) key[i] = 0u;
+            if (!((open >> i) & 1u)) c[i] = -INFINITY;
     }
 
     // the border: the K-th largest of the lanes' largest (equal ones leave together), lower by the bounds
-    uint32_t mine_best = key[0], border = 0;
+    float mine_best = c[0], border = -INFINITY;
 #pragma unroll
-    for (int i = 1; i < EPL; ++i) mine_best = max(mine_best, key[i]);
+    for (int i = 1; i < EPL; ++i) mine_best = fmaxf(mine_best, c[i]);
     for (int k = 0; k < K; ++k) {
-        border = __reduce_max_sync(kAll, mine_best);
-        if (mine_best == border) mine_best = 0u;
+        border = warp_largest(mine_best);
+        if (mine_best == border) mine_best = -INFINITY;
     }
-    if (border != 0u && biased) {
-        const float v = value_of(border);
-        border = order_of(v - 2.1f * err_of(v));
-    }
-    border = max(border, 1u);
+    if (biased) border -= 2.1f * err_of(border);
+    border = fmaxf(border, -FLT_MAX);           // (-infinity, or less and so NaN: all that can be chosen)
     // the experts from there on, in their order
     uint32_t near = 0;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) near |= key[i] >= border ? 1u << i : 0u;
-    int pos = __popc(near);
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(kAll, pos, o);
-        if (lane >= o) pos += v;
-    }
-    const int n = __shfl_sync(kAll, pos, 31);
+    for (int i = 0; i < EPL; ++i) near |= c[i] >= border ? 1u << i : 0u;
+    int n, pos = before_lane(__popc(near), &n);
     int mine = -1, slot = lane;     // this lane's expert and its place
     if (n <= 32) {
-        pos -= __popc(near);
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
-            if ((near >> i) & 1u) s_near[warp][pos++] = make_uint2(key[i], (uint32_t)(e0 + i));
+            if ((near >> i) & 1u) s_near[warp][pos++] = make_uint2(__float_as_uint(c[i]), (uint32_t)(e0 + i));
         __syncwarp();
-        const uint2 own = lane < n ? s_near[warp][lane] : make_uint2(0u, 0u);
-        if (lane < n) mine = (int)own.y;
+        uint2 own = lane < n ? s_near[warp][lane] : make_uint2(0u, 0u);
+        const float my_c = __uint_as_float(own.x);
+        if (lane < n) {
+            mine = (int)own.y;
+            own.x = order_of(my_c + 0.0f);      // zeros alike
+        }
         slot = 0;
         for (int j0 = 0; j0 < n; j0 += 4)
 #pragma unroll
@@ -417,14 +439,14 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const Rout
         if (biased) {
             // is the order of the chosen, and of the first that is not, beyond doubt?
             __syncwarp();
-            if (lane < n) s_near[warp][slot] = own;
+            if (lane < n) s_near[warp][slot] = make_uint2(__float_as_uint(my_c), own.y);
             __syncwarp();
             bool doubt = false;
             if (lane < min(n - 1, K)) {
                 const uint2 u = s_near[warp][lane], v = s_near[warp][lane + 1];
-                const float c = value_of(u.x), d = value_of(v.x);
+                const float cu = __uint_as_float(u.x), cv = __uint_as_float(v.x);
                 // equal inputs are equal exactly, in the lower expert's favour
-                doubt = !(c - d > err_of(c) + err_of(d)) &&
+                doubt = !(cu - cv > err_of(cu) + err_of(cv)) &&
                         !(load_logit(row + u.y) == load_logit(row + v.y) && as_logit(a.bias[u.y]) == as_logit(a.bias[v.y]));
             }
             if (__any_sync(kAll, doubt)) slot = exact_rank<T_, EPL>(row, a.bias, sigmoid, E, soft.max, mine, n);
@@ -433,7 +455,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const Rout
     } else if (biased) {
         mine = exact_choice<T_, EPL>(row, a.bias, sigmoid, E, soft.max, K, near, s_c);
     } else {
-        mine = rounds_choice<EPL>(key, K);
+        mine = rounds_choice<EPL>(c, K);
     }
 
     // weights: of renormalized sigmoids the common factor e^-min(max, 0) is left
@@ -441,11 +463,9 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const Rout
     const float my_l = mine >= 0 ? load_logit(row + mine) : -INFINITY;
     float s;
     if (a.rule.renormalize) {
-        float m = warp_max(my_l);
-        if (!(m > -INFINITY)) m = 0.0f;
-        s = sigmoid ? expf(fminf(my_l, 0.0f) - fminf(m, 0.0f)) / (1.0f + expf(-fabsf(my_l))) : expf(my_l - m);
-        const float sum = warp_sum(mine >= 0 ? s : 0.0f);
-        s = s / sum;
+        const float m = fmaxf(warp_largest(my_l), -FLT_MAX);
+        s = sigmoid ? __fdividef(exp_fast(fminf(my_l, 0.0f) - fminf(m, 0.0f)), 1.0f + exp_fast(-fabsf(my_l))) : exp_fast(my_l - m);
+        s = __fdividef(s, warp_sum(mine >= 0 ? s : 0.0f));
     } else if (sigmoid) {
         s = 1.0f / (1.0f + expf(-my_l));
     } else {
@@ -573,6 +593,10 @@ template <typename T_, int EPL>
 cudaError_t forward_epl(const LaunchCtx& c, RouteArgs a) {
     constexpr int kMost = 16 / sizeof(T_), VEC = EPL < kMost ? EPL : kMost;
     a.wide = a.E % VEC == 0 && row_at(a.logits, a.stride, sizeof(T_)) % (VEC * sizeof(T_)) == 0;
+    a.size = a.E / a.rule.groups;
+    a.span = -1;
+    for (int n = 0; n < 6; ++n)
+        if (a.size == EPL << n) a.span = n;
     const int warps = route_warps(a.T);
     const bool scratch = a.bias || a.rule.topk_groups < a.rule.groups;
     constexpr int kBias = EPL < 4 ? EPL : 4;
@@ -620,7 +644,7 @@ cudaError_t setup_route_topk_kernels() {
 
 cudaError_t launch_route_topk(const LaunchCtx& c, int T, int E, int K, int elem, const void* logits, int64_t stride,
                               const float* bias, const moe_route_rule& rule, int* ids, float* w) {
-    const RouteArgs a{T, E, K, logits, stride, bias, rule, ids, w, false, false};
+    const RouteArgs a{T, E, K, logits, stride, bias, rule, ids, w, false, false, 0, 0};
     return elem == 2 ? forward_of<__nv_bfloat16>(c, a) : forward_of<float>(c, a);
 }
 
