@@ -392,16 +392,19 @@ __device__ __forceinline__ void adam_chunk(const AdamStep& s, const AdamEntry& e
             }
         }
     }
-    // buffers off their vectors, and a tensor's last groups.  Past the end all is
-    // zero and stays zero (or NaN, where the clipping factor is)
+    // the last groups, and buffers off their vectors.  Past the end all is zero and
+    // stays zero (or NaN, where the clipping factor is)
 #pragma unroll 1
     for (; at - lane * 8 < count; at += kStep) {
         const int some = max(0, min(8, count - at));
+        const bool full = e.wide && some == 8;
         AdamGroup<BITS, KIND> x;
         float2 p[4];
-        x.load_some(c, at, some);
+        if (full) x.load(c, at);
+        else x.load_some(c, at, some);
         x.compute(s, p);
-        x.store_some(c, at, some, p);
+        if (full) x.store(c, at, p);
+        else x.store_some(c, at, some, p);
     }
 }
 
