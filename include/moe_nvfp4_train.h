@@ -48,7 +48,7 @@ extern "C" {
  * if computed in 64 bits: where FP32 cannot tell two apart, they are computed
  * in FP64.  An expert whose logit or bias is -infinity or NaN is not chosen (a
  * logit's also has the score 0) and does not count for its group; a logit of
- * +infinity counts as the largest FP32 number.  Slots beyond the experts that
+ * +infinity counts as the largest FP32 number (a bias of it is ahead of all).  Slots beyond the experts that
  * can be chosen get id -1 and weight 0: dropped routes of the calls below.
  * Renormalized weights do not underflow together: they come from l, relative to
  * the largest chosen.
@@ -308,7 +308,8 @@ MOE_API moe_status moe_nvfp4_grad_clip(int n, const void* const* grads, void* co
  * [2]: lr and t, a whole number up to 2^24) these replace rule.lr and rule.step,
  * so that a captured graph can be replayed with other ones; the corrections
  * are FP32 then.
- * Squares and v are FP32; v below 2^-126 counts as zero.
+ * Squares and v are FP32; v below 2^-126 counts as zero, and so does a rate lr /
+ * (1 - beta1^t) below 1e-30.
  * 0 <= n <= 65536, 0 <= numel < 2^40; pointers aligned to their element; a
  * tensor of no elements may have NULL pointers.  lr and weight_decay >= 0,
  * 0 <= beta < 1, eps >= 2^-126, max_norm and clip_eps >= 0, all finite; step >= 1

@@ -86,9 +86,9 @@ __device__ __forceinline__ AdamStep step_of(const AdamNumbers& k, const float* n
         rate = lr / -expm1f(t * k.log_b1);
         s.root = 1.0f / sqrtf(-expm1f(t * k.log_b2));
     }
-    // (a rate of zero: a denominator whose reciprocal is zero)
-    s.root = rate != 0.0f ? -s.root / rate : 0.0f;
-    s.eps = rate != 0.0f ? -s.eps / rate : -FLT_MAX;
+    // (a rate that is zero, or too small to divide by: a denominator whose reciprocal is zero)
+    s.root = rate >= 1e-30f ? -s.root / rate : 0.0f;
+    s.eps = rate >= 1e-30f ? -s.eps / rate : -FLT_MAX;
     return s;
 }
 

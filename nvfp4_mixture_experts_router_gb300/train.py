@@ -293,9 +293,11 @@ class AdamW:
     state_bits 8 keeps both moments in E4M3 with a scale for each 256 elements, of
     tensors from min_8bit elements on; master keeps FP32 values of BF16
     parameters, from which these are rounded.  Parameters without a gradient are
-    left as they are.  capturable: the learning rate and the number of the step
-    are read on the device (self.lr_step), so that a step captured into a CUDA
-    graph counts on when it is replayed; run one step before the capture."""
+    left as they are, and count their steps by themselves (a launch for each number).
+    capturable: the learning rate and the number of the step are read on the device
+    (self.lr_step), so that a step captured into a CUDA graph counts on when it is
+    replayed; run one step before the capture.  All parameters then have a gradient
+    in every step, or never."""
 
     def __init__(self, params: Iterable[torch.Tensor], lr: float = 1e-3, betas: Tuple[float, float] = (0.9, 0.999),
                  eps: float = 1e-8, weight_decay: float = 0.01, state_bits: int = 32, master: bool = True,
@@ -304,7 +306,7 @@ class AdamW:
             raise ValueError("state_bits must be 8 or 32")
         self.params = list(params)
         self.lr, self.betas, self.eps, self.weight_decay = lr, betas, eps, weight_decay
-        self.steps = 0
+        self.steps = [0] * len(self.params)     # of each parameter
         self.state = []
         for p in self.params:
             n, s, dev = p.numel(), {}, dict(device=p.device)
@@ -322,7 +324,7 @@ class AdamW:
         if capturable and self.params:
             self.lr_step = torch.tensor([lr, 0.0], dtype=torch.float32, device=self.params[0].device)
             self._device_lr = lr
-        self._list, self._of = None, None
+        self._lists = {}        # parameters of a launch -> their addresses and the list
 
     def zero_grad(self, set_to_none: bool = True) -> None:
         for p in self.params:
@@ -335,40 +337,53 @@ class AdamW:
     def step(self, norm: Optional[torch.Tensor] = None, max_norm: float = 1.0, clip_eps: float = 1e-6) -> None:
         """One step.  norm: the gradients' global norm (grad_norm), by which they are
         clipped to max_norm on the way."""
-        used = [i for i, p in enumerate(self.params) if p.grad is not None]
-        of = [(i, self.params[i].data_ptr()) for i in used]
-        grads = [self.params[i].grad.contiguous() for i in used]
-        if of != self._of:
-            get = lambda name: [self.state[i].get(name) for i in used]      # noqa: E731
-            self._list = api.AdamWList([self.params[i] for i in used], grads, get("exp_avg"), get("exp_avg_sq"),
-                                       get("exp_avg_scale"), get("exp_avg_sq_scale"), get("master"))
-            self._of = of
-        else:
-            self._list.set_grads(grads)
-        self.steps += 1
-        if self.lr_step is not None:
+        groups = {}
+        for i, p in enumerate(self.params):
+            if p.grad is not None:
+                groups.setdefault(self.steps[i], []).append(i)
+        if self.lr_step is not None and groups:
+            if len(groups) > 1:
+                raise ValueError("a capturable AdamW's parameters have a gradient in every step, or never")
             if self._device_lr != self.lr and not torch.cuda.is_current_stream_capturing():
                 self.lr_step[0].fill_(self.lr)
                 self._device_lr = self.lr
             self.lr_step[1].add_(1.0)
         rule = api.AdamWRule(self.lr, *self.betas, self.eps, self.weight_decay, max_norm, clip_eps)
-        api.moe_nvfp4_adamw(self._list, rule, self.steps, norm, self.lr_step)
-        self._list.grads = []       # the gradients may go
+        for steps, used in groups.items():
+            at = [self.params[i].data_ptr() for i in used]
+            grads = [self.params[i].grad.contiguous() for i in used]
+            kept = self._lists.get(tuple(used))
+            if kept is None or kept[0] != at:
+                get = lambda name: [self.state[i].get(name) for i in used]      # noqa: E731, B023
+                kept = at, api.AdamWList([self.params[i] for i in used], grads, get("exp_avg"), get("exp_avg_sq"),
+                                         get("exp_avg_scale"), get("exp_avg_sq_scale"), get("master"))
+                self._lists[tuple(used)] = kept
+            else:
+                kept[1].set_grads(grads)
+            api.moe_nvfp4_adamw(kept[1], rule, steps + 1, norm, self.lr_step)
+            kept[1].grads = []       # the gradients may go
+            for i in used:
+                self.steps[i] += 1
 
     def state_dict(self) -> dict:
-        return {"steps": self.steps if self.lr_step is None else int(self.lr_step[1]), "state": self.state}
+        steps = list(self.steps)
+        if self.lr_step is not None:        # replays count on the device alone
+            steps = [int(self.lr_step[1]) if n else 0 for n in steps]
+        return {"steps": steps, "state": self.state}
 
     def load_state_dict(self, saved: dict) -> None:
         """Copies the states of an optimizer of the same parameters and kind."""
         if [{k: (v.shape, v.dtype) for k, v in s.items()} for s in saved["state"]] != \
                 [{k: (v.shape, v.dtype) for k, v in s.items()} for s in self.state]:
             raise ValueError("the states are of other parameters, or of another kind")
+        if self.lr_step is not None and len(set(saved["steps"]) - {0}) > 1:
+            raise ValueError("a capturable AdamW's parameters have the same number of steps")
         for mine, theirs in zip(self.state, saved["state"]):
             for k, v in theirs.items():
                 mine[k].copy_(v)
-        self.steps = saved["steps"]
+        self.steps = list(saved["steps"])
         if self.lr_step is not None:
-            self.lr_step[1].fill_(self.steps)
+            self.lr_step[1].fill_(max(self.steps, default=0))
 
 
 def clip_grad_norm_(parameters: Union[torch.Tensor, Iterable[torch.Tensor]], max_norm: float,
