@@ -60,7 +60,7 @@ __device__ __forceinline__ float as_logit(float v) { return fminf(fmaxf(v, -INFI
 __device__ __forceinline__ float load_logit(const float* p) { return as_logit(*p); }
 __device__ __forceinline__ float load_logit(const __nv_bfloat16* p) { return as_logit(__bfloat162float(*p)); }
 
-// The lane's EPL logits, -infinity past the row's end.
+// The lane's EPL values, -infinity past the row's end.
 template <typename T_, int EPL>
 __device__ __forceinline__ void load_row(const T_* row, int E, bool wide, float (&l)[EPL]) {
     const int e0 = (threadIdx.x & 31) * EPL;
@@ -76,12 +76,18 @@ __device__ __forceinline__ void load_row(const T_* row, int E, bool wide, float 
                 for (int k = 0; k < VEC; ++k) u[k] = -INFINITY;
             }
 #pragma unroll
-            for (int k = 0; k < VEC; ++k) l[i + k] = as_logit(u[k]);
+            for (int k = 0; k < VEC; ++k) l[i + k] = u[k];
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) l[i] = e0 + i < E ? load_logit(row + e0 + i) : -INFINITY;
+        for (int i = 0; i < EPL; ++i) l[i] = e0 + i < E ? (float)row[e0 + i] : -INFINITY;
     }
+}
+
+template <int EPL>
+__device__ __forceinline__ void as_logits(float (&l)[EPL]) {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) l[i] = as_logit(l[i]);
 }
 
 // Scores in FP32.  Of sigmoid the absolute error is below kSigmoidErr: e^-l is
@@ -122,11 +128,38 @@ __device__ __forceinline__ Softmax softmax_of(const float (&l)[EPL]) {
     return Softmax{m, s > 0.0f ? __fdividef(1.0f, s) : 0.0f};
 }
 
+// The scores of the lane's logits, in their place.
+template <int EPL>
+__device__ __forceinline__ void scores(bool sigmoid, const Softmax& soft, float (&l)[EPL]) {
+    if (sigmoid) {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) l[i] = sigmoid_fast(l[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) l[i] = soft.of(l[i]);
+    }
+}
+
 // The largest over the warp (no NaN).
 __device__ __forceinline__ float warp_largest(float v) {
     float r;
     asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
     return r;
+}
+// The first `lanes` lanes' values from the largest down, with those of the lanes up
+// to the next power of two (a bitonic sort: Batcher 1968).
+__device__ __forceinline__ float sorted_lanes(float v, int lanes) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int size = 2; size <= 32; size <<= 1) {
+        if (size >= 2 * lanes) break;
+#pragma unroll
+        for (int o = size >> 1; o > 0; o >>= 1) {
+            const float u = __shfl_xor_sync(kAll, v, o);
+            v = ((lane & o) == 0) == ((lane & size) == 0 || size == 32) ? fmaxf(v, u) : fminf(v, u);
+        }
+    }
+    return v;
 }
 // The lane's number of `mine` things before its own in the order of the lanes, and of all.
 __device__ __forceinline__ int before_lane(int mine, int* all) {
@@ -142,7 +175,7 @@ __device__ __forceinline__ int before_lane(int mine, int* all) {
 
 // The two largest of a group of lanes' values, a >= b.
 __device__ __forceinline__ void join_top2(float& a, float& b, float a2, float b2) {
-    b = fmaxf(fminf(a, a2), a >= a2 ? b : b2);
+    b = fmaxf(fminf(a, a2), fmaxf(b, b2));
     a = fmaxf(a, a2);
 }
 __device__ __forceinline__ void into_top2(float& a, float& b, float v) {
@@ -340,14 +373,17 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const Rout
     const bool pair = grouped && a.rule.group_score == MOE_GROUP_TOP2, biased = a.bias != nullptr;
     float l[EPL], b[EPL];
     load_row<T_, EPL>(row, E, a.wide, l);
-    if (biased) load_row<float, EPL>(a.bias, E, a.wide_bias, b);    // (of +infinity, the largest number: no c is closer to it)
+    if (biased) load_row<float, EPL>(a.bias, E, a.wide_bias, b);
+    if (!(sigmoid && biased)) as_logits<EPL>(l);        // (sigmoid takes infinity as it is, and NaN is compared away)
     Softmax soft{0.0f, 0.0f};
     if (!sigmoid && (biased || pair || !a.rule.renormalize)) soft = softmax_of<EPL>(l);
     float c[EPL];       // -infinity: cannot be chosen
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-        if (biased) c[i] = fminf(l[i], b[i]) > -INFINITY ? (sigmoid ? sigmoid_fast(l[i]) : soft.of(l[i])) + b[i] : -INFINITY;
-        else c[i] = l[i];
+    for (int i = 0; i < EPL; ++i) c[i] = l[i];
+    if (biased) {
+        scores<EPL>(sigmoid, soft, c);
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) c[i] = l[i] > -INFINITY && b[i] > -INFINITY ? c[i] + b[i] : -INFINITY;
     }
     // a bound of the error of c: its score's, and c's own rounding
     const float most = sigmoid ? kSigmoidErr : 32.0f * kUnit * soft.inv;
@@ -358,12 +394,17 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const Rout
         const bool whole = a.span >= 0;         // a group is 2^span whole lanes
         const bool plain = pair && !biased;     // sums of the scores
         float x = -INFINITY, y = -INFINITY, border = -INFINITY;     // lane g: the two largest of group g
-        auto value = [&](int i) {
-            return !plain ? c[i] : c[i] > -INFINITY ? (sigmoid ? sigmoid_fast(c[i]) : soft.of(c[i])) : -INFINITY;
-        };
+        float v[EPL];
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) v[i] = c[i];
+        if (plain) {
+            scores<EPL>(sigmoid, soft, v);
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) v[i] = l[i] > -INFINITY ? v[i] : -INFINITY;
+        }
         if (whole) {
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) into_top2(x, y, value(i));
+            for (int i = 0; i < EPL; ++i) into_top2(x, y, v[i]);
             for (int o = 1; o < 1 << a.span; o <<= 1) {
                 const float x2 = __shfl_xor_sync(kAll, x, o), y2 = __shfl_xor_sync(kAll, y, o);
                 join_top2(x, y, x2, y2);
@@ -376,26 +417,28 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const Rout
             float* s_v = reinterpret_cast<float*>(s_c);
 #pragma unroll
             for (int i = 0; i < EPL; ++i)
-                if (e0 + i < E) s_v[e0 + i] = value(i);
+                if (e0 + i < E) s_v[e0 + i] = v[i];
             __syncwarp();
             if (lane < groups)
                 for (int i = 0; i < a.size; ++i) into_top2(x, y, s_v[lane * a.size + i]);
             __syncwarp();
         }
-        const float score = lane >= groups ? NAN : pair && y > -INFINITY ? x + y : x;
-        uint32_t taken = best_groups(score, groups, a.rule.topk_groups);
-        if (biased || pair) {
-            const float err = 2.0f * err_of(score) + 4.0f * kUnit * fabsf(x);
-            const bool in = (taken >> lane) & 1u && score > -INFINITY, out = !((taken >> lane) & 1u) && score > -INFINITY;
-            const float low = -warp_largest(in ? err - score : -INFINITY);
-            const float high = warp_largest(out ? score + err : -INFINITY);
-            if (high > -INFINITY && !(high < low)) {
+        const float score = lane >= groups ? -INFINITY : pair && y > -INFINITY ? x + y : x;
+        // the worst that is taken and the best that is not
+        const int take = a.rule.topk_groups;
+        const float ranked = sorted_lanes(score, groups);
+        const float low = __shfl_sync(kAll, ranked, take - 1), high = __shfl_sync(kAll, ranked, take);
+        uint32_t taken = __ballot_sync(kAll, score >= low);
+        if (high > -INFINITY) {
+            const float size = biased || pair ? warp_largest(lane < groups && score > -INFINITY ? fabsf(score) + fabsf(x) : 0.0f) : 0.0f;
+            const float err = biased || pair ? 2.0f * err_of(size) : 0.0f;      // of each score
+            if (biased || pair ? !(low - high > 2.0f * err) : low == high) {
                 border = fmaxf(border - 2.1f * err_of(border), -FLT_MAX);      // (none: all that can be chosen)
                 uint32_t can = 0;
 #pragma unroll
-                for (int i = 0; i < EPL; ++i) can |= value(i) >= border ? 1u << i : 0u;
-                taken = exact_groups<T_, EPL>(row, a.bias, sigmoid, E, soft.max, groups, a.rule.topk_groups, pair, can, s_c,
-                                              s_near[warp]);
+                for (int i = 0; i < EPL; ++i) can |= v[i] >= border ? 1u << i : 0u;
+                taken = biased || pair ? exact_groups<T_, EPL>(row, a.bias, sigmoid, E, soft.max, groups, take, pair, can, s_c, s_near[warp])
+                                       : best_groups(lane < groups ? score : NAN, groups, take);
             }
         }
         const uint32_t open = whole ? (taken >> (lane >> a.span)) & 1u ? kAll : 0u : lane_mask<EPL>(taken, a.size);
@@ -404,14 +447,11 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const Rout
             if (!((open >> i) & 1u)) c[i] = -INFINITY;
     }
 
-    // the border: the K-th largest of the lanes' largest (equal ones leave together), lower by the bounds
-    float mine_best = c[0], border = -INFINITY;
+    // the border: the K-th largest of the lanes' largest, lower by the bounds
+    float mine_best = c[0];
 #pragma unroll
     for (int i = 1; i < EPL; ++i) mine_best = fmaxf(mine_best, c[i]);
-    for (int k = 0; k < K; ++k) {
-        border = warp_largest(mine_best);
-        if (mine_best == border) mine_best = -INFINITY;
-    }
+    float border = __shfl_sync(kAll, sorted_lanes(mine_best, 32), K - 1);
     if (biased) border -= 2.1f * err_of(border);
     border = fmaxf(border, -FLT_MAX);           // (-infinity, or less and so NaN: all that can be chosen)
     // the experts from there on, in their order
@@ -434,8 +474,9 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const Rout
         slot = 0;
         for (int j0 = 0; j0 < n; j0 += 4)
 #pragma unroll
-            for (int j = j0; j < j0 + 4; ++j)       // (0 in the lanes past n - 1)
-                slot += __shfl_sync(kAll, own.x, j) + (j < lane) > own.x;
+            for (int j = j0; j < j0 + 4; ++j) slot += __shfl_sync(kAll, own.x, j) > own.x;      // (0 in the lanes past n - 1)
+        if (__reduce_or_sync(kAll, lane < n ? 1u << slot : 0u) != (n ? kAll >> (32 - n) : 0u))     // equal ones in their order
+            for (int j = 0; j < n; ++j) slot += __shfl_sync(kAll, own.x, j) == own.x && j < lane;
         if (biased) {
             // is the order of the chosen, and of the first that is not, beyond doubt?
             __syncwarp();
@@ -528,6 +569,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_backward_kernel(c
     Softmax soft{0.0f, 0.0f};
     if (full) {
         load_row<T_, EPL>(row, E, a.wide, l);
+        as_logits<EPL>(l);
         soft = softmax_of<EPL>(l);
         base = -warp_sum(e >= 0 ? soft.of(my_l) * u : 0.0f);
         d = u;
