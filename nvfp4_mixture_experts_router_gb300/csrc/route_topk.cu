@@ -360,7 +360,7 @@ __device__ __forceinline__ int rounds_choice(float (&c)[EPL], int K) {
 // ---- forward ------------------------------------------------------------------------
 
 template <typename T_, int EPL>
-__global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(32 * kRouteWarps, EPL == 32 ? 2 : EPL == 16 ? 3 : 4) route_topk_kernel(const RouteArgs a) {
     __shared__ uint2 s_near[kRouteWarps][33];   // key and expert; then the keys by rank
     extern __shared__ double s_exact[];         // [warps][E], with a bias or sums of two
     pdl_wait();
