@@ -98,7 +98,7 @@ __device__ __forceinline__ RowJoin join_row(float sum, float m, bool most, int W
 }
 
 // A scale of `amax` by the mode's rule, stored at `to[i]`, and what y is multiplied by.
-__device__ __forceinline__ float put_scale(int mode, void* to, int64_t i, float amax, bool writes) {
+__device__ __forceinline__ float put_scale(int mode, void* to, int i, float amax, bool writes) {
     if (mode == MOE_SCALE_MX) {
         // mx_block_exp in the fields of FP32: the code is the exponent's less 8, 0 below that (and of infinity)
         const int field = (int)(__float_as_uint(amax) >> 23), code = field < 255 ? max(field - 8, 0) : 0;
@@ -297,6 +297,9 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) rms_rows_kernel(const RmsArgs
     // gamma of vector c (from L1)
     auto gamma_of = [&](int c, float2 (&ga)[P]) { gamma_vector<VEC, STAGED>(a.gamma, a.H, c, wide_gamma, ga); };
     const bool by_row = Q && a.scale_mode == MOE_SCALE_ROW;
+    // the row's scales of blocks
+    uint8_t* scales = static_cast<uint8_t*>(a.scales) +
+                      (a.scale_mode == MOE_SCALE_MX ? t * ((a.H + 31) / 32) : t * ((a.H + 127) / 128) * 4);
     float2 sq = both(0.0f);
     float most = 0.0f;
 #pragma unroll
@@ -317,7 +320,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) rms_rows_kernel(const RmsArgs
     const Rstd r = rstd_of(row.sum, inv_h, a.eps);
     if (a.rstd && live && j == 0) a.rstd[t] = r.hi + r.lo;
     float inv = 1.0f;
-    if (by_row) inv = put_scale(MOE_SCALE_ROW, a.scales, t, row.most * r.hi, live && j == 0);
+    if (by_row) inv = put_scale(MOE_SCALE_ROW, a.scales, (int)t, row.most * r.hi, live && j == 0);
     if constexpr (STAGED)
         if (W == 1) __syncthreads();        // (else join_row's: every thread has taken its vectors)
 #pragma unroll
@@ -333,17 +336,16 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) rms_rows_kernel(const RmsArgs
         if (y && there) store(y, slot1, c, pack_pairs<T_, VEC>(u));
         if constexpr (Q) {
             if (!by_row) {
-                const bool mx = a.scale_mode == MOE_SCALE_MX;
                 float m = max_of<VEC>(0.0f, u);
 #pragma unroll
                 for (int o = 1; o < 32 / VEC; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                if (!mx) {
+                if (a.scale_mode == MOE_SCALE_MX) {
+                    inv = put_scale(MOE_SCALE_MX, scales, c / (32 / VEC), m, there && c % (32 / VEC) == 0);
+                } else {
 #pragma unroll
                     for (int o = 32 / VEC; o < 128 / VEC; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    inv = put_scale(MOE_SCALE_BLOCK128, scales, c / (128 / VEC), m, there && c % (128 / VEC) == 0);
                 }
-                const int per = mx ? 32 : 128;
-                inv = put_scale(a.scale_mode, a.scales, t * ((a.H + per - 1) / per) + c * VEC / per, m,
-                                there && c * VEC % per == 0);
             }
             if (q && there) {
                 if constexpr (STAGED) put_codes<VEC>(slot_q + RowSlot::offset(q) + c * VEC, u, inv, count_of(c));
@@ -802,7 +804,8 @@ cudaError_t forward_short(const LaunchCtx& c, const RmsArgs& a) {
     constexpr int kWhole = 16 / sizeof(T_);
     if constexpr (VEC < 4 && (sizeof(T_) == 2 || Q)) {
         // through shared memory, where a vector (or its codes) is less than eight bytes
-        if (sizeof(T_) == 2 && a.H > 4096) return forward_rows<T_, kWhole, 32, Q, true, 256, 4>(c, a);
+        if constexpr (sizeof(T_) == 2)
+            if (a.H > 4096) return forward_rows<T_, kWhole, 32, Q, true, 256, 4>(c, a);
         if (a.H > 256) return forward_rows<T_, kWhole, 16, Q, true, 512, 2>(c, a);
         return forward_rows<T_, kWhole, 8, Q, true, 256, 4>(c, a);
     } else {
