@@ -7,7 +7,11 @@
 // kind of states; nothing is copied to the device beforehand, and a captured
 // graph replays it.  A warp takes 256 consecutive elements, eight a lane: a
 // block of the states in 8 bits, whose largest magnitude is one warp-wide
-// maximum.  HBM is the bound: every buffer read and written once.
+// maximum.  HBM is the bound: every buffer read and written once; with states in 8
+// bits the instructions are near it (39 an element).  Measured on GB300 (copy rate
+// 6.8 TB/s), 302 million BF16 in 130 tensors: with FP32 master values and states
+// 1204 us (7.0 TB/s), with states in 8 bits and no master 540 (5.6); 67 million
+// FP32 269 (7.0) and 186 (5.7); 0.77 million FP32 in 18 tensors 4.9.
 #include <float.h>
 #include <math.h>
 
@@ -26,7 +30,7 @@ constexpr int kAdamMax = 384;           // tensors of a launch: 27.6 KB of its 3
 // Blocks: states in 32 bits, one for each chunk, so that the SMs sweep the buffers
 // in step (1207 us against 1428 with as many blocks as are resident, 302 million
 // BF16 with master values); in 8 bits the resident ones, as a block's start weighs
-// more beside the shorter chunks (560 us against 628).
+// more beside the fewer bytes of a chunk (560 us against 628).
 constexpr int kResident = 152 * 3;
 constexpr int kStarts = 152 * 6;        // blocks whose first entry travels with the list
 constexpr int kChunkMost = 4096, kChunkLeast = 2048;    // elements

@@ -18,8 +18,15 @@
 // rounding.  Logits compare exactly.  Scores with a bias, and sums of two
 // scores, are computed in FP32 with a bound of their error, and the border lies
 // lower by twice that; where two values that decide are closer than their bounds,
-// each lane computes its own again in FP64 (about one token in 300 with 256
+// each lane computes its own again in FP64 (about one token in 700 with 256
 // experts, standard normal logits and a bias).
+//
+// Bound by instructions: about 750 a token with a bias, groups and 256 experts,
+// 5 times what the logits' bytes take.  Measured on GB300, 16384 tokens, FP32: 256
+// experts, top-8, sigmoid, bias, 4 of 8 groups 18 us; without groups 13, softmax
+// without a bias 10.6; 64 experts, top-6 7.8; 1024 with a bias 53; top-32 of 256 47
+// (in rounds).  Backward 7.0 (2.6 TB/s: latency of ids, their logits and the row's
+// stores, in one wave and a half).  One token: 2.8 and 2.7.
 #include <float.h>
 #include <math.h>
 
