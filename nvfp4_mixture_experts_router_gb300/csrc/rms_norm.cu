@@ -322,7 +322,11 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) rms_rows_kernel(const RmsArgs
         }
     }
     // gamma of vector c (from L1)
-    auto gamma_of = [&](int c, float2 (&ga)[P]) { gamma_vector<VEC, STAGED>(a.gamma, a.H, c, wide_gamma, ga); };
+    // (past the row's end the last vector's: h is zero there)
+    auto gamma_of = [&](int c, float2 (&ga)[P]) {
+        if constexpr (STAGED) gamma_vector<VEC, true>(a.gamma, a.H, c, wide_gamma, ga);
+        else load_vector<VEC>(a.gamma, min(c, n - 1), wide_gamma, ga);
+    };
     const bool by_row = Q && a.scale_mode == MOE_SCALE_ROW;
     // the row's scales of blocks
     uint8_t* scales = static_cast<uint8_t*>(a.scales) +
