@@ -29,8 +29,8 @@
 // served by the caches, and dgamma is a pass of its own.
 //
 // Measured on GB300 (copy rate 6.8 TB/s): 16384 x 7168 BF16 with residual and MX
-// codes 127 us (6.5 TB/s), with y instead 135 (7.0), y of x alone 86 (5.4), codes
-// by row alone 122 (2.9: two looks at gamma and the row's maximum bound it); FP32
+// codes 126 us (6.6 TB/s), with y instead 135 (7.0), y of x alone 84 (5.6), codes
+// by row alone 121 (2.9: two looks at gamma and the row's maximum bound it); FP32
 // 225, 265, 138.  Backward with dh, 8191 x 7168: BF16 80 us (5.9), FP32 141 (6.7).
 // 8191 x 7167 BF16: 163 with residual and y (2.9), backward 251 (1.9).  2000 x
 // 16384 BF16: 60 with residual and y, backward 127.  One row of 7168: 3.6.

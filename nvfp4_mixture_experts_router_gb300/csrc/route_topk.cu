@@ -57,9 +57,6 @@ __device__ __forceinline__ uint32_t order_of(float v) {
     const int b = __float_as_int(v);
     return (uint32_t)(b ^ ((b >> 31) | (int)0x80000000));
 }
-__device__ __forceinline__ float value_of(uint32_t k) {
-    return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
-}
 
 // A logit as it counts: NaN as -infinity, at most the largest FP32 number.
 __device__ __forceinline__ float as_logit(float v) { return fminf(fmaxf(v, -INFINITY), FLT_MAX); }
@@ -485,13 +482,13 @@ __global__ void __launch_bounds__(32 * kRouteWarps, EPL == 32 ? 2 : EPL == 16 ? 
         if (__reduce_or_sync(kAll, lane < n ? 1u << slot : 0u) != (n ? kAll >> (32 - n) : 0u))     // equal ones in their order
             for (int j = 0; j < n; ++j) slot += __shfl_sync(kAll, own.x, j) == own.x && j < lane;
         if (biased) {
-            // is the order of the chosen, and of the first that is not, beyond doubt?
+            // is the order of the chosen beyond doubt, and the last of them ahead of every one that is not?
             __syncwarp();
             if (lane < n) s_near[warp][slot] = make_uint2(__float_as_uint(my_c), own.y);
             __syncwarp();
             bool doubt = false;
-            if (lane < min(n - 1, K)) {
-                const uint2 u = s_near[warp][lane], v = s_near[warp][lane + 1];
+            if (lane < n && lane != K - 1 && (lane >= K || lane + 1 < n)) {
+                const uint2 u = s_near[warp][min(lane, K - 1)], v = s_near[warp][lane < K ? lane + 1 : lane];
                 const float cu = __uint_as_float(u.x), cv = __uint_as_float(v.x);
                 // equal inputs are equal exactly, in the lower expert's favour
                 doubt = !(cu - cv > err_of(cu) + err_of(cv)) &&

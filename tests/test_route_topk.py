@@ -180,6 +180,20 @@ def test_near_ties(kind, E):
         check(rows, bias, api.RouteRule(score=kind, groups=4, topk_groups=2, group_score=gs), min(K, E // 4))
 
 
+@pytest.mark.parametrize("copies", [1, 2, 5, 40])
+@pytest.mark.parametrize("K", [1, 2, 3])
+def test_equal_experts_before_a_better_one(copies, K):
+    """Scores that FP32 takes for equal: `copies` of one expert, which are equal exactly, and behind them one that
+    is better in the thirteenth digit."""
+    E = 64
+    l, bias = torch.full((3, E), -50.0, device="cuda"), torch.zeros(E, device="cuda")
+    for at in (3, 50):
+        l[:, at:at + min(copies, E - at)], bias[at:at + min(copies, E - at)] = -30.0, 1.0
+    l[:, 60], bias[60] = -28.5, 1.0
+    ids, _ = check(l, bias, api.RouteRule(score=SIGMOID), K)
+    assert bool((ids[:, 0] == 60).all())
+
+
 @pytest.mark.parametrize("dt", [F32, BF])
 @pytest.mark.parametrize("kind", [SOFTMAX, SIGMOID])
 def test_ties_go_to_the_lower_expert(kind, dt):
