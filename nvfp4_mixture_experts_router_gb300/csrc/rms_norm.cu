@@ -49,7 +49,13 @@ constexpr float kE4M3Max = 448.0f;
 // A row's scale from the largest |y|, and what y is multiplied by.  At least
 // 2^-126: the reciprocal stays finite.
 __device__ __forceinline__ float linear_scale(float amax) {
-    return amax == 0.0f ? 1.0f : fmaxf(amax / kE4M3Max, 1.17549435e-38f);
+    return amax == 0.0f ? 1.0f : fmaxf(amax * (1.0f / kE4M3Max), 1.17549435e-38f);
+}
+// 1 / scale: the reciprocal within a unit and Newton's correction.
+__device__ __forceinline__ float inverse(float scale) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(scale));
+    return fmaf(fmaf(-scale, r, 1.0f), r, r);
 }
 
 // A vector's values in pairs (a single one with 0).
@@ -102,13 +108,14 @@ struct RowJoin {
 };
 __device__ __forceinline__ RowJoin join_row(float sum, float m, bool most, int W, float2* s) {
     sum = warp_sum(sum);
-    if (most) m = warp_max(m);
+    if (most) m = warp_largest(m);
     float2 v = make_float2(sum, 0.0f);
     if (W > 1) {
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        if (lane == 0) s[warp] = make_float2(sum, m);
+        const int lane = threadIdx.x & 31;
+        s += threadIdx.y * W;
+        if (lane == 0) s[threadIdx.x >> 5] = make_float2(sum, m);
         __syncthreads();
-        const float2 u = lane < W ? s[warp / W * W + lane] : make_float2(0.0f, 0.0f);
+        const float2 u = lane < W ? s[lane] : make_float2(0.0f, 0.0f);
         v.x = u.x;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1)
@@ -119,7 +126,7 @@ __device__ __forceinline__ RowJoin join_row(float sum, float m, bool most, int W
         // (lanes past the next power of two have not met the row's)
         v.x = __shfl_sync(0xffffffffu, v.x, 0);
         v.y = __shfl_sync(0xffffffffu, v.y, 0);
-        if (most) m = warp_max(u.y);
+        if (most) m = warp_largest(u.y);
     }
     return RowJoin{v, m};
 }
@@ -134,7 +141,7 @@ __device__ __forceinline__ float put_scale(int mode, void* to, int i, float amax
     }
     const float scale = linear_scale(amax);
     if (writes) static_cast<float*>(to)[i] = scale;
-    return 1.0f / scale;
+    return inverse(scale);
 }
 
 // Four E4M3 codes.
@@ -260,8 +267,8 @@ __device__ __forceinline__ void gamma_vector(const float* gamma, int H, int c, b
 constexpr int kRowColumns = 8192;   // rows up to here lie in registers
 
 // Rows of up to kRowColumns columns in registers: C columns a thread, V vectors
-// that lie `lanes` vectors apart; W warps a row, eight warps a block or one row.
-// STAGED: the rows pass through shared memory (RowSlot).
+// that lie `lanes` vectors apart; W warps a row, eight warps a block or one row
+// (a block of 32 W by rows).  STAGED: the rows pass through shared memory (RowSlot).
 template <typename T_, int VEC, int C, bool RES, bool Q, bool STAGED, int THREADS, int BLOCKS>
 __global__ void __launch_bounds__(THREADS, BLOCKS) rms_rows_kernel(const RmsArgs a, int W, float2 inv_h, bool wide_gamma) {
     using RV = RowVec<T_, VEC>;
@@ -273,7 +280,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) rms_rows_kernel(const RmsArgs
     __shared__ float2 s_red[32];
     extern __shared__ __align__(16) uint8_t s_mem[];    // STAGED: a group's slots
     pdl_wait();
-    const int lanes = W * 32, j = threadIdx.x % lanes, g = threadIdx.x / lanes, G = blockDim.x / lanes;
+    const int lanes = blockDim.x, j = threadIdx.x, g = threadIdx.y, G = blockDim.y;
     const int n = (a.H + VEC - 1) / VEC;                // (not STAGED: H is a multiple)
     const int64_t t = (int64_t)blockIdx.x * G + g;
     const bool live = t < a.T;
@@ -820,14 +827,14 @@ __global__ void __launch_bounds__(kRmsThreads) rms_dx_kernel(const RmsGradArgs a
 // C columns a thread.
 template <typename T_, int VEC, int C, bool Q, bool STAGED, int THREADS, int BLOCKS>
 cudaError_t forward_rows(const LaunchCtx& c, const RmsArgs& a) {
-    const int W = (a.H + 32 * C - 1) / (32 * C), G = W >= 8 ? 1 : 8 / W, threads = W * G * 32;
+    const int W = (a.H + 32 * C - 1) / (32 * C), G = W >= 8 ? 1 : 8 / W;
     const double inv = 1.0 / a.H;
     const float2 inv_h = make_float2((float)inv, (float)(inv - (double)(float)inv));
     const bool wide_gamma = row_at(a.gamma) % 16 == 0;
     const size_t slots = STAGED ? G * (2 * RowSlot::bytes(a.H * sizeof(T_)) + RowSlot::bytes(a.H)) : 0;
     auto kernel = a.residual ? rms_rows_kernel<T_, VEC, C, true, Q, STAGED, THREADS, BLOCKS>
                              : rms_rows_kernel<T_, VEC, C, false, Q, STAGED, THREADS, BLOCKS>;
-    return c.launch(kernel, dim3((unsigned)((a.T + G - 1) / G)), dim3(threads), slots, a, W, inv_h, wide_gamma);
+    return c.launch(kernel, dim3((unsigned)((a.T + G - 1) / G)), dim3(32 * W, G), slots, a, W, inv_h, wide_gamma);
 }
 
 template <typename T_, int VEC, bool Q>

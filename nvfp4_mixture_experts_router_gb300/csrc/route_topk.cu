@@ -144,12 +144,6 @@ __device__ __forceinline__ void scores(bool sigmoid, const Softmax& soft, float 
     }
 }
 
-// The largest over the warp (no NaN).
-__device__ __forceinline__ float warp_largest(float v) {
-    float r;
-    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-    return r;
-}
 // The first `lanes` lanes' values from the largest down, with those of the lanes up
 // to the next power of two (a bitonic sort: Batcher 1968).
 __device__ __forceinline__ float sorted_lanes(float v, int lanes) {
