@@ -181,6 +181,15 @@ __device__ __forceinline__ float max_of(float m, const float2 (&v)[(VEC + 1) / 2
     return m;
 }
 
+// Fetches BYTES (4, 8 or 16) into shared memory behind the thread's back.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* to, const void* from) {
+    if constexpr (BYTES == 16)      // (past L1)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(to)), "l"(from), "n"(BYTES) : "memory");
+}
+
 // A row off 16-byte blocks through shared memory: it lies there with its place
 // within 16 bytes, so that its whole blocks move in vectors and its ends alone by
 // elements, and the threads take and put vectors of the row at that offset.
@@ -202,6 +211,28 @@ struct RowSlot {
                 *(out ? d : c) = *(out ? c : d);
             }
         }
+    }
+    // The same into a slot behind the threads' back: `begin`, and after
+    // cp.async.wait_all `end`, which puts the thread's element of the ends.
+    static __device__ __forceinline__ uint32_t edge(uint32_t off, uint32_t bytes, uint32_t k, bool* there) {
+        const uint32_t lead = min((16u - off) & 15u, bytes), whole = (bytes - lead) & ~15u;
+        const uint32_t at = k < 16 ? k : lead + whole + (k - 16);
+        *there = k < 32 && at < (k < 16 ? lead : bytes);
+        return at;
+    }
+    template <typename One>
+    static __device__ __forceinline__ void begin(uint8_t* slot, const uint8_t* row, uint32_t bytes, int j, int lanes, One& end) {
+        const uint32_t off = offset(row), lead = min((16u - off) & 15u, bytes), whole = (bytes - lead) & ~15u;
+        for (uint32_t k = j * 16; k < whole; k += lanes * 16) copy_async<16>(slot + off + lead + k, row + lead + k);
+        bool there;
+        const uint32_t at = edge(off, bytes, j * sizeof(One), &there);
+        if (there) end = *reinterpret_cast<const One*>(row + at);
+    }
+    template <typename One>
+    static __device__ __forceinline__ void end(uint8_t* slot, const uint8_t* row, uint32_t bytes, int j, One end) {
+        bool there;
+        const uint32_t at = edge(offset(row), bytes, j * sizeof(One), &there);
+        if (there) *reinterpret_cast<One*>(slot + offset(row) + at) = end;
     }
     // Vector c of a row at `off`: two blocks, shifted.  Of the last one `count`
     // elements count, the others become 0.
@@ -516,14 +547,6 @@ __global__ void __launch_bounds__(kRmsThreads)
 
 // ---- backward -----------------------------------------------------------------------
 
-template <int BYTES>
-__device__ __forceinline__ void copy_async(void* to, const void* from) {
-    if constexpr (BYTES == 16)      // (past L1)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(to)), "l"(from), "n"(BYTES) : "memory");
-}
-
 // A block's sums of dgamma, its groups' in order, to the block's row of `part`.
 template <int VEC, int V>
 __device__ __forceinline__ void put_sums(const RmsGradArgs& a, const float2 (&dg)[V][(VEC + 1) / 2], int j, int lanes, int g,
@@ -668,7 +691,9 @@ __global__ void __launch_bounds__(512, 1) rms_ring_backward_kernel(const RmsGrad
 }
 
 // The same for rows off 16-byte blocks, in vectors of two bytes: each row through
-// slots (RowSlot), one after the other.
+// slots (RowSlot), the next one on its way meanwhile.  dy, whose slot takes dx, stays
+// in registers; h and dh are taken twice (all three in registers spill: 208 us
+// against 191 for 8191 x 7167 with dh; one row after the other 251).
 template <typename T_, int C, bool DH, int BLOCKS>
 __global__ void __launch_bounds__(512, BLOCKS) rms_slot_backward_kernel(const RmsGradArgs a, int W, float inv_h, bool wide_gamma) {
     constexpr int VEC = 16 / sizeof(T_);
@@ -676,7 +701,7 @@ __global__ void __launch_bounds__(512, BLOCKS) rms_slot_backward_kernel(const Rm
     using One = typename RowVec<T_, 1>::Raw;
     constexpr int V = C / VEC, P = VEC / 2, N = DH ? 3 : 2;
     __shared__ float s_red[2][32];
-    extern __shared__ __align__(16) uint8_t s_mem[];    // [groups][N] slots; in the end the groups' sums
+    extern __shared__ __align__(16) uint8_t s_mem[];    // [groups][2][N] slots; in the end the groups' sums
     pdl_wait();
     const int lanes = W * 32, j = threadIdx.x % lanes, g = threadIdx.x / lanes, G = blockDim.x / lanes;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = (a.H + VEC - 1) / VEC;
@@ -685,34 +710,44 @@ __global__ void __launch_bounds__(512, BLOCKS) rms_slot_backward_kernel(const Rm
     const int64_t strides[3] = {a.dy_stride, a.h_stride, a.dh_stride};
     const uint32_t row_bytes = (uint32_t)a.H * sizeof(T_);
     const size_t slot = RowSlot::bytes(row_bytes);
-    uint8_t* slots = s_mem + g * N * slot;
+    uint8_t *slots = s_mem + g * 2 * N * slot, *others = slots + N * slot;
     float2 dg[V][P];
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
         for (int k = 0; k < P; ++k) dg[i][k] = both(0.0f);
+    One ends[N] = {};
+    auto begin = [&](int64_t t, uint8_t* to) {
+        if (t < a.T)
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                RowSlot::begin<One>(to + k * slot, reinterpret_cast<const uint8_t*>(rows[k] + t * strides[k]), row_bytes, j, lanes, ends[k]);
+    };
+    begin(first, slots);
     int turn = 0;
     for (int64_t t = first; t - g < a.T; t += step) {        // uniform over the block
         const bool live = t < a.T;
         const float rstd = live ? a.rstd[t] : 0.0f;
+        asm volatile("cp.async.wait_all;" ::: "memory");
         if (live)
 #pragma unroll
             for (int k = 0; k < N; ++k)
-                RowSlot::move<One>(slots + k * slot, (uint8_t*)(rows[k] + t * strides[k]), row_bytes, j, lanes, false);
-        __syncthreads();
-        Raw r[N][V];
+                RowSlot::end<One>(slots + k * slot, reinterpret_cast<const uint8_t*>(rows[k] + t * strides[k]), row_bytes, j, ends[k]);
+        __syncthreads();            // and the row before has left the other slots
+        begin(t + step, others);
+        auto take = [&](int k, int c) {
+            return live && c < n ? RowSlot::take<T_>(slots + k * slot, RowSlot::offset(rows[k] + t * strides[k]), c, min(VEC, a.H - c * VEC))
+                                 : Raw{};
+        };
+        Raw r[V];
         float2 sum = both(0.0f);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int c = j + i * lanes;
-#pragma unroll
-            for (int k = 0; k < N; ++k)
-                r[k][i] = live && c < n ? RowSlot::take<T_>(slots + k * slot, RowSlot::offset(rows[k] + t * strides[k]), c,
-                                                            min(VEC, a.H - c * VEC))
-                                        : Raw{};
+            r[i] = take(0, c);
             float2 d[P], h[P], ga[P];
-            unpack_pairs<T_, VEC>(r[0][i], d);
-            unpack_pairs<T_, VEC>(r[1][i], h);
+            unpack_pairs<T_, VEC>(r[i], d);
+            unpack_pairs<T_, VEC>(take(1, c), h);
             gamma_vector<VEC, true>(a.gamma, a.H, c, wide_gamma, ga);
 #pragma unroll
             for (int k = 0; k < P; ++k) {
@@ -732,9 +767,9 @@ __global__ void __launch_bounds__(512, BLOCKS) rms_slot_backward_kernel(const Rm
         for (int i = 0; i < V; ++i) {
             const int c = j + i * lanes;
             float2 d[P], h[P], ga[P], u[P];
-            unpack_pairs<T_, VEC>(r[0][i], d);
-            unpack_pairs<T_, VEC>(r[1][i], h);
-            if (DH) unpack_pairs<T_, VEC>(r[N - 1][i], u);
+            unpack_pairs<T_, VEC>(r[i], d);
+            unpack_pairs<T_, VEC>(take(1, c), h);
+            if (DH) unpack_pairs<T_, VEC>(take(N - 1, c), u);
             gamma_vector<VEC, true>(a.gamma, a.H, c, wide_gamma, ga);
 #pragma unroll
             for (int k = 0; k < P; ++k) {
@@ -745,8 +780,11 @@ __global__ void __launch_bounds__(512, BLOCKS) rms_slot_backward_kernel(const Rm
         }
         __syncthreads();
         if (live) RowSlot::move<One>(slots, reinterpret_cast<uint8_t*>(out), row_bytes, j, lanes, true);
-        __syncthreads();
+        uint8_t* const now = slots;
+        slots = others;
+        others = now;
     }
+    __syncthreads();
     put_sums<VEC, V>(a, dg, j, lanes, g, G, reinterpret_cast<float*>(s_mem));
     pdl_launch_dependents();
 }
@@ -895,7 +933,7 @@ template <typename T_, int C>
 cudaError_t slot_backward(const LaunchCtx& c, const RmsGradArgs& a, const BackwardShape& s) {
     constexpr int kBlocks = sizeof(T_) == 2 ? 2 : 1;
     auto kernel = a.dh ? rms_slot_backward_kernel<T_, C, true, kBlocks> : rms_slot_backward_kernel<T_, C, false, kBlocks>;
-    const size_t slots = s.G * (a.dh ? 3 : 2) * RowSlot::bytes(a.H * sizeof(T_)), sums = s.G > 1 ? (size_t)s.G * a.H * 4 : 0;
+    const size_t slots = 2 * s.G * (a.dh ? 3 : 2) * RowSlot::bytes(a.H * sizeof(T_)), sums = s.G > 1 ? (size_t)s.G * a.H * 4 : 0;
     return c.launch(kernel, dim3(backward_blocks(a.T, s)), dim3(s.threads), slots > sums ? slots : sums, a, s.W,
                     1.0f / (float)a.H, row_at(a.gamma) % 16 == 0);
 }
