@@ -295,9 +295,10 @@ __device__ __forceinline__ void gamma_vector(const float* gamma, int H, int c, b
     }
 }
 
-constexpr int kRowColumns = 8192;   // rows up to here lie in registers
+constexpr int kRowColumns = 8192;   // rows up to here lie in registers,
+constexpr int kWideColumns = 16384; // and up to here those in vectors of 16 bytes
 
-// Rows of up to kRowColumns columns in registers: C columns a thread, V vectors
+// Rows of up to kRowColumns (kWideColumns) columns in registers: C columns a thread, V vectors
 // that lie `lanes` vectors apart; W warps a row, eight warps a block or one row
 // (a block of 32 W by rows).  STAGED: the rows pass through shared memory (RowSlot).
 template <typename T_, int VEC, int C, bool RES, bool Q, bool STAGED, int THREADS, int BLOCKS>
@@ -432,7 +433,6 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) rms_rows_kernel(const RmsArgs
 }
 
 constexpr int kRmsThreads = 512;
-constexpr int kRmsParts = 152;      // row groups of dgamma
 
 // Sum (or maximum) over the block; every thread gets it.
 template <bool MAX>
@@ -789,23 +789,45 @@ __global__ void __launch_bounds__(512, BLOCKS) rms_slot_backward_kernel(const Rm
     pdl_launch_dependents();
 }
 
-// Partial sums of dgamma for longer rows: a thread per column, a group of rows per
-// blockIdx.y.
-template <typename T_>
+// Partial sums of dgamma for longer rows: 256 columns a block and 256 / VEC threads
+// a row, VEC rows at a time; blockIdx.y takes a share of the rows.
+template <typename T_, int VEC>
 __global__ void __launch_bounds__(256) rms_partial_kernel(const RmsGradArgs a) {
-    using RV = RowVec<T_, 1>;
+    using RV = RowVec<T_, VEC>;
     using Raw = typename RV::Raw;
+    __shared__ float s[VEC][256];
     pdl_wait();
-    const int c = blockIdx.x * 256 + threadIdx.x;
-    if (c >= a.H) return;
-    float sum = 0.0f;
-    for (int64_t t = blockIdx.y; t < a.T; t += kRmsParts) {
-        float g[1], v[1];
-        RV::unpack(static_cast<const Raw*>(a.dy)[t * a.dy_stride + c], g);
-        RV::unpack(static_cast<const Raw*>(a.h)[t * a.h_stride + c], v);
-        sum = fmaf(g[0], v[0] * a.rstd[t], sum);
+    constexpr int kLanes = 256 / VEC;
+    const int j = threadIdx.x % kLanes, g = threadIdx.x / kLanes, first = blockIdx.x * 256, c = first / VEC + j;
+    float sum[VEC] = {};
+    if (c < a.H / VEC) {
+        const Raw* dy = static_cast<const Raw*>(a.dy) + c;
+        const Raw* h = static_cast<const Raw*>(a.h) + c;
+        const int64_t dy_stride = a.dy_stride / VEC, h_stride = a.h_stride / VEC;
+#pragma unroll 4
+        for (int64_t t = (int64_t)blockIdx.y * VEC + g; t < a.T; t += gridDim.y * VEC) {
+            float d[VEC], v[VEC];
+            RV::unpack(dy[t * dy_stride], d);
+            RV::unpack(h[t * h_stride], v);
+            const float rstd = a.rstd[t];
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) sum[k] = fmaf(d[k], v[k] * rstd, sum[k]);
+        }
     }
-    a.part[(size_t)blockIdx.y * a.H + c] = sum;
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) s[g][j * VEC + k] = sum[k];
+    __syncthreads();
+    const int column = first + threadIdx.x;
+    float v = 0.0f;
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) v += s[k][threadIdx.x];
+    if (column < a.H) a.part[(size_t)blockIdx.y * a.H + column] = v;
+    pdl_launch_dependents();
+}
+// Shares of the rows: eight blocks an SM, each with 64 rows or more.
+int partial_shares(int T, int H) {
+    const int strips = (H + 255) / 256, most = (152 * 8 + strips - 1) / strips, need = (T + 63) / 64;
+    return need < 1 ? 1 : need < most ? need : most;
 }
 
 // dgamma from `parts` partial sums [parts][H]: 32 columns a block, a 32nd of the
@@ -862,6 +884,59 @@ __global__ void __launch_bounds__(kRmsThreads) rms_dx_kernel(const RmsGradArgs a
     }
 }
 
+// The same with a row of dy and h in the registers of a block, sixteen columns a
+// thread (2000 x 16384 BF16 81 us with the sums of dgamma against 89 with 32, and 122
+// when each is read twice; the slots' kernel, one pass for both, 103).
+template <typename T_, int VEC>
+__global__ void __launch_bounds__(1024, 1) rms_dx_rows_kernel(const RmsGradArgs a, float inv_h, bool wide_gamma) {
+    using RV = RowVec<T_, VEC>;
+    using Raw = typename RV::Raw;
+    constexpr int V = 16 / VEC, P = VEC / 2;
+    __shared__ float s[32];
+    pdl_wait();
+    const int64_t t = blockIdx.x;
+    const int n = a.H / VEC, lanes = blockDim.x, j = threadIdx.x;
+    const Raw* dy = static_cast<const Raw*>(a.dy) + t * (a.dy_stride / VEC);
+    const Raw* h = static_cast<const Raw*>(a.h) + t * (a.h_stride / VEC);
+    const Raw* dh = a.dh ? static_cast<const Raw*>(a.dh) + t * (a.dh_stride / VEC) : nullptr;
+    Raw* dx = static_cast<Raw*>(a.dx) + t * (a.dx_stride / VEC);
+    const float rstd = a.rstd[t];
+    Raw rd[V], rh[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = j + i * lanes;
+        rd[i] = c < n ? dy[c] : Raw{};
+        rh[i] = c < n ? h[c] : Raw{};
+    }
+    float2 sum = both(0.0f);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        float2 d[P], v[P], ga[P];
+        unpack_pairs<T_, VEC>(rd[i], d);
+        unpack_pairs<T_, VEC>(rh[i], v);
+        load_vector<VEC>(a.gamma, min(j + i * lanes, n - 1), wide_gamma, ga);    // (past the end dy is zero)
+#pragma unroll
+        for (int k = 0; k < P; ++k) sum = fma2(mul2(d[k], ga[k]), mul2(v[k], both(rstd)), sum);
+    }
+    const float mean = block_join<false>(sum.x + sum.y, s) * inv_h * rstd;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = j + i * lanes;
+        float2 d[P], v[P], ga[P], u[P];
+        unpack_pairs<T_, VEC>(rd[i], d);
+        unpack_pairs<T_, VEC>(rh[i], v);
+        load_vector<VEC>(a.gamma, min(c, n - 1), wide_gamma, ga);
+        unpack_pairs<T_, VEC>(dh && c < n ? dh[c] : Raw{}, u);
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+            const float2 w = mul2(fma2(v[k], both(-mean), mul2(d[k], ga[k])), both(rstd));
+            d[k] = dh ? add2(w, u[k]) : w;
+        }
+        if (c < n) dx[c] = pack_pairs<T_, VEC>(d);
+    }
+    pdl_launch_dependents();
+}
+
 // C columns a thread.
 template <typename T_, int VEC, int C, bool Q, bool STAGED, int THREADS, int BLOCKS>
 cudaError_t forward_rows(const LaunchCtx& c, const RmsArgs& a) {
@@ -893,9 +968,18 @@ cudaError_t forward_short(const LaunchCtx& c, const RmsArgs& a) {
     }
 }
 
+template <typename T_, int VEC, bool Q>
+cudaError_t forward_wide(const LaunchCtx& c, const RmsArgs& a) {
+    if constexpr (sizeof(T_) == 2)
+        if (a.T > 152) return forward_rows<T_, VEC, 32, Q, false, 512, 2>(c, a);
+    return forward_rows<T_, VEC, 16, Q, false, 1024, 1>(c, a);
+}
+
 template <typename T_, int VEC>
 cudaError_t forward_any(const LaunchCtx& c, const RmsArgs& a) {
     if (a.H <= kRowColumns) return a.q ? forward_short<T_, VEC, true>(c, a) : forward_short<T_, VEC, false>(c, a);
+    if constexpr (VEC * sizeof(T_) == 16)
+        if (a.H <= kWideColumns) return a.q ? forward_wide<T_, VEC, true>(c, a) : forward_wide<T_, VEC, false>(c, a);
     const size_t smem = a.q && a.scale_mode != MOE_SCALE_ROW ? (size_t)(a.H + 31) / 32 * 4 : 0;
     return c.launch(rms_norm_kernel<T_, VEC>, dim3((unsigned)a.T), dim3(kRmsThreads), smem, a);
 }
@@ -949,7 +1033,19 @@ cudaError_t launch_backward_rows(const LaunchCtx& c, int elem, int bytes, const 
 }
 
 template <typename T_, int VEC>
+cudaError_t partial_any(const LaunchCtx& c, const RmsGradArgs& a, dim3 grid) {
+    return c.launch(rms_partial_kernel<T_, VEC>, grid, dim3(256), 0, a);
+}
+cudaError_t launch_partial(const LaunchCtx& c, int elem, int bytes, const RmsGradArgs& a, dim3 grid) {
+    MOE_ROW_VEC(elem, bytes, partial_any, c, a, grid);
+}
+
+template <typename T_, int VEC>
 cudaError_t dx_any(const LaunchCtx& c, const RmsGradArgs& a) {
+    if constexpr (VEC * sizeof(T_) == 16)
+        if (a.H <= kWideColumns)
+            return c.launch(rms_dx_rows_kernel<T_, VEC>, dim3((unsigned)a.T), dim3((a.H + 511) / 512 * 32), 0, a, 1.0f / (float)a.H,
+                            row_at(a.gamma) % 16 == 0);
     return c.launch(rms_dx_kernel<T_, VEC>, dim3((unsigned)a.T), dim3(kRmsThreads), 0, a);
 }
 cudaError_t launch_dx(const LaunchCtx& c, int elem, int bytes, const RmsGradArgs& a) {
@@ -1013,7 +1109,7 @@ cudaError_t setup_rms_norm_kernels() {
 
 // Partial sums of dgamma, a row of H for each block of the backward kernels.
 size_t rms_norm_workspace_bytes(int T, int H) {
-    const int parts = H > kRowColumns ? kRmsParts : backward_blocks(T, backward_shape(H, true));
+    const int parts = H > kRowColumns ? partial_shares(T, H) : backward_blocks(T, backward_shape(H, true));
     return align_up((uint64_t)parts * H * 4, 256);
 }
 
@@ -1024,15 +1120,14 @@ cudaError_t launch_rms_norm_backward(const LaunchCtx& c, int elem, const RmsGrad
                                         row_at(a.h, a.h_stride, elem) | row_at(a.dx, a.dx_stride, elem));
     const bool rows = a.H <= kRowColumns;
     const BackwardShape s = backward_shape(a.H, in_slots(elem, bytes));
-    const int parts = rows ? backward_blocks(a.T, s) : kRmsParts;
+    const int parts = rows ? backward_blocks(a.T, s) : partial_shares(a.T, a.H);
     if (parts == 1) a.part = a.dgamma;          // one block's sums are the result
     cudaError_t e;
     if (rows) {
         e = launch_backward_rows(c, elem, bytes, a, s);
     } else {
         // the column sums first: dx may overwrite dy or h
-        const dim3 grid((unsigned)((a.H + 255) / 256), kRmsParts);
-        e = c.launch(elem == 2 ? rms_partial_kernel<__nv_bfloat16> : rms_partial_kernel<float>, grid, dim3(256), 0, a);
+        e = launch_partial(c, elem, bytes, a, dim3((unsigned)((a.H + 255) / 256), (unsigned)parts));
     }
     if (e == cudaSuccess && parts > 1)
         e = c.launch(rms_reduce_kernel, dim3((unsigned)((a.H + 31) / 32)), dim3(1024), 0, a.H, parts, (const float*)a.part,

@@ -252,6 +252,27 @@ def test_backward_in_place_and_strided(T, H, dt):
             assert bool((b == 7.0).all())
 
 
+@pytest.mark.parametrize("T,H", [(153, 8256), (200, 16384), (160, 12296), (154, 16392)])
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("mode", MODES)
+def test_forward_of_many_long_rows(T, H, dt, mode):
+    x, res, gamma = inputs(T, H, dt)
+    check_forward(x, res, gamma, forward(x, res, gamma, mode), mode)
+
+
+@pytest.mark.parametrize("T,H", [(200, 16384), (1000, 9000), (321, 12300), (130, 16392), (257, 9001), (65, 40000)])
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("with_dh", [False, True])
+def test_backward_of_many_long_rows(T, H, dt, with_dh):
+    test_backward(T, H, dt, with_dh)
+
+
+@pytest.mark.parametrize("T,H", [(2600, 1001), (400, 7167), (200, 16384)])
+def test_backward_in_place_of_rows_under_way(T, H):
+    """A block copies its next row while dx goes over an earlier one."""
+    test_backward_in_place_and_strided(T, H, BF)
+
+
 def test_backward_against_differences():
     """Central differences of sum(dy y) in 64 bits, h = 1e-5: off by h^2 and 1e-16 / h, on gradients of up to
     10; the kernel's own error is below 1e-5 (H = 24: 50 units of 2^-24)."""
