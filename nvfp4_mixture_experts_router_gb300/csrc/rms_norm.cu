@@ -884,14 +884,15 @@ __global__ void __launch_bounds__(kRmsThreads) rms_dx_kernel(const RmsGradArgs a
     }
 }
 
-// The same with a row of dy and h in the registers of a block, sixteen columns a
-// thread (2000 x 16384 BF16 81 us with the sums of dgamma against 89 with 32, and 122
-// when each is read twice; the slots' kernel, one pass for both, 103).
-template <typename T_, int VEC>
-__global__ void __launch_bounds__(1024, 1) rms_dx_rows_kernel(const RmsGradArgs a, float inv_h, bool wide_gamma) {
+// The same with a row of dy and h in the registers of a block, C columns a thread: 32
+// of BF16 and two blocks an SM (2000 x 16384 with dh 83 us, the sums of dgamma among
+// them, against 95 with 16 and one block), 16 of FP32 (136).  Reading both twice took
+// 127 and 159, one pass for both results through slots 122 (BF16).
+template <typename T_, int VEC, int C>
+__global__ void __launch_bounds__(16384 / C, C / 16) rms_dx_rows_kernel(const RmsGradArgs a, float inv_h, bool wide_gamma) {
     using RV = RowVec<T_, VEC>;
     using Raw = typename RV::Raw;
-    constexpr int V = 16 / VEC, P = VEC / 2;
+    constexpr int V = C / VEC, P = VEC / 2;
     __shared__ float s[32];
     pdl_wait();
     const int64_t t = blockIdx.x;
@@ -908,31 +909,47 @@ __global__ void __launch_bounds__(1024, 1) rms_dx_rows_kernel(const RmsGradArgs 
         rd[i] = c < n ? dy[c] : Raw{};
         rh[i] = c < n ? h[c] : Raw{};
     }
+    // gamma four by four, and the rows unpacked twice: in 32 bits they would spill
     float2 sum = both(0.0f);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        float2 d[P], v[P], ga[P];
+        const int c = min(j + i * lanes, n - 1);            // (past the end dy is zero)
+        float2 d[P], v[P], ga[2];
         unpack_pairs<T_, VEC>(rd[i], d);
         unpack_pairs<T_, VEC>(rh[i], v);
-        load_vector<VEC>(a.gamma, min(j + i * lanes, n - 1), wide_gamma, ga);    // (past the end dy is zero)
 #pragma unroll
-        for (int k = 0; k < P; ++k) sum = fma2(mul2(d[k], ga[k]), mul2(v[k], both(rstd)), sum);
+        for (int k = 0; k < P; ++k) {
+            if (k % 2 == 0) {
+                asm volatile("" ::: "memory");
+                load_vector<4>(a.gamma, c * (VEC / 4) + k / 2, wide_gamma, ga);
+            }
+            sum = fma2(mul2(d[k], ga[k % 2]), mul2(v[k], both(rstd)), sum);
+        }
     }
     const float mean = block_join<false>(sum.x + sum.y, s) * inv_h * rstd;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
+        asm volatile("" : "+r"(rd[i].x), "+r"(rd[i].y), "+r"(rd[i].z), "+r"(rd[i].w));
+        asm volatile("" : "+r"(rh[i].x), "+r"(rh[i].y), "+r"(rh[i].z), "+r"(rh[i].w));
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
         const int c = j + i * lanes;
-        float2 d[P], v[P], ga[P], u[P];
+        if (c >= n) break;
+        float2 d[P], v[P], u[P], ga[2];
         unpack_pairs<T_, VEC>(rd[i], d);
         unpack_pairs<T_, VEC>(rh[i], v);
-        load_vector<VEC>(a.gamma, min(c, n - 1), wide_gamma, ga);
-        unpack_pairs<T_, VEC>(dh && c < n ? dh[c] : Raw{}, u);
+        unpack_pairs<T_, VEC>(dh ? dh[c] : Raw{}, u);
 #pragma unroll
         for (int k = 0; k < P; ++k) {
-            const float2 w = mul2(fma2(v[k], both(-mean), mul2(d[k], ga[k])), both(rstd));
+            if (k % 2 == 0) {
+                asm volatile("" ::: "memory");
+                load_vector<4>(a.gamma, c * (VEC / 4) + k / 2, wide_gamma, ga);
+            }
+            const float2 w = mul2(fma2(v[k], both(-mean), mul2(d[k], ga[k % 2])), both(rstd));
             d[k] = dh ? add2(w, u[k]) : w;
         }
-        if (c < n) dx[c] = pack_pairs<T_, VEC>(d);
+        dx[c] = pack_pairs<T_, VEC>(d);
     }
     pdl_launch_dependents();
 }
@@ -1043,9 +1060,11 @@ cudaError_t launch_partial(const LaunchCtx& c, int elem, int bytes, const RmsGra
 template <typename T_, int VEC>
 cudaError_t dx_any(const LaunchCtx& c, const RmsGradArgs& a) {
     if constexpr (VEC * sizeof(T_) == 16)
-        if (a.H <= kWideColumns)
-            return c.launch(rms_dx_rows_kernel<T_, VEC>, dim3((unsigned)a.T), dim3((a.H + 511) / 512 * 32), 0, a, 1.0f / (float)a.H,
-                            row_at(a.gamma) % 16 == 0);
+        if (a.H <= kWideColumns) {
+            constexpr int C = 64 / sizeof(T_);
+            return c.launch(rms_dx_rows_kernel<T_, VEC, C>, dim3((unsigned)a.T), dim3((a.H + 32 * C - 1) / (32 * C) * 32), 0, a,
+                            1.0f / (float)a.H, row_at(a.gamma) % 16 == 0);
+        }
     return c.launch(rms_dx_kernel<T_, VEC>, dim3((unsigned)a.T), dim3(kRmsThreads), 0, a);
 }
 cudaError_t launch_dx(const LaunchCtx& c, int elem, int bytes, const RmsGradArgs& a) {
