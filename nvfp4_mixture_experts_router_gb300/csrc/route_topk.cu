@@ -28,6 +28,7 @@
 // (in rounds).  Backward 7.0 (2.6 TB/s: latency of ids, their logits and the row's
 // stores, in one wave and a half).  One token: 2.8 and 2.7.
 #include <float.h>
+#include <limits.h>
 #include <math.h>
 
 #include "row_vec.cuh"
@@ -209,8 +210,17 @@ __device__ __forceinline__ Exact<T_> exact_of(const T_* row, const float* bias, 
     return Exact<T_>{row, bias, sigmoid, (double)max, s};
 }
 
+// FP64 values are compared as integers in their order (FP64 runs at a 64th of the
+// rate): those of all that is no NaN lie above kNoKey.
+constexpr long long kNoKey = LLONG_MIN;
+__device__ __forceinline__ long long key_of(double v) {
+    const long long b = __double_as_longlong(v + 0.0);      // zeros alike
+    return b ^ ((b >> 63) & LLONG_MAX);
+}
+__device__ __forceinline__ double of_key(long long k) { return __longlong_as_double(k ^ ((k >> 63) & LLONG_MAX)); }
+
 // The topk_groups best groups, as a mask: lane g has group g's score, or NaN
-// for a group that does not exist.
+// (kNoKey) for a group that does not exist.
 template <typename F>
 __device__ __forceinline__ uint32_t best_groups(F score, int groups, int take) {
     const int lane = threadIdx.x & 31;
@@ -258,17 +268,16 @@ __device__ __noinline__ uint32_t exact_groups(const T_* row, const float* bias, 
     __syncwarp();
     if (n <= 32 && lane < n) s_c[s_list[lane].x] = f((int)s_list[lane].x);     // one each
     __syncwarp();
-    double a = -INFINITY, b = -INFINITY;
+    long long a = kNoKey, b = kNoKey;
     if (lane < groups) {
-#pragma unroll 1
+#pragma unroll 4
         for (int i = 0; i < size; ++i) {
-            const double v = s_c[lane * size + i];
-            b = fmax(b, fmin(a, v));
-            a = fmax(a, v);
+            const long long v = key_of(s_c[lane * size + i]);
+            const long long low = v > a ? a : v;
+            if (v > a) a = v;
+            if (low > b) b = low;
         }
-        if (pair && b > -INFINITY) a += b;
-    } else {
-        a = NAN;
+        if (pair && b > key_of(-INFINITY)) a = key_of(of_key(a) + of_key(b));
     }
     __syncwarp();
     return best_groups(a, groups, take);
@@ -279,11 +288,11 @@ template <typename T_, int EPL>
 __device__ __noinline__ int exact_rank(const T_* row, const float* bias, bool sigmoid, int E, float max, int e, int n) {
     const int lane = threadIdx.x & 31;
     const Exact<T_> f = exact_of<T_, EPL>(row, bias, sigmoid, E, max);
-    const double c = e >= 0 ? f(e) : -INFINITY;
+    const long long c = e >= 0 ? key_of(f(e)) : kNoKey;
     int rank = 0;
-#pragma unroll 1
+#pragma unroll 4
     for (int j = 0; j < n; ++j) {
-        const double v = __shfl_sync(kAll, c, j);
+        const long long v = __shfl_sync(kAll, c, j);
         rank += v > c || (v == c && j < lane);
     }
     return rank;
