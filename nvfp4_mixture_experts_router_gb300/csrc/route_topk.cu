@@ -19,13 +19,13 @@
 // scores, are computed in FP32 with a bound of their error, and the border lies
 // lower by twice that; where two values that decide are closer than their bounds,
 // each lane computes its own again in FP64 (about one token in 700 with 256
-// experts, standard normal logits and a bias).
+// experts, standard normal logits and a bias: 2 of 17 us, as such a token ends last).
 //
 // Bound by instructions: about 750 a token with a bias, groups and 256 experts,
 // 5 times what the logits' bytes take.  Measured on GB300, 16384 tokens, FP32: 256
-// experts, top-8, sigmoid, bias, 4 of 8 groups 18 us; without groups 13, softmax
-// without a bias 10.6; 64 experts, top-6 7.8; 1024 with a bias 53; top-32 of 256 47
-// (in rounds).  Backward 7.0 (2.6 TB/s: latency of ids, their logits and the row's
+// experts, top-8, sigmoid, bias, 4 of 8 groups 17 us (29 for 32768 tokens); without
+// groups 13, softmax without a bias 10.6 and with one 19 (its FP64 sums); 64 experts,
+// top-6 8.1; 1024 with a bias 53; top-32 of 256 46 (in rounds).  Backward 7.0 (2.6 TB/s: latency of ids, their logits and the row's
 // stores, in one wave and a half).  One token: 2.8 and 2.7.
 #include <float.h>
 #include <limits.h>
