@@ -48,8 +48,9 @@ extern "C" {
  * if computed in 64 bits: where FP32 cannot tell two apart, they are computed
  * in FP64.  An expert whose logit or bias is -infinity or NaN is not chosen (a
  * logit's also has the score 0) and does not count for its group; a logit of
- * +infinity counts as the largest FP32 number (a bias of it is ahead of all).  Slots beyond the experts that
- * can be chosen get id -1 and weight 0: dropped routes of the calls below.
+ * +infinity counts as the largest FP32 number (a bias of it is ahead of all).
+ * Slots beyond the experts that can be chosen get id -1 and weight 0: dropped
+ * routes of the calls below.
  * Renormalized weights do not underflow together: they come from l, relative to
  * the largest chosen.
  * Backward, dlogits [T][E] of the logits' type from dw [T][K], with the same

@@ -88,7 +88,7 @@ Rows rows2d(PyObject* o, const char* name) {
     if (t.dim() != 2) wrong_value(std::string(name) + " must be [T, H]");
     const int64_t T = t.size(0), H = t.size(1);
     if (T > INT32_MAX || H > INT32_MAX) wrong_value(std::string(name) + " is too large");
-    if (H > 1 && t.stride(1) != 1) wrong_value(std::string(name) + " must have contiguous rows");
+    if (T > 0 && H > 1 && t.stride(1) != 1) wrong_value(std::string(name) + " must have contiguous rows");
     // the stride of a single row, and of none, says nothing
     return Rows{t.data_ptr(), (int)T, (int)H, dtype_of(t, name), T > 1 ? t.stride(0) : H, t.scalar_type()};
 }

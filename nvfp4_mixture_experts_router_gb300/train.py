@@ -17,7 +17,7 @@ and its optimizer:
     opt = train.AdamW(parameters, lr=1e-3, state_bits=8)
     opt.step(norm=train.grad_norm(parameters), max_norm=1.0)
 
-examples/moe_block.py trains one.
+examples/moe_block.py trains one such block, examples/moe_stack.py a stack of them.
 """
 from __future__ import annotations
 

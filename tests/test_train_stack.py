@@ -132,3 +132,21 @@ def test_a_step_in_a_graph():
         graph.replay()
         step(b, ob)
     assert all(torch.equal(u, v) for u, v in zip(a, b))
+
+
+@pytest.mark.parametrize("T", [0, 1, 5])
+def test_gradients_of_plain_sums(T):
+    """A sum's gradient is one broadcast number: without tokens its strides are 0 still."""
+    H = 40
+    x, r = (torch.randn(T, H, device="cuda", requires_grad=True) for _ in range(2))
+    gamma = torch.randn(H, device="cuda", requires_grad=True)
+    beta = torch.zeros(H, device="cuda", requires_grad=True)
+    y, h = train.rms_norm(x, gamma, r)
+    (y.sum() + h.sum()).backward()
+    train.layer_norm(x, gamma, beta).sum().backward()
+    logits = torch.randn(T, 6, device="cuda", requires_grad=True)
+    train.route(logits, 2)[1].sum().backward()
+    for t in (x, r, gamma, beta, logits):
+        assert t.grad.shape == t.shape and bool(t.grad.isfinite().all())
+    # beta's gradient is T, whatever x is
+    assert torch.equal(beta.grad, torch.full_like(beta, float(T)))
