@@ -25,7 +25,7 @@
 // 5 times what the logits' bytes take.  Measured on GB300, 16384 tokens, FP32: 256
 // experts, top-8, sigmoid, bias, 4 of 8 groups 17 us (29 for 32768 tokens); without
 // groups 13, softmax without a bias 10.6 and with one 19 (its FP64 sums); 64 experts,
-// top-6 8.1; 1024 with a bias 53; top-32 of 256 46 (in rounds).  Backward 7.0 (2.6 TB/s: latency of ids, their logits and the row's
+// top-6 8.1; 1024 with a bias 48; top-32 of 256 46 (in rounds).  Backward 7.0 (2.6 TB/s: latency of ids, their logits and the row's
 // stores, in one wave and a half).  One token: 2.8 and 2.7.
 #include <float.h>
 #include <limits.h>
@@ -366,9 +366,14 @@ __device__ __forceinline__ int rounds_choice(float (&c)[EPL], int K) {
 
 // ---- forward ------------------------------------------------------------------------
 
+// Tokens of a block of the forward kernel.  (16384 tokens of 1024 experts with a bias
+// 48 us with four and 53 with eight, of 512 with groups 25.9 and 23.9.)
+template <int EPL>
+constexpr int kForwardWarps = EPL == 32 ? 4 : kRouteWarps;
+
 template <typename T_, int EPL>
-__global__ void __launch_bounds__(32 * kRouteWarps, EPL == 32 ? 2 : EPL == 16 ? 3 : 4) route_topk_kernel(const RouteArgs a) {
-    __shared__ uint2 s_near[kRouteWarps][33];   // key and expert; then the keys by rank
+__global__ void __launch_bounds__(32 * kForwardWarps<EPL>, EPL == 16 ? 3 : 4) route_topk_kernel(const RouteArgs a) {
+    __shared__ uint2 s_near[kForwardWarps<EPL>][33];   // key and expert; then the keys by rank
     extern __shared__ double s_exact[];         // [warps][E], with a bias or sums of two
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.E, K = a.K, e0 = lane * EPL;
@@ -621,8 +626,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_backward_kernel(c
 }
 
 // Tokens of a block: as many blocks as SMs first.
-int route_warps(int T) {
-    int w = kRouteWarps;
+int route_warps(int T, int most = kRouteWarps) {
+    int w = most;
     while (w > 1 && T <= 152 * (w / 2)) w /= 2;
     return w;
 }
@@ -646,7 +651,7 @@ cudaError_t forward_epl(const LaunchCtx& c, RouteArgs a) {
     a.span = -1;
     for (int n = 0; n < 6; ++n)
         if (a.size == EPL << n) a.span = n;
-    const int warps = route_warps(a.T);
+    const int warps = route_warps(a.T, kForwardWarps<EPL>);
     const bool scratch = a.bias || a.rule.topk_groups < a.rule.groups;
     constexpr int kBias = EPL < 4 ? EPL : 4;
     a.wide_bias = a.E % kBias == 0 && row_at(a.bias) % (kBias * 4) == 0;
