@@ -555,54 +555,39 @@ struct RouteGradArgs {
 template <typename T_>
 __device__ __forceinline__ void put(T_* p, float v) { *p = (T_)v; }
 
-// Lane k has slot k:
+// Slot k:
 //   softmax, renormalized   w (u - sum w u)                u = scale dw
 //   softmax                 p_e (u_e - sum_k p_k u_k)      over all experts
 //   sigmoid, renormalized   w (1 - s) (u - sum w u)
 //   sigmoid                 u s (1 - s)
 // The row is written as if no expert were chosen, and then the chosen ones, by
-// the same warp.  Bound by the row's bytes.
+// the same warp.
+
+// A softmax that is not renormalized: a warp a token, slot k in lane k.
 template <typename T_, int EPL>
-__global__ void __launch_bounds__(32 * kRouteWarps) route_topk_backward_kernel(const RouteGradArgs a) {
+__global__ void __launch_bounds__(32 * kRouteWarps) route_softmax_backward_kernel(const RouteGradArgs a) {
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.E, K = a.K, e0 = lane * EPL;
     const int t = blockIdx.x * (blockDim.x >> 5) + warp;
     if (t >= a.T) return;
     const T_* row = static_cast<const T_*>(a.logits) + (int64_t)t * a.stride;
     T_* out = static_cast<T_*>(a.out) + (int64_t)t * a.out_stride;
-    const bool sigmoid = a.rule.score == MOE_SCORE_SIGMOID, full = !sigmoid && !a.rule.renormalize;
     int e = lane < K ? a.ids[(int64_t)t * K + lane] : -1;
     const float dw = lane < K ? a.dw[(int64_t)t * K + lane] : 0.0f;
     if (e < 0 || e >= E) e = -1;
     const float u = e >= 0 ? dw * a.rule.scale : 0.0f;
     const float my_l = e >= 0 ? load_logit(row + e) : -INFINITY;
-    float d = 0.0f, base = 0.0f;
     float l[EPL];
-    Softmax soft{0.0f, 0.0f};
-    if (full) {
-        load_row<T_, EPL>(row, E, a.wide, l);
-        as_logits<EPL>(l);
-        soft = softmax_of<EPL>(l);
-        base = -warp_sum(e >= 0 ? soft.of(my_l) * u : 0.0f);
-        d = u;
-    } else if (a.rule.renormalize) {
-        float m = warp_max(my_l);
-        if (!(m > -INFINITY)) m = 0.0f;
-        float w = sigmoid ? expf(fminf(my_l, 0.0f) - fminf(m, 0.0f)) / (1.0f + expf(-fabsf(my_l))) : expf(my_l - m);
-        const float sum = warp_sum(e >= 0 ? w : 0.0f);
-        w = e >= 0 ? w / sum : 0.0f;
-        d = w * (u - warp_sum(w * u));
-        if (sigmoid) d *= 1.0f / (1.0f + expf(my_l));
-    } else {
-        const float x = expf(-fabsf(my_l));
-        d = u * (x / ((1.0f + x) * (1.0f + x)));
-    }
+    load_row<T_, EPL>(row, E, a.wide, l);
+    as_logits<EPL>(l);
+    const Softmax soft = softmax_of<EPL>(l);
+    const float base = -warp_sum(e >= 0 ? soft.of(my_l) * u : 0.0f);
     // slots of one expert add up
     float sum = 0.0f;
     for (int k = 0; k < K; ++k) {
         const int e2 = __shfl_sync(kAll, e, k);
-        const float d2 = __shfl_sync(kAll, d, k);
-        if (e2 == e) sum += d2;
+        const float u2 = __shfl_sync(kAll, u, k);
+        if (e2 == e) sum += u2;
     }
     __syncwarp();       // dlogits may be the logits: every lane has read them
     constexpr int kMost = 16 / sizeof(T_), VEC = EPL < kMost ? EPL : kMost;
@@ -611,17 +596,78 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_backward_kernel(c
         for (int i = 0; i < EPL; i += VEC) {
             float v[VEC];
 #pragma unroll
-            for (int k = 0; k < VEC; ++k) v[k] = full ? soft.of(l[i + k]) * base : 0.0f;
+            for (int k = 0; k < VEC; ++k) v[k] = soft.of(l[i + k]) * base;
             if (e0 + i < E)
                 *reinterpret_cast<typename RowVec<T_, VEC>::Raw*>(out + e0 + i) = RowVec<T_, VEC>::pack(v);
         }
     } else {
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
-            if (e0 + i < E) put(out + e0 + i, full ? soft.of(l[i]) * base : 0.0f);
+            if (e0 + i < E) put(out + e0 + i, soft.of(l[i]) * base);
     }
     __syncwarp();
-    if (e >= 0) put(out + e, full ? soft.of(my_l) * (sum + base) : sum);
+    if (e >= 0) put(out + e, soft.of(my_l) * (sum + base));
+    pdl_launch_dependents();
+}
+
+// The others need the chosen logits alone: LANES lanes a token, so that a warp's loads
+// are of all its lanes and a token takes a share of its instructions (16384 tokens of
+// 256 experts, top-8: 5.2 us against 7.0 with a warp each; of 1024: 13.0 and 25.3).
+template <typename T_, int LANES>
+__global__ void __launch_bounds__(32 * kRouteWarps) route_slots_backward_kernel(const RouteGradArgs a) {
+    pdl_wait();
+    constexpr int N = 32 / LANES, VEC = 16 / sizeof(T_);
+    const int lane = threadIdx.x & 31, j = lane % LANES, E = a.E, K = a.K;
+    const int first = (blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) * N, t = first + lane / LANES;
+    if (first >= a.T) return;
+    const bool has = j < K && t < a.T;
+    const int64_t slot = (int64_t)t * K + j;
+    int e = has ? a.ids[slot] : -1;
+    const float dw = has ? a.dw[slot] : 0.0f;
+    if (e < 0 || e >= E) e = -1;
+    const float u = e >= 0 ? dw * a.rule.scale : 0.0f;
+    const float l = e >= 0 ? load_logit(static_cast<const T_*>(a.logits) + t * a.stride + e) : -INFINITY;
+    auto sum_of = [](float v) {
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+        return v;
+    };
+    const bool sigmoid = a.rule.score == MOE_SCORE_SIGMOID;
+    float d;
+    if (a.rule.renormalize) {
+        float m = l;
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+        if (!(m > -INFINITY)) m = 0.0f;
+        float w = sigmoid ? expf(fminf(l, 0.0f) - fminf(m, 0.0f)) / (1.0f + expf(-fabsf(l))) : expf(l - m);
+        const float all = sum_of(e >= 0 ? w : 0.0f);
+        w = e >= 0 ? w / all : 0.0f;
+        d = w * (u - sum_of(w * u));
+        if (sigmoid) d *= 1.0f / (1.0f + expf(l));
+    } else {
+        const float x = expf(-fabsf(l));
+        d = u * (x / ((1.0f + x) * (1.0f + x)));
+    }
+    float sum = 0.0f;       // slots of one expert add up
+#pragma unroll
+    for (int k = 0; k < LANES; ++k) {
+        const int e2 = __shfl_sync(kAll, e, k, LANES);
+        const float d2 = __shfl_sync(kAll, d, k, LANES);
+        if (e2 == e) sum += d2;
+    }
+    __syncwarp();           // dlogits may be the logits: every lane has read them
+    T_* out = static_cast<T_*>(a.out) + first * a.out_stride;
+#pragma unroll
+    for (int r = 0; r < N; ++r, out += a.out_stride) {
+        if (first + r >= a.T) break;
+        if (a.wide) {
+            for (int c = lane; c < E / VEC; c += 32) reinterpret_cast<uint4*>(out)[c] = make_uint4(0, 0, 0, 0);
+        } else {
+            for (int c = lane; c < E; c += 32) put(out + c, 0.0f);
+        }
+    }
+    __syncwarp();
+    if (e >= 0) put(static_cast<T_*>(a.out) + t * a.out_stride + e, sum);
     pdl_launch_dependents();
 }
 
@@ -669,11 +715,20 @@ cudaError_t backward_epl(const LaunchCtx& c, RouteGradArgs a) {
     a.wide = a.E % VEC == 0 &&
              (row_at(a.logits, a.stride, sizeof(T_)) | row_at(a.out, a.out_stride, sizeof(T_))) % (VEC * sizeof(T_)) == 0;
     const int warps = route_warps(a.T);
-    return c.launch(route_topk_backward_kernel<T_, EPL>, dim3((unsigned)((a.T + warps - 1) / warps)), dim3(32 * warps),
+    return c.launch(route_softmax_backward_kernel<T_, EPL>, dim3((unsigned)((a.T + warps - 1) / warps)), dim3(32 * warps),
                     0, a);
+}
+template <typename T_, int LANES>
+cudaError_t backward_slots(const LaunchCtx& c, RouteGradArgs a) {
+    constexpr int VEC = 16 / sizeof(T_), N = 32 / LANES;
+    a.wide = a.E % VEC == 0 && row_at(a.out, a.out_stride, sizeof(T_)) % 16 == 0;
+    const int warps = route_warps((a.T + N - 1) / N), tokens = warps * N;
+    return c.launch(route_slots_backward_kernel<T_, LANES>, dim3((unsigned)((a.T + tokens - 1) / tokens)), dim3(32 * warps), 0, a);
 }
 template <typename T_>
 cudaError_t backward_of(const LaunchCtx& c, const RouteGradArgs& a) {
+    if (a.rule.score == MOE_SCORE_SIGMOID || a.rule.renormalize)
+        return a.K <= 8 ? backward_slots<T_, 8>(c, a) : a.K <= 16 ? backward_slots<T_, 16>(c, a) : backward_slots<T_, 32>(c, a);
     MOE_ROUTE_EPL(a.E, backward_epl, T_, c, a);
 }
 
