@@ -25,8 +25,9 @@
 // 5 times what the logits' bytes take.  Measured on GB300, 16384 tokens, FP32: 256
 // experts, top-8, sigmoid, bias, 4 of 8 groups 17 us (29 for 32768 tokens); without
 // groups 13, softmax without a bias 10.6 and with one 19 (its FP64 sums); 64 experts,
-// top-6 8.1; 1024 with a bias 48; top-32 of 256 46 (in rounds).  Backward 7.0 (2.6 TB/s: latency of ids, their logits and the row's
-// stores, in one wave and a half).  One token: 2.8 and 2.7.
+// top-6 8.1; 1024 with a bias 48; top-32 of 256 46 (in rounds).  Backward
+// 4.8 (3.8 TB/s: a launch's 2.6 and the latency of ids, their logits and the rows'
+// stores), softmax not renormalized 8.4.  One token: 2.8 and 2.6.
 #include <float.h>
 #include <limits.h>
 #include <math.h>
