@@ -311,7 +311,9 @@ MOE_API moe_status moe_nvfp4_grad_clip(int n, const void* const* grads, void* co
  * so that a captured graph can be replayed with other ones; the corrections
  * are FP32 then.
  * Squares and v are FP32; v below 2^-126 counts as zero, and so does a rate lr /
- * (1 - beta1^t) below 1e-30.
+ * (1 - beta1^t) below 1e-30.  eps counts as 2^-126 times the rate at least, and an
+ * element whose denominator passes 2^126 times the rate takes no step.  The rate is
+ * 2^126 at most (one of lr_step that is not makes the parameters NaN).
  * 0 <= n <= 65536, 0 <= numel < 2^40; pointers aligned to their element; a
  * tensor of no elements may have NULL pointers.  lr and weight_decay >= 0,
  * 0 <= beta < 1, eps >= 2^-126, max_norm and clip_eps >= 0, all finite; step >= 1

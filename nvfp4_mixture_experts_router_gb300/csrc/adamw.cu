@@ -72,38 +72,30 @@ struct AdamTable {
     AdamEntry e[MAX];
 };
 
-// The formula's numbers as they stand; a rate below 1e-30 counts as zero.
-struct AdamRate {
-    float keep, rate, root, eps;
-};
-__shared__ AdamRate s_rate;     // for update_any, whose calls it keeps short of registers
-__device__ __forceinline__ AdamRate rate_of(const AdamNumbers& k, const float* lr_step) {
-    AdamRate r{k.keep, k.rate, k.root, k.eps};
-    if (lr_step) {
-        const float lr = lr_step[0], t = lr_step[1];
-        r.keep = 1.0f - lr * k.wd;
-        r.rate = lr / -expm1f(t * k.log_b1);
-        r.root = 1.0f / sqrtf(-expm1f(t * k.log_b2));
-    }
-    if (!(r.rate >= 1e-30f)) r.rate = 0.0f;
-    return r;
-}
-
 // What a thread needs of the numbers: with the rate -lr / (1 - b1^t) divided into
-// the denominator's terms, p' = p keep + m / (sqrt(v) root + eps).
+// the denominator's terms, p' = p keep + m / (sqrt(v) root + eps).  The denominator
+// stays from 2^-126 on, below which its reciprocal would be infinite (and 0 times that
+// NaN): eps counts as 2^-126 times the rate at least.
 struct AdamStep {
     float clip, b1, one_b1, minus_b2, minus_one_b2, keep, root, eps;
 };
-__device__ __forceinline__ AdamStep step_of(const AdamNumbers& k, const float* norm, const AdamRate& r) {
-    AdamStep s{1.0f, k.b1, k.one_b1, -k.b2, -k.one_b2, r.keep, 0.0f, -FLT_MAX};
+__device__ __forceinline__ AdamStep step_of(const AdamNumbers& k, const float* norm, const float* lr_step) {
+    AdamStep s{1.0f, k.b1, k.one_b1, -k.b2, -k.one_b2, k.keep, k.root, k.eps};
+    float rate = k.rate;
     if (norm) {
         const float q = k.max_norm / (norm[0] + k.clip_eps);
         s.clip = q > 1.0f ? 1.0f : q;       // NaN stays NaN
     }
-    if (r.rate > 0.0f) {        // (else a denominator whose reciprocal is zero)
-        s.root = -r.root / r.rate;
-        s.eps = -r.eps / r.rate;
+    if (lr_step) {
+        const float lr = lr_step[0], t = lr_step[1];
+        s.keep = 1.0f - lr * k.wd;
+        rate = lr / -expm1f(t * k.log_b1);
+        s.root = 1.0f / sqrtf(-expm1f(t * k.log_b2));
     }
+    // (a rate that is zero, or too small to divide by: a denominator whose reciprocal is zero)
+    s.root = rate >= 1e-30f ? -s.root / rate : -1.0f;
+    s.eps = rate >= 1e-30f ? fminf(-s.eps / rate, -0x1p-126f) : -FLT_MAX;
+    if (rate > 0x1p126f) s.eps = NAN;       // (of lr_step; the host's is refused)
     return s;
 }
 
@@ -157,12 +149,10 @@ __device__ __forceinline__ float2 update(const AdamStep& s, float2 grad, float2&
     p = fma2(m, make_float2(rcp_fast(over.x), rcp_fast(over.y)), mul2(p, both(s.keep)));
     return root;
 }
-// The root and the parameter where a v is not finite: by the formula as it stands,
-// so that a rate of zero moves nothing.
-__device__ __noinline__ float2 update_any(float m, float v, float p) {
-    const AdamRate r = s_rate;
+// The root and the parameter where a v is not finite.
+__device__ __noinline__ float2 update_any(float root_factor, float eps, float keep, float m, float v, float p) {
     const float root = sqrtf(v);
-    return make_float2(root, p * r.keep - r.rate * (m / fmaf(root, r.root, r.eps)));
+    return make_float2(root, p * keep + m / fmaf(root, root_factor, eps));
 }
 
 // Eight elements of type T_: packed in vectors, or the first `count` of them.
@@ -342,8 +332,8 @@ struct AdamGroup {
             most = 0.0f;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const float2 x = update_any(fm[k].x, -fv[k].x, fp[k].x);
-                const float2 y = update_any(fm[k].y, -fv[k].y, fp[k].y);
+                const float2 x = update_any(s.root, s.eps, s.keep, fm[k].x, -fv[k].x, fp[k].x);
+                const float2 y = update_any(s.root, s.eps, s.keep, fm[k].y, -fv[k].y, fp[k].y);
                 root[k] = make_float2(x.x, y.x);
                 fp[k] = make_float2(x.y, y.y);
                 most = max3(most, root[k]);
@@ -438,10 +428,7 @@ __global__ void __launch_bounds__(kAdamThreads, kResident / 152) adamw_kernel(co
         }
     }
     pdl_wait();
-    const AdamRate r = rate_of(t.k, t.lr_step);
-    if (threadIdx.x == 0) s_rate = r;
-    __syncthreads();
-    const AdamStep s = step_of(t.k, t.norm, r);
+    const AdamStep s = step_of(t.k, t.norm, t.lr_step);
     for (int c = blockIdx.x; c < t.chunks; c += gridDim.x) {
         while (c >= t.e[i].last_chunk) ++i;
         const AdamEntry& e = t.e[i];

@@ -474,6 +474,7 @@ moe_status moe_nvfp4_adamw(int n, const moe_adamw_tensor* tensors, moe_adamw_rul
     if (!number(rule.weight_decay) || !number(rule.eps) || !((float)rule.eps >= 1.17549435e-38f)) return MOE_ERR_INVALID_ARG;
     if (!(rule.beta1 >= 0.0 && rule.beta1 < 1.0) || !(rule.beta2 >= 0.0 && rule.beta2 < 1.0)) return MOE_ERR_INVALID_ARG;
     if (!lr_step && (!number(rule.lr) || rule.step < 1)) return MOE_ERR_INVALID_ARG;
+    if (!lr_step && !(rule.lr <= 0x1p126 * (1.0 - pow(rule.beta1, (double)rule.step)))) return MOE_ERR_INVALID_ARG;
     if (norm && (!number(rule.max_norm) || !number(rule.clip_eps))) return MOE_ERR_INVALID_ARG;
     if (!aligned(norm, 4) || !aligned(lr_step, 4)) return MOE_ERR_INVALID_ARG;
     bool any = false;
