@@ -393,7 +393,8 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) rms_rows_kernel(const RmsArgs
     const Rstd r = rstd_of(row.sum, inv_h, a.eps);
     if (a.rstd && live && j == 0) a.rstd[t] = r.hi + r.lo;
     float inv = 1.0f;
-    if (by_row) inv = put_scale(MOE_SCALE_ROW, a.scales, (int)t, row.most * r.hi, live && j == 0);
+    // (a product that is NaN, of a row with NaN or an infinity: no y but zeros and NaN)
+    if (by_row) inv = put_scale(MOE_SCALE_ROW, a.scales, (int)t, fmaxf(row.most * r.hi, 0.0f), live && j == 0);
     if constexpr (STAGED)
         if (W == 1) __syncthreads();        // (else join_row's: every thread has taken its vectors)
 #pragma unroll

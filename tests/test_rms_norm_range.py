@@ -1,0 +1,44 @@
+"""RMS norm of rows that are not finite, or whose squares are not, at widths of each kernel."""
+import math
+
+import pytest
+import torch
+
+from nvfp4_mixture_experts_router_gb300 import api, build
+from test_rms_norm import BF, F32, MODES, check_forward, forward, inputs
+
+pytestmark = pytest.mark.gpu
+# in registers (8, 16 and 32 columns a thread by the number of rows), through shared memory, long
+WIDTHS = [40, 1000, 1001, 2050, 7167, 7168, 9000, 16384, 9001, 16400]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    build.build()
+    api.lib()
+
+
+@pytest.mark.parametrize("T", [7, 400])
+@pytest.mark.parametrize("H", WIDTHS)
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("mode", ["row", "block", "mx"])
+def test_scales_of_rows_that_are_not_finite(T, H, dt, mode):
+    """NaN does not enter the scales: a row of NaN has those of a row of zeros, and so has one with an infinity, whose
+    rstd is zero."""
+    x, _, gamma = inputs(T, H, dt)
+    x[1, 5] = math.nan
+    x[2] = math.nan
+    x[3, H - 1] = math.inf
+    x[4, 7], x[4, 9] = -math.inf, math.inf
+    _, y, q, s, rstd = forward(x, None, gamma, mode)
+    s, q = s.view(T, -1), q.float()
+    assert bool((s[1:5] == (0 if mode == "mx" else 1)).all())
+    assert bool(torch.isnan(q[1:3]).all()) and bool(torch.isnan(y[1:3]).all()) and not rstd[3:5].any()
+    for row, at in ((3, [H - 1]), (4, [7, 9])):
+        rest = torch.ones(H, dtype=torch.bool, device="cuda")
+        rest[at] = False
+        assert bool(torch.isnan(q[row, at]).all()) and bool(torch.isnan(y[row, at]).all())
+        assert not q[row, rest].any() and not y[row, rest].any()
+    keep = [0] + list(range(5, T))
+    pick = lambda v: v[keep].contiguous()       # noqa: E731
+    check_forward(pick(x), None, gamma, (None, pick(y), pick(q), pick(s), pick(rstd)), mode)
