@@ -227,7 +227,9 @@ MOE_API moe_status moe_nvfp4_layer_norm_backward(int T, int H, int dtype,
  *   rstd   [T] FP32
  * A NaN of y is a NaN of q, and does not enter the scales.  gamma FP32 [H];
  * eps >= 0, finite.  The squares and their sum are FP32: a row whose sum of
- * squares passes 3.4e38 has rstd 0.  1 <= H <= 65536, 0 <= T <= 2^22; pointers
+ * squares passes 3.4e38 has rstd 0, and y 0 where h is finite; with eps = 0 one
+ * whose sum is zero has an infinite rstd, and y is not finite.  By row h * gamma
+ * has to be within FP32, unless rstd is 0.  1 <= H <= 65536, 0 <= T <= 2^22; pointers
  * aligned to their element.
  * Backward, from the forward's h and rstd, with hhat = h * rstd and g = dy * gamma:
  *   dx     = dh + rstd * (g - hhat * sum_h (g * hhat) / H)     (dh NULL: 0)

@@ -42,3 +42,36 @@ def test_scales_of_rows_that_are_not_finite(T, H, dt, mode):
     keep = [0] + list(range(5, T))
     pick = lambda v: v[keep].contiguous()       # noqa: E731
     check_forward(pick(x), None, gamma, (None, pick(y), pick(q), pick(s), pick(rstd)), mode)
+
+
+@pytest.mark.parametrize("T", [7, 400])
+@pytest.mark.parametrize("H", WIDTHS)
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("mode", MODES)
+def test_finite_rows_whose_squares_are_not(T, H, dt, mode):
+    """rstd is 0, and y with it, however large gamma is beside h (an infinity, of BF16 here, times 0 is NaN)."""
+    x, _, gamma = inputs(T, H, dt)
+    gamma = gamma.abs() + 0.5
+    x[1] = 3e38
+    x[2, ::2] *= 2e38
+    x[3, 3] = -3e38
+    _, y, q, s, rstd = forward(x, None, gamma, mode)
+    want = torch.where(x[1:4].isfinite(), 0.0, math.nan)
+    same = lambda v: bool(((v == want) | (v.isnan() & want.isnan())).all())     # noqa: E731
+    assert bool(x[1].isfinite().all()) and bool(x[3].isfinite().all())
+    assert not rstd[1:4].any() and same(y[1:4].float())
+    if mode is not None:
+        assert same(q.float()[1:4]) and bool((s.view(T, -1)[1:4] == (0 if mode == "mx" else 1)).all())
+    keep = [0] + list(range(4, T))
+    pick = lambda v: None if v is None else v[keep].contiguous()       # noqa: E731
+    check_forward(pick(x), None, gamma, (None, pick(y), pick(q), pick(s), pick(rstd)), mode)
+
+
+@pytest.mark.parametrize("H", WIDTHS)
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("mode", [None, "block", "mx"])
+def test_large_gamma(H, dt, mode):
+    """h gamma passes FP32, y does not."""
+    x, _, gamma = inputs(9, H, dt, scale=1e17)
+    gamma = gamma * 1e22
+    check_forward(x, None, gamma, forward(x, None, gamma, mode), mode)
