@@ -456,9 +456,10 @@ __device__ __forceinline__ float block_join(float v, float* s) {
 // A block a row, which is walked once for each of its results.
 template <typename T_, int VEC>
 __global__ void __launch_bounds__(kRmsThreads)
-    rms_norm_kernel(const RmsArgs a) {
+    rms_norm_kernel(const RmsArgs a, float2 inv_h, bool wide_gamma) {
     using RV = RowVec<T_, VEC>;
     using Raw = typename RV::Raw;
+    constexpr int P = (VEC + 1) / 2, U = VEC > 2 ? 1 : 4 / VEC;     // vectors in flight
     __shared__ float s[32];
     extern __shared__ float s_block[];      // the largest |y| of each 32 elements
     pdl_wait();
@@ -483,6 +484,14 @@ __global__ void __launch_bounds__(kRmsThreads)
             RV::unpack(sum, v);
         }
     };
+    // a vector of h, and of gamma
+    auto pairs = [&](int c, float2 (&v)[P], float2 (&ga)[P]) {
+        float u[VEC];
+        row(c, true, u);
+#pragma unroll
+        for (int k = 0; k < P; ++k) v[k] = make_float2(u[2 * k], VEC > 1 ? u[(2 * k + 1) % VEC] : 0.0f);
+        load_vector<VEC>(a.gamma, c, wide_gamma, ga);
+    };
     float sq = 0.0f;
     for (int c = threadIdx.x; c < n; c += kRmsThreads) {
         float v[VEC];
@@ -490,64 +499,58 @@ __global__ void __launch_bounds__(kRmsThreads)
 #pragma unroll
         for (int k = 0; k < VEC; ++k) sq = fmaf(v[k], v[k], sq);
     }
-    const float rstd = 1.0f / sqrtf(block_join<false>(sq, s) / (float)a.H + a.eps);
-    if (threadIdx.x == 0 && a.rstd) a.rstd[t] = rstd;
-    float scale = 1.0f;
-    if (a.q) {
-        float amax = 0.0f;
-        if (a.scale_mode != MOE_SCALE_ROW) {
-            for (int b = threadIdx.x; b < n32; b += kRmsThreads) s_block[b] = 0.0f;
-            __syncthreads();
-        }
+    const Rstd r = rstd_of(make_float2(block_join<false>(sq, s), 0.0f), inv_h, a.eps);
+    if (threadIdx.x == 0 && a.rstd) a.rstd[t] = r.hi + r.lo;
+    float inv = 1.0f;
+    if (a.q && a.scale_mode == MOE_SCALE_ROW) {
+        float most = 0.0f;
+#pragma unroll U
         for (int c = threadIdx.x; c < n; c += kRmsThreads) {
-            float v[VEC], m = 0.0f;
-            row(c, true, v);
+            float2 v[P], ga[P];
+            pairs(c, v, ga);
 #pragma unroll
-            for (int k = 0; k < VEC; ++k) m = fmaxf(m, fabsf(v[k] * rstd * a.gamma[c * VEC + k]));
-            amax = fmaxf(amax, m);
+            for (int k = 0; k < P; ++k) v[k] = mul2(v[k], ga[k]);
+            most = max_of<VEC>(most, v);
+        }
+        most = block_join<true>(most, s);
+        inv = put_scale(MOE_SCALE_ROW, a.scales, (int)t, fmaxf(most * r.hi, 0.0f), threadIdx.x == 0);
+    } else if (a.q) {
+        for (int b = threadIdx.x; b < n32; b += kRmsThreads) s_block[b] = 0.0f;
+        __syncthreads();
+#pragma unroll U
+        for (int c = threadIdx.x; c < n; c += kRmsThreads) {
+            float2 v[P], ga[P];
+            pairs(c, v, ga);
+#pragma unroll
+            for (int k = 0; k < P; ++k) v[k] = scaled(v[k], ga[k], r);
             // of non-negative floats the order of the bits is that of the values
-            if (a.scale_mode != MOE_SCALE_ROW)
-                atomicMax(reinterpret_cast<int*>(s_block) + c * VEC / 32, __float_as_int(m));
+            atomicMax(reinterpret_cast<int*>(s_block) + c * VEC / 32, __float_as_int(max_of<VEC>(0.0f, v)));
         }
-        if (a.scale_mode == MOE_SCALE_ROW) {
-            scale = linear_scale(block_join<true>(amax, s));
-            if (threadIdx.x == 0) static_cast<float*>(a.scales)[t] = scale;
+        __syncthreads();
+        if (a.scale_mode == MOE_SCALE_MX) {
+            for (int b = threadIdx.x; b < n32; b += kRmsThreads)
+                s_block[b] = put_scale(MOE_SCALE_MX, static_cast<uint8_t*>(a.scales) + t * n32, b, s_block[b], true);
         } else {
-            __syncthreads();
-            if (a.scale_mode == MOE_SCALE_MX) {
-                for (int b = threadIdx.x; b < n32; b += kRmsThreads) {
-                    const int e = mx_block_exp(s_block[b]);
-                    static_cast<uint8_t*>(a.scales)[t * n32 + b] = (uint8_t)(e + 127);
-                    s_block[b] = pow2f(-e);
-                }
-            } else {
-                const int n128 = (a.H + 127) / 128;
-                for (int b = threadIdx.x; b < n128; b += kRmsThreads) {
-                    float m = 0.0f;
-                    for (int k = 4 * b; k < 4 * b + 4 && k < n32; ++k) m = fmaxf(m, s_block[k]);
-                    const float sc = linear_scale(m);
-                    static_cast<float*>(a.scales)[t * n128 + b] = sc;
-                    for (int k = 4 * b; k < 4 * b + 4 && k < n32; ++k) s_block[k] = 1.0f / sc;
-                }
+            const int n128 = (a.H + 127) / 128;
+            for (int b = threadIdx.x; b < n128; b += kRmsThreads) {
+                float m = 0.0f;
+                for (int k = 4 * b; k < 4 * b + 4 && k < n32; ++k) m = fmaxf(m, s_block[k]);
+                m = put_scale(MOE_SCALE_BLOCK128, static_cast<float*>(a.scales) + t * n128, b, m, true);
+                for (int k = 4 * b; k < 4 * b + 4 && k < n32; ++k) s_block[k] = m;
             }
-            __syncthreads();
         }
+        __syncthreads();
     }
     Raw* y = a.y ? static_cast<Raw*>(a.y) + t * (a.y_stride / VEC) : nullptr;
     uint8_t* q = a.q ? static_cast<uint8_t*>(a.q) + t * a.H : nullptr;
-    const float inv = 1.0f / scale;
+#pragma unroll U
     for (int c = threadIdx.x; c < n; c += kRmsThreads) {
-        float v[VEC];
-        row(c, true, v);
+        float2 v[P], ga[P];
+        pairs(c, v, ga);
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) v[k] = v[k] * rstd * a.gamma[c * VEC + k];
-        if (y) y[c] = RV::pack(v);
-        if (q) {
-            float2 u[(VEC + 1) / 2];
-#pragma unroll
-            for (int k = 0; k < (VEC + 1) / 2; ++k) u[k] = make_float2(v[2 * k], VEC > 1 ? v[(2 * k + 1) % VEC] : 0.0f);
-            store_codes<VEC>(q + c * VEC, u, a.scale_mode == MOE_SCALE_ROW ? inv : s_block[c * VEC / 32]);
-        }
+        for (int k = 0; k < P; ++k) v[k] = scaled(v[k], ga[k], r);
+        if (y) y[c] = pack_pairs<T_, VEC>(v);
+        if (q) store_codes<VEC>(q + c * VEC, v, a.scale_mode == MOE_SCALE_ROW ? inv : s_block[c * VEC / 32]);
     }
     pdl_launch_dependents();
 }
@@ -961,17 +964,21 @@ __global__ void __launch_bounds__(16384 / C, C / 16) rms_dx_rows_kernel(const Rm
     pdl_launch_dependents();
 }
 
+// 1 / H in two FP32 numbers.
+float2 inverse_pair(int H) {
+    const double inv = 1.0 / H;
+    return make_float2((float)inv, (float)(inv - (double)(float)inv));
+}
+
 // C columns a thread.
 template <typename T_, int VEC, int C, bool Q, bool STAGED, int THREADS, int BLOCKS>
 cudaError_t forward_rows(const LaunchCtx& c, const RmsArgs& a) {
     const int W = (a.H + 32 * C - 1) / (32 * C), G = W >= 8 ? 1 : 8 / W;
-    const double inv = 1.0 / a.H;
-    const float2 inv_h = make_float2((float)inv, (float)(inv - (double)(float)inv));
     const bool wide_gamma = row_at(a.gamma) % 16 == 0;
     const size_t slots = STAGED ? G * (2 * RowSlot::bytes(a.H * sizeof(T_)) + RowSlot::bytes(a.H)) : 0;
     auto kernel = a.residual ? rms_rows_kernel<T_, VEC, C, true, Q, STAGED, THREADS, BLOCKS>
                              : rms_rows_kernel<T_, VEC, C, false, Q, STAGED, THREADS, BLOCKS>;
-    return c.launch(kernel, dim3((unsigned)((a.T + G - 1) / G)), dim3(32 * W, G), slots, a, W, inv_h, wide_gamma);
+    return c.launch(kernel, dim3((unsigned)((a.T + G - 1) / G)), dim3(32 * W, G), slots, a, W, inverse_pair(a.H), wide_gamma);
 }
 
 template <typename T_, int VEC, bool Q>
@@ -1006,7 +1013,8 @@ cudaError_t forward_any(const LaunchCtx& c, const RmsArgs& a) {
     if constexpr (VEC * sizeof(T_) == 16)
         if (a.H <= kWideColumns) return a.q ? forward_wide<T_, VEC, true>(c, a) : forward_wide<T_, VEC, false>(c, a);
     const size_t smem = a.q && a.scale_mode != MOE_SCALE_ROW ? (size_t)(a.H + 31) / 32 * 4 : 0;
-    return c.launch(rms_norm_kernel<T_, VEC>, dim3((unsigned)a.T), dim3(kRmsThreads), smem, a);
+    return c.launch(rms_norm_kernel<T_, VEC>, dim3((unsigned)a.T), dim3(kRmsThreads), smem, a, inverse_pair(a.H),
+                    row_at(a.gamma) % 16 == 0);
 }
 // The shape of the backward kernels of short rows: warps a row, rows a block, and
 // blocks on an SM (512 threads, or twice as many for the slots of BF16 rows).

@@ -101,8 +101,8 @@ struct RowVec<float, 1> {
     }
 };
 
-// VEC consecutive parameters, of vector c of the row.  `wide`: 16-byte loads
-// (an aligned array; vectors of four or eight).
+// VEC consecutive parameters, of vector c of the row.  `wide`: loads of up
+// to 16 bytes (an array aligned to that; vectors of two or more).
 template <int VEC>
 __device__ __forceinline__ void load_vector(const float* p, int c, bool wide, float2 (&v)[(VEC + 1) / 2]) {
     p += (size_t)c * VEC;
@@ -114,6 +114,11 @@ __device__ __forceinline__ void load_vector(const float* p, int c, bool wide, fl
                 v[2 * k] = make_float2(w.x, w.y);
                 v[2 * k + 1] = make_float2(w.z, w.w);
             }
+            return;
+        }
+    } else if constexpr (VEC == 2) {
+        if (wide) {
+            v[0] = *reinterpret_cast<const float2*>(p);
             return;
         }
     }

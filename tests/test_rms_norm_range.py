@@ -75,3 +75,36 @@ def test_large_gamma(H, dt, mode):
     x, _, gamma = inputs(9, H, dt, scale=1e17)
     gamma = gamma * 1e22
     check_forward(x, None, gamma, forward(x, None, gamma, mode), mode)
+
+
+def whole(T, H, dt, seed=0):
+    """Rows of whole numbers, whose squares add up exactly in any order."""
+    g = torch.Generator("cuda").manual_seed(seed + H)
+    x = torch.randint(-3, 4, (T, H), generator=g, device="cuda")
+    return x.to(dt), 0.1 + torch.rand(H, generator=g, device="cuda")
+
+
+@pytest.mark.parametrize("T", [5, 330])
+@pytest.mark.parametrize("H", WIDTHS)
+def test_one_rounding(T, H):
+    """Where the sum of squares is exact, y is rounded once: half a unit, and the 2^-30 of rstd and h rstd in two numbers."""
+    x, gamma = whole(T, H, F32)
+    _, y, _, _, rstd = forward(x, None, gamma)
+    r = (x.double().square().mean(1) + 1e-6).rsqrt()
+    want = x.double() * r[:, None] * gamma.double()
+    assert bool(((y.double() - want).abs() <= (2.0 ** -24 + 2.0 ** -30) * want.abs()).all())
+    assert bool(((rstd.double() - r).abs() <= (2.0 ** -24 + 2.0 ** -30) * r).all())
+
+
+@pytest.mark.parametrize("T", [5, 330])
+@pytest.mark.parametrize("H", [8200, 12288, 16384])
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("mode", MODES)
+def test_a_row_at_an_odd_offset(T, H, dt, mode):
+    """The kernel of rows off their vectors gives the same y, codes and scales where the sum is exact."""
+    x, gamma = whole(T, H, dt)
+    buf = torch.zeros(T, H + 5, dtype=dt, device="cuda")
+    buf[:, 3:3 + H] = x
+    a, b = forward(x, None, gamma, mode), forward(buf[:, 3:3 + H], None, gamma, mode)
+    for u, v in zip(a[1:], b[1:]):
+        assert u is None or torch.equal(u.view(torch.uint8), v.view(torch.uint8))
