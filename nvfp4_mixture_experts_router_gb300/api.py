@@ -611,7 +611,8 @@ def moe_nvfp4_adamw(tensors: AdamWList, rule: AdamWRule, step: int, norm: Option
     """One AdamW step, number ``step`` from 1, in place.  norm (device float32 [1]):
     the gradients count times min(1, max_norm / (norm + clip_eps)).  lr_step
     (device float32 [2]): the learning rate and the step's number in place of the
-    rule's and ``step``."""
+    rule's and ``step``.  Autograd is not told that the parameters change
+    (train.AdamW does)."""
     _check("moe_nvfp4_adamw", (_native or native()).adamw(tensors.n, tensors.index, tensors._tensors, rule, step, norm,
                                                           lr_step, stream))
 

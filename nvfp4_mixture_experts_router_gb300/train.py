@@ -362,6 +362,7 @@ class AdamW:
                 kept[1].set_grads(grads)
             api.moe_nvfp4_adamw(kept[1], rule, steps + 1, norm, self.lr_step)
             kept[1].grads = []       # the gradients may go
+            torch.autograd.graph.increment_version(kept[1].params)      # graphs that saved them raise
             for i in used:
                 self.steps[i] += 1
 
