@@ -410,6 +410,7 @@ def clip_grad_norm_(parameters: Union[torch.Tensor, Iterable[torch.Tensor]], max
     gl = api.GradList(packed)
     api.moe_nvfp4_grad_norm(gl, norm, ws)
     api.moe_nvfp4_grad_clip(gl, norm, max_norm, eps)
+    torch.autograd.graph.increment_version(grads)       # graphs that saved them raise
     for i in strided:
         grads[i].detach().copy_(packed[i])
     return norm

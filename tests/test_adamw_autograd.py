@@ -24,3 +24,16 @@ def test_a_step_between_forward_and_backward():
     with pytest.raises(RuntimeError, match="inplace"):
         y.backward()
     train.rms_norm(x, gamma).sum().backward()
+
+
+@pytest.mark.parametrize("strided", [False, True])
+def test_clipping_between_forward_and_backward(strided):
+    """A graph that saved a gradient is refused once that is scaled."""
+    p = torch.nn.Parameter(torch.ones(6, 4, device="cuda"))
+    p.grad = torch.full((4, 6), 3.0, device="cuda").t() if strided else torch.full((6, 4), 3.0, device="cuda")
+    w = torch.ones(6, 4, device="cuda", requires_grad=True)
+    loss = (w * p.grad).sum()
+    train.clip_grad_norm_([p], 0.5)
+    assert abs(float(p.grad.norm()) - 0.5) < 1e-5
+    with pytest.raises(RuntimeError, match="inplace"):
+        loss.backward()
