@@ -292,7 +292,11 @@ class AdamW:
 
     state_bits 8 keeps both moments in E4M3 with a scale for each 256 elements, of
     tensors from min_8bit elements on; master keeps FP32 values of BF16
-    parameters, from which these are rounded.  Parameters without a gradient are
+    parameters, from which these are rounded.  Parameters that changed since their
+    last step (a checkpoint loaded, weights swapped in) are read again, as autograd's
+    count of changes or their address tells; after a change that neither tells of
+    (through .data, or before the replay of a captured step) call read_parameters.
+    Parameters without a gradient are
     left as they are, and count their steps by themselves (a launch for each number).
     capturable: the learning rate and the number of the step are read on the device
     (self.lr_step), so that a step captured into a CUDA graph counts on when it is
@@ -320,6 +324,7 @@ class AdamW:
             if master and p.dtype == torch.bfloat16:
                 s["master"] = p.detach().float().reshape(-1)
             self.state.append(s)
+        self._seen = [self._mark(p) for p in self.params]      # of the values that the masters are of
         self.lr_step = None
         if capturable and self.params:
             self.lr_step = torch.tensor([lr, 0.0], dtype=torch.float32, device=self.params[0].device)
@@ -332,6 +337,23 @@ class AdamW:
                 p.grad = None
             else:
                 p.grad.zero_()
+
+    @staticmethod
+    def _mark(p: torch.Tensor) -> Tuple[int, int]:
+        return p._version, p.data_ptr()
+
+    @torch.no_grad()
+    def _read(self, i: int) -> None:
+        """Parameter i into its master: where the two agree, the master's digits stay."""
+        w, p = self.state[i].get("master"), self.params[i].detach().reshape(-1)
+        if w is not None:
+            w.copy_(torch.where(w.to(p.dtype) == p, w, p.float()))
+        self._seen[i] = self._mark(self.params[i])
+
+    def read_parameters(self) -> None:
+        """Takes the parameters as they are for the next step, however they were changed."""
+        for i in range(len(self.params)):
+            self._read(i)
 
     @torch.no_grad()
     def step(self, norm: Optional[torch.Tensor] = None, max_norm: float = 1.0, clip_eps: float = 1e-6) -> None:
@@ -349,6 +371,8 @@ class AdamW:
                 self._device_lr = self.lr
             self.lr_step[1].add_(1.0)
         rule = api.AdamWRule(self.lr, *self.betas, self.eps, self.weight_decay, max_norm, clip_eps)
+        for i in [i for used in groups.values() for i in used if self._mark(self.params[i]) != self._seen[i]]:
+            self._read(i)
         for steps, used in groups.items():
             at = [self.params[i].data_ptr() for i in used]
             grads = [self.params[i].grad.contiguous() for i in used]
@@ -365,6 +389,7 @@ class AdamW:
             torch.autograd.graph.increment_version(kept[1].params)      # graphs that saved them raise
             for i in used:
                 self.steps[i] += 1
+                self._seen[i] = self._mark(self.params[i])
 
     def state_dict(self) -> dict:
         steps = list(self.steps)

@@ -59,3 +59,77 @@ def test_a_graph_from_before_the_step_is_refused(launches):
         loss.backward()
     other.backward()        # (of a parameter without a step)
     assert bool((params[2].grad == 8.0).all())
+
+
+def tiny_steps(dtype=BF):
+    """An optimizer whose masters hold what BF16 parameters cannot: three steps of 2^-12 from 2."""
+    params = parameters(2, dtype)
+    opt = train.AdamW(params, lr=2.0 ** -12)
+    give(params, 0, 1)
+    for _ in range(3):
+        opt.step()
+    assert bool((params[0] == 2.0).all()) and bool((opt.state[0]["master"] == 2.0 - 3 * 2.0 ** -12).all())
+    return params, opt
+
+
+@pytest.mark.parametrize("how", ["copy", "load", "data", "address", "address of the same"])
+def test_parameters_that_change_between_steps(launches, how):
+    """A checkpoint loaded after the optimizer was made, weights swapped in: the step is from them."""
+    params, opt = tiny_steps()
+    new = torch.tensor([7.0, 2.0, 8.0, 2.0], dtype=BF)
+    if how == "copy":
+        with torch.no_grad():
+            params[0].copy_(new)
+    elif how == "load":
+        torch.nn.ParameterList(params).load_state_dict({"0": new, "1": params[1].detach().clone()})
+    elif how == "data":             # nothing tells of this one
+        params[0].data.copy_(new)
+        opt.read_parameters()
+    elif how == "address":
+        params[0].data = new.clone()
+    else:
+        new = params[0].detach().clone()
+        params[0].data = new.clone()
+    opt.step()
+    d = 2.0 ** -12
+    want = torch.where(new == 2.0, 2.0 - 4 * d, new.float() - d)     # where nothing changed, the master's digits stay
+    assert torch.equal(opt.state[0]["master"], want) and torch.equal(params[0], want.to(BF))
+    assert bool((opt.state[1]["master"] == 3.0 - 4 * d).all())
+
+
+def test_weights_swapped_in_and_out_keep_the_masters(launches):
+    params, opt = tiny_steps()
+    with torch.no_grad():
+        mine = params[0].clone()
+        params[0].fill_(5.0)
+        params[0].copy_(mine)
+    opt.step()
+    assert bool((opt.state[0]["master"] == 2.0 - 4 * 2.0 ** -12).all())
+
+
+@pytest.mark.parametrize("model_first", [False, True])
+def test_a_checkpoint_of_both_keeps_the_masters(launches, model_first):
+    params, opt = tiny_steps()
+    mine = parameters(2, BF)
+    again = train.AdamW(mine, lr=2.0 ** -12)
+    for part in (model_first, not model_first):
+        if part:
+            with torch.no_grad():
+                for p, q in zip(mine, params):
+                    p.copy_(q)
+        else:
+            again.load_state_dict(opt.state_dict())
+    give(mine, 0, 1)
+    again.step()
+    assert bool((again.state[0]["master"] == 2.0 - 4 * 2.0 ** -12).all())
+
+
+def test_float_parameters_have_no_masters(launches):
+    params = parameters(1)
+    opt = train.AdamW(params, lr=0.5)
+    with torch.no_grad():
+        params[0].fill_(9.0)
+    give(params, 0)
+    opt.step()
+    opt.read_parameters()
+    assert bool((params[0] == 8.5).all())
