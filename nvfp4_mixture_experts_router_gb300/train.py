@@ -324,7 +324,9 @@ class AdamW:
             if master and p.dtype == torch.bfloat16:
                 s["master"] = p.detach().float().reshape(-1)
             self.state.append(s)
-        self._seen = [self._mark(p) for p in self.params]      # of the values that the masters are of
+        # autograd's count of changes, and the address, of the values that the masters are of
+        self._seen = [(p._version, p.data_ptr()) for p in self.params]
+        self._masters = any("master" in s for s in self.state)
         self.lr_step = None
         if capturable and self.params:
             self.lr_step = torch.tensor([lr, 0.0], dtype=torch.float32, device=self.params[0].device)
@@ -338,17 +340,14 @@ class AdamW:
             else:
                 p.grad.zero_()
 
-    @staticmethod
-    def _mark(p: torch.Tensor) -> Tuple[int, int]:
-        return p._version, p.data_ptr()
-
     @torch.no_grad()
     def _read(self, i: int) -> None:
         """Parameter i into its master: where the two agree, the master's digits stay."""
-        w, p = self.state[i].get("master"), self.params[i].detach().reshape(-1)
+        p, w = self.params[i], self.state[i].get("master")
         if w is not None:
-            w.copy_(torch.where(w.to(p.dtype) == p, w, p.float()))
-        self._seen[i] = self._mark(self.params[i])
+            q = p.detach().reshape(-1)
+            w.copy_(torch.where(w.to(q.dtype) == q, w, q.float()))
+        self._seen[i] = p._version, p.data_ptr()
 
     def read_parameters(self) -> None:
         """Takes the parameters as they are for the next step, however they were changed."""
@@ -371,25 +370,30 @@ class AdamW:
                 self._device_lr = self.lr
             self.lr_step[1].add_(1.0)
         rule = api.AdamWRule(self.lr, *self.betas, self.eps, self.weight_decay, max_norm, clip_eps)
-        for i in [i for used in groups.values() for i in used if self._mark(self.params[i]) != self._seen[i]]:
-            self._read(i)
         for steps, used in groups.items():
-            at = [self.params[i].data_ptr() for i in used]
-            grads = [self.params[i].grad.contiguous() for i in used]
+            params = [self.params[i] for i in used]
+            at = [p.data_ptr() for p in params]
+            grads = [p.grad.contiguous() for p in params]
+            if self._masters:
+                for i, p, a in zip(used, params, at):
+                    if self._seen[i] != (p._version, a):
+                        self._read(i)
             kept = self._lists.get(tuple(used))
             if kept is None or kept[0] != at:
                 get = lambda name: [self.state[i].get(name) for i in used]      # noqa: E731, B023
-                kept = at, api.AdamWList([self.params[i] for i in used], grads, get("exp_avg"), get("exp_avg_sq"),
+                kept = at, api.AdamWList(params, grads, get("exp_avg"), get("exp_avg_sq"),
                                          get("exp_avg_scale"), get("exp_avg_sq_scale"), get("master"))
                 self._lists[tuple(used)] = kept
             else:
                 kept[1].set_grads(grads)
             api.moe_nvfp4_adamw(kept[1], rule, steps + 1, norm, self.lr_step)
             kept[1].grads = []       # the gradients may go
-            torch.autograd.graph.increment_version(kept[1].params)      # graphs that saved them raise
+            torch.autograd.graph.increment_version(params)      # graphs that saved them raise
             for i in used:
                 self.steps[i] += 1
-                self._seen[i] = self._mark(self.params[i])
+            if self._masters:
+                for i, p, a in zip(used, params, at):
+                    self._seen[i] = p._version, a
 
     def state_dict(self) -> dict:
         steps = list(self.steps)
