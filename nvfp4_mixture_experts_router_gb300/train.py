@@ -286,6 +286,9 @@ def grad_norm(parameters: Union[torch.Tensor, Iterable[torch.Tensor]]) -> torch.
     return norm
 
 
+_LISTS_KEPT = 8     # of AdamW; those of one step where they are more
+
+
 class AdamW:
     """AdamW over parameters (BF16 or FP32, contiguous, on one device), a launch for
     each kind of states and 384 tensors (moe_nvfp4_adamw).
@@ -331,7 +334,7 @@ class AdamW:
         if capturable and self.params:
             self.lr_step = torch.tensor([lr, 0.0], dtype=torch.float32, device=self.params[0].device)
             self._device_lr = lr
-        self._lists = {}        # parameters of a launch -> their addresses and the list
+        self._lists = {}        # parameters of a launch -> their addresses and the list, the last used behind
 
     def zero_grad(self, set_to_none: bool = True) -> None:
         for p in self.params:
@@ -378,14 +381,14 @@ class AdamW:
                 for i, p, a in zip(used, params, at):
                     if self._seen[i] != (p._version, a):
                         self._read(i)
-            kept = self._lists.get(tuple(used))
+            kept = self._lists.pop(tuple(used), None)
             if kept is None or kept[0] != at:
                 get = lambda name: [self.state[i].get(name) for i in used]      # noqa: E731, B023
                 kept = at, api.AdamWList(params, grads, get("exp_avg"), get("exp_avg_sq"),
                                          get("exp_avg_scale"), get("exp_avg_sq_scale"), get("master"))
-                self._lists[tuple(used)] = kept
             else:
                 kept[1].set_grads(grads)
+            self._lists[tuple(used)] = kept
             api.moe_nvfp4_adamw(kept[1], rule, steps + 1, norm, self.lr_step)
             kept[1].grads = []       # the gradients may go
             torch.autograd.graph.increment_version(params)      # graphs that saved them raise
@@ -394,6 +397,8 @@ class AdamW:
             if self._masters:
                 for i, p, a in zip(used, params, at):
                     self._seen[i] = p._version, a
+        while len(self._lists) > max(_LISTS_KEPT, len(groups)):     # sets of parameters that may not come back
+            del self._lists[next(iter(self._lists))]
 
     def state_dict(self) -> dict:
         steps = list(self.steps)

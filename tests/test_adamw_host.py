@@ -133,3 +133,33 @@ def test_float_parameters_have_no_masters(launches):
     opt.step()
     opt.read_parameters()
     assert bool((params[0] == 8.5).all())
+
+
+def test_sets_of_parameters_that_change_from_step_to_step(launches):
+    """Experts without tokens have no gradient: the lists kept are bounded, and sets that alternate are built once."""
+    params = parameters(9)
+    opt = train.AdamW(params, lr=2.0 ** -10)
+    for k in range(1, 200):
+        give(params, *[i for i in range(9) if k >> i & 1])
+        opt.step()
+    assert len(opt._lists) <= 16
+    for i, (p, s) in enumerate(zip(params, opt.steps)):
+        assert s == sum(k >> i & 1 for k in range(1, 200)) and bool((p == 2.0 + i - s * 2.0 ** -10).all())
+    params = parameters(4)
+    opt = train.AdamW(params)
+    List.built = 0
+    for k in range(20):
+        give(params, *((0, 1) if k % 2 else (2, 3)))
+        opt.step()
+    assert List.built == 2
+    # more numbers of steps at once than lists are kept for: a launch each, in every step
+    params = parameters(40)
+    opt = train.AdamW(params)
+    for k in range(40):
+        give(params, *range(k + 1))
+        opt.step()
+    launches.clear()
+    List.built = 0
+    for _ in range(3):
+        opt.step()
+    assert len(launches) == 120 and List.built <= 40 and len(opt._lists) <= 40
