@@ -366,7 +366,7 @@ class AdamW:
             if p.grad is not None:
                 groups.setdefault(self.steps[i], []).append(i)
         if self.lr_step is not None and groups:
-            if len(groups) > 1:
+            if any(self.steps) and [bool(n) for n in self.steps] != [p.grad is not None for p in self.params]:
                 raise ValueError("a capturable AdamW's parameters have a gradient in every step, or never")
             if self._device_lr != self.lr and not torch.cuda.is_current_stream_capturing():
                 self.lr_step[0].fill_(self.lr)

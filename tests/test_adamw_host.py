@@ -163,3 +163,28 @@ def test_sets_of_parameters_that_change_from_step_to_step(launches):
     for _ in range(3):
         opt.step()
     assert len(launches) == 120 and List.built <= 40 and len(opt._lists) <= 40
+
+
+def test_capturable_parameters_are_the_same_in_every_step(launches):
+    """They share the number of the step: another set would take the wrong one."""
+    params = parameters(2)
+    opt = train.AdamW(params, capturable=True)
+    opt.step()                  # without any gradient
+    give(params, 0)
+    opt.step()
+    for which in ((1,), (0, 1)):
+        give(params, *which)
+        with pytest.raises(ValueError, match="never"):
+            opt.step()
+    give(params, 0)
+    opt.step()
+    assert launches == [(1, 1, 1.0), (1, 2, 2.0)] and opt.state_dict()["steps"] == [2, 0]
+    # and of a saved state's
+    again = train.AdamW(parameters(2), capturable=True)
+    again.load_state_dict(opt.state_dict())
+    give(again.params, 1)
+    with pytest.raises(ValueError, match="never"):
+        again.step()
+    give(again.params, 0)
+    again.step()
+    assert launches[-1] == (1, 3, 3.0)
