@@ -371,7 +371,6 @@ class AdamW:
             if self._device_lr != self.lr and not torch.cuda.is_current_stream_capturing():
                 self.lr_step[0].fill_(self.lr)
                 self._device_lr = self.lr
-            self.lr_step[1].add_(1.0)
         rule = api.AdamWRule(self.lr, *self.betas, self.eps, self.weight_decay, max_norm, clip_eps)
         for steps, used in groups.items():
             params = [self.params[i] for i in used]
@@ -389,7 +388,14 @@ class AdamW:
             else:
                 kept[1].set_grads(grads)
             self._lists[tuple(used)] = kept
-            api.moe_nvfp4_adamw(kept[1], rule, steps + 1, norm, self.lr_step)
+            if self.lr_step is not None:
+                self.lr_step[1].add_(1.0)
+            try:
+                api.moe_nvfp4_adamw(kept[1], rule, steps + 1, norm, self.lr_step)
+            except Exception:
+                if self.lr_step is not None:
+                    self.lr_step[1].sub_(1.0)       # a refused step does not count
+                raise
             kept[1].grads = []       # the gradients may go
             torch.autograd.graph.increment_version(params)      # graphs that saved them raise
             for i in used:

@@ -25,7 +25,7 @@ def launches(monkeypatch):
     seen = []
 
     def launch(tensors, rule, step, norm=None, lr_step=None, stream=None):
-        if rule.lr < 0:
+        if rule.eps < 0:
             raise api.MoEError("moe_nvfp4_adamw", api.MOE_ERR_INVALID_ARG)
         seen.append((len(tensors.params), step, None if lr_step is None else float(lr_step[1])))
         for p, w in zip(tensors.params, tensors.master):
@@ -35,6 +35,7 @@ def launches(monkeypatch):
     List.built = 0
     monkeypatch.setattr(api, "AdamWList", List)
     monkeypatch.setattr(api, "moe_nvfp4_adamw", launch)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
     return seen
 
 
@@ -188,3 +189,17 @@ def test_capturable_parameters_are_the_same_in_every_step(launches):
     give(again.params, 0)
     again.step()
     assert launches[-1] == (1, 3, 3.0)
+
+
+def test_a_refused_step_does_not_count(launches):
+    params = parameters(1)
+    opt = train.AdamW(params, lr=0.5, capturable=True)
+    give(params, 0)
+    opt.step()
+    opt.eps = -1.0
+    with pytest.raises(api.MoEError):
+        opt.step()
+    assert opt.steps == [1] and opt.state_dict()["steps"] == [1]
+    opt.eps = 1e-8
+    opt.step()
+    assert launches == [(1, 1, 1.0), (1, 2, 2.0)] and bool((params[0] == 1.0).all())
