@@ -303,8 +303,9 @@ class AdamW:
     left as they are, and count their steps by themselves (a launch for each number).
     capturable: the learning rate and the number of the step are read on the device
     (self.lr_step), so that a step captured into a CUDA graph counts on when it is
-    replayed; run one step before the capture.  All parameters then have a gradient
-    in every step, or never."""
+    replayed; run one step before the capture.  A replay takes its rate from
+    lr_step[0]; a step outside of one writes self.lr there where that changed.  All
+    parameters then have a gradient in every step, or never."""
 
     def __init__(self, params: Iterable[torch.Tensor], lr: float = 1e-3, betas: Tuple[float, float] = (0.9, 0.999),
                  eps: float = 1e-8, weight_decay: float = 0.01, state_bits: int = 32, master: bool = True,
@@ -368,7 +369,9 @@ class AdamW:
         if self.lr_step is not None and groups:
             if any(self.steps) and [bool(n) for n in self.steps] != [p.grad is not None for p in self.params]:
                 raise ValueError("a capturable AdamW's parameters have a gradient in every step, or never")
-            if self._device_lr != self.lr and not torch.cuda.is_current_stream_capturing():
+            if self._device_lr != self.lr:
+                if torch.cuda.is_current_stream_capturing():
+                    raise ValueError("the learning rate changed since the last step: run one before the capture")
                 self.lr_step[0].fill_(self.lr)
                 self._device_lr = self.lr
         rule = api.AdamWRule(self.lr, *self.betas, self.eps, self.weight_decay, max_norm, clip_eps)

@@ -203,3 +203,21 @@ def test_a_refused_step_does_not_count(launches):
     opt.eps = 1e-8
     opt.step()
     assert launches == [(1, 1, 1.0), (1, 2, 2.0)] and bool((params[0] == 1.0).all())
+
+
+def test_a_learning_rate_that_a_capture_would_not_see(launches, monkeypatch):
+    """It is on the device since the last step outside a capture."""
+    params = parameters(1)
+    opt = train.AdamW(params, lr=0.5, capturable=True)
+    give(params, 0)
+    opt.step()
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    opt.step()
+    opt.lr = 0.25
+    with pytest.raises(ValueError, match="learning rate"):
+        opt.step()
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    opt.step()
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    opt.step()
+    assert opt.lr_step.tolist() == [0.25, 4.0] and len(launches) == 4
