@@ -100,11 +100,14 @@ __device__ __forceinline__ void as_logits(float (&l)[EPL]) {
 // off by (3 + 1.18 |l|) 2^-23 of itself at most (the product with log2 e and ex2's
 // documented 2^-22), which s (1 - s) takes to 0.75 + 0.27 units of 2^-23, and the
 // sum and the reciprocal (documented 2^-23) add 2.5.  Of softmax, p = e^x / S with
-// x = l - max, it is below (32 + 1.2 |x|) 2^-23 p: e^x as above, S a sum of at most
-// 32 + 5 roundings and of terms each that exact (their mean |x| is at most log E);
-// that is largest at p's largest.
+// x = l - max, it is below (kSoftmaxErr + 1.18 |x|) 2^-23 p: 3 + 1.18 |x| of e^x as
+// above; of S half a unit for each of its EPL + 4 roundings and 3 + 1.18 log E by its
+// terms (their mean |x| is log E at most); 2.5 of the reciprocal and the product.  In
+// all 15.1, 16.4, 18.2, 21.1, 25.9 and 34.7 for EPL = 1 to 32.  That is largest at x = 0.
 constexpr float kUnit = 1.1920929e-07f;     // 2^-23
 constexpr float kSigmoidErr = 4.0f * kUnit;
+template <int EPL>
+constexpr float kSoftmaxErr = (17.0f + 0.65f * EPL) * kUnit;    // times the largest p
 constexpr float kTiny = 7.5e-37f;           // 2^-120, where the approximations flush to zero
 __device__ __forceinline__ float exp_fast(float x) {
     float r;
@@ -399,7 +402,7 @@ __global__ void __launch_bounds__(32 * kForwardWarps<EPL>, EPL == 16 ? 3 : 4) ro
         for (int i = 0; i < EPL; ++i) c[i] = l[i] > -INFINITY && b[i] > -INFINITY ? c[i] + b[i] : -INFINITY;
     }
     // a bound of the error of c: its score's, and c's own rounding
-    const float most = sigmoid ? kSigmoidErr : 32.0f * kUnit * soft.inv;
+    const float most = sigmoid ? kSigmoidErr : kSoftmaxErr<EPL> * soft.inv;
     auto err_of = [&](float v) { return most + kTiny + 2.0f * kUnit * fabsf(v); };
 
     if (grouped) {

@@ -442,3 +442,17 @@ def test_with_the_layer_s_forward():
     y = layer.forward_routed(x, ids, w)
     assert torch.equal(layer.view("topk_ids", torch.int32, T * K).view(T, K), ids)
     assert bool(((y.float() - own.float()).abs() <= 2.1 * 2.0 ** -8 * own.float().abs() + 1e-5 * own.float().abs().max()).all())
+
+
+@pytest.mark.parametrize("E", [1024, 1000, 513])
+@pytest.mark.parametrize("dt", [F32, BF])
+def test_softmax_with_a_bias_that_nearly_ties(E, dt):
+    """Flat rows, whose sums take the most roundings, and a bias that puts neighbours a few units of the scores' error
+    apart, in either order."""
+    g = torch.Generator("cuda").manual_seed(E)
+    logits = (1e-2 * torch.randn(400, E, generator=g, device="cuda")).to(dt)
+    p = torch.softmax(logits[0].double(), 0)
+    units = torch.randint(-45, 46, (E,), generator=g, device="cuda").double()
+    bias = (0.5 - p + units * 2.0 ** -23 / E).float()
+    check(logits, bias, api.RouteRule(), 8)
+    check(logits[:1].expand(300, E).contiguous(), bias, api.RouteRule(renormalize=False), 32)
