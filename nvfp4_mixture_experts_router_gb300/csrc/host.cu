@@ -48,7 +48,7 @@ moe_status device_state(int* sms, int* device) {
                    setup_router_gemm_kernel() != cudaSuccess ||
                    setup_expert_linear_kernels(dev, d.sms) != cudaSuccess ||
                    setup_layer_norm_kernels() != cudaSuccess || setup_sort_kernels() != cudaSuccess ||
-                   setup_route_topk_kernels() != cudaSuccess || setup_rms_norm_kernels() != cudaSuccess) {
+                   setup_rms_norm_kernels() != cudaSuccess) {
             d.status = MOE_ERR_CUDA;
         } else {
             d.status = MOE_OK;

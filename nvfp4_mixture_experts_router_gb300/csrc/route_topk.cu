@@ -705,7 +705,8 @@ cudaError_t forward_epl(const LaunchCtx& c, RouteArgs a) {
     const bool scratch = a.bias || a.rule.topk_groups < a.rule.groups;
     constexpr int kBias = EPL < 4 ? EPL : 4;
     a.wide_bias = a.E % kBias == 0 && row_at(a.bias) % (kBias * 4) == 0;
-    const size_t smem = scratch ? (size_t)warps * a.E * 8 : 0;
+    const size_t smem = scratch ? (size_t)warps * a.E * 8 : 0;     // 32 KB at most, which needs no leave
+    static_assert(kForwardWarps<EPL> * EPL * 32 * 8 <= 32 * 1024, "beside s_near within 48 KB");
     return c.launch(route_topk_kernel<T_, EPL>, dim3((unsigned)((a.T + warps - 1) / warps)), dim3(32 * warps), smem, a);
 }
 template <typename T_>
@@ -736,24 +737,7 @@ cudaError_t backward_of(const LaunchCtx& c, const RouteGradArgs& a) {
     MOE_ROUTE_EPL(a.E, backward_epl, T_, c, a);
 }
 
-template <typename T_>
-cudaError_t allow_forward() {
-    cudaError_t e = cudaSuccess;
-    auto allow = [&](auto kernel) {     // 8 warps of 1024 experts: 64 KB
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRouteWarps * 1024 * 8);
-    };
-    allow(route_topk_kernel<T_, 16>);
-    allow(route_topk_kernel<T_, 32>);
-    return e;
-}
-
 }  // namespace
-
-cudaError_t setup_route_topk_kernels() {
-    const cudaError_t e = allow_forward<float>();
-    return e != cudaSuccess ? e : allow_forward<__nv_bfloat16>();
-}
 
 cudaError_t launch_route_topk(const LaunchCtx& c, int T, int E, int K, int elem, const void* logits, int64_t stride,
                               const float* bias, const moe_route_rule& rule, int* ids, float* w) {

@@ -21,7 +21,6 @@ cudaError_t launch_combine_backward(const LaunchCtx& c, int T, int H, int K, int
                                     const int* rows_used, void* d_o, float* dw);
 
 // route_topk.cu
-cudaError_t setup_route_topk_kernels();
 cudaError_t launch_route_topk(const LaunchCtx& c, int T, int E, int K, int elem, const void* logits, int64_t stride,
                               const float* bias, const moe_route_rule& rule, int* ids, float* w);
 cudaError_t launch_route_topk_backward(const LaunchCtx& c, int T, int E, int K, int elem, const void* logits,
