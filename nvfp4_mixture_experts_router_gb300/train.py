@@ -329,7 +329,8 @@ class AdamW:
                 s["master"] = p.detach().float().reshape(-1)
             self.state.append(s)
         # autograd's count of changes, and the address, of the values that the masters are of
-        self._seen = [(p._version, p.data_ptr()) for p in self.params]
+        # (None: tensors of inference mode, whose changes are not counted)
+        self._seen = [None if p.is_inference() else (p._version, p.data_ptr()) for p in self.params]
         self._masters = any("master" in s for s in self.state)
         self.lr_step = None
         if capturable and self.params:
@@ -351,7 +352,8 @@ class AdamW:
         if w is not None:
             q = p.detach().reshape(-1)
             w.copy_(torch.where(w.to(q.dtype) == q, w, q.float()))
-        self._seen[i] = p._version, p.data_ptr()
+        if self._seen[i] is not None:
+            self._seen[i] = p._version, p.data_ptr()
 
     def read_parameters(self) -> None:
         """Takes the parameters as they are for the next step, however they were changed."""
@@ -381,7 +383,7 @@ class AdamW:
             grads = [p.grad.contiguous() for p in params]
             if self._masters:
                 for i, p, a in zip(used, params, at):
-                    if self._seen[i] != (p._version, a):
+                    if self._seen[i] is not None and self._seen[i] != (p._version, a):
                         self._read(i)
             kept = self._lists.pop(tuple(used), None)
             if kept is None or kept[0] != at:
@@ -405,7 +407,8 @@ class AdamW:
                 self.steps[i] += 1
             if self._masters:
                 for i, p, a in zip(used, params, at):
-                    self._seen[i] = p._version, a
+                    if self._seen[i] is not None:
+                        self._seen[i] = p._version, a
         while len(self._lists) > max(_LISTS_KEPT, len(groups)):     # sets of parameters that may not come back
             del self._lists[next(iter(self._lists))]
 

@@ -221,3 +221,17 @@ def test_a_learning_rate_that_a_capture_would_not_see(launches, monkeypatch):
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
     opt.step()
     assert opt.lr_step.tolist() == [0.25, 4.0] and len(launches) == 4
+
+
+def test_parameters_of_inference_mode(launches):
+    """Autograd does not count their changes: they have masters all the same."""
+    with torch.inference_mode():
+        params = parameters(2, BF)
+        opt = train.AdamW(params, lr=0.5)
+        give(params, 0, 1)
+        opt.step()
+        assert bool((params[0] == 1.5).all())
+        params[0].fill_(7.0)
+        opt.read_parameters()
+        opt.step()
+        assert bool((params[0] == 6.5).all()) and bool((params[1] == 2.0).all())
