@@ -108,3 +108,17 @@ def test_a_row_at_an_odd_offset(T, H, dt, mode):
     a, b = forward(x, None, gamma, mode), forward(buf[:, 3:3 + H], None, gamma, mode)
     for u, v in zip(a[1:], b[1:]):
         assert u is None or torch.equal(u.view(torch.uint8), v.view(torch.uint8))
+
+
+@pytest.mark.parametrize("T", [3, 200, 400])
+@pytest.mark.parametrize("H", [8, 33, 100, 500, 1000, 1001, 1032, 2050, 4100, 7168, 8200, 9001, 16384, 16400])
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_y_with_codes_and_without(T, H, dt):
+    """The same y: BF16 rows, and FP32 rows of whole 16-byte blocks."""
+    if dt == F32 and H % 4:
+        H += 4 - H % 4
+    x, res, gamma = inputs(T, H, dt)
+    plain = forward(x, res, gamma)
+    for mode in MODES[1:]:
+        got = forward(x, res, gamma, mode)
+        assert torch.equal(got[1], plain[1]) and torch.equal(got[0], plain[0]) and torch.equal(got[4], plain[4])
