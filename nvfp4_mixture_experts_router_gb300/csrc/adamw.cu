@@ -30,7 +30,7 @@ constexpr int kAdamMax = 384;           // tensors of a launch: 27.6 KB of its 3
 // Blocks: states in 32 bits, one for each chunk, so that the SMs sweep the buffers
 // in step (1207 us against 1428 with as many blocks as are resident, 302 million
 // BF16 with master values); in 8 bits the resident ones, as a block's start weighs
-// more beside the fewer bytes of a chunk (560 us against 628).
+// more beside the fewer bytes of a chunk (541 us against 597).
 constexpr int kResident = 152 * 3;
 constexpr int kStarts = 152 * 6;        // blocks whose first entry travels with the list
 constexpr int kChunkMost = 4096, kChunkLeast = 2048;    // elements

@@ -13,13 +13,13 @@
 // share of the rows for each costs up to a sixth), so rows are handed out as blocks
 // end, and several blocks an SM cover one another's reductions.  Columns of a
 // thread (times with residual and MX codes): 32 for many BF16 rows of more than 512
-// columns (16384 x 7168: 121 us against 158 with 16 and 275 with 8; 8191 x 2048: 21.8,
+// columns (16384 x 7168: 122 us against 158 with 16 and 275 with 8; 8191 x 2048: 21.5,
 // 21.6, 25.7, codes by row 15.7, 18.5, 22.6), 16 for more than 256 columns and for
 // FP32 (16383 x 512 BF16: 11.2 against 15.0 with 32 and 13.7 with 8; 8191 x 4096 FP32:
 // 65, 73, 67), 8 for short rows (16383 x 128: 6.6 against 8.5 with 16).  gamma is read
 // from L1 as it is needed: in registers beside the row it spilled (150 us against 131
 // at the same step).  Rows off 16-byte blocks in vectors of less than four elements
-// pass through shared memory (8191 x 7167 BF16, residual and MX codes: 164 against
+// pass through shared memory (8191 x 7167 BF16, residual and MX codes: 161 against
 // 333 by elements).  Rows of up to 16384 columns in whole vectors lie in one block of
 // up to 512 threads (32 columns of BF16) or 1024 (FP32, and few rows).
 //
@@ -31,12 +31,14 @@
 // Longer rows are walked two or three times, the re-reads served by the caches.
 //
 // Measured on GB300 (copy rate 6.8 TB/s): 16384 x 7168 BF16 with residual and MX
-// codes 121 us (6.8 TB/s), with y instead 135 (7.0), y of x alone 80 (5.9), codes
-// by row alone 101 (3.5: two looks at gamma and the row's maximum bound it); FP32
-// 217, 265, 133, 139.  Backward with dh, 8191 x 7168: BF16 80 us (5.9), FP32 141
-// (6.7).  8191 x 7167 BF16: 139 with residual and y (3.4), backward with dh 191
-// (2.5).  2000 x 16384 BF16: 42 with residual and y (6.3), 40 with MX codes, backward
-// with dh 83 (3.2).  1000 x 65536 BF16: 145, 173, 235.  One row of 7168: 3.5.
+// codes 122 us (6.8 TB/s), with y instead 135 (7.0), y of x alone 79 (5.9), codes
+// by row alone 102 (3.4: two looks at gamma and the row's maximum bound it); FP32
+// 216, 267, 133, 138.  Backward with dh, 8191 x 7168: BF16 80 us (5.9), FP32 141
+// (6.7); from 512 to 4096 columns 38 to 68 % of the copy rate (8191 x 1024 19 us,
+// 2000 x 4096 22, from HBM: a block has six or seven rows, and the blocks' sums are
+// written and read again).  8191 x 7167 BF16: 141 with residual and y (3.3), backward
+// with dh 191 (2.5).  2000 x 16384 BF16: 42 with residual and y (6.3), 41 with MX codes,
+// backward with dh 83 (3.2).  1000 x 65536 BF16: 117, 139, 235.  One row of 7168: 3.5.
 #include <math.h>
 
 #include "f32x2.cuh"

@@ -21,10 +21,12 @@
 // each lane computes its own again in FP64 (about one token in 700 with 256
 // experts, standard normal logits and a bias: 2 of 17 us, as such a token ends last).
 //
-// Bound by instructions: about 750 a token with a bias, groups and 256 experts,
-// 5 times what the logits' bytes take.  Measured on GB300, 16384 tokens, FP32: 256
+// Bound by a token's instructions and their latency, 6 times what the logits' bytes
+// take: 760 with a bias, groups and 256 experts, which would be 10 of 17 us if the
+// schedulers issued all the time; they do 47 % of it, as sorts and prefix sums are
+// chains of dependent shuffles.  Measured on GB300, 16384 tokens, FP32: 256
 // experts, top-8, sigmoid, bias, 4 of 8 groups 17 us (29 for 32768 tokens); without
-// groups 13, softmax without a bias 10.6 and with one 19 (its FP64 sums); 64 experts,
+// groups 13, softmax without a bias 10.4 and with one 18 (its FP64 sums); 64 experts,
 // top-6 8.1; 1024 with a bias 48; top-32 of 256 46 (in rounds).  Backward
 // 4.8 (3.8 TB/s: a launch's 2.6 and the latency of ids, their logits and the rows'
 // stores), softmax not renormalized 8.4.  One token: 2.8 and 2.6.
@@ -616,7 +618,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_softmax_backward_kerne
 
 // The others need the chosen logits alone: LANES lanes a token, so that a warp's loads
 // are of all its lanes and a token takes a share of its instructions (16384 tokens of
-// 256 experts, top-8: 5.2 us against 7.0 with a warp each; of 1024: 13.0 and 25.3).
+// 256 experts, top-8: 4.8 us against 7.0 with a warp each; of 1024: 13.0 and 25.3).
 template <typename T_, int LANES>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_slots_backward_kernel(const RouteGradArgs a) {
     pdl_wait();

@@ -160,8 +160,8 @@ class _RmsNorm(torch.autograd.Function):
 
 
 def rms_norm(x: torch.Tensor, gamma: torch.Tensor, residual: Optional[torch.Tensor] = None, eps: float = 1e-6):
-    """RMS norm of h = x + residual, [T, H] (BF16 or FP32), gamma [H] FP32.  Returns y
-    and h, or y alone without a residual (h is x then)."""
+    """RMS norm of h = x + residual, [T, H] (BF16 or FP32, both of one type), gamma [H]
+    FP32.  Returns y and h, or y alone without a residual (h is x then)."""
     return _RmsNorm.apply(x, residual, gamma, eps)
 
 
@@ -299,8 +299,10 @@ class AdamW:
     last step (a checkpoint loaded, weights swapped in) are read again, as autograd's
     count of changes or their address tells; after a change that neither tells of
     (through .data, or before the replay of a captured step) call read_parameters.
-    Parameters without a gradient are
-    left as they are, and count their steps by themselves (a launch for each number).
+    Parameters without a gradient are left as they are, and count their steps by
+    themselves (a launch for each number).
+    lr, betas, eps and weight_decay may be set between steps, by a schedule for one;
+    parameters that take other ones have an optimizer of their own.
     capturable: the learning rate and the number of the step are read on the device
     (self.lr_step), so that a step captured into a CUDA graph counts on when it is
     replayed; run one step before the capture.  A replay takes its rate from
@@ -362,8 +364,8 @@ class AdamW:
 
     @torch.no_grad()
     def step(self, norm: Optional[torch.Tensor] = None, max_norm: float = 1.0, clip_eps: float = 1e-6) -> None:
-        """One step.  norm: the gradients' global norm (grad_norm), by which they are
-        clipped to max_norm on the way."""
+        """One step.  norm: the gradients' global norm (grad_norm; float32 [1]), by which
+        they are clipped to max_norm on the way."""
         groups = {}
         for i, p in enumerate(self.params):
             if p.grad is not None:
